@@ -12,7 +12,8 @@ been built (``fine_tuning_gb300.build.build()``); there is no fallback.
 __version__ = "0.1.0"
 
 _BINDING = ("rmsnorm_fwd", "rmsnorm_bwd", "rmsnorm_bwd_workspace_bytes", "swiglu_fwd",
-            "swiglu_bwd", "qk_rope_fwd", "qk_rope_bwd", "FtkError", "library")
+            "swiglu_bwd", "qk_rope_fwd", "qk_rope_bwd", "qk_mrope_fwd", "qk_mrope_bwd", "attn_fwd",
+            "attn_bwd", "attn_bwd_workspace_bytes", "FtkError", "library")
 
 
 def __getattr__(name):

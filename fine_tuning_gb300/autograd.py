@@ -113,6 +113,43 @@ class QKNormRope(torch.autograd.Function):
         return gq, gk, dwq.to(wq.dtype), dwk.to(wk.dtype), None, None, None, None
 
 
+class QKMrope(torch.autograd.Function):
+    """q [T, Hq, D] and k [T, Hkv, D] turned by positions on several axes
+    (pos int32 [axes, T]; axis_of: D/2 axes on the host)."""
+
+    @staticmethod
+    def forward(ctx, q, k, pos, axis_of, theta: float, inv_freq=None):
+        ctx.save_for_backward(pos)
+        ctx.axis_of, ctx.theta, ctx.inv_freq = axis_of, theta, inv_freq
+        return ftk.qk_mrope_fwd(q, k, pos, axis_of, theta=theta, inv_freq=inv_freq)
+
+    @staticmethod
+    def backward(ctx, dq, dk):
+        (pos,) = ctx.saved_tensors
+        dq, dk = ftk.qk_mrope_bwd(dq.contiguous(), dk.contiguous(), pos, ctx.axis_of,
+                                  theta=ctx.theta, inv_freq=ctx.inv_freq)
+        return dq, dk, None, None, None, None
+
+
+class Attention(torch.autograd.Function):
+    """Attention inside every sequence of a packed batch (ftk.attn_fwd).  Every
+    token must belong to a sequence (cu_seqlens from 0 to T)."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, cu_seqlens, scale=None, causal: bool = True):
+        o, lse = ftk.attn_fwd(q, k, v, cu_seqlens, scale=scale, causal=causal)
+        ctx.save_for_backward(q, k, v, o, lse, cu_seqlens)
+        ctx.scale, ctx.causal = scale, causal
+        return o
+
+    @staticmethod
+    def backward(ctx, do):
+        q, k, v, o, lse, cu = ctx.saved_tensors
+        dq, dk, dv = ftk.attn_bwd(do.contiguous(), q, k, v, o, lse, cu, scale=ctx.scale,
+                                  causal=ctx.causal)
+        return dq, dk, dv, None, None, None
+
+
 class CrossEntropyHead(torch.autograd.Function):
     """Mean cross-entropy of the logits h W^T against y (int32; y outside
     [0, V) is ignored), the logits never materialised."""
@@ -149,6 +186,14 @@ def qk_rope(q, k, cu_seqlens, theta: float, inv_freq=None):
 
 def qk_norm_rope(q, k, wq, wk, cu_seqlens, eps: float, theta: float, inv_freq=None):
     return QKNormRope.apply(q, k, wq, wk, cu_seqlens, eps, theta, inv_freq)
+
+
+def qk_mrope(q, k, pos, axis_of, theta: float, inv_freq=None):
+    return QKMrope.apply(q, k, pos, axis_of, theta, inv_freq)
+
+
+def attention(q, k, v, cu_seqlens, scale=None, causal: bool = True):
+    return Attention.apply(q, k, v, cu_seqlens, scale, causal)
 
 
 def cross_entropy_head(h, W, y):

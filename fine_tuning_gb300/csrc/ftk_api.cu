@@ -780,6 +780,200 @@ FTK_API ftk_status ftk_qk_norm_rope_bwd_checked(
                           B, T, Hq, Hkv, D, theta, inv_freq, eps, dtype, stream, seqlens_status);
 }
 
+// ------------------------------------------------ QK-RoPE on several axes
+
+}  // extern "C"
+
+namespace {
+
+ftk_status qk_mrope(const void *q, int64_t ld_q, const void *k, int64_t ld_k, void *q_out,
+                    int64_t ld_qo, void *k_out, int64_t ld_ko, const int32_t *pos, int64_t ld_pos,
+                    int32_t axes, const int32_t *axis_of, int64_t T, int32_t Hq, int32_t Hkv,
+                    int32_t D, double theta, const double *inv_freq, ftk_dtype dtype,
+                    ftk_stream_t stream, bool backward) {
+  if (!valid_dtype(dtype)) return FTK_ERR_DTYPE;
+  if (T < 0 || Hq < 0 || Hkv < 0 || (int64_t)Hq + Hkv < 1 || D < 2 || D % 2 != 0 ||
+      D / 2 > ftk::kRopeMaxHalf || T >= (int64_t(1) << 31) || axes < 1 || axes > 256 || ld_pos < T)
+    return FTK_ERR_SHAPE;
+  if (!axis_of) return FTK_ERR_NULL;
+  for (int32_t i = 0; i < D / 2; ++i)
+    if (axis_of[i] < 0 || axis_of[i] >= axes) return FTK_ERR_SHAPE;
+  if (inv_freq) {
+    for (int32_t i = 0; i < D / 2; ++i)
+      if (!(inv_freq[i] >= 0.0 && inv_freq[i] <= 1.0)) return FTK_ERR_SHAPE;  // NaN fails too
+  } else if (!(theta > 0.0)) {
+    return FTK_ERR_SHAPE;
+  }
+  const int64_t wq = (int64_t)Hq * D, wk = (int64_t)Hkv * D;
+  if ((Hq > 0 && (ld_q < wq || ld_qo < wq)) || (Hkv > 0 && (ld_k < wk || ld_ko < wk)))
+    return FTK_ERR_SHAPE;
+  if (T == 0) return FTK_OK;
+  if (!pos || (Hq > 0 && (!q || !q_out)) || (Hkv > 0 && (!k || !k_out))) return FTK_ERR_NULL;
+  const DType dt = (DType)dtype;
+  const int64_t es = ftk::dtype_bytes(dt);
+  if (!aligned(pos, 4) || (Hq > 0 && (!aligned(q, es) || !aligned(q_out, es))) ||
+      (Hkv > 0 && (!aligned(k, es) || !aligned(k_out, es))))
+    return FTK_ERR_ALIGN;
+  const int64_t tq = Hq > 0 ? T : 0, tk = Hkv > 0 ? T : 0;
+  const View vq = view(q, tq, ld_q, wq, es), vk = view(k, tk, ld_k, wk, es);
+  const View vqo = view(q_out, tq, ld_qo, wq, es), vko = view(k_out, tk, ld_ko, wk, es);
+  const View vp = view(pos, axes, ld_pos, T, 4);
+  // each output may replace its input exactly
+  if (!same_view(vq, vqo) && may_overlap(vq, vqo)) return FTK_ERR_ALIAS;
+  if (!same_view(vk, vko) && may_overlap(vk, vko)) return FTK_ERR_ALIAS;
+  if (may_overlap(vqo, vko) || may_overlap(vqo, vk) || may_overlap(vko, vq) ||
+      may_overlap(vp, vqo) || may_overlap(vp, vko))
+    return FTK_ERR_ALIAS;
+  const int n = dt == DType::F32 ? 4 : 8;
+  const bool vec =
+      (D / 2) % n == 0 &&
+      (Hq == 0 || (aligned(q, 16) && aligned(q_out, 16) && ld_q % n == 0 && ld_qo % n == 0)) &&
+      (Hkv == 0 || (aligned(k, 16) && aligned(k_out, 16) && ld_k % n == 0 && ld_ko % n == 0));
+  ftk::DeviceInfo dev;
+  cudaError_t e = device_info(&dev);
+  if (e != cudaSuccess) return cuda_fail(e);
+  ftk::QkMropeArgs a{q,      ld_q, k,   ld_k, q_out, ld_qo, k_out,    ld_ko,   pos,
+                     ld_pos, axis_of, T, Hq,   Hkv,   D,     theta, inv_freq, backward};
+  return finish(ftk::launch_qk_mrope(dt, vec, a, dev, (cudaStream_t)stream));
+}
+
+}  // namespace
+
+extern "C" {
+
+FTK_API ftk_status ftk_qk_mrope_fwd(const void *q, int64_t ld_q, const void *k, int64_t ld_k,
+                                    void *q_out, int64_t ld_qo, void *k_out, int64_t ld_ko,
+                                    const int32_t *pos, int64_t ld_pos, int32_t axes,
+                                    const int32_t *axis_of, int64_t T, int32_t Hq, int32_t Hkv,
+                                    int32_t D, double theta, const double *inv_freq,
+                                    ftk_dtype dtype, ftk_stream_t stream) {
+  return qk_mrope(q, ld_q, k, ld_k, q_out, ld_qo, k_out, ld_ko, pos, ld_pos, axes, axis_of, T, Hq,
+                  Hkv, D, theta, inv_freq, dtype, stream, false);
+}
+
+FTK_API ftk_status ftk_qk_mrope_bwd(const void *dq_out, int64_t ld_gq, const void *dk_out,
+                                    int64_t ld_gk, void *dq, int64_t ld_dq, void *dk,
+                                    int64_t ld_dk, const int32_t *pos, int64_t ld_pos,
+                                    int32_t axes, const int32_t *axis_of, int64_t T, int32_t Hq,
+                                    int32_t Hkv, int32_t D, double theta, const double *inv_freq,
+                                    ftk_dtype dtype, ftk_stream_t stream) {
+  return qk_mrope(dq_out, ld_gq, dk_out, ld_gk, dq, ld_dq, dk, ld_dk, pos, ld_pos, axes, axis_of,
+                  T, Hq, Hkv, D, theta, inv_freq, dtype, stream, true);
+}
+
+// ---------------------------------------------------------------- attention
+
+}  // extern "C"
+
+namespace {
+
+// Sizes shared by the forward and the backward; row strides are the caller's.
+ftk_status attn_shape(int32_t B, int64_t T, int32_t Hq, int32_t Hkv, int32_t D, float scale) {
+  if (T < 0 || T >= (int64_t(1) << 31) || B < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || D < 1 ||
+      D > ftk::kAttnMaxD || !(scale > 0.f) || !std::isfinite(scale))
+    return FTK_ERR_SHAPE;
+  if (T > 0 && B < 1) return FTK_ERR_SHAPE;
+  // one block per (tile, head): the count must fit a grid
+  if ((T / ftk::kAttnMinTile + B) > ((int64_t(1) << 31) - 1) / Hq) return FTK_ERR_SHAPE;
+  return FTK_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+FTK_API ftk_status ftk_attn_fwd(const void *q, int64_t ld_q, const void *k, int64_t ld_k,
+                                const void *v, int64_t ld_v, void *o, int64_t ld_o, float *lse,
+                                const int32_t *cu_seqlens, int32_t B, int64_t T, int32_t Hq,
+                                int32_t Hkv, int32_t D, float scale, int32_t causal,
+                                const uint32_t *seqlens_status, ftk_dtype dtype,
+                                ftk_stream_t stream) {
+  if (!valid_dtype(dtype)) return FTK_ERR_DTYPE;
+  ftk_status st = attn_shape(B, T, Hq, Hkv, D, scale);
+  if (st != FTK_OK) return st;
+  const int64_t wq = (int64_t)Hq * D, wk = (int64_t)Hkv * D;
+  if (ld_q < wq || ld_k < wk || ld_v < wk || ld_o < wq) return FTK_ERR_SHAPE;
+  if (T == 0) return FTK_OK;
+  if (!q || !k || !v || !o || !cu_seqlens) return FTK_ERR_NULL;
+  const DType dt = (DType)dtype;
+  const int64_t es = ftk::dtype_bytes(dt);
+  if (!aligned(q, es) || !aligned(k, es) || !aligned(v, es) || !aligned(o, es) ||
+      !aligned(lse, 4) || !aligned(cu_seqlens, 4) || !aligned(seqlens_status, 4))
+    return FTK_ERR_ALIGN;
+  const View vq = view(q, T, ld_q, wq, es), vk = view(k, T, ld_k, wk, es);
+  const View vv = view(v, T, ld_v, wk, es), vo = view(o, T, ld_o, wq, es);
+  const View vl = view(lse, lse ? 1 : 0, (int64_t)Hq * T, (int64_t)Hq * T, 4);
+  const View vc = view(cu_seqlens, 1, (int64_t)B + 1, (int64_t)B + 1, 4);
+  const View vs = view(seqlens_status, seqlens_status ? 1 : 0, 1, 1, 4);
+  for (const View &in : {vq, vk, vv, vc, vs})
+    if (may_overlap(vo, in) || may_overlap(vl, in)) return FTK_ERR_ALIAS;
+  if (may_overlap(vo, vl)) return FTK_ERR_ALIAS;
+  ftk::DeviceInfo dev;
+  cudaError_t e = device_info(&dev);
+  if (e != cudaSuccess) return cuda_fail(e);
+  ftk::AttnArgs a{q,  ld_q, k,   ld_k, v, ld_v,  o,      ld_o,          lse, cu_seqlens,
+                  B,  T,    Hq,  Hkv,  D, scale, causal, seqlens_status};
+  return finish(ftk::launch_attn_fwd_generic(dt, a, dev, (cudaStream_t)stream));
+}
+
+FTK_API size_t ftk_attn_bwd_workspace_bytes(int64_t T, int32_t Hq, int32_t Hkv, int32_t D,
+                                            ftk_dtype dtype) {
+  if (!valid_dtype(dtype) || T <= 0 || attn_shape(1, T, Hq, Hkv, D, 1.f) != FTK_OK) return 0;
+  return (size_t)T * (size_t)Hq * sizeof(float);
+}
+
+FTK_API ftk_status ftk_attn_bwd(const void *do_, int64_t ld_do, const void *q, int64_t ld_q,
+                                const void *k, int64_t ld_k, const void *v, int64_t ld_v,
+                                const void *o, int64_t ld_o, const float *lse, void *dq,
+                                int64_t ld_dq, void *dk, int64_t ld_dk, void *dv, int64_t ld_dv,
+                                void *workspace, size_t workspace_bytes,
+                                const int32_t *cu_seqlens, int32_t B, int64_t T, int32_t Hq,
+                                int32_t Hkv, int32_t D, float scale, int32_t causal,
+                                const uint32_t *seqlens_status, ftk_dtype dtype,
+                                ftk_stream_t stream) {
+  if (!valid_dtype(dtype)) return FTK_ERR_DTYPE;
+  ftk_status st = attn_shape(B, T, Hq, Hkv, D, scale);
+  if (st != FTK_OK) return st;
+  const int64_t wq = (int64_t)Hq * D, wk = (int64_t)Hkv * D;
+  if (ld_do < wq || ld_q < wq || ld_o < wq || ld_dq < wq || ld_k < wk || ld_v < wk || ld_dk < wk ||
+      ld_dv < wk)
+    return FTK_ERR_SHAPE;
+  if (T == 0) return FTK_OK;
+  if (!do_ || !q || !k || !v || !o || !lse || !dq || !dk || !dv || !cu_seqlens)
+    return FTK_ERR_NULL;
+  const size_t need = ftk_attn_bwd_workspace_bytes(T, Hq, Hkv, D, dtype);
+  if (!workspace || workspace_bytes < need) return FTK_ERR_WORKSPACE;
+  const DType dt = (DType)dtype;
+  const int64_t es = ftk::dtype_bytes(dt);
+  for (const void *p : {do_, q, k, v, o, (const void *)dq, (const void *)dk, (const void *)dv})
+    if (!aligned(p, es)) return FTK_ERR_ALIGN;
+  if (!aligned(lse, 4) || !aligned(cu_seqlens, 4) || !aligned(seqlens_status, 4) ||
+      !aligned(workspace, 16))
+    return FTK_ERR_ALIGN;
+  const int64_t ws_len = (int64_t)need;
+  const View outs[4] = {view(dq, T, ld_dq, wq, es), view(dk, T, ld_dk, wk, es),
+                        view(dv, T, ld_dv, wk, es), view(workspace, 1, ws_len, ws_len, 1)};
+  const View ins[8] = {view(do_, T, ld_do, wq, es), view(q, T, ld_q, wq, es),
+                       view(k, T, ld_k, wk, es),    view(v, T, ld_v, wk, es),
+                       view(o, T, ld_o, wq, es),
+                       view(lse, 1, (int64_t)Hq * T, (int64_t)Hq * T, 4),
+                       view(cu_seqlens, 1, (int64_t)B + 1, (int64_t)B + 1, 4),
+                       view(seqlens_status, seqlens_status ? 1 : 0, 1, 1, 4)};
+  for (int i = 0; i < 4; ++i) {
+    for (int m = 0; m < 8; ++m)
+      if (may_overlap(outs[i], ins[m])) return FTK_ERR_ALIAS;
+    for (int m = i + 1; m < 4; ++m)
+      if (may_overlap(outs[i], outs[m])) return FTK_ERR_ALIAS;
+  }
+  ftk::DeviceInfo dev;
+  cudaError_t e = device_info(&dev);
+  if (e != cudaSuccess) return cuda_fail(e);
+  ftk::AttnArgs a{q,  ld_q, k,  ld_k, v,     ld_v,   (void *)o,      ld_o, (float *)lse, cu_seqlens,
+                  B,  T,    Hq, Hkv,  D,     scale,  causal, seqlens_status, do_,  ld_do,
+                  dq, ld_dq, dk, ld_dk, dv, ld_dv, (float *)workspace};
+  return finish(ftk::launch_attn_bwd_generic(dt, a, dev, (cudaStream_t)stream));
+}
+
 // ------------------------------------------------------ tensor-core GEMM
 
 FTK_API ftk_status ftk_gemm_bf16_ex(const void *a, int64_t lda, int a_mn, const void *b,

@@ -94,6 +94,16 @@ def library() -> ctypes.CDLL:
                                          vp, dt, vp]),
         "ftk_qk_rope_bwd_checked": (st, [vp, i64, vp, i64, vp, i32, i64, i32, i32, i32, f64, vp,
                                          vp, dt, vp]),
+        "ftk_qk_mrope_fwd": (st, [vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, i32, vp, i64, i32,
+                                  i32, i32, f64, vp, dt, vp]),
+        "ftk_qk_mrope_bwd": (st, [vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, i32, vp, i64, i32,
+                                  i32, i32, f64, vp, dt, vp]),
+        "ftk_attn_fwd": (st, [vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, i32, i64, i32, i32,
+                              i32, f32, i32, vp, dt, vp]),
+        "ftk_attn_bwd_workspace_bytes": (sz, [i64, i32, i32, i32, dt]),
+        "ftk_attn_bwd": (st, [vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, i64, vp, i64,
+                              vp, i64, vp, sz, vp, i32, i64, i32, i32, i32, f32, i32, vp, dt,
+                              vp]),
         "ftk_bfd_pack": (st, [vp, i64, i32, vp, vp, vp, vp]),
         "ftk_device_status": (st, [ctypes.POINTER(ctypes.c_uint32), ctypes.c_int]),
         "ftk_selftest_wait_timeout": (st, [i64, vp]),
@@ -534,6 +544,175 @@ def rope_llama3_inv_freq(D: int, theta: float, factor: float, low_freq_factor: f
           float(high_freq_factor), float(original_max_position),
           out.ctypes.data_as(ctypes.c_void_p))
     return out
+
+
+# ------------------------------------------------ QK-RoPE on several axes
+
+def _same_device(ref: torch.Tensor, *ts):
+    """Every tensor given lives on ref's CUDA device."""
+    if not ref.is_cuda:
+        raise ValueError("ftk ops take CUDA tensors (move inputs with .cuda())")
+    for t in ts:
+        if t is not None and t.device != ref.device:
+            raise ValueError(f"tensors on different devices: {t.device} and {ref.device}")
+
+
+def _call_on(ref: torch.Tensor, name: str, *args) -> None:
+    """_call on ref's device (made the current one for the launch) and that
+    device's current stream."""
+    if ref.device.index == torch.cuda.current_device():
+        _call(name, *args, _stream(ref))
+    else:
+        with torch.cuda.device(ref.device):
+            _call(name, *args, _stream(ref))
+
+
+def mrope_axis_of(sections) -> np.ndarray:
+    """int32 [D/2]: the axis of each frequency when axis a takes the next
+    sections[a] of the D/2 frequencies, in order."""
+    sec = np.asarray(sections)
+    if sec.ndim != 1 or sec.size < 1 or not np.issubdtype(sec.dtype, np.integer) \
+            or int(sec.min()) < 0 or int(sec.sum()) < 1:
+        raise ValueError("sections must be non-negative integers that sum to D/2")
+    return np.repeat(np.arange(sec.size), sec).astype(np.int32)
+
+
+def _mrope(name, q, k, pos, axis_of, theta, inv_freq, q_out, k_out):
+    ref = q if q is not None else k
+    if ref is None:
+        raise ValueError("q or k is needed")
+    _same_device(ref, q, k, pos, q_out, k_out)
+    if q is not None and q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if k is not None and k_out is None:
+        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    ldq, Hq, Dq = _heads(q, "q")
+    ldk, Hkv, Dk = _heads(k, "k")
+    ldqo, ldko = _heads(q_out, "q_out")[0], _heads(k_out, "k_out")[0]
+    T, D = ref.shape[0], ref.shape[2]
+    if q is not None and k is not None and (k.shape[0] != T or Dk != Dq or k.dtype != q.dtype):
+        raise ValueError("q and k must agree in tokens, head_dim and dtype")
+    for x, y in ((q, q_out), (k, k_out)):
+        if (x is None) != (y is None) or (x is not None and (y.shape != x.shape
+                                                             or y.dtype != x.dtype)):
+            raise ValueError("q_out and k_out must match q and k in shape and dtype")
+    if pos.dtype != torch.int32 or pos.dim() != 2 or pos.shape[1] != T \
+            or (T > 1 and pos.stride(1) != 1):
+        raise ValueError("pos must be int32 [axes, T] with unit stride along tokens")
+    axes = pos.shape[0]
+    ldp = max(pos.stride(0), T) if axes == 1 else pos.stride(0)
+    table = np.ascontiguousarray(np.asarray(axis_of, dtype=np.int32))
+    if table.shape != (D // 2,):
+        raise ValueError("axis_of must hold D/2 axes")
+    freq, freq_p = _table(inv_freq, D)
+    _call_on(ref, name, _ptr(q), ldq, _ptr(k), ldk, _ptr(q_out), ldqo, _ptr(k_out), ldko,
+             _ptr(pos), ldp, axes, table.ctypes.data, T, Hq, Hkv, D, float(theta or 0.0), freq_p,
+             _code(ref))
+    del table, freq
+    return q_out, k_out
+
+
+def qk_mrope_fwd(q, k, pos, axis_of, theta: float = 0.0, inv_freq=None, q_out=None, k_out=None):
+    """q [T, Hq, D] and k [T, Hkv, D] turned by positions on several axes:
+    frequency i by pos[axis_of[i], t] * theta^(-2i/D) (or * inv_freq[i]).
+    pos: int32 [axes, T] on the device; axis_of: D/2 axes on the host (see
+    mrope_axis_of).  Returns (q_out, k_out); q_out=q / k_out=k turn in place."""
+    return _mrope("ftk_qk_mrope_fwd", q, k, pos, axis_of, theta, inv_freq, q_out, k_out)
+
+
+def qk_mrope_bwd(dq_out, dk_out, pos, axis_of, theta: float = 0.0, inv_freq=None, dq=None,
+                 dk=None):
+    """Backward of qk_mrope_fwd: (dq, dk), the gradients turned by -phi
+    (dq=dq_out / dk=dk_out in place)."""
+    return _mrope("ftk_qk_mrope_bwd", dq_out, dk_out, pos, axis_of, theta, inv_freq, dq, dk)
+
+
+# -------------------------------------------------------------- attention
+
+def _attn_check(q, k, v, cu_seqlens, seqlens_status, *rest):
+    _same_device(q, k, v, cu_seqlens, seqlens_status, *rest)
+    _cu_check(cu_seqlens)
+    if cu_seqlens.numel() < 1:
+        raise ValueError("cu_seqlens must hold at least one boundary")
+    if seqlens_status is not None:
+        _status_check(seqlens_status)
+    if k.shape != v.shape or k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2] \
+            or k.dtype != q.dtype or v.dtype != q.dtype:
+        raise ValueError("q [T, Hq, D], k and v [T, Hkv, D] must agree in tokens, head_dim, dtype")
+
+
+def _like(x: torch.Tensor, y: Optional[torch.Tensor], name: str) -> torch.Tensor:
+    if y is None:
+        return torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    if y.shape != x.shape or y.dtype != x.dtype:
+        raise ValueError(f"{name} must be {tuple(x.shape)} {x.dtype}")
+    return y
+
+
+def attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
+             scale: Optional[float] = None, causal: bool = True,
+             o: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+             save_lse: bool = True, seqlens_status: Optional[torch.Tensor] = None
+             ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Attention of q [T, Hq, D] over k, v [T, Hkv, D] inside every sequence of
+    a packed batch; returns (o [T, Hq, D], lse fp32 [Hq, T]).  scale defaults
+    to D^-0.5.  Rows of no sequence are left as they were (uninitialised in an
+    output allocated here).  seqlens_status: the word check_seqlens wrote; a
+    non-zero word leaves every output untouched."""
+    ldq, Hq, D = _heads(q, "q")
+    ldk, Hkv, _ = _heads(k, "k")
+    ldv, _, _ = _heads(v, "v")
+    _attn_check(q, k, v, cu_seqlens, seqlens_status, o, lse)
+    T = q.shape[0]
+    o = _like(q, o, "o")
+    if lse is None and save_lse:
+        lse = torch.empty((Hq, T), dtype=torch.float32, device=q.device)
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (Hq, T)
+                            or not lse.is_contiguous()):
+        raise ValueError("lse must be a contiguous fp32 [Hq, T] tensor")
+    _call_on(q, "ftk_attn_fwd", _ptr(q), ldq, _ptr(k), ldk, _ptr(v), ldv, _ptr(o),
+             _heads(o, "o")[0], _ptr(lse), _ptr(cu_seqlens), cu_seqlens.numel() - 1, T, Hq, Hkv, D,
+             float(D ** -0.5 if scale is None else scale), int(bool(causal)),
+             _ptr(seqlens_status), _code(q))
+    return o, lse
+
+
+def attn_bwd_workspace_bytes(T: int, Hq: int, Hkv: int, D: int, dtype: torch.dtype) -> int:
+    return int(library().ftk_attn_bwd_workspace_bytes(T, Hq, Hkv, D, _DTYPES[dtype]))
+
+
+def attn_bwd(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
+             lse: torch.Tensor, cu_seqlens: torch.Tensor, scale: Optional[float] = None,
+             causal: bool = True, dq: Optional[torch.Tensor] = None,
+             dk: Optional[torch.Tensor] = None, dv: Optional[torch.Tensor] = None,
+             workspace: Optional[torch.Tensor] = None,
+             seqlens_status: Optional[torch.Tensor] = None
+             ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """Backward of attn_fwd from its output o and lse: (dq, dk, dv).  The
+    probabilities are recomputed; the results are bitwise reproducible.
+    dq, dk, dv may be slices of one fused [T, Hq + 2 Hkv, D] buffer."""
+    ldq, Hq, D = _heads(q, "q")
+    ldk, Hkv, _ = _heads(k, "k")
+    ldv, _, _ = _heads(v, "v")
+    _attn_check(q, k, v, cu_seqlens, seqlens_status, do, o, lse, dq, dk, dv, workspace)
+    T = q.shape[0]
+    for t, name in ((do, "do"), (o, "o")):
+        if t.shape != q.shape or t.dtype != q.dtype:
+            raise ValueError(f"{name} must match q in shape and dtype")
+    if lse.dtype != torch.float32 or lse.shape != (Hq, T) or not lse.is_contiguous():
+        raise ValueError("lse must be a contiguous fp32 [Hq, T] tensor")
+    dq, dk, dv = _like(q, dq, "dq"), _like(k, dk, "dk"), _like(v, dv, "dv")
+    if workspace is None:
+        workspace = torch.empty(max(16, attn_bwd_workspace_bytes(T, Hq, Hkv, D, q.dtype)),
+                                dtype=torch.uint8, device=q.device)
+    _call_on(q, "ftk_attn_bwd", _ptr(do), _heads(do, "do")[0], _ptr(q), ldq, _ptr(k), ldk, _ptr(v),
+             ldv, _ptr(o), _heads(o, "o")[0], _ptr(lse), _ptr(dq), _heads(dq, "dq")[0], _ptr(dk),
+             _heads(dk, "dk")[0], _ptr(dv), _heads(dv, "dv")[0], _ptr(workspace),
+             workspace.numel() * workspace.element_size(), _ptr(cu_seqlens),
+             cu_seqlens.numel() - 1, T, Hq, Hkv, D,
+             float(D ** -0.5 if scale is None else scale), int(bool(causal)),
+             _ptr(seqlens_status), _code(q))
+    return dq, dk, dv
 
 
 # ------------------------------------------------------ Cut Cross-Entropy

@@ -413,6 +413,109 @@ FTK_API ftk_status ftk_qk_norm_rope_bwd_checked(
     const double *inv_freq, float eps, const uint32_t *seqlens_status, ftk_dtype dtype,
     ftk_stream_t stream);
 
+/* ------------------------------------------------ QK-RoPE on several axes */
+
+/* Rotary embedding of Q and K by positions on several axes (time, height and
+ * width of image and video tokens, say; any number of axes), rotate-half
+ * layout, both in one kernel:
+ *   phi_i(t) = pos[axis_of[i]][t] * f_i,  f_i = theta^(-2i/D) or inv_freq[i]
+ * and every head vector x of Q and K at token t becomes
+ *   y[i]     = x[i] cos(phi_i) - x[i+D/2] sin(phi_i)
+ *   y[i+D/2] = x[i+D/2] cos(phi_i) + x[i] sin(phi_i),     i < D/2.
+ * With every axis holding a token's place in its sequence this is
+ * ftk_qk_rope_fwd's rotation.  The pages rotate by one axis; this is the
+ * library's variant for the models that take images.
+ * q [T, ld_q] with Hq heads of D contiguous values, k [T, ld_k] with Hkv
+ * (Hq, Hkv >= 0, Hq + Hkv >= 1; the pointers of an absent one may be NULL);
+ * q_out [T, ld_qo], k_out [T, ld_ko]: q_out may be q and k_out may be k
+ * exactly (rotation in place), otherwise outputs overlap nothing.
+ * pos: DEVICE int32 [axes, ld_pos], axes <= 256, ld_pos >= T, any value (negative
+ * ones too); axis_of: HOST int32 [D/2], entries in [0, axes), else FTK_ERR_SHAPE,
+ * so that runs of frequencies and interleaved ones are both a table;
+ * inv_freq: HOST double [D/2] in [0, 1], nullable (then theta > 0 is used);
+ * both are read during the call only.  0 < D <= 512, D even.
+ * The angle is formed as in ftk_qk_rope_fwd (~1e-7 rad at positions below
+ * 2^20, growing with the position beyond).  Offsets are 64-bit. */
+FTK_API ftk_status ftk_qk_mrope_fwd(const void *q, int64_t ld_q, const void *k, int64_t ld_k,
+                                    void *q_out, int64_t ld_qo, void *k_out, int64_t ld_ko,
+                                    const int32_t *pos, int64_t ld_pos, int32_t axes,
+                                    const int32_t *axis_of, int64_t T, int32_t Hq, int32_t Hkv,
+                                    int32_t D, double theta, const double *inv_freq,
+                                    ftk_dtype dtype, ftk_stream_t stream);
+
+/* Backward of ftk_qk_mrope_fwd: the gradients dq_out, dk_out turned by
+ * -phi into dq, dk (which may be dq_out, dk_out exactly).  Same rules. */
+FTK_API ftk_status ftk_qk_mrope_bwd(const void *dq_out, int64_t ld_gq, const void *dk_out,
+                                    int64_t ld_gk, void *dq, int64_t ld_dq, void *dk,
+                                    int64_t ld_dk, const int32_t *pos, int64_t ld_pos,
+                                    int32_t axes, const int32_t *axis_of, int64_t T, int32_t Hq,
+                                    int32_t Hkv, int32_t D, double theta, const double *inv_freq,
+                                    ftk_dtype dtype, ftk_stream_t stream);
+
+/* -------------------------------------------------------------- attention */
+
+/* Self-attention over a packed batch of B variable-length sequences, the
+ * consumer of the rotated Q and K (the auto-packing paragraph of the Unsloth
+ * item on seventnews.com: one 1-D token tensor plus sequence-length metadata;
+ * the page prints no formula, this is the standard softmax attention).  For
+ * query head h, key head h' = h / (Hq / Hkv) and tokens i, j of one sequence:
+ *   s[i,j]    = scale * sum_d q[i,h,d] k[j,h',d]   (j <= i when causal != 0)
+ *   lse[h,i]  = log sum_j exp(s[i,j])
+ *   o[i,h,d]  = sum_j exp(s[i,j] - lse[h,i]) v[j,h',d]
+ * No score reaches memory: keys are walked in tiles with a running maximum
+ * and sum (fp32).
+ * q [T, ld_q] with Hq heads of D contiguous values per token, k [T, ld_k] and
+ * v [T, ld_v] with Hkv heads, o [T, ld_o] with Hq; Hq a multiple of Hkv; q, k
+ * and v may be interleaved slices of one fused QKV buffer, o must overlap no
+ * input.  lse: fp32 [Hq, T] contiguous (head-major), nullable; the backward
+ * needs it.  1 <= D <= 256; scale > 0 and finite.
+ * cu_seqlens: DEVICE int32 [B+1], non-decreasing within [0, T]; read on the
+ * device.  Rows of o and lse that belong to no sequence (before cu[0], at or
+ * past cu[B]) are left as they were.  Boundaries that decrease or leave
+ * [0, T] give unspecified results, every access inside the tensors;
+ * seqlens_status (DEVICE uint32, nullable) is the word ftk_check_seqlens
+ * wrote: when it is non-zero the kernels return without writing anything.
+ * A sequence never sees another's values, infinities and NaN included; inside
+ * a sequence a masked infinity or NaN may reach the rows of its own tile
+ * (0 * inf), as in any product with masked probabilities.
+ * bf16 with D a multiple of 8 up to 128, 16-byte aligned pointers and row
+ * strides that are multiples of 8 runs on the tensor cores (probabilities
+ * rounded to bf16 for the second product); anything else on the CUDA cores in
+ * fp32.  (T / 32 + B) * Hq must stay below 2^31, else FTK_ERR_SHAPE. */
+FTK_API ftk_status ftk_attn_fwd(const void *q, int64_t ld_q, const void *k, int64_t ld_k,
+                                const void *v, int64_t ld_v, void *o, int64_t ld_o, float *lse,
+                                const int32_t *cu_seqlens, int32_t B, int64_t T, int32_t Hq,
+                                int32_t Hkv, int32_t D, float scale, int32_t causal,
+                                const uint32_t *seqlens_status, ftk_dtype dtype,
+                                ftk_stream_t stream);
+
+/* Bytes of device workspace ftk_attn_bwd needs (0 when T is 0 or the
+ * arguments are invalid). */
+FTK_API size_t ftk_attn_bwd_workspace_bytes(int64_t T, int32_t Hq, int32_t Hkv, int32_t D,
+                                            ftk_dtype dtype);
+
+/* Backward of ftk_attn_fwd.  The probabilities are made again from q, k and
+ * the forward's lse; with delta[h,i] = sum_d do[i,h,d] o[i,h,d]:
+ *   p  = exp(s - lse),  dv[j,h'] = sum_{h,i} p[i,j] do[i,h]
+ *   ds = p * (do v^T - delta)
+ *   dq[i,h] = scale sum_j ds[i,j] k[j,h'],  dk[j,h'] = scale sum_{h,i} ds[i,j] q[i,h]
+ * (sums over h: the query heads that share h').  do_ and o [T, Hq heads],
+ * lse as the forward wrote it; dq [T, ld_dq], dk [T, ld_dk], dv [T, ld_dv]
+ * (may be slices of one fused buffer) overlap no input; rows of no sequence
+ * are left as they were.  workspace: >= ftk_attn_bwd_workspace_bytes(...)
+ * bytes, 16-byte aligned, contents ignored and clobbered; calls that overlap
+ * on the GPU need one each.  Every sum has a fixed order (no atomics): the
+ * gradients are bitwise reproducible run to run.  Other rules as above. */
+FTK_API ftk_status ftk_attn_bwd(const void *do_, int64_t ld_do, const void *q, int64_t ld_q,
+                                const void *k, int64_t ld_k, const void *v, int64_t ld_v,
+                                const void *o, int64_t ld_o, const float *lse, void *dq,
+                                int64_t ld_dq, void *dk, int64_t ld_dk, void *dv, int64_t ld_dv,
+                                void *workspace, size_t workspace_bytes,
+                                const int32_t *cu_seqlens, int32_t B, int64_t T, int32_t Hq,
+                                int32_t Hkv, int32_t D, float scale, int32_t causal,
+                                const uint32_t *seqlens_status, ftk_dtype dtype,
+                                ftk_stream_t stream);
+
 /* ------------------------------------------------------ tensor-core GEMM */
 
 /* C = A B^T on the 5th-generation tensor cores: A bf16 [M, lda], B bf16
