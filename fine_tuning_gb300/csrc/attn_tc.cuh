@@ -1,0 +1,215 @@
+// Tensor-core pieces shared by the attention kernels (attn_fwd_tc.cu,
+// attn_bwd_tc.cu): single-CTA tcgen05 instructions, tile loads, descriptors
+// of the staged tiles, tensor-memory loads and stores, bounded waits.
+//
+// Every operand tile is kTile = 128 rows (tokens) of one head, staged as boxes
+// of 64 columns: 128 rows x 128 bytes with the 128-byte swizzle, 16 KB each,
+// box j at j x 16 KB.  The same bytes serve as a K-major operand (rows = M or
+// N, the head's columns contracted) and as an MN-major one (columns = N, the
+// rows contracted), so no tile is ever transposed or staged twice.
+#pragma once
+
+#include "attn_common.cuh"
+#include "tc_gemm.cuh"
+
+namespace ftk {
+namespace attn {
+
+using tc::tc_fence_after;
+using tc::tc_fence_before;
+using tc::tmem_ld32;
+using tc::tmem_ld64;
+
+constexpr int kTile = 128;
+constexpr uint32_t kBoxBytes = kTile * 128;  // 64 bf16 columns of a tile
+
+// One tensor [T, H, D] read in boxes of 128 tokens x one head x 64 columns;
+// columns past D and tokens past T read as zeros.
+cudaError_t make_head_map(CUtensorMap *map, const void *base, int64_t T, int64_t H, int64_t D,
+                          int64_t ld);
+
+__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *map, int col, int head,
+                                         int row, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(col), "r"(head), "r"(row), "r"(smem_addr(bar))
+      : "memory");
+}
+
+// A whole tile: DP / 64 boxes.
+template <int DP>
+__device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap *map, int head, int row,
+                                          uint64_t *bar) {
+  mbar_arrive_expect_tx(bar, (DP / 64) * kBoxBytes);
+#pragma unroll
+  for (int j = 0; j < DP / 64; ++j) load_box(dst + j * kBoxBytes, map, 64 * j, head, row, bar);
+}
+
+__device__ __forceinline__ void tmem_alloc1(uint32_t *slot, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                   smem_addr(slot)),
+               "r"(ncols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc1(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols)
+               : "memory");
+}
+
+// One lane of a converged warp.  The instructions below read their operands
+// from the warp's uniform registers; with elect.sync the compiler knows that
+// one lane runs them and keeps those registers right.  Under a plain test of
+// the lane number inside a loop, MMAs were measured to run with another MMA's
+// descriptor (wrong scores at best, an illegal address at worst), so every
+// tensor-core and tile-load instruction of the attention kernels is issued by
+// a whole warp's control flow under this election.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r)::"memory");
+  return r != 0;
+}
+
+// D [128 x N] (+)= A B^T, A and B in shared memory.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// The same with A in tensor memory: row i in lane i, two bf16 per column.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Arrives once on bar when this thread's earlier MMAs have completed.
+__device__ __forceinline__ void mma_commit(uint64_t *bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+          smem_addr(bar))
+      : "memory");
+}
+
+// Instruction descriptor, kind::f16, M = 128: D fp32, A and B bf16.
+__device__ __forceinline__ uint32_t idesc_of(int n, bool b_mn) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) |
+         ((uint32_t)(kTile >> 4) << 24);
+}
+// K-major operand, contraction step kk of 16 columns: box kk / 4, 32 bytes per step.
+__device__ __forceinline__ uint64_t desc_k(uint32_t tile, int kk) {
+  return tc::desc_sw128(tile + (uint32_t)(kk >> 2) * kBoxBytes + (uint32_t)(kk & 3) * 32u);
+}
+// MN-major operand, contraction step kk of 16 rows; 64-column blocks kBoxBytes
+// apart (leading byte offset), 8-row swizzle atoms 1024 bytes apart.
+__device__ __forceinline__ uint64_t desc_mn(uint32_t tile, int kk) {
+  const uint32_t addr = tile + (uint32_t)kk * (16u * 128u);
+  return (uint64_t)((addr & 0x3FFFF) >> 4) | ((uint64_t)(kBoxBytes >> 4) << 16) |
+         ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+// acc [128 x 128] = A B^T over nk steps of 16 columns (both tiles K-major).
+__device__ __forceinline__ void mma_rows(uint32_t acc, uint32_t a, uint32_t b, int nk) {
+  const uint32_t id = idesc_of(kTile, false);
+#pragma unroll
+  for (int kk = 0; kk < 8; ++kk)
+    if (kk < nk) mma_ss(acc, desc_k(a, kk), desc_k(b, kk), id, kk != 0);
+}
+// acc [128 x n] (+)= P B, P [128 x 128] bf16 in tensor memory, B's 128 rows contracted.
+__device__ __forceinline__ void mma_prob(uint32_t acc, uint32_t p, uint32_t b, int n,
+                                         bool accumulate) {
+  const uint32_t id = idesc_of(n, true);
+#pragma unroll
+  for (int kk = 0; kk < 8; ++kk)
+    mma_ts(acc, p + (uint32_t)kk * 8u, desc_mn(b, kk), id, accumulate || kk != 0);
+}
+
+// 16 (32) columns of this thread's lane from registers.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, "
+      "%29, %30, %31, %32};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]),
+      "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]),
+      "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]),
+      "r"(v[30]), "r"(v[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
+// 2^x by the hardware approximation (relative error about 2^-22, 2^-inf = +0).
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// The waits of a CTA: bounded, and over as soon as any role has given up.
+struct Waits {
+  volatile int *abort;
+  unsigned *status;
+  long long limit;
+  __device__ __forceinline__ bool operator()(uint64_t *bar, uint32_t parity) const {
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (!mbar_try_wait(bar, parity)) {
+      if (*abort) return false;
+      if (clock64() - t0 > limit) {
+        atomicOr(status, kStatusWaitTimeout);
+        *abort = 1;
+        return false;
+      }
+    }
+    return true;
+  }
+  // for a whole warp that goes on together or stops together
+  __device__ __forceinline__ bool all(uint64_t *bar, uint32_t parity) const {
+    return __all_sync(0xffffffffu, (*this)(bar, parity));
+  }
+};
+
+// Zeroes rows [from, 128) of a staged tile (whole warp): rows behind a
+// sequence's end hold another sequence's values, whose infinities would turn a
+// zero probability's product into NaN.
+template <int DP>
+__device__ __forceinline__ void zero_rows(unsigned char *tile, int from, int lane) {
+#pragma unroll
+  for (int j = 0; j < DP / 64; ++j) {
+    uint4 *p = reinterpret_cast<uint4 *>(tile + j * kBoxBytes);
+    for (int i = from * 8 + lane; i < kTile * 8; i += 32) p[i] = make_uint4(0u, 0u, 0u, 0u);
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+
+}  // namespace attn
+}  // namespace ftk

@@ -878,6 +878,13 @@ ftk_status attn_shape(int32_t B, int64_t T, int32_t Hq, int32_t Hkv, int32_t D, 
   return FTK_OK;
 }
 
+// What the tensor-core kernels take: bf16 heads of whole 16-byte packets that
+// fit two 64-column boxes, and tensors that TMA can address.
+bool attn_tc_shape(DType dt, int32_t D) { return dt == DType::BF16 && D % 8 == 0 && D <= 128; }
+bool attn_tc_tensor(const void *p, int64_t ld) {
+  return aligned(p, 16) && ld % 8 == 0 && ld < (int64_t(1) << 38);
+}
+
 }  // namespace
 
 extern "C" {
@@ -913,7 +920,10 @@ FTK_API ftk_status ftk_attn_fwd(const void *q, int64_t ld_q, const void *k, int6
   if (e != cudaSuccess) return cuda_fail(e);
   ftk::AttnArgs a{q,  ld_q, k,   ld_k, v, ld_v,  o,      ld_o,          lse, cu_seqlens,
                   B,  T,    Hq,  Hkv,  D, scale, causal, seqlens_status};
-  return finish(ftk::launch_attn_fwd_generic(dt, a, dev, (cudaStream_t)stream));
+  const bool tc = attn_tc_shape(dt, D) && attn_tc_tensor(q, ld_q) && attn_tc_tensor(k, ld_k) &&
+                  attn_tc_tensor(v, ld_v) && attn_tc_tensor(o, ld_o);
+  return finish(tc ? ftk::launch_attn_fwd_tc(a, dev, (cudaStream_t)stream)
+                   : ftk::launch_attn_fwd_generic(dt, a, dev, (cudaStream_t)stream));
 }
 
 FTK_API size_t ftk_attn_bwd_workspace_bytes(int64_t T, int32_t Hq, int32_t Hkv, int32_t D,

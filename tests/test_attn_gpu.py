@@ -409,7 +409,7 @@ def test_a_layers_attention_block_with_its_gradients():
         a += n
     ro = torch.cat(out)
     ro.backward(do.double())
-    far = lambda x, y: float((x.detach().double() - y.detach()).norm() / y.norm())  # noqa: E731
+    far = lambda x, y: float((x.detach().double() - y.detach()).norm() / y.detach().norm())  # noqa: E731
     # o: q, k rounded (2^-8 of scores of size ~sqrt(D) / 8 = 1, twice), p and o: 4 roundings;
     # the gradients pass dp, ds and the turned-back rounding as well: 8
     assert far(o, ro) < 4 * 2.0 ** -8
