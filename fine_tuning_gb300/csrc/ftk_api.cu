@@ -981,7 +981,12 @@ FTK_API ftk_status ftk_attn_bwd(const void *do_, int64_t ld_do, const void *q, i
   ftk::AttnArgs a{q,  ld_q, k,  ld_k, v,     ld_v,   (void *)o,      ld_o, (float *)lse, cu_seqlens,
                   B,  T,    Hq, Hkv,  D,     scale,  causal, seqlens_status, do_,  ld_do,
                   dq, ld_dq, dk, ld_dk, dv, ld_dv, (float *)workspace};
-  return finish(ftk::launch_attn_bwd_generic(dt, a, dev, (cudaStream_t)stream));
+  const bool tc = attn_tc_shape(dt, D) && attn_tc_tensor(do_, ld_do) && attn_tc_tensor(q, ld_q) &&
+                  attn_tc_tensor(k, ld_k) && attn_tc_tensor(v, ld_v) && attn_tc_tensor(o, ld_o) &&
+                  attn_tc_tensor(dq, ld_dq) && attn_tc_tensor(dk, ld_dk) &&
+                  attn_tc_tensor(dv, ld_dv);
+  return finish(tc ? ftk::launch_attn_bwd_tc(a, dev, (cudaStream_t)stream)
+                   : ftk::launch_attn_bwd_generic(dt, a, dev, (cudaStream_t)stream));
 }
 
 // ------------------------------------------------------ tensor-core GEMM
