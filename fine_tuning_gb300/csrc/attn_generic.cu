@@ -9,12 +9,15 @@
 // A CTA of 256 threads owns a tile of BT rows of one head (queries in the
 // forward and in dq, keys in dk/dv) and walks the tiles of the other side,
 // so every sum has one owner and a fixed order: no atomics, and dk, dv of a
-// shared key head are summed over its query heads inside the CTA.  Thread
-// (ty, tx) of 16 x 16 holds BT/16 rows x BT/16 columns of the score tile and
-// BT/16 rows x D/16 columns of the outputs; operands are read from shared
-// memory as float4 along d, rows padded by 4 words so that 8 lanes' float4
-// reads fall into different banks.  Bound by shared-memory reads: 2 x 4
-// LDS.128 feed 64 multiply-adds.
+// shared key head are summed over its query heads inside the CTA.  The
+// backward is one launch: the first blocks own key tiles, the others query
+// tiles, and each forms the delta of the rows it needs while it loads them.
+// Thread (ty, tx) of 16 x 16 holds BT/16 rows x BT/16 columns of the score
+// tile and, of the outputs, BT/16 rows x groups of 4 columns 64 apart.  Every
+// operand is read from shared memory as float4 (rows padded by 4 words so that
+// 8 lanes' reads fall into different banks), so that the multiply-adds, not
+// the shared-memory reads, are the bound: 12 (20) wavefronts of LDS for 64
+// (128) warp instructions of FFMA in the two products of a 64 x 64 tile.
 #include <cmath>
 
 #include "attn_common.cuh"
@@ -68,29 +71,41 @@ __device__ __forceinline__ void rows_dot(float (&acc)[TM][TM], const float *a, c
   }
 }
 
-// out[i][n] += sum_c p[ty TM + i][c] b[c][tx + 16 n], c < nc
+// out[i][n][e] += sum_c p[ty TM + i][c] b[c][4 tx + 64 n + e], c < nc (p and b
+// hold zeros, or products that are zero, up to the next multiple of 4)
 template <int TM, int NN>
-__device__ __forceinline__ void rows_mul(float (&out)[TM][NN], const float *p, int ldp,
+__device__ __forceinline__ void rows_mul(float (&out)[TM][NN][4], const float *p, int ldp,
                                          const float *b, int ld, int nc, int DP) {
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  for (int c = 0; c < nc; ++c) {
-    float x[TM];
+  if (4 * tx >= DP) return;
+  for (int c = 0; c < nc; c += 4) {
+    float x[TM][4];
 #pragma unroll
-    for (int i = 0; i < TM; ++i) x[i] = p[(ty * TM + i) * ldp + c];
+    for (int i = 0; i < TM; ++i)
+      *reinterpret_cast<float4 *>(x[i]) =
+          *reinterpret_cast<const float4 *>(p + (ty * TM + i) * ldp + c);
 #pragma unroll
     for (int n = 0; n < NN; ++n) {
-      const int d = tx + 16 * n;
+      const int d = 4 * tx + 64 * n;
       if (d >= DP) break;
-      const float y = b[c * ld + d];
 #pragma unroll
-      for (int i = 0; i < TM; ++i) out[i][n] = fmaf(x[i], y, out[i][n]);
+      for (int u = 0; u < 4; ++u) {
+        const float4 y = *reinterpret_cast<const float4 *>(b + (c + u) * ld + d);
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+          out[i][n][0] = fmaf(x[i][u], y.x, out[i][n][0]);
+          out[i][n][1] = fmaf(x[i][u], y.y, out[i][n][1]);
+          out[i][n][2] = fmaf(x[i][u], y.z, out[i][n][2]);
+          out[i][n][3] = fmaf(x[i][u], y.w, out[i][n][3]);
+        }
+      }
     }
   }
 }
 
 template <typename T, int TM, int NN>
 __device__ __forceinline__ void store_rows(T *base, int64_t stride, int row0, int len, int D,
-                                           const float (&out)[TM][NN], const float (&f)[TM]) {
+                                           const float (&out)[TM][NN][4], const float (&f)[TM]) {
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
@@ -99,8 +114,21 @@ __device__ __forceinline__ void store_rows(T *base, int64_t stride, int row0, in
     T *p = base + (int64_t)r * stride;
 #pragma unroll
     for (int n = 0; n < NN; ++n)
-      if (tx + 16 * n < D) p[tx + 16 * n] = from_float<T>(out[i][n] * f[i]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int d = 4 * tx + 64 * n + e;
+        if (d < D) p[d] = from_float<T>(out[i][n][e] * f[i]);
+      }
   }
+}
+
+template <int TM, int NN> __device__ __forceinline__ void clear(float (&out)[TM][NN][4]) {
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int n = 0; n < NN; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) out[i][n][e] = 0.f;
 }
 
 // The sum (or maximum) over the 16 lanes that hold one row.
@@ -115,10 +143,31 @@ __device__ __forceinline__ float row_max(float v) {
   return v;
 }
 
+// load_rows of do that also leaves delta[r] = sum_d do o of its rows in s_delta.
+template <typename T, int BT>
+__device__ __forceinline__ void load_rows_delta(float *s, float *s_delta, int ld, const T *base,
+                                                int64_t stride, const T *o, int64_t ld_o, int row0,
+                                                int len, int D, int DP) {
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  for (int r = ty; r < BT; r += 16) {
+    const bool in = row0 + r < len;
+    const T *p = base + (int64_t)(row0 + r) * stride, *po = o + (int64_t)(row0 + r) * ld_o;
+    float dot = 0.f;
+    for (int d = tx; d < DP; d += 16) {
+      const bool real = in && d < D;
+      const float g = real ? to_float(p[d]) : 0.f;
+      if (real) dot = fmaf(g, to_float(po[d]), dot);
+      s[r * ld + d] = g;
+    }
+    dot = row_sum(dot);
+    if (tx == 0) s_delta[r] = dot;
+  }
+}
+
 template <typename T, int BT, int DMAX>
 __global__ void __launch_bounds__(kThreads)
 attn_fwd_generic(const AttnArgs a, int slots) {
-  constexpr int TM = BT / 16, NN = DMAX / 16, LDP = BT + 4;
+  constexpr int TM = BT / 16, NN = DMAX / 64, LDP = BT + 4;
   extern __shared__ float sm[];
   pdl_wait();
   pdl_trigger();
@@ -135,13 +184,12 @@ attn_fwd_generic(const AttnArgs a, int slots) {
   const T *v = (const T *)a.v + t.start * a.ld_v + (int64_t)hk * a.D;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   load_rows<T, BT>(Qs, ld, q, a.ld_q, t.row0, t.len, a.D, DP);
-  float out[TM][NN], m[TM], l[TM];
+  float out[TM][NN][4], m[TM], l[TM];
+  clear(out);
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
     m[i] = -INFINITY;
     l[i] = 0.f;
-#pragma unroll
-    for (int n = 0; n < NN; ++n) out[i][n] = 0.f;
   }
   const int end = a.causal ? min(t.len, t.row0 + BT) : t.len;
   for (int c0 = 0; c0 < end; c0 += BT) {
@@ -174,7 +222,9 @@ attn_fwd_generic(const AttnArgs a, int slots) {
       }
       l[i] = l[i] * f + row_sum(sum);
 #pragma unroll
-      for (int n = 0; n < NN; ++n) out[i][n] *= f;
+      for (int n = 0; n < NN; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) out[i][n][e] *= f;
     }
     __syncthreads();
     rows_mul<TM, NN>(out, Ps, LDP, Vs, ld, min(BT, t.len - c0), DP);
@@ -190,58 +240,31 @@ attn_fwd_generic(const AttnArgs a, int slots) {
   store_rows<T, TM, NN>(o, a.ld_o, t.row0, t.len, a.D, out, inv);
 }
 
-// delta[h, t] = sum_d do[t, h, d] o[t, h, d]: a warp per (token, head).
-template <typename T>
-__global__ void __launch_bounds__(kThreads) attn_delta_generic(const AttnArgs a) {
-  pdl_wait();
-  pdl_trigger();
-  if (attn_skipped(a.skip)) return;
-  const int64_t rows = a.T * a.Hq;
-  const int lane = threadIdx.x & 31;
-  for (int64_t i = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); i < rows;
-       i += (int64_t)gridDim.x * (kThreads / 32)) {
-    const int64_t t = i / a.Hq;
-    const int h = (int)(i - t * a.Hq);
-    const T *g = (const T *)a.do_ + t * a.ld_do + (int64_t)h * a.D;
-    const T *o = (const T *)a.o + t * a.ld_o + (int64_t)h * a.D;
-    float s = 0.f;
-    for (int d = lane; d < a.D; d += 32) s = fmaf(to_float(g[d]), to_float(o[d]), s);
-    s = warp_sum(s);
-    if (lane == 0) a.delta[(int64_t)h * a.T + t] = s;
-  }
-}
-
+// dq of one query tile.
 template <typename T, int BT, int DMAX>
-__global__ void __launch_bounds__(kThreads)
-attn_dq_generic(const AttnArgs a, int slots) {
-  constexpr int TM = BT / 16, NN = DMAX / 16, LDP = BT + 4;
-  extern __shared__ float sm[];
-  pdl_wait();
-  pdl_trigger();
-  if (attn_skipped(a.skip)) return;
+__device__ __forceinline__ void dq_tile(const AttnArgs &a, float *sm, int h, int slot) {
+  constexpr int TM = BT / 16, NN = DMAX / 64, LDP = BT + 4;
   const int DP = (a.D + 3) & ~3, ld = DP + 4;
   float *Qs = sm, *Gs = Qs + BT * ld, *Ks = Gs + BT * ld, *Vs = Ks + BT * ld, *Ds = Vs + BT * ld;
-  const int h = blockIdx.x % a.Hq, slot = slots - 1 - (int)(blockIdx.x / a.Hq);
+  float *Dl = Ds + BT * LDP;
   const SeqTile t = seq_tile(slot, a.cu, a.B, (int)a.T, BT);
   if (t.len == 0) return;
   const int hk = h / (a.Hq / a.Hkv);
   const T *q = (const T *)a.q + t.start * a.ld_q + (int64_t)h * a.D;
   const T *g = (const T *)a.do_ + t.start * a.ld_do + (int64_t)h * a.D;
+  const T *o = (const T *)a.o + t.start * a.ld_o + (int64_t)h * a.D;
   const T *k = (const T *)a.k + t.start * a.ld_k + (int64_t)hk * a.D;
   const T *v = (const T *)a.v + t.start * a.ld_v + (int64_t)hk * a.D;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   load_rows<T, BT>(Qs, ld, q, a.ld_q, t.row0, t.len, a.D, DP);
-  load_rows<T, BT>(Gs, ld, g, a.ld_do, t.row0, t.len, a.D, DP);
-  float out[TM][NN], lse[TM], delta[TM], f[TM];
+  load_rows_delta<T, BT>(Gs, Dl, ld, g, a.ld_do, o, a.ld_o, t.row0, t.len, a.D, DP);
+  float out[TM][NN][4], lse[TM], f[TM];
+  clear(out);
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
     const int r = t.row0 + ty * TM + i;
-    const int64_t at = (int64_t)h * a.T + t.start + r;
-    lse[i] = r < t.len ? a.lse[at] : 0.f;
-    delta[i] = r < t.len ? a.delta[at] : 0.f;
+    lse[i] = r < t.len ? a.lse[(int64_t)h * a.T + t.start + r] : 0.f;
     f[i] = a.scale;
-#pragma unroll
-    for (int n = 0; n < NN; ++n) out[i][n] = 0.f;
   }
   const int end = a.causal ? min(t.len, t.row0 + BT) : t.len;
   for (int c0 = 0; c0 < end; c0 += BT) {
@@ -255,12 +278,13 @@ attn_dq_generic(const AttnArgs a, int slots) {
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
       const int r = t.row0 + ty * TM + i;
+      const float delta = Dl[ty * TM + i];
 #pragma unroll
       for (int j = 0; j < TM; ++j) {
         const int c = c0 + tx + 16 * j;
         const bool see = c < t.len && r < t.len && (!a.causal || c <= r);
         const float p = see ? expf(fmaf(s[i][j], a.scale, -lse[i])) : 0.f;
-        Ds[(ty * TM + i) * LDP + tx + 16 * j] = see ? p * (dp[i][j] - delta[i]) : 0.f;
+        Ds[(ty * TM + i) * LDP + tx + 16 * j] = see ? p * (dp[i][j] - delta) : 0.f;
       }
     }
     __syncthreads();
@@ -270,19 +294,14 @@ attn_dq_generic(const AttnArgs a, int slots) {
   store_rows<T, TM, NN>(dq, a.ld_dq, t.row0, t.len, a.D, out, f);
 }
 
-// Rows are keys, columns queries: the score tile is transposed.
+// dk and dv of one key tile.  Rows are keys, columns queries: the score tile is
+// transposed.
 template <typename T, int BT, int DMAX>
-__global__ void __launch_bounds__(kThreads)
-attn_dkv_generic(const AttnArgs a) {
-  constexpr int TM = BT / 16, NN = DMAX / 16, LDP = BT + 4;
-  extern __shared__ float sm[];
-  pdl_wait();
-  pdl_trigger();
-  if (attn_skipped(a.skip)) return;
+__device__ __forceinline__ void dkv_tile(const AttnArgs &a, float *sm, int hk, int slot) {
+  constexpr int TM = BT / 16, NN = DMAX / 64, LDP = BT + 4;
   const int DP = (a.D + 3) & ~3, ld = DP + 4;
   float *Ks = sm, *Vs = Ks + BT * ld, *Qs = Vs + BT * ld, *Gs = Qs + BT * ld, *Ps = Gs + BT * ld;
   float *Ds = Ps + BT * LDP, *Ls = Ds + BT * LDP, *Dl = Ls + BT;
-  const int hk = blockIdx.x % a.Hkv, slot = (int)(blockIdx.x / a.Hkv);
   const SeqTile t = seq_tile(slot, a.cu, a.B, (int)a.T, BT);
   if (t.len == 0) return;
   const int G = a.Hq / a.Hkv;
@@ -291,26 +310,25 @@ attn_dkv_generic(const AttnArgs a) {
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   load_rows<T, BT>(Ks, ld, k, a.ld_k, t.row0, t.len, a.D, DP);
   load_rows<T, BT>(Vs, ld, v, a.ld_v, t.row0, t.len, a.D, DP);
-  float dk[TM][NN], dv[TM][NN], fk[TM], fv[TM];
+  float dk[TM][NN][4], dv[TM][NN][4], fk[TM], fv[TM];
+  clear(dk);
+  clear(dv);
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
     fk[i] = a.scale;
     fv[i] = 1.f;
-#pragma unroll
-    for (int n = 0; n < NN; ++n) dk[i][n] = dv[i][n] = 0.f;
   }
   for (int h = hk * G; h < (hk + 1) * G; ++h) {
     const T *q = (const T *)a.q + t.start * a.ld_q + (int64_t)h * a.D;
     const T *g = (const T *)a.do_ + t.start * a.ld_do + (int64_t)h * a.D;
+    const T *o = (const T *)a.o + t.start * a.ld_o + (int64_t)h * a.D;
     for (int c0 = a.causal ? t.row0 : 0; c0 < t.len; c0 += BT) {
       __syncthreads();
       load_rows<T, BT>(Qs, ld, q, a.ld_q, c0, t.len, a.D, DP);
-      load_rows<T, BT>(Gs, ld, g, a.ld_do, c0, t.len, a.D, DP);
+      load_rows_delta<T, BT>(Gs, Dl, ld, g, a.ld_do, o, a.ld_o, c0, t.len, a.D, DP);
       if (threadIdx.x < BT) {
         const int c = c0 + threadIdx.x;
-        const int64_t at = (int64_t)h * a.T + t.start + c;
-        Ls[threadIdx.x] = c < t.len ? a.lse[at] : 0.f;
-        Dl[threadIdx.x] = c < t.len ? a.delta[at] : 0.f;
+        Ls[threadIdx.x] = c < t.len ? a.lse[(int64_t)h * a.T + t.start + c] : 0.f;
       }
       __syncthreads();
       float s[TM][TM], dp[TM][TM];
@@ -340,72 +358,72 @@ attn_dkv_generic(const AttnArgs a) {
   store_rows<T, TM, NN>(pv, a.ld_dv, t.row0, t.len, a.D, dv, fv);
 }
 
+// Blocks 0 .. slots Hkv - 1 own key tiles (from the first one on: in a causal
+// sequence the one that most rows see), the others query tiles (from the last
+// one back).
+template <typename T, int BT, int DMAX>
+__global__ void __launch_bounds__(kThreads) attn_bwd_generic(const AttnArgs a, int slots) {
+  extern __shared__ float sm[];
+  pdl_wait();
+  pdl_trigger();
+  if (attn_skipped(a.skip)) return;
+  const int keys = slots * a.Hkv, b = (int)blockIdx.x;
+  if (b < keys)
+    dkv_tile<T, BT, DMAX>(a, sm, b % a.Hkv, b / a.Hkv);
+  else
+    dq_tile<T, BT, DMAX>(a, sm, (b - keys) % a.Hq, slots - 1 - (b - keys) / a.Hq);
+}
+
 template <typename T, int BT, int DMAX> struct Generic {
   static size_t smem(const AttnArgs &a, int bufs, int tiles) {
     const int ld = ((a.D + 3) & ~3) + 4;
     return (size_t)(bufs * BT * ld + tiles * BT * (BT + 4) + 2 * BT) * sizeof(float);
   }
-  template <typename K> static cudaError_t prepare(K kern, size_t smem, const DeviceInfo &dev) {
-    blocks_per_sm((const void *)kern, kThreads, smem, dev, 1);  // lifts the shared memory limit
-    return cudaSuccess;
-  }
   static int slots(const AttnArgs &a) { return (int)(a.T / BT + a.B); }
 
   static cudaError_t fwd(const AttnArgs &a, const DeviceInfo &dev, cudaStream_t s) {
     const size_t n = smem(a, 3, 1);
-    cudaError_t e = prepare(attn_fwd_generic<T, BT, DMAX>, n, dev);
-    if (e != cudaSuccess) return e;
+    blocks_per_sm((const void *)attn_fwd_generic<T, BT, DMAX>, kThreads, n, dev, 1);  // lifts the limit
     return launch_pdl(attn_fwd_generic<T, BT, DMAX>, dim3((unsigned)slots(a) * (unsigned)a.Hq),
                       dim3(kThreads), n, s, a, slots(a));
   }
   static cudaError_t bwd(const AttnArgs &a, const DeviceInfo &dev, cudaStream_t s) {
-    size_t n = smem(a, 4, 1);
-    cudaError_t e = prepare(attn_dq_generic<T, BT, DMAX>, n, dev);
-    if (e != cudaSuccess) return e;
-    e = launch_pdl(attn_dq_generic<T, BT, DMAX>, dim3((unsigned)slots(a) * (unsigned)a.Hq),
-                   dim3(kThreads), n, s, a, slots(a));
-    if (e != cudaSuccess) return e;
-    n = smem(a, 4, 2);
-    e = prepare(attn_dkv_generic<T, BT, DMAX>, n, dev);
-    if (e != cudaSuccess) return e;
-    return launch_pdl(attn_dkv_generic<T, BT, DMAX>, dim3((unsigned)slots(a) * (unsigned)a.Hkv),
-                      dim3(kThreads), n, s, a);
+    const size_t n = smem(a, 4, 2);
+    blocks_per_sm((const void *)attn_bwd_generic<T, BT, DMAX>, kThreads, n, dev, 1);
+    return launch_pdl(attn_bwd_generic<T, BT, DMAX>,
+                      dim3((unsigned)slots(a) * (unsigned)(a.Hq + a.Hkv)), dim3(kThreads), n, s, a,
+                      slots(a));
   }
 };
 
-template <typename T> cudaError_t delta_of(const AttnArgs &a, const DeviceInfo &dev, cudaStream_t s) {
-  const int64_t want = ceil_div(a.T * a.Hq, (int64_t)(kThreads / 32));
-  const int64_t most = (int64_t)dev.sms * 16;
-  return launch_pdl(attn_delta_generic<T>, dim3((unsigned)(want < most ? want : most)),
-                    dim3(kThreads), 0, s, a);
+// 64-row tiles while four of them fit beside the score tiles (D <= 128), 32-row
+// tiles for the larger heads, and for calls whose 64-row tiles would leave SMs
+// without one.
+bool small_tiles(const AttnArgs &a, const DeviceInfo &dev) {
+  return a.D > 128 || (a.T / 64 + a.B) * a.Hq < dev.sms;
+}
+
+template <typename T>
+cudaError_t fwd_of(const AttnArgs &a, const DeviceInfo &dev, cudaStream_t s) {
+  if (!small_tiles(a, dev)) return Generic<T, 64, 128>::fwd(a, dev, s);
+  return a.D <= 128 ? Generic<T, 32, 128>::fwd(a, dev, s) : Generic<T, 32, 256>::fwd(a, dev, s);
+}
+template <typename T>
+cudaError_t bwd_of(const AttnArgs &a, const DeviceInfo &dev, cudaStream_t s) {
+  if (!small_tiles(a, dev)) return Generic<T, 64, 128>::bwd(a, dev, s);
+  return a.D <= 128 ? Generic<T, 32, 128>::bwd(a, dev, s) : Generic<T, 32, 256>::bwd(a, dev, s);
 }
 
 }  // namespace
 
-cudaError_t launch_attn_delta(DType dt, const AttnArgs &a, const DeviceInfo &dev, cudaStream_t s) {
-  return dt == DType::F32 ? delta_of<float>(a, dev, s) : delta_of<bf16>(a, dev, s);
-}
-
-// 64-row tiles while four of them fit beside the score tiles (D <= 128),
-// 32-row tiles for the larger heads.
 cudaError_t launch_attn_fwd_generic(DType dt, const AttnArgs &a, const DeviceInfo &dev,
                                     cudaStream_t s) {
-  if (dt == DType::F32)
-    return a.D <= 128 ? Generic<float, 64, 128>::fwd(a, dev, s)
-                      : Generic<float, 32, 256>::fwd(a, dev, s);
-  return a.D <= 128 ? Generic<bf16, 64, 128>::fwd(a, dev, s)
-                    : Generic<bf16, 32, 256>::fwd(a, dev, s);
+  return dt == DType::F32 ? fwd_of<float>(a, dev, s) : fwd_of<bf16>(a, dev, s);
 }
 
 cudaError_t launch_attn_bwd_generic(DType dt, const AttnArgs &a, const DeviceInfo &dev,
                                     cudaStream_t s) {
-  cudaError_t e = launch_attn_delta(dt, a, dev, s);
-  if (e != cudaSuccess) return e;
-  if (dt == DType::F32)
-    return a.D <= 128 ? Generic<float, 64, 128>::bwd(a, dev, s)
-                      : Generic<float, 32, 256>::bwd(a, dev, s);
-  return a.D <= 128 ? Generic<bf16, 64, 128>::bwd(a, dev, s)
-                    : Generic<bf16, 32, 256>::bwd(a, dev, s);
+  return dt == DType::F32 ? bwd_of<float>(a, dev, s) : bwd_of<bf16>(a, dev, s);
 }
 
 }  // namespace ftk

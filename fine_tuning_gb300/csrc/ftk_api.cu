@@ -873,8 +873,9 @@ ftk_status attn_shape(int32_t B, int64_t T, int32_t Hq, int32_t Hkv, int32_t D, 
       D > ftk::kAttnMaxD || !(scale > 0.f) || !std::isfinite(scale))
     return FTK_ERR_SHAPE;
   if (T > 0 && B < 1) return FTK_ERR_SHAPE;
-  // one block per (tile, head): the count must fit a grid
-  if ((T / ftk::kAttnMinTile + B) > ((int64_t(1) << 31) - 1) / Hq) return FTK_ERR_SHAPE;
+  // one block per (tile, head), of queries and of keys: the count must fit a grid
+  if ((T / ftk::kAttnMinTile + B) > ((int64_t(1) << 31) - 1) / ((int64_t)Hq + Hkv))
+    return FTK_ERR_SHAPE;
   return FTK_OK;
 }
 

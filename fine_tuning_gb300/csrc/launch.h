@@ -275,7 +275,6 @@ cudaError_t launch_attn_bwd_generic(DType dt, const AttnArgs &a, const DeviceInf
 // bf16, D % 8 == 0, D <= 128, 16-byte aligned tensors, row strides % 8 == 0.
 cudaError_t launch_attn_fwd_tc(const AttnArgs &a, const DeviceInfo &dev, cudaStream_t s);
 cudaError_t launch_attn_bwd_tc(const AttnArgs &a, const DeviceInfo &dev, cudaStream_t s);
-cudaError_t launch_attn_delta(DType dt, const AttnArgs &a, const DeviceInfo &dev, cudaStream_t s);
 
 // Cross-entropy of the LM head (cce.cu).  bf16 h [T, ldh], W [V, ldw];
 // y int32 [T] (valid when 0 <= y < V).  Forward: loss (1 float) and lse [T].

@@ -84,6 +84,14 @@ def test_cuda_core_forms(dtype, Hq, Hkv, D, causal):
 
 
 @pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("dtype,Hq,Hkv,D", [(torch.float32, 6, 2, 64), (torch.float32, 6, 6, 20),
+                                            (torch.float32, 8, 2, 128), (torch.bfloat16, 6, 3, 33)])
+def test_cuda_core_forms_that_fill_the_gpu(dtype, Hq, Hkv, D, causal):
+    """Enough tiles for the larger tile of these kernels."""
+    check(*inputs((700, 1, 513, 64, 0, 400), Hq, Hkv, D, dtype, fused=True), causal)
+
+
+@pytest.mark.parametrize("causal", [True, False])
 @pytest.mark.parametrize("Hq,Hkv,D", [(14, 2, 64), (4, 1, 64), (2, 2, 128), (8, 2, 128), (5, 1, 128),
                                       (3, 3, 80), (2, 1, 8), (4, 2, 16), (1, 1, 120), (6, 2, 72),
                                       (7, 1, 96), (1, 1, 64)])
