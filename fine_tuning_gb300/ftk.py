@@ -552,19 +552,37 @@ def _same_device(ref: torch.Tensor, *ts):
     """Every tensor given lives on ref's CUDA device."""
     if not ref.is_cuda:
         raise ValueError("ftk ops take CUDA tensors (move inputs with .cuda())")
+    dev = ref.device
     for t in ts:
-        if t is not None and t.device != ref.device:
-            raise ValueError(f"tensors on different devices: {t.device} and {ref.device}")
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors on different devices: {t.device} and {dev}")
 
 
 def _call_on(ref: torch.Tensor, name: str, *args) -> None:
     """_call on ref's device (made the current one for the launch) and that
     device's current stream."""
-    if ref.device.index == torch.cuda.current_device():
-        _call(name, *args, _stream(ref))
+    i = ref.device.index
+    if i == torch.cuda.current_device():
+        _call(name, *args, _raw_stream(i))
     else:
-        with torch.cuda.device(ref.device):
-            _call(name, *args, _stream(ref))
+        with torch.cuda.device(i):
+            _call(name, *args, _raw_stream(i))
+
+
+def _raw_stream(index: int) -> int:
+    """The handle of device `index`'s current stream (without the Stream object
+    that current_stream builds: 2 us of a small call's host time)."""
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
+def _head_rows(t: torch.Tensor, name: str) -> int:
+    """_heads' checks and row stride, in one look at the strides."""
+    st = t.stride()
+    if len(st) == 3:
+        T, nh, D = t.shape
+        if st[2] == 1 and st[1] == D and T > 1:
+            return st[0]
+    return _heads(t, name)[0]
 
 
 def mrope_axis_of(sections) -> np.ndarray:
@@ -586,11 +604,14 @@ def _mrope(name, q, k, pos, axis_of, theta, inv_freq, q_out, k_out):
         q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     if k is not None and k_out is None:
         k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-    ldq, Hq, Dq = _heads(q, "q")
-    ldk, Hkv, Dk = _heads(k, "k")
-    ldqo, ldko = _heads(q_out, "q_out")[0], _heads(k_out, "k_out")[0]
-    T, D = ref.shape[0], ref.shape[2]
-    if q is not None and k is not None and (k.shape[0] != T or Dk != Dq or k.dtype != q.dtype):
+    ldq = ldk = ldqo = ldko = Hq = Hkv = 0
+    T, D = ref.shape[0], ref.shape[-1]
+    if q is not None:
+        ldq, ldqo, Hq = _head_rows(q, "q"), _head_rows(q_out, "q_out"), q.shape[1]
+    if k is not None:
+        ldk, ldko, Hkv = _head_rows(k, "k"), _head_rows(k_out, "k_out"), k.shape[1]
+    if q is not None and k is not None and (k.shape[0] != T or k.shape[2] != D
+                                            or k.dtype != q.dtype):
         raise ValueError("q and k must agree in tokens, head_dim and dtype")
     for x, y in ((q, q_out), (k, k_out)):
         if (x is None) != (y is None) or (x is not None and (y.shape != x.shape
@@ -601,13 +622,19 @@ def _mrope(name, q, k, pos, axis_of, theta, inv_freq, q_out, k_out):
         raise ValueError("pos must be int32 [axes, T] with unit stride along tokens")
     axes = pos.shape[0]
     ldp = max(pos.stride(0), T) if axes == 1 else pos.stride(0)
-    table = np.ascontiguousarray(np.asarray(axis_of, dtype=np.int32))
+    table = np.asarray(axis_of)
+    if table.dtype != np.int32:
+        if table.shape and not np.issubdtype(table.dtype, np.integer):
+            raise ValueError("axis_of must hold integers")
+        if table.size and (int(table.min()) < 0 or int(table.max()) >= axes):
+            raise ValueError("axis_of must hold axes of pos")  # before the cast could wrap
+    table = np.ascontiguousarray(table, dtype=np.int32)
     if table.shape != (D // 2,):
         raise ValueError("axis_of must hold D/2 axes")
-    freq, freq_p = _table(inv_freq, D)
+    freq, freq_p = (None, None) if inv_freq is None else _table(inv_freq, D)
     _call_on(ref, name, _ptr(q), ldq, _ptr(k), ldk, _ptr(q_out), ldqo, _ptr(k_out), ldko,
-             _ptr(pos), ldp, axes, table.ctypes.data, T, Hq, Hkv, D, float(theta or 0.0), freq_p,
-             _code(ref))
+             _ptr(pos), ldp, axes, table.__array_interface__["data"][0], T, Hq, Hkv, D,
+             float(theta or 0.0), freq_p, _code(ref))
     del table, freq
     return q_out, k_out
 
@@ -659,11 +686,10 @@ def attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torc
     to D^-0.5.  Rows of no sequence are left as they were (uninitialised in an
     output allocated here).  seqlens_status: the word check_seqlens wrote; a
     non-zero word leaves every output untouched."""
-    ldq, Hq, D = _heads(q, "q")
-    ldk, Hkv, _ = _heads(k, "k")
-    ldv, _, _ = _heads(v, "v")
+    ldq, ldk, ldv = _head_rows(q, "q"), _head_rows(k, "k"), _head_rows(v, "v")
     _attn_check(q, k, v, cu_seqlens, seqlens_status, o, lse)
-    T = q.shape[0]
+    T, Hq, D = q.shape
+    Hkv = k.shape[1]
     o = _like(q, o, "o")
     if lse is None and save_lse:
         lse = torch.empty((Hq, T), dtype=torch.float32, device=q.device)
@@ -671,7 +697,7 @@ def attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torc
                             or not lse.is_contiguous()):
         raise ValueError("lse must be a contiguous fp32 [Hq, T] tensor")
     _call_on(q, "ftk_attn_fwd", _ptr(q), ldq, _ptr(k), ldk, _ptr(v), ldv, _ptr(o),
-             _heads(o, "o")[0], _ptr(lse), _ptr(cu_seqlens), cu_seqlens.numel() - 1, T, Hq, Hkv, D,
+             _head_rows(o, "o"), _ptr(lse), _ptr(cu_seqlens), cu_seqlens.numel() - 1, T, Hq, Hkv, D,
              float(D ** -0.5 if scale is None else scale), int(bool(causal)),
              _ptr(seqlens_status), _code(q))
     return o, lse
@@ -691,11 +717,10 @@ def attn_bwd(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor
     """Backward of attn_fwd from its output o and lse: (dq, dk, dv).  The
     probabilities are recomputed; the results are bitwise reproducible.
     dq, dk, dv may be slices of one fused [T, Hq + 2 Hkv, D] buffer."""
-    ldq, Hq, D = _heads(q, "q")
-    ldk, Hkv, _ = _heads(k, "k")
-    ldv, _, _ = _heads(v, "v")
+    ldq, ldk, ldv = _head_rows(q, "q"), _head_rows(k, "k"), _head_rows(v, "v")
     _attn_check(q, k, v, cu_seqlens, seqlens_status, do, o, lse, dq, dk, dv, workspace)
-    T = q.shape[0]
+    T, Hq, D = q.shape
+    Hkv = k.shape[1]
     for t, name in ((do, "do"), (o, "o")):
         if t.shape != q.shape or t.dtype != q.dtype:
             raise ValueError(f"{name} must match q in shape and dtype")
@@ -705,9 +730,9 @@ def attn_bwd(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor
     if workspace is None:
         workspace = torch.empty(max(16, attn_bwd_workspace_bytes(T, Hq, Hkv, D, q.dtype)),
                                 dtype=torch.uint8, device=q.device)
-    _call_on(q, "ftk_attn_bwd", _ptr(do), _heads(do, "do")[0], _ptr(q), ldq, _ptr(k), ldk, _ptr(v),
-             ldv, _ptr(o), _heads(o, "o")[0], _ptr(lse), _ptr(dq), _heads(dq, "dq")[0], _ptr(dk),
-             _heads(dk, "dk")[0], _ptr(dv), _heads(dv, "dv")[0], _ptr(workspace),
+    _call_on(q, "ftk_attn_bwd", _ptr(do), _head_rows(do, "do"), _ptr(q), ldq, _ptr(k), ldk, _ptr(v),
+             ldv, _ptr(o), _head_rows(o, "o"), _ptr(lse), _ptr(dq), _head_rows(dq, "dq"), _ptr(dk),
+             _head_rows(dk, "dk"), _ptr(dv), _head_rows(dv, "dv"), _ptr(workspace),
              workspace.numel() * workspace.element_size(), _ptr(cu_seqlens),
              cu_seqlens.numel() - 1, T, Hq, Hkv, D,
              float(D ** -0.5 if scale is None else scale), int(bool(causal)),
