@@ -8,24 +8,28 @@
 // rows at a time, both of one key head, so that a staged K or V tile feeds
 // two MMAs and one tile's softmax runs under the other's MMAs.  The pair is
 // taken along (row tile, head of the group): with an even group both tiles see
-// the same keys.  12 warps (one idle):
+// the same keys.  12 warps:
 //   warp 0      one lane issues the TMA tile loads: Q of the pair, then K and V
 //               tiles through a ring of kStages;
-//   warp 1      one lane issues the MMAs (S = Q K^T from shared memory; O += P V
-//               with P read from tensor memory);
-//   warps 2-5   softmax of tile 0, one query row per thread (its 128 scores in
-//   warps 6-9   registers: no shuffles), and of tile 1;
+//   warps 1,11  one lane each issues the MMAs of tile 0 and 1 (S = Q K^T from
+//               shared memory; O += P V with P read from tensor memory);
+//   warps 2-5   softmax of tile 0, one query row per thread (no shuffles),
+//   warps 6-9   and of tile 1;
 //   warp 10     zeroes the rows of a V tile that lie behind its sequence's end
 //               before the MMAs may read them.
-// Tensor memory: S0 S1 (128 columns each) and O0 O1.  P, in bf16, replaces the
-// scores it came from.  While softmax t works on S_t(i), the tensor pipe runs
-// P V of the other tile and that tile's next scores.
-//
-// The maximum is only raised when a row's scores pass it by more than 2^8
-// (kRaise): until then the old one stands, which changes nothing in exact
-// arithmetic (o and l carry the same factor) and keeps p <= 256; a raise
-// rescales O in tensor memory.  Rounding p to bf16 (2^-8 relative at most, per
-// term) is the price of the tensor cores' second product.
+// A key tile's 128 scores are taken as two halves of 64, each a step of the
+// running softmax of its own: the first half's P V runs while the second
+// half's exponentials are formed.  Within a half the exponentials do not wait
+// for the maximum: they are formed against the one that stands, the half's own
+// maximum beside them, and only if some row passes the standing one by more
+// than 2^kRaise are they formed again (after O and l were brought to the new
+// maximum).  Keeping a lower maximum changes nothing in exact arithmetic (o
+// and l carry the same factor) and keeps p <= 2^kRaise.  Rounding p to bf16
+// (2^-8 relative at most, per term) is the price of the tensor cores' second
+// product.
+// Tensor memory: S0 S1 (128 columns each), O0 O1.  P, in bf16, replaces the
+// scores it came from; with head sizes up to 64 there is room for P beside S,
+// and the next scores are formed while the current ones are still worked on.
 #include <cudaTypedefs.h>
 
 #include <cmath>
@@ -76,7 +80,7 @@ namespace {
 using namespace attn;
 
 constexpr int kFwdThreads = 384;
-constexpr float kRaise = 8.f;  // powers of two
+constexpr float kRaise = 8.f;
 
 struct FwdParams {
   CUtensorMap tq, tk, tv;
@@ -90,7 +94,23 @@ struct FwdItem {
   int start, len, hk;
   int h[2], row0[2], n[2];
   __device__ __forceinline__ int tiles() const { return max(n[0], n[1]); }
+  __device__ __forceinline__ void make_uniform() {
+    start = uniform(start);
+    len = uniform(len);
+    hk = uniform(hk);
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      h[t] = uniform(h[t]);
+      row0[t] = uniform(row0[t]);
+      n[t] = uniform(n[t]);
+    }
+  }
 };
+
+// Halves of key tile i that hold keys: only a sequence's last tile may have one.
+__device__ __forceinline__ int halves_of(const FwdItem &x, int i) {
+  return x.len - i * kTile > 64 ? 2 : 1;
+}
 
 // Pairs of (row tile, head of the group) of one sequence: the slots of
 // attn_common.cuh with floor((slot G + 1) / 2) + b in place of the slot.
@@ -98,8 +118,12 @@ __device__ __forceinline__ int pair_base(int c, int b, int G) {
   return ((max(c, 0) / kTile + b) * G + 1) / 2 + b;
 }
 
-__device__ __forceinline__ FwdItem fwd_item(const AttnArgs &a, int nslots, int item) {
+__device__ __forceinline__ FwdItem fwd_item(const AttnArgs &a, int nslots, int item, int items) {
   FwdItem w;
+  if (item >= items) {
+    w = FwdItem{};
+    return w;
+  }
   const int G = a.Hq / a.Hkv;
   w.hk = item % a.Hkv;
   // from the last slot back: in one long causal sequence the longest rows first
@@ -136,7 +160,7 @@ template <int DP> struct FwdLayout {
   static constexpr int kStages = DP == 128 ? 5 : 8;
   static constexpr uint32_t off_ring = 2 * tile_bytes;
   static constexpr uint32_t off_bar = off_ring + kStages * tile_bytes;
-  static constexpr uint32_t smem = off_bar + (3 * kStages + 13) * 8 + 16 + 1024;
+  static constexpr uint32_t smem = off_bar + (3 * kStages + 20) * 8 + 16 + 1024;
   static_assert(smem <= 227 * 1024, "shared memory per CTA");
 };
 
@@ -145,6 +169,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 attn_fwd_tc(const __grid_constant__ FwdParams p, unsigned *status, long long wait_limit) {
   using L = FwdLayout<DP>;
   constexpr int kStages = L::kStages;
+  constexpr bool kApart = DP <= 64;  // P beside S in tensor memory, not over it
   extern __shared__ unsigned char smem_raw[];
   unsigned char *sm = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
   const uint32_t sbase = smem_addr(sm);
@@ -155,28 +180,34 @@ attn_fwd_tc(const __grid_constant__ FwdParams p, unsigned *status, long long wai
   uint64_t *q_empty = q_full + 2;
   uint64_t *s_full = q_empty + 2;
   uint64_t *p_full = s_full + 2;
-  uint64_t *o_full = p_full + 2;
-  uint64_t *o_empty = o_full + 2;
-  uint64_t *drain = o_empty + 2;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+  // p_full and o_full per [tile][half]: with one barrier for both halves, the
+  // second could complete before the other side looked for the first
+  uint64_t *o_full = p_full + 4;
+  uint64_t *o_empty = o_full + 4;
+  uint64_t *s_read = o_empty + 2;
+  uint64_t *drain = s_read + 2;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 2);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&kv_full[s], 1);
-      mbar_init(&kv_empty[s], 2);  // the MMAs and the tail warp
+      mbar_init(&kv_empty[s], 3);  // both MMA warps and the tail warp
       mbar_init(&v_ready[s], 1);
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&q_full[t], 1);
       mbar_init(&q_empty[t], 1);
       mbar_init(&s_full[t], 1);
-      mbar_init(&p_full[t], 4);
-      mbar_init(&o_full[t], 1);
+      mbar_init(&p_full[2 * t], 4);
+      mbar_init(&p_full[2 * t + 1], 4);
+      mbar_init(&o_full[2 * t], 1);
+      mbar_init(&o_full[2 * t + 1], 1);
       mbar_init(&o_empty[t], 4);
+      mbar_init(&s_read[t], 4);
+      mbar_init(&drain[t], 1);
     }
-    mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -184,7 +215,7 @@ attn_fwd_tc(const __grid_constant__ FwdParams p, unsigned *status, long long wai
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = uniform(*tmem_slot);
   const Waits wait{abort_flag, status, wait_limit};
   const AttnArgs &a = p.a;
   pdl_wait();
@@ -204,8 +235,9 @@ attn_fwd_tc(const __grid_constant__ FwdParams p, unsigned *status, long long wai
       __syncwarp();
       ++it;
     };
-    for (int w = blockIdx.x; ok && w < items; w += gridDim.x) {
-      const FwdItem x = fwd_item(a, p.nslots, w);
+    for (int r = 0; ok && r * (int)gridDim.x < items; ++r) {
+      FwdItem x = fwd_item(a, p.nslots, snake_item(r), items);
+      x.make_uniform();
       const int n = x.tiles();
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
@@ -223,95 +255,104 @@ attn_fwd_tc(const __grid_constant__ FwdParams p, unsigned *status, long long wai
       }
     }
     // every load has landed before the CTA may leave
+#pragma unroll
     for (int t = 0; t < 2; ++t)
       if (nq[t]) mbar_wait_bounded(&q_full[t], (nq[t] - 1) & 1, wait_limit, status);
     for (int i = max(it - kStages, 0); i < it; ++i)
       mbar_wait_bounded(&kv_full[i % kStages], (i / kStages) & 1, wait_limit, status);
-  } else if (warp == 1) {
-    // -------------------------------------------------------- MMAs
+  } else if (warp == 1 || warp == 11) {
+    // -------------------------------------------------------- MMAs of tile t
+    const int t = warp == 11;
     const int nk = (a.D + 15) / 16, no = nk * 16;  // contraction steps of S, columns of O
-    int it = 0, nq[2] = {0, 0}, np[2] = {0, 0};
+    const uint32_t t_s = tmem + t * 128, t_o = tmem + 256 + t * DP;
+    const uint32_t t_p = kApart ? tmem + 384 + t * 64 : t_s;
+    int it = 0, nq = 0, ns = 0;  // ring entries, items, score tiles so far
+    int np[2] = {0, 0};          // first and second halves so far
     bool ok = true;
-    for (int w = blockIdx.x; ok && w < items; w += gridDim.x) {
-      const FwdItem x = fwd_item(a, p.nslots, w);
-      const int n = x.tiles();
+    for (int r = 0; ok && r * (int)gridDim.x < items; ++r) {
+      FwdItem x = fwd_item(a, p.nslots, snake_item(r), items);
+      x.make_uniform();
+      const int n = x.tiles(), mine = t ? x.n[1] : x.n[0];
       if (n == 0) continue;
-      // scores of key tile i (in `stage`) against query tile t
-      auto scores = [&](int t, int i, int stage) {
+      // scores of key tile i, ring entry e
+      auto scores = [&](int i, int e) {
+        const int s = e % kStages;
+        ok = wait.all(&kv_full[s], (e / kStages) & 1);
+        if (!ok) return;
+        if (i >= mine) {  // the other tile's keys: pass the stage on
+          if (lane == 0) mbar_arrive(&kv_empty[s]);
+          __syncwarp();
+          return;
+        }
+        if (kApart && i > 0) {  // the scores before these have been read
+          ok = wait.all(&s_read[t], (ns - 1) & 1);
+          if (!ok) return;
+        }
+        tc_fence_after();
         if (elect_one()) {
-          mma_rows(tmem + t * 128, sbase + t * L::tile_bytes,
-                   sbase + L::off_ring + stage * L::tile_bytes, nk);
+          mma_rows(t_s, sbase + t * L::tile_bytes, sbase + L::off_ring + s * L::tile_bytes, nk);
           mma_commit(&s_full[t]);
-          if (i == x.n[t] - 1) mma_commit(&q_empty[t]);  // the last use of this Q tile
+          mma_commit(&kv_empty[s]);
+          if (i == mine - 1) mma_commit(&q_empty[t]);  // the last use of this Q tile
         }
         __syncwarp();
+        ++ns;
       };
-      int sk = it % kStages;
-      ok = wait.all(&kv_full[sk], (it / kStages) & 1);
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        if (!ok || x.n[t] == 0) continue;
-        ok = wait.all(&q_full[t], nq[t] & 1);
-        if (!ok) break;
-        tc_fence_after();
-        scores(t, 0, sk);
-      }
-      if (!ok) break;
-      if (elect_one()) mma_commit(&kv_empty[sk]);
-      __syncwarp();
-      ++it;
+      if (mine) ok = wait.all(&q_full[t], nq & 1);
+      if (ok) scores(0, it);
       for (int i = 0; ok && i < n; ++i) {
-        const int sv = it % kStages;  // V of tile i, then K of tile i + 1
+        const int ev = it + 2 * i + 1, sv = ev % kStages;
         // the load first: it came after kv_empty of the stage's last use, hence
         // after that use's v_ready, so the second wait sees no older phase
-        ok = wait.all(&kv_full[sv], (it / kStages) & 1) &&
-             wait.all(&v_ready[sv], (it / kStages) & 1);
+        ok = wait.all(&kv_full[sv], (ev / kStages) & 1);
+        if (ok && x.len - i * kTile < kTile) ok = wait.all(&v_ready[sv], (ev / kStages) & 1);
         if (!ok) break;
-        ++it;
-        const bool more = i + 1 < n;
-        sk = it % kStages;
-        if (more) {
-          ok = wait.all(&kv_full[sk], (it / kStages) & 1);
-          if (!ok) break;
-          ++it;
-        }
+        if (i < mine) {
+          const int halves = halves_of(x, i);
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (!ok || i >= x.n[t]) continue;
-          ok = wait.all(&p_full[t], np[t] & 1);
-          if (ok && i == 0) ok = wait.all(&o_empty[t], (nq[t] & 1) ^ 1);
-          if (!ok) break;
-          ++np[t];
-          tc_fence_after();
-          if (elect_one()) {
-            mma_prob(tmem + 256 + t * DP, tmem + t * 128,
-                     sbase + L::off_ring + sv * L::tile_bytes, no, i != 0);
-            mma_commit(&o_full[t]);
+          for (int h = 0; h < 2; ++h) {
+            if (h == halves) break;
+            ok = wait.all(&p_full[2 * t + h], np[h] & 1);
+            if (ok && i == 0 && h == 0) ok = wait.all(&o_empty[t], (nq & 1) ^ 1);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+              mma_half(t_o, t_p + h * (kApart ? 32 : 64), sbase + L::off_ring + sv * L::tile_bytes,
+                       h, no, i != 0 || h != 0);
+              mma_commit(&o_full[2 * t + h]);
+              if (h == halves - 1) mma_commit(&kv_empty[sv]);
+            }
+            __syncwarp();
+            ++np[h];
+            // S has been read up to its second half by now: the next scores run
+            // under the second half's exponentials
+            if (kApart && h == 0 && i + 1 < n) {
+              scores(i + 1, ev + 1);
+              if (!ok) break;
+            }
           }
+          if (!ok) break;
+        } else {
+          if (lane == 0) mbar_arrive(&kv_empty[sv]);
           __syncwarp();
-          if (i + 1 < x.n[t]) scores(t, i + 1, sk);
         }
-        if (!ok) break;
-        if (elect_one()) {
-          mma_commit(&kv_empty[sv]);
-          if (more) mma_commit(&kv_empty[sk]);
-        }
-        __syncwarp();
+        if ((!kApart || i >= mine) && i + 1 < n) scores(i + 1, ev + 1);
       }
-      nq[0] += x.n[0] != 0;
-      nq[1] += x.n[1] != 0;
+      it += 2 * n;
+      nq += mine != 0;
     }
-    if (it) {  // every MMA issued has completed
-      if (elect_one()) mma_commit(drain);
+    if (ns) {  // every MMA issued has completed
+      if (elect_one()) mma_commit(&drain[t]);
       __syncwarp();
-      mbar_wait_bounded(drain, 0, wait_limit, status);
+      mbar_wait_bounded(&drain[t], 0, wait_limit, status);
     }
   } else if (warp == 10) {
     // -------------------------------------------------------- V tiles' tails
     int it = 0;
     bool ok = true;
-    for (int w = blockIdx.x; ok && w < items; w += gridDim.x) {
-      const FwdItem x = fwd_item(a, p.nslots, w);
+    for (int r = 0; ok && r * (int)gridDim.x < items; ++r) {
+      FwdItem x = fwd_item(a, p.nslots, snake_item(r), items);
+      x.make_uniform();
       const int n = x.tiles();
       for (int i = 0; i < 2 * n; ++i, ++it) {  // K0 V0 K1 V1 ..., as loaded
         const int s = it % kStages;
@@ -329,95 +370,134 @@ attn_fwd_tc(const __grid_constant__ FwdParams p, unsigned *status, long long wai
     }
   } else if (warp < 10) {
     // -------------------------------------------------------- softmax
-    const int t = (warp - 2) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+    const int t = (warp - 2) >> 2, quarter = warp & 3;
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     const uint32_t ts = tmem + t * 128 + lanes, to = tmem + 256 + t * DP + lanes;
+    const uint32_t tp = kApart ? tmem + 384 + t * 64 + lanes : ts;
     const float s2 = a.scale * kLog2E;
-    int np = 0;
+    const float2 sc = make_float2(s2, s2);
+    int ns = 0, np0 = 0, np1 = 0;  // score tiles, first and second halves so far
     bool ok = true;
-    for (int w = blockIdx.x; ok && w < items; w += gridDim.x) {
-      const FwdItem x = fwd_item(a, p.nslots, w);
-      const int n = x.n[t];
+    for (int r = 0; ok && r * (int)gridDim.x < items; ++r) {
+      FwdItem x = fwd_item(a, p.nslots, snake_item(r), items);
+      x.make_uniform();
+      // selected, not indexed: an index would put the item into local memory,
+      // and beside this much shared memory L1 holds next to nothing of it
+      const int n = t ? x.n[1] : x.n[0], row0 = t ? x.row0[1] : x.row0[0];
+      const int head = t ? x.h[1] : x.h[0];
       if (n == 0) continue;
-      const int row = x.row0[t] + r;                              // within the sequence
+      const int row = row0 + quarter * 32 + lane;                   // within the sequence
       const int last = a.causal ? min(row, x.len - 1) : x.len - 1;  // the last key seen
-      const int last_all = a.causal ? min(x.row0[t], x.len - 1) : x.len - 1;  // by every row
+      const int last_all = a.causal ? min(row0, x.len - 1) : x.len - 1;  // by every row
       float m = -INFINITY, ms = 0.f;
       float2 l2 = make_float2(0.f, 0.f);
-      for (int i = 0; i < n; ++i, ++np) {
-        ok = wait.all(&s_full[t], np & 1);
+      for (int i = 0; ok && i < n; ++i, ++ns) {
+        ok = wait.all(&s_full[t], ns & 1);
         if (!ok) break;
         tc_fence_after();
-        uint32_t s[2][64];
-        tmem_ld64(ts, s[0]);
-        tmem_ld64(ts + 64, s[1]);
-        if (i * kTile + kTile - 1 > last_all) {
-          const int lim = last - i * kTile;
-#pragma unroll
-          for (int c = 0; c < kTile; ++c)
-            if (c > lim) s[c >> 6][c & 63] = 0xff800000u;  // -inf
-        }
-        float mx[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) mx[e] = __uint_as_float(s[0][e]);
-#pragma unroll
-        for (int c = 4; c < kTile; ++c)
-          mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(s[c >> 6][c & 63]));
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        if (i == 0) {
-          m = top;
-          ms = m == -INFINITY ? 0.f : m * s2;
-        } else if (__any_sync(0xffffffffu, (top - m) * s2 > kRaise)) {
-          const float mn = fmaxf(m, top);
-          const float ns = mn == -INFINITY ? 0.f : mn * s2;
-          const float f = ex2(m * s2 - ns);
-          ok = wait.all(&o_full[t], (np - 1) & 1);  // P V of the tile before is in O
-          if (!ok) break;
-          tc_fence_after();
+        const int halves = halves_of(x, i);
+#pragma unroll 1
+        for (int h = 0; h < halves; ++h) {
+          uint32_t s[64];
           __syncwarp();
-#pragma unroll
-          for (int c = 0; c < DP; c += 32) {
-            uint32_t o[32];
-            tmem_ld32(to + c, o);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-            tmem_st32(to + c, o);
+          tmem_ld64(ts + 64 * h, s);
+          if (kApart && h == halves - 1) {  // the next scores may replace these
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s_read[t]);
           }
-          l2.x *= f;
-          l2.y *= f;
-          m = mn;
-          ms = ns;
-        }
-        __syncwarp();
-        const float2 sc = make_float2(s2, s2), off = make_float2(-ms, -ms);
+          const int c0 = i * kTile + 64 * h;
+          if (c0 + 63 > last_all) {
+            const int lim = last - c0;
 #pragma unroll
-        for (int c = 0; c < kTile; c += 32) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            const int g = c + e;
-            float2 v = make_float2(__uint_as_float(s[g >> 6][g & 63]),
-                                   __uint_as_float(s[g >> 6][(g & 63) + 1]));
-            v = __ffma2_rn(v, sc, off);
-            v.x = ex2(v.x);
-            v.y = ex2(v.y);
-            l2 = __fadd2_rn(l2, v);
-            pk[e >> 1] = pack_bf16(v.x, v.y);
+            for (int c = 0; c < 64; ++c)
+              if (c > lim) s[c] = 0xff800000u;  // -inf
           }
-          tmem_st16(ts + (c >> 1), pk);
+          const int nh = h ? np1 : np0;
+          if (kApart && nh > 0) {  // the last P V of this half's columns has read them
+            ok = wait.all(&o_full[2 * t + h], (nh - 1) & 1);
+            if (!ok) break;
+            tc_fence_after();
+          }
+          // p against the standing maximum, into tensor memory; returns the sum
+          auto probs = [&]() {
+            const float2 off = make_float2(-ms, -ms);
+            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+            uint32_t pk[32];  // one block without a barrier, for the scheduler to interleave
+#pragma unroll
+            for (int c = 0; c < 64; c += 2) {
+              float2 v =
+                  make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+              v = __ffma2_rn(v, sc, off);
+              v.x = ex2(v.x);
+              v.y = ex2(v.y);
+              sum[(c >> 1) & 1] = __fadd2_rn(sum[(c >> 1) & 1], v);
+              pk[c >> 1] = pack_bf16(v.x, v.y);
+            }
+            __syncwarp();
+            tmem_st32(tp + h * (kApart ? 32 : 64), pk);
+            return __fadd2_rn(sum[0], sum[1]);
+          };
+          float top;
+          {
+            float mx[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              mx[e] = fmaxf(__uint_as_float(s[e]), __uint_as_float(s[e + 4]));
+#pragma unroll
+            for (int c = 8; c < 64; c += 8)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                mx[e] = max3(mx[e], __uint_as_float(s[c + e]), __uint_as_float(s[c + e + 4]));
+            top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
+          }
+          if (i == 0 && h == 0) {
+            m = top;
+            ms = m == -INFINITY ? 0.f : m * s2;
+          }
+          float2 sum = probs();
+          if (__any_sync(0xffffffffu, (top - m) * s2 > kRaise)) {
+            const float mn = fmaxf(m, top);
+            const float nm = mn == -INFINITY ? 0.f : mn * s2;
+            const float f = ex2(m * s2 - nm);
+            // the P V before this half is in O (there is one: the first half of the
+            // first tile set the maximum itself)
+            ok = wait.all(&o_full[2 * t + 1 - h], ((h ? np0 : np1) - 1) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            __syncwarp();
+            tmem_wait_st();  // the p that will be written again
+#pragma unroll 1
+            for (int c = 0; c < DP; c += 16) {
+              uint32_t o[16];
+              tmem_ld16(to + c, o);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st16(to + c, o);
+            }
+            l2.x *= f;
+            l2.y *= f;
+            m = mn;
+            ms = nm;
+            sum = probs();
+          }
+          l2 = __fadd2_rn(l2, sum);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[2 * t + h]);
+          np0 += h == 0;
+          np1 += h;
         }
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[t]);
       }
       if (!ok) break;
-      ok = wait.all(&o_full[t], (np - 1) & 1);
+      ok = halves_of(x, n - 1) == 2 ? wait.all(&o_full[2 * t + 1], (np1 - 1) & 1)
+                                    : wait.all(&o_full[2 * t], (np0 - 1) & 1);
       if (!ok) break;
       tc_fence_after();
       const float l = l2.x + l2.y, inv = 1.f / l;
       const bool in = row < x.len;
-      bf16 *o = (bf16 *)a.o + (int64_t)(x.start + row) * a.ld_o + (int64_t)x.h[t] * a.D;
+      bf16 *o = (bf16 *)a.o + (int64_t)(x.start + row) * a.ld_o + (int64_t)head * a.D;
       // the whole row first, the warp converged, then the divergent stores: a
       // tensor-memory load must never sit behind a branch that lanes take apart
       uint32_t v[DP / 64][64];
@@ -441,7 +521,7 @@ attn_fwd_tc(const __grid_constant__ FwdParams p, unsigned *status, long long wai
         }
       }
       if (in && a.lse)
-        a.lse[(int64_t)x.h[t] * a.T + x.start + row] = ms * kLn2 + logf(l);
+        a.lse[(int64_t)head * a.T + x.start + row] = ms * kLn2 + logf(l);
       __syncwarp();
     }
   }

@@ -58,6 +58,15 @@ __device__ __forceinline__ void tmem_dealloc1(uint32_t taddr, uint32_t ncols) {
                : "memory");
 }
 
+// v, which every lane of the warp holds, in a form that the compiler knows to
+// be one value per warp (the reduction's result is a uniform register).  The
+// MMAs and tile loads take their operands from uniform registers: values that
+// only happen to be equal are moved there one by one before each of them.
+__device__ __forceinline__ int uniform(int v) { return __reduce_max_sync(0xffffffffu, v); }
+__device__ __forceinline__ uint32_t uniform(uint32_t v) {
+  return __reduce_max_sync(0xffffffffu, v);
+}
+
 // One lane of a converged warp.  The instructions below read their operands
 // from the warp's uniform registers; with elect.sync the compiler knows that
 // one lane runs them and keeps those registers right.  Under a plain test of
@@ -123,16 +132,38 @@ __device__ __forceinline__ void mma_rows(uint32_t acc, uint32_t a, uint32_t b, i
   for (int kk = 0; kk < 8; ++kk)
     if (kk < nk) mma_ss(acc, desc_k(a, kk), desc_k(b, kk), id, kk != 0);
 }
-// acc [128 x n] (+)= P B, P [128 x 128] bf16 in tensor memory, B's 128 rows contracted.
-__device__ __forceinline__ void mma_prob(uint32_t acc, uint32_t p, uint32_t b, int n,
+// acc [128 x n] (+)= P B over rows 64 half .. 64 half + 63 of B; P [128 x 64] of
+// that half in bf16 in 32 columns of tensor memory from p on.
+__device__ __forceinline__ void mma_half(uint32_t acc, uint32_t p, uint32_t b, int half, int n,
                                          bool accumulate) {
   const uint32_t id = idesc_of(n, true);
 #pragma unroll
-  for (int kk = 0; kk < 8; ++kk)
-    mma_ts(acc, p + (uint32_t)kk * 8u, desc_mn(b, kk), id, accumulate || kk != 0);
+  for (int kk = 0; kk < 4; ++kk)
+    mma_ts(acc, p + (uint32_t)kk * 8u, desc_mn(b, 4 * half + kk), id, accumulate || kk != 0);
 }
 
-// 16 (32) columns of this thread's lane from registers.
+// This CTA's item of round r: rounds run through the grid back
+// and forth, so that items sorted by cost even out.  May be >= the number of
+// items in the last round; the loop goes on while r * grid < items.
+__device__ __forceinline__ int snake_item(int r) {
+  const int g = (int)gridDim.x, b = (int)blockIdx.x;
+  return r * g + ((r & 1) ? g - 1 - b : b);
+}
+
+// The larger of three (one instruction).
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// 8, 16 or 32 columns of this thread's lane from registers.
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+      : "memory");
+}
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
@@ -152,6 +183,56 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32
       "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]),
       "r"(v[30]), "r"(v[31])
       : "memory");
+}
+// 16 columns of this thread's lane, waited for in the same statement.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+        "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
+        "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr)
+      : "memory");
+}
+// tmem_ld64 in two steps: the load, and the wait that makes the values usable
+// (the values pass through it, so no use can be placed before it).
+__device__ __forceinline__ void tmem_ld64_start(uint32_t taddr, uint32_t (&v)[64]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
+      "%28, %29, %30, %31, %32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, "
+      "%45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, "
+      "%62, %63}, [%64];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+        "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
+        "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]),
+        "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]),
+        "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31]), "=r"(v[32]), "=r"(v[33]), "=r"(v[34]),
+        "=r"(v[35]), "=r"(v[36]), "=r"(v[37]), "=r"(v[38]), "=r"(v[39]), "=r"(v[40]), "=r"(v[41]),
+        "=r"(v[42]), "=r"(v[43]), "=r"(v[44]), "=r"(v[45]), "=r"(v[46]), "=r"(v[47]), "=r"(v[48]),
+        "=r"(v[49]), "=r"(v[50]), "=r"(v[51]), "=r"(v[52]), "=r"(v[53]), "=r"(v[54]), "=r"(v[55]),
+        "=r"(v[56]), "=r"(v[57]), "=r"(v[58]), "=r"(v[59]), "=r"(v[60]), "=r"(v[61]), "=r"(v[62]),
+        "=r"(v[63])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld64_finish(uint32_t (&v)[64]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]),
+                 "+r"(v[6]), "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]),
+                 "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]), "+r"(v[16]), "+r"(v[17]),
+                 "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]),
+                 "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]),
+                 "+r"(v[30]), "+r"(v[31]), "+r"(v[32]), "+r"(v[33]), "+r"(v[34]), "+r"(v[35]),
+                 "+r"(v[36]), "+r"(v[37]), "+r"(v[38]), "+r"(v[39]), "+r"(v[40]), "+r"(v[41]),
+                 "+r"(v[42]), "+r"(v[43]), "+r"(v[44]), "+r"(v[45]), "+r"(v[46]), "+r"(v[47]),
+                 "+r"(v[48]), "+r"(v[49]), "+r"(v[50]), "+r"(v[51]), "+r"(v[52]), "+r"(v[53]),
+                 "+r"(v[54]), "+r"(v[55]), "+r"(v[56]), "+r"(v[57]), "+r"(v[58]), "+r"(v[59]),
+                 "+r"(v[60]), "+r"(v[61]), "+r"(v[62]), "+r"(v[63])
+               :
+               : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -173,15 +254,31 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return *reinterpret_cast<const uint32_t *>(&h);
 }
 
+// One look at a barrier that may suspend the warp for up to about a
+// millisecond.  A wait that spins instead takes issue slots and shared-memory
+// queue entries (which the exponentials go through as well) from the warps
+// that work.
+__device__ __forceinline__ bool mbar_try_wait_long(uint64_t *bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_addr(bar)), "r"(parity), "r"(1000000)
+      : "memory");
+  return done != 0;
+}
+
 // The waits of a CTA: bounded, and over as soon as any role has given up.
 struct Waits {
   volatile int *abort;
   unsigned *status;
   long long limit;
   __device__ __forceinline__ bool operator()(uint64_t *bar, uint32_t parity) const {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (mbar_try_wait_long(bar, parity)) return true;
     const long long t0 = clock64();
-    while (!mbar_try_wait(bar, parity)) {
+    while (!mbar_try_wait_long(bar, parity)) {
       if (*abort) return false;
       if (clock64() - t0 > limit) {
         atomicOr(status, kStatusWaitTimeout);
