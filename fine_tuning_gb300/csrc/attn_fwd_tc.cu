@@ -267,23 +267,20 @@ attn_fwd_tc(const __grid_constant__ FwdParams p, unsigned *status, long long wai
     const uint32_t t_s = tmem + t * 128, t_o = tmem + 256 + t * DP;
     const uint32_t t_p = kApart ? tmem + 384 + t * 64 : t_s;
     int it = 0, nq = 0, ns = 0;  // ring entries, items, score tiles so far
-    int np[2] = {0, 0};          // first and second halves so far
+    int np0 = 0, np1 = 0;        // first and second halves so far
     bool ok = true;
     for (int r = 0; ok && r * (int)gridDim.x < items; ++r) {
       FwdItem x = fwd_item(a, p.nslots, snake_item(r), items);
       x.make_uniform();
       const int n = x.tiles(), mine = t ? x.n[1] : x.n[0];
       if (n == 0) continue;
-      // scores of key tile i, ring entry e
-      auto scores = [&](int i, int e) {
+      auto keys = [&](int e) {  // ring entry e has been loaded
         const int s = e % kStages;
         ok = wait.all(&kv_full[s], (e / kStages) & 1);
-        if (!ok) return;
-        if (i >= mine) {  // the other tile's keys: pass the stage on
-          if (lane == 0) mbar_arrive(&kv_empty[s]);
-          __syncwarp();
-          return;
-        }
+      };
+      // scores of key tile i, whose keys (loaded) are ring entry e
+      auto scores = [&](int i, int e) {
+        const int s = e % kStages;
         if (kApart && i > 0) {  // the scores before these have been read
           ok = wait.all(&s_read[t], (ns - 1) & 1);
           if (!ok) return;
@@ -298,45 +295,62 @@ attn_fwd_tc(const __grid_constant__ FwdParams p, unsigned *status, long long wai
         __syncwarp();
         ++ns;
       };
-      if (mine) ok = wait.all(&q_full[t], nq & 1);
-      if (ok) scores(0, it);
+      auto pass = [&](int e) {  // an entry of the other tile's alone
+        keys(e);
+        if (ok && lane == 0) mbar_arrive(&kv_empty[e % kStages]);
+        __syncwarp();
+      };
+      if (mine) {
+        ok = wait.all(&q_full[t], nq & 1);
+        if (ok) keys(it);
+        if (ok) scores(0, it);
+      } else {
+        pass(it);
+      }
       for (int i = 0; ok && i < n; ++i) {
-        const int ev = it + 2 * i + 1, sv = ev % kStages;
-        // the load first: it came after kv_empty of the stage's last use, hence
-        // after that use's v_ready, so the second wait sees no older phase
-        ok = wait.all(&kv_full[sv], (ev / kStages) & 1);
+        const int ev = it + 2 * i + 1, sv = ev % kStages;  // V of this tile; K of the next follows
+        const bool next = i + 1 < mine;
+        if (i >= mine) {
+          pass(ev);
+          if (ok && i + 1 < n) pass(ev + 1);
+          continue;
+        }
+        if (kApart && next) {  // the next scores run under this tile's exponentials
+          keys(ev + 1);
+          if (ok) scores(i + 1, ev + 1);
+          if (!ok) break;
+        }
+        keys(ev);
+        // after the load, which came after kv_empty of the stage's last use, hence
+        // after that use's v_ready: this wait sees no older phase
         if (ok && x.len - i * kTile < kTile) ok = wait.all(&v_ready[sv], (ev / kStages) & 1);
         if (!ok) break;
-        if (i < mine) {
-          const int halves = halves_of(x, i);
+        const int halves = halves_of(x, i);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (h == halves) break;
-            ok = wait.all(&p_full[2 * t + h], np[h] & 1);
-            if (ok && i == 0 && h == 0) ok = wait.all(&o_empty[t], (nq & 1) ^ 1);
-            if (!ok) break;
-            tc_fence_after();
-            if (elect_one()) {
-              mma_half(t_o, t_p + h * (kApart ? 32 : 64), sbase + L::off_ring + sv * L::tile_bytes,
-                       h, no, i != 0 || h != 0);
-              mma_commit(&o_full[2 * t + h]);
-              if (h == halves - 1) mma_commit(&kv_empty[sv]);
-            }
-            __syncwarp();
-            ++np[h];
-            // S has been read up to its second half by now: the next scores run
-            // under the second half's exponentials
-            if (kApart && h == 0 && i + 1 < n) {
-              scores(i + 1, ev + 1);
-              if (!ok) break;
-            }
-          }
+        for (int h = 0; h < 2; ++h) {
+          // with room beside S the softmax hands over a tile's p at once
+          if (h == halves) break;
+          if (!kApart || h == 0) ok = wait.all(&p_full[2 * t + h], (h ? np1 : np0) & 1);
+          if (ok && i == 0 && h == 0) ok = wait.all(&o_empty[t], (nq & 1) ^ 1);
           if (!ok) break;
-        } else {
-          if (lane == 0) mbar_arrive(&kv_empty[sv]);
+          tc_fence_after();
+          if (elect_one()) {
+            mma_half(t_o, t_p + h * (kApart ? 32 : 64), sbase + L::off_ring + sv * L::tile_bytes, h,
+                     no, i != 0 || h != 0);
+            if (!kApart || h == halves - 1) mma_commit(&o_full[kApart ? 2 * t : 2 * t + h]);
+            if (h == halves - 1) mma_commit(&kv_empty[sv]);
+          }
           __syncwarp();
+          np0 += h == 0;
+          np1 += h;
+          if (!kApart && h == 0 && next) {  // looked at while the second half is formed
+            keys(ev + 1);
+            if (!ok) break;
+          }
         }
-        if ((!kApart || i >= mine) && i + 1 < n) scores(i + 1, ev + 1);
+        if (!ok) break;
+        if (!kApart && next) scores(i + 1, ev + 1);
+        if (ok && !next && i + 1 < n) pass(ev + 1);
       }
       it += 2 * n;
       nq += mine != 0;
@@ -396,16 +410,10 @@ attn_fwd_tc(const __grid_constant__ FwdParams p, unsigned *status, long long wai
         if (!ok) break;
         tc_fence_after();
         const int halves = halves_of(x, i);
-#pragma unroll 1
-        for (int h = 0; h < halves; ++h) {
-          uint32_t s[64];
+        // 64 columns from column 64 h on, masked
+        auto load = [&](int h, uint32_t (&s)[64]) {
           __syncwarp();
           tmem_ld64(ts + 64 * h, s);
-          if (kApart && h == halves - 1) {  // the next scores may replace these
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&s_read[t]);
-          }
           const int c0 = i * kTile + 64 * h;
           if (c0 + 63 > last_all) {
             const int lim = last - c0;
@@ -413,85 +421,130 @@ attn_fwd_tc(const __grid_constant__ FwdParams p, unsigned *status, long long wai
             for (int c = 0; c < 64; ++c)
               if (c > lim) s[c] = 0xff800000u;  // -inf
           }
-          const int nh = h ? np1 : np0;
-          if (kApart && nh > 0) {  // the last P V of this half's columns has read them
-            ok = wait.all(&o_full[2 * t + h], (nh - 1) & 1);
-            if (!ok) break;
-            tc_fence_after();
-          }
-          // p against the standing maximum, into tensor memory; returns the sum
-          auto probs = [&]() {
-            const float2 off = make_float2(-ms, -ms);
-            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-            uint32_t pk[32];  // one block without a barrier, for the scheduler to interleave
+        };
+        auto highest = [&](const uint32_t (&s)[64]) {
+          float mx[4];
 #pragma unroll
-            for (int c = 0; c < 64; c += 2) {
-              float2 v =
-                  make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
-              v = __ffma2_rn(v, sc, off);
-              v.x = ex2(v.x);
-              v.y = ex2(v.y);
-              sum[(c >> 1) & 1] = __fadd2_rn(sum[(c >> 1) & 1], v);
-              pk[c >> 1] = pack_bf16(v.x, v.y);
-            }
-            __syncwarp();
-            tmem_st32(tp + h * (kApart ? 32 : 64), pk);
-            return __fadd2_rn(sum[0], sum[1]);
-          };
-          float top;
-          {
-            float mx[4];
+          for (int e = 0; e < 4; ++e)
+            mx[e] = fmaxf(__uint_as_float(s[e]), __uint_as_float(s[e + 4]));
+#pragma unroll
+          for (int c = 8; c < 64; c += 8)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              mx[e] = fmaxf(__uint_as_float(s[e]), __uint_as_float(s[e + 4]));
+              mx[e] = max3(mx[e], __uint_as_float(s[c + e]), __uint_as_float(s[c + e + 4]));
+          return fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
+        };
+        // p against the standing maximum: 32 words of bf16 pairs, and their sum
+        auto probs = [&](const uint32_t (&s)[64], uint32_t (&pk)[32]) {
+          const float2 off = make_float2(-ms, -ms);
+          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-            for (int c = 8; c < 64; c += 8)
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                mx[e] = max3(mx[e], __uint_as_float(s[c + e]), __uint_as_float(s[c + e + 4]));
-            top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
+          for (int c = 0; c < 64; c += 2) {
+            float2 v = make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+            v = __ffma2_rn(v, sc, off);
+            v.x = ex2(v.x);
+            v.y = ex2(v.y);
+            sum[(c >> 1) & 1] = __fadd2_rn(sum[(c >> 1) & 1], v);
+            pk[c >> 1] = pack_bf16(v.x, v.y);
           }
-          if (i == 0 && h == 0) {
+          return __fadd2_rn(sum[0], sum[1]);
+        };
+        // brings O and l from the standing maximum to `to_m`, once the P V that
+        // `bar` counts is in O
+        auto raise = [&](float to_m, uint64_t *bar, int count) {
+          const float nm = to_m == -INFINITY ? 0.f : to_m * s2;
+          const float f = ex2(m * s2 - nm);
+          ok = wait.all(bar, (count - 1) & 1);
+          if (!ok) return;
+          tc_fence_after();
+          __syncwarp();
+#pragma unroll 1
+          for (int c = 0; c < DP; c += 16) {
+            uint32_t o[16];
+            tmem_ld16(to + c, o);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tmem_st16(to + c, o);
+          }
+          l2.x *= f;
+          l2.y *= f;
+          m = to_m;
+          ms = nm;
+        };
+        if constexpr (kApart) {
+          uint32_t s[64], p0[32], p1[32];
+          load(0, s);
+          float top = highest(s);
+          if (i == 0) {
             m = top;
             ms = m == -INFINITY ? 0.f : m * s2;
           }
-          float2 sum = probs();
+          float2 sum = probs(s, p0);
+          if (halves == 2) {
+            load(1, s);
+            top = fmaxf(top, highest(s));
+          }
           if (__any_sync(0xffffffffu, (top - m) * s2 > kRaise)) {
-            const float mn = fmaxf(m, top);
-            const float nm = mn == -INFINITY ? 0.f : mn * s2;
-            const float f = ex2(m * s2 - nm);
-            // the P V before this half is in O (there is one: the first half of the
-            // first tile set the maximum itself)
-            ok = wait.all(&o_full[2 * t + 1 - h], ((h ? np0 : np1) - 1) & 1);
+            if (i > 0) {
+              raise(fmaxf(m, top), &o_full[2 * t], np0);
+              if (!ok) break;
+            } else {  // nothing in O yet: the first half's maximum was too low
+              m = fmaxf(m, top);
+              ms = m * s2;
+            }
+            load(0, s);
+            sum = probs(s, p0);
+            if (halves == 2) load(1, s);
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s_read[t]);  // the next scores may replace these
+          if (halves == 2) sum = __fadd2_rn(sum, probs(s, p1));
+          l2 = __fadd2_rn(l2, sum);
+          if (np0 > 0) {  // the last P V has read P's columns
+            ok = wait.all(&o_full[2 * t], (np0 - 1) & 1);
             if (!ok) break;
             tc_fence_after();
-            __syncwarp();
-            tmem_wait_st();  // the p that will be written again
-#pragma unroll 1
-            for (int c = 0; c < DP; c += 16) {
-              uint32_t o[16];
-              tmem_ld16(to + c, o);
-#pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-              tmem_st16(to + c, o);
-            }
-            l2.x *= f;
-            l2.y *= f;
-            m = mn;
-            ms = nm;
-            sum = probs();
           }
-          l2 = __fadd2_rn(l2, sum);
+          __syncwarp();
+          tmem_st32(tp, p0);
+          if (halves == 2) tmem_st32(tp + 32, p1);
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&p_full[2 * t + h]);
-          np0 += h == 0;
-          np1 += h;
+          if (lane == 0) mbar_arrive(&p_full[2 * t]);
+          ++np0;
+        } else {
+#pragma unroll 1
+          for (int h = 0; h < halves; ++h) {
+            uint32_t s[64], pk[32];
+            load(h, s);
+            const float top = highest(s);
+            if (i == 0 && h == 0) {
+              m = top;
+              ms = m == -INFINITY ? 0.f : m * s2;
+            }
+            float2 sum = probs(s, pk);
+            if (__any_sync(0xffffffffu, (top - m) * s2 > kRaise)) {
+              // (never the first half of the first tile, which set the maximum)
+              raise(fmaxf(m, top), &o_full[2 * t + 1 - h], h ? np0 : np1);
+              if (!ok) break;
+              sum = probs(s, pk);
+            }
+            l2 = __fadd2_rn(l2, sum);
+            __syncwarp();
+            tmem_st32(tp + 64 * h, pk);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_full[2 * t + h]);
+            np0 += h == 0;
+            np1 += h;
+          }
         }
       }
       if (!ok) break;
-      ok = halves_of(x, n - 1) == 2 ? wait.all(&o_full[2 * t + 1], (np1 - 1) & 1)
+      ok = !kApart && halves_of(x, n - 1) == 2 ? wait.all(&o_full[2 * t + 1], (np1 - 1) & 1)
                                     : wait.all(&o_full[2 * t], (np0 - 1) & 1);
       if (!ok) break;
       tc_fence_after();
