@@ -41,6 +41,10 @@ struct BwdParams {
   int slots;
 };
 
+__device__ __forceinline__ SeqTile uniform_tile(const SeqTile &x) {
+  return SeqTile{uniform(x.start), uniform(x.len), uniform(x.row0)};
+}
+
 // acc [128 x n] (+)= P B with P's bf16 halves in columns 0..31 and 64..95 of p.
 __device__ __forceinline__ void mma_halves(uint32_t acc, uint32_t p, uint32_t b, int n,
                                            bool accumulate) {
@@ -141,7 +145,7 @@ attn_dq_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wait
   uint64_t *drain = acc_empty + 1;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 2);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kK; ++s) {
@@ -170,7 +174,7 @@ attn_dq_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wait
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = uniform(*tmem_slot);
   const uint32_t t_dp = tmem + 256, t_dq = tmem + 384;
   const Waits wait{abort_flag, status, wait_limit};
   const AttnArgs &a = p.a;
@@ -178,11 +182,13 @@ attn_dq_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wait
   pdl_trigger();
   const int G = a.Hq / a.Hkv;
   const int items = attn_skipped(a.skip) ? 0 : p.slots * a.Hq;
-  // item w: head w % Hq (the heads of a group follow each other and share K and
+  // item of round r: head w % Hq (the heads of a group follow each other and share K and
   // V in L2), tiles from the last one back, whose rows see most keys
-  auto item = [&](int w, int &h) {
-    h = w % a.Hq;
-    return seq_tile(p.slots - 1 - w / a.Hq, a.cu, a.B, (int)a.T, kTile);
+  auto item = [&](int r, int &h) {
+    const int w = snake_item(r);
+    if (w >= items) return SeqTile{0, 0, 0};
+    h = uniform(w % a.Hq);
+    return uniform_tile(seq_tile(p.slots - 1 - w / a.Hq, a.cu, a.B, (int)a.T, kTile));
   };
   auto tiles = [&](const SeqTile &x) {
     return x.len == 0 ? 0 : a.causal ? x.row0 / kTile + 1 : ceil_div(x.len, kTile);
@@ -192,9 +198,9 @@ attn_dq_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wait
     // -------------------------------------------------------- tile loads
     int it = 0, nq = 0;
     bool ok = true;
-    for (int w = blockIdx.x; ok && w < items; w += gridDim.x) {
-      int h;
-      const SeqTile x = item(w, h);
+    for (int r = 0; ok && r * (int)gridDim.x < items; ++r) {
+      int h = 0;
+      const SeqTile x = item(r, h);
       const int n = tiles(x);
       if (n == 0) continue;
       ok = wait.all(q_empty, (nq & 1) ^ 1);
@@ -239,9 +245,9 @@ attn_dq_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wait
     const int nk = (a.D + 15) / 16, no = nk * 16;
     int it = 0, nq = 0;  // key tiles and items so far
     bool ok = true;
-    for (int w = blockIdx.x; ok && w < items; w += gridDim.x) {
-      int h;
-      const SeqTile x = item(w, h);
+    for (int r = 0; ok && r * (int)gridDim.x < items; ++r) {
+      int h = 0;
+      const SeqTile x = item(r, h);
       const int n = tiles(x);
       if (n == 0) continue;
       auto scores = [&](int i) {  // S of key tile i of this item
@@ -302,9 +308,9 @@ attn_dq_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wait
     // -------------------------------------------------------- K tiles' tails
     int it = 0;
     bool ok = true;
-    for (int w = blockIdx.x; ok && w < items; w += gridDim.x) {
-      int h;
-      const SeqTile x = item(w, h);
+    for (int r = 0; ok && r * (int)gridDim.x < items; ++r) {
+      int h = 0;
+      const SeqTile x = item(r, h);
       const int n = tiles(x);
       for (int i = 0; i < n; ++i, ++it) {
         const int s = it % kK;
@@ -321,17 +327,18 @@ attn_dq_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wait
     }
   } else if (warp < 10) {
     // -------------------------------------------------------- p and ds
-    const int half = (warp - 2) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+    const int half = (warp - 2) >> 2, quarter = warp & 3;
+    const int in_tile = quarter * 32 + lane;
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     const float s2 = a.scale * kLog2E;
     int it = 0, nq = 0;
     bool ok = true;
-    for (int w = blockIdx.x; ok && w < items; w += gridDim.x) {
-      int h;
-      const SeqTile x = item(w, h);
+    for (int r = 0; ok && r * (int)gridDim.x < items; ++r) {
+      int h = 0;
+      const SeqTile x = item(r, h);
       const int n = tiles(x);
       if (n == 0) continue;
-      const int row = x.row0 + r;
+      const int row = x.row0 + in_tile;
       const bool in = row < x.len;
       const int64_t at = (int64_t)h * a.T + x.start + row;
       const float lse2 = in ? a.lse[at] * kLog2E : 0.f, delta = in ? a.delta[at] : 0.f;
@@ -363,17 +370,21 @@ attn_dq_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wait
           uint32_t d[64];
           tmem_ld64(t_dp + 64 * half + lanes, d);
           const float2 off = make_float2(-delta, -delta);
-          const int lim = last - i * kTile - 64 * half;  // the last column seen
 #pragma unroll
           for (int c = 0; c < 32; ++c) {
-            float2 v = make_float2(__uint_as_float(d[2 * c]), __uint_as_float(d[2 * c + 1]));
-            v = __fmul2_rn(pr[c], __fadd2_rn(v, off));
-            if (masked) {  // selected, not multiplied: what lies behind may be NaN
-              v.x = 2 * c > lim ? 0.f : v.x;
-              v.y = 2 * c + 1 > lim ? 0.f : v.y;
-            }
-            pk[c] = pack_bf16(v.x, v.y);
+            const float2 v = make_float2(__uint_as_float(d[2 * c]), __uint_as_float(d[2 * c + 1]));
+            pr[c] = __fmul2_rn(pr[c], __fadd2_rn(v, off));
           }
+          if (masked) {  // selected, not multiplied: what lies behind may be NaN
+            const int lim = last - i * kTile - 64 * half;  // the last column seen
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+              pr[c].x = 2 * c > lim ? 0.f : pr[c].x;
+              pr[c].y = 2 * c + 1 > lim ? 0.f : pr[c].y;
+            }
+          }
+#pragma unroll
+          for (int c = 0; c < 32; ++c) pk[c] = pack_bf16(pr[c].x, pr[c].y);
         }
         __syncwarp();
         tmem_st32(ts, pk);
@@ -453,7 +464,7 @@ attn_dkv_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wai
   uint64_t *acc_full = ds_ready + 1, *acc_empty = acc_full + 1, *drain = acc_empty + 1;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kS; ++s) {
@@ -480,7 +491,7 @@ attn_dkv_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wai
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = uniform(*tmem_slot);
   const uint32_t t_dp = tmem + 128, t_dv = tmem + 256, t_dk = tmem + 256 + DP;
   const Waits wait{abort_flag, status, wait_limit};
   const AttnArgs &a = p.a;
@@ -488,10 +499,12 @@ attn_dkv_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wai
   pdl_trigger();
   const int G = a.Hq / a.Hkv;
   const int items = attn_skipped(a.skip) ? 0 : p.slots * a.Hkv;
-  // item w: key head w % Hkv; tiles from the first one on, which most rows see
-  auto item = [&](int w, int &hk) {
-    hk = w % a.Hkv;
-    return seq_tile(w / a.Hkv, a.cu, a.B, (int)a.T, kTile);
+  // item of round r: key head w % Hkv; tiles from the first one on, which most rows see
+  auto item = [&](int r, int &hk) {
+    const int w = snake_item(r);
+    if (w >= items) return SeqTile{0, 0, 0};
+    hk = uniform(w % a.Hkv);
+    return uniform_tile(seq_tile(w / a.Hkv, a.cu, a.B, (int)a.T, kTile));
   };
   // query tiles first .. first + count - 1 of every head; step j of the item is
   // query tile first + j % count of head hk G + j / count
@@ -504,9 +517,9 @@ attn_dkv_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wai
     // -------------------------------------------------------- tile loads
     int it = 0, nkv = 0;
     bool ok = true, half_step = false;
-    for (int w = blockIdx.x; ok && w < items; w += gridDim.x) {
-      int hk;
-      const SeqTile x = item(w, hk);
+    for (int r = 0; ok && r * (int)gridDim.x < items; ++r) {
+      int hk = 0;
+      const SeqTile x = item(r, hk);
       const int nt = count(x), f = first_tile(x);
       if (nt == 0) continue;
       ok = wait.all(kv_empty, (nkv & 1) ^ 1);
@@ -548,9 +561,9 @@ attn_dkv_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wai
     const int nk = (a.D + 15) / 16, no = nk * 16;
     int it = 0, nkv = 0;
     bool ok = true;
-    for (int w = blockIdx.x; ok && w < items; w += gridDim.x) {
-      int hk;
-      const SeqTile x = item(w, hk);
+    for (int r = 0; ok && r * (int)gridDim.x < items; ++r) {
+      int hk = 0;
+      const SeqTile x = item(r, hk);
       const int n = count(x) * G;
       if (n == 0) continue;
       auto scores = [&](int j) {
@@ -617,9 +630,9 @@ attn_dkv_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wai
     // ---------------------------- lse, delta, and the tails of the Q, dO tiles
     int it = 0;
     bool ok = true;
-    for (int w = blockIdx.x; ok && w < items; w += gridDim.x) {
-      int hk;
-      const SeqTile x = item(w, hk);
+    for (int r = 0; ok && r * (int)gridDim.x < items; ++r) {
+      int hk = 0;
+      const SeqTile x = item(r, hk);
       const int nt = count(x), f = first_tile(x);
       for (int g = 0; ok && g < G; ++g)
         for (int i = 0; i < nt; ++i, ++it) {
@@ -658,18 +671,19 @@ attn_dkv_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wai
     }
   } else if (warp < 10) {
     // -------------------------------------------------------- p and ds
-    const int half = (warp - 2) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+    const int half = (warp - 2) >> 2, quarter = warp & 3;
+    const int in_tile = quarter * 32 + lane;
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     const uint32_t ts = tmem + 64 * half + lanes, td = t_dp + 64 * half + lanes;
     const float s2 = a.scale * kLog2E;
     int it = 0, nkv = 0;
     bool ok = true;
-    for (int w = blockIdx.x; ok && w < items; w += gridDim.x) {
-      int hk;
-      const SeqTile x = item(w, hk);
+    for (int r = 0; ok && r * (int)gridDim.x < items; ++r) {
+      int hk = 0;
+      const SeqTile x = item(r, hk);
       const int nt = count(x), f = first_tile(x);
       if (nt == 0) continue;
-      const int row = x.row0 + r;  // key row within the sequence
+      const int row = x.row0 + in_tile;  // key row within the sequence
       for (int j = 0; j < nt * G; ++j, ++it) {
         const int s = it % kS, q0 = (f + j % nt) * kTile + 64 * half;
         ok = wait.all(s_full, it & 1) && wait.all(&t_ready[s], (it / kS) & 1);
@@ -723,17 +737,18 @@ attn_dkv_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wai
             const float4 d = delta[c];
             float2 x0 = make_float2(__uint_as_float(v[4 * c]), __uint_as_float(v[4 * c + 1]));
             float2 x1 = make_float2(__uint_as_float(v[4 * c + 2]), __uint_as_float(v[4 * c + 3]));
-            x0 = __fmul2_rn(pr[2 * c], __fadd2_rn(x0, make_float2(-d.x, -d.y)));
-            x1 = __fmul2_rn(pr[2 * c + 1], __fadd2_rn(x1, make_float2(-d.z, -d.w)));
-            if (masked) {  // selected again: 0 times what lies behind may be NaN
-              x0.x = (4 * c < lo || 4 * c >= hi) ? 0.f : x0.x;
-              x0.y = (4 * c + 1 < lo || 4 * c + 1 >= hi) ? 0.f : x0.y;
-              x1.x = (4 * c + 2 < lo || 4 * c + 2 >= hi) ? 0.f : x1.x;
-              x1.y = (4 * c + 3 < lo || 4 * c + 3 >= hi) ? 0.f : x1.y;
-            }
-            pk[2 * c] = pack_bf16(x0.x, x0.y);
-            pk[2 * c + 1] = pack_bf16(x1.x, x1.y);
+            pr[2 * c] = __fmul2_rn(pr[2 * c], __fadd2_rn(x0, make_float2(-d.x, -d.y)));
+            pr[2 * c + 1] = __fmul2_rn(pr[2 * c + 1], __fadd2_rn(x1, make_float2(-d.z, -d.w)));
           }
+          if (masked) {  // selected again: 0 times what lies behind may be NaN
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+              pr[c].x = (2 * c < lo || 2 * c >= hi) ? 0.f : pr[c].x;
+              pr[c].y = (2 * c + 1 < lo || 2 * c + 1 >= hi) ? 0.f : pr[c].y;
+            }
+          }
+#pragma unroll
+          for (int c = 0; c < 32; ++c) pk[c] = pack_bf16(pr[c].x, pr[c].y);
         }
         __syncwarp();
         tmem_st32(td, pk);
