@@ -250,10 +250,16 @@ attn_dq_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wait
       const SeqTile x = item(r, h);
       const int n = tiles(x);
       if (n == 0) continue;
-      auto scores = [&](int i) {  // S of key tile i of this item
+      auto keys = [&](int i) {  // K of key tile i of this item has been loaded
+        const int u = it + i;
+        ok = wait.all(&k_full[u % kK], (u / kK) & 1);
+      };
+      auto values = [&](int i) {
+        const int u = it + i;
+        ok = wait.all(&v_full[u % kV], (u / kV) & 1);
+      };
+      auto scores = [&](int i) {  // S of key tile i
         const int u = it + i, s = u % kK;
-        ok = wait.all(&k_full[s], (u / kK) & 1);
-        if (!ok) return;
         if (elect_one()) {
           mma_rows(tmem + (u & 1) * 128, sbase, sbase + L::off_k + s * L::tile_bytes, nk);
           mma_commit(&s_full[u & 1]);
@@ -262,8 +268,6 @@ attn_dq_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wait
       };
       auto grads = [&](int i) {  // do v^T of key tile i
         const int u = it + i, s = u % kV;
-        ok = wait.all(&v_full[s], (u / kV) & 1);
-        if (!ok) return;
         if (elect_one()) {
           mma_rows(t_dp, sbase + L::off_g, sbase + L::off_v + s * L::tile_bytes, nk);
           mma_commit(dp_full);
@@ -275,23 +279,30 @@ attn_dq_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wait
       ok = wait.all(q_full, nq & 1);
       if (!ok) break;
       tc_fence_after();
-      scores(0);
+      keys(0);
+      if (ok) scores(0);
+      if (ok) values(0);
       if (ok) grads(0);
+      if (ok && n > 1) keys(1);
       if (ok && n > 1) scores(1);
+      if (ok) ok = wait.all(acc_empty, (nq & 1) ^ 1);
       for (int i = 0; ok && i < n; ++i) {
         const int u = it + i, s = u % kK;
-        ok = wait.all(&ds_ready[u & 1], (u >> 1) & 1) && wait.all(&k_ready[s], (u / kK) & 1);
-        if (ok && i == 0) ok = wait.all(acc_empty, (nq & 1) ^ 1);
+        // looked at while ds is formed, so that the queue below goes out at once
+        if (i + 1 < n) values(i + 1);
+        // (k_ready after the load, which came after the stage's last k_ready)
+        if (ok && x.len - i * kTile < kTile) ok = wait.all(&k_ready[s], (u / kK) & 1);
+        if (ok) ok = wait.all(&ds_ready[u & 1], (u >> 1) & 1);
         if (!ok) break;
         tc_fence_after();
         if (i + 1 < n) grads(i + 1);
-        if (!ok) break;
         if (elect_one()) {
           mma_halves(t_dq, tmem + (u & 1) * 128, sbase + L::off_k + s * L::tile_bytes, no, i != 0);
           mma_commit(&k_empty[s]);
         }
         __syncwarp();
-        if (i + 2 < n) scores(i + 2);
+        if (i + 2 < n) keys(i + 2);
+        if (ok && i + 2 < n) scores(i + 2);
       }
       if (!ok) break;
       if (elect_one()) mma_commit(acc_full);
@@ -438,12 +449,13 @@ attn_dq_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wait
 // do v^T (j+1).
 template <int DP> struct DkvLayout {
   static constexpr uint32_t tile_bytes = (DP / 64) * kBoxBytes;
-  static constexpr int kS = DP == 128 ? 2 : 4;
+  // Q stages (a Q tile is held from S to dk), dO stages, stages of row values
+  static constexpr int kQ = DP == 128 ? 3 : 4, kG = DP == 128 ? 2 : 4, kR = 2;
   static constexpr uint32_t off_v = tile_bytes, off_q = 2 * tile_bytes;
-  static constexpr uint32_t off_g = off_q + kS * tile_bytes;
-  static constexpr uint32_t off_row = off_g + kS * tile_bytes;  // [kS][lse 128, delta 128] floats
-  static constexpr uint32_t off_bar = off_row + kS * 2 * kTile * 4;
-  static constexpr uint32_t smem = off_bar + (6 * kS + 9) * 8 + 16 + 1024;
+  static constexpr uint32_t off_g = off_q + kQ * tile_bytes;
+  static constexpr uint32_t off_row = off_g + kG * tile_bytes;  // [kR][-lse 128, -delta 128] floats
+  static constexpr uint32_t off_bar = off_row + kR * 2 * kTile * 4;
+  static constexpr uint32_t smem = off_bar + (2 * kQ + 2 * kG + 2 * kR + 8) * 8 + 16;
   static_assert(smem <= 227 * 1024, "shared memory per CTA");
 };
 
@@ -451,33 +463,37 @@ template <int DP>
 __global__ void __launch_bounds__(kBwdThreads, 1)
 attn_dkv_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wait_limit) {
   using L = DkvLayout<DP>;
-  constexpr int kS = L::kS;
-  extern __shared__ unsigned char smem_raw[];
-  unsigned char *sm = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
+  constexpr int kQ = L::kQ, kG = L::kG, kR = L::kR;
+  // all of the 227 KB are spoken for, none is left to align the tiles by hand
+  extern __shared__ __align__(1024) unsigned char smem_aligned[];
+  unsigned char *sm = smem_aligned;
   const uint32_t sbase = smem_addr(sm);
   float *rows = reinterpret_cast<float *>(sm + L::off_row);
   uint64_t *q_full = reinterpret_cast<uint64_t *>(sm + L::off_bar);
-  uint64_t *q_empty = q_full + kS, *g_full = q_empty + kS, *g_empty = g_full + kS;
-  uint64_t *t_ready = g_empty + kS, *row_empty = t_ready + kS;
-  uint64_t *kv_full = row_empty + kS, *kv_empty = kv_full + 1, *s_full = kv_empty + 1;
-  uint64_t *dp_full = s_full + 1, *p_ready = dp_full + 1, *ds_ready = p_ready + 1;
+  uint64_t *q_empty = q_full + kQ, *g_full = q_empty + kQ, *g_empty = g_full + kG;
+  uint64_t *s_full = g_empty + kG, *row_empty = s_full + kR;
+  uint64_t *kv_full = row_empty + kR, *kv_empty = kv_full + 1;
+  uint64_t *dp_full = kv_empty + 1, *p_ready = dp_full + 1, *ds_ready = p_ready + 1;
   uint64_t *acc_full = ds_ready + 1, *acc_empty = acc_full + 1, *drain = acc_empty + 1;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   const int warp = uniform((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kS; ++s) {
+    for (int s = 0; s < kQ; ++s) {
       mbar_init(&q_full[s], 1);
       mbar_init(&q_empty[s], 2);  // the MMAs and the tail warp
+    }
+    for (int s = 0; s < kG; ++s) {
       mbar_init(&g_full[s], 1);
       mbar_init(&g_empty[s], 2);
-      mbar_init(&t_ready[s], 1);
+    }
+    for (int s = 0; s < kR; ++s) {
+      mbar_init(&s_full[s], 2);  // the scores, and the row values with the tails' zeros
       mbar_init(&row_empty[s], kComputeWarps);
     }
     mbar_init(kv_full, 1);
     mbar_init(kv_empty, 1);
-    mbar_init(s_full, 1);
     mbar_init(dp_full, 1);
     mbar_init(p_ready, kComputeWarps);
     mbar_init(ds_ready, kComputeWarps);
@@ -535,27 +551,27 @@ attn_dkv_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wai
       ++nkv;
       for (int g = 0; ok && g < G; ++g)
         for (int i = 0; i < nt; ++i, ++it) {
-          const int s = it % kS, h = hk * G + g, row = x.start + (f + i) * kTile;
-          ok = wait.all(&q_empty[s], ((it / kS) & 1) ^ 1);
+          const int sq = it % kQ, sg = it % kG, h = hk * G + g, row = x.start + (f + i) * kTile;
+          ok = wait.all(&q_empty[sq], ((it / kQ) & 1) ^ 1);
           if (!ok) break;
           if (elect_one())
-            load_tile<DP>(sbase + L::off_q + s * L::tile_bytes, &p.tq, h, row, &q_full[s]);
+            load_tile<DP>(sbase + L::off_q + sq * L::tile_bytes, &p.tq, h, row, &q_full[sq]);
           __syncwarp();
-          ok = wait.all(&g_empty[s], ((it / kS) & 1) ^ 1);
+          ok = wait.all(&g_empty[sg], ((it / kG) & 1) ^ 1);
           half_step = !ok;
           if (!ok) break;
           if (elect_one())
-            load_tile<DP>(sbase + L::off_g + s * L::tile_bytes, &p.tg, h, row, &g_full[s]);
+            load_tile<DP>(sbase + L::off_g + sg * L::tile_bytes, &p.tg, h, row, &g_full[sg]);
           __syncwarp();
         }
     }
     // every load has landed before the CTA may leave
     if (nkv) mbar_wait_bounded(kv_full, (nkv - 1) & 1, wait_limit, status);
-    for (int i = max(it - kS, 0); i < it; ++i) {
-      mbar_wait_bounded(&q_full[i % kS], (i / kS) & 1, wait_limit, status);
-      mbar_wait_bounded(&g_full[i % kS], (i / kS) & 1, wait_limit, status);
-    }
-    if (half_step) mbar_wait_bounded(&q_full[it % kS], (it / kS) & 1, wait_limit, status);
+    for (int i = max(it - kQ, 0); i < it; ++i)
+      mbar_wait_bounded(&q_full[i % kQ], (i / kQ) & 1, wait_limit, status);
+    for (int i = max(it - kG, 0); i < it; ++i)
+      mbar_wait_bounded(&g_full[i % kG], (i / kG) & 1, wait_limit, status);
+    if (half_step) mbar_wait_bounded(&q_full[it % kQ], (it / kQ) & 1, wait_limit, status);
   } else if (warp == 1) {
     // -------------------------------------------------------- MMAs
     const int nk = (a.D + 15) / 16, no = nk * 16;
@@ -567,19 +583,21 @@ attn_dkv_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wai
       const int n = count(x) * G;
       if (n == 0) continue;
       auto scores = [&](int j) {
-        const int u = it + j, s = u % kS;
-        ok = wait.all(&q_full[s], (u / kS) & 1);
+        const int u = it + j, s = u % kQ;
+        ok = wait.all(&q_full[s], (u / kQ) & 1);
         if (!ok) return;
         if (elect_one()) {
           mma_rows(tmem, sbase, sbase + L::off_q + s * L::tile_bytes, nk);
-          mma_commit(s_full);
+          mma_commit(&s_full[u % kR]);
         }
         __syncwarp();
       };
+      auto outer = [&](int j) {  // dO of step j has been loaded
+        const int u = it + j;
+        ok = wait.all(&g_full[u % kG], (u / kG) & 1);
+      };
       auto grads = [&](int j) {
-        const int u = it + j, s = u % kS;
-        ok = wait.all(&g_full[s], (u / kS) & 1);
-        if (!ok) return;
+        const int u = it + j, s = u % kG;
         if (elect_one()) {
           mma_rows(t_dp, sbase + L::off_v, sbase + L::off_g + s * L::tile_bytes, nk);
           mma_commit(dp_full);
@@ -591,26 +609,26 @@ attn_dkv_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wai
       if (!ok) break;
       tc_fence_after();
       scores(0);
+      if (ok) outer(0);
       if (ok) grads(0);
+      if (ok) ok = wait.all(acc_empty, (nkv & 1) ^ 1);
       for (int j = 0; ok && j < n; ++j) {
-        const int u = it + j, s = u % kS;
-        // t_ready after the loads of this step (waited for above), which came
-        // after the stage's last t_ready
-        ok = wait.all(p_ready, u & 1) && wait.all(&t_ready[s], (u / kS) & 1);
-        if (ok && j == 0) ok = wait.all(acc_empty, (nkv & 1) ^ 1);
+        const int u = it + j, sq = u % kQ, sg = u % kG;
+        // p is formed from the row values, so the tails of this step are zeroed
+        ok = wait.all(p_ready, u & 1);
         if (!ok) break;
         tc_fence_after();
-        if (elect_one()) mma_halves(t_dv, tmem, sbase + L::off_g + s * L::tile_bytes, no, j != 0);
+        if (elect_one()) mma_halves(t_dv, tmem, sbase + L::off_g + sg * L::tile_bytes, no, j != 0);
         __syncwarp();
         if (j + 1 < n) scores(j + 1);
-        if (!ok) break;
-        ok = wait.all(ds_ready, u & 1);
+        if (ok && j + 1 < n) outer(j + 1);  // looked at while ds is formed
+        if (ok) ok = wait.all(ds_ready, u & 1);
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
-          mma_commit(&g_empty[s]);
-          mma_halves(t_dk, t_dp, sbase + L::off_q + s * L::tile_bytes, no, j != 0);
-          mma_commit(&q_empty[s]);
+          mma_commit(&g_empty[sg]);
+          mma_halves(t_dk, t_dp, sbase + L::off_q + sq * L::tile_bytes, no, j != 0);
+          mma_commit(&q_empty[sq]);
         }
         __syncwarp();
         if (j + 1 < n) grads(j + 1);
@@ -636,20 +654,20 @@ attn_dkv_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wai
       const int nt = count(x), f = first_tile(x);
       for (int g = 0; ok && g < G; ++g)
         for (int i = 0; i < nt; ++i, ++it) {
-          const int s = it % kS, q0 = (f + i) * kTile;
+          const int sq = it % kQ, sg = it % kG, sr = it % kR, q0 = (f + i) * kTile;
           const int64_t at = (int64_t)(hk * G + g) * a.T + x.start + q0;
           float v[2][4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {  // in flight while the stage is waited for
             const int c = lane + 32 * e;
             const bool in = q0 + c < x.len;
-            v[0][e] = in ? a.lse[at + c] * kLog2E : 0.f;
-            v[1][e] = in ? a.delta[at + c] : 0.f;
+            v[0][e] = in ? a.lse[at + c] * -kLog2E : 0.f;  // as the sums below take them
+            v[1][e] = in ? -a.delta[at + c] : 0.f;
           }
-          ok = wait.all(&row_empty[s], ((it / kS) & 1) ^ 1) &&
-               wait.all(&q_full[s], (it / kS) & 1) && wait.all(&g_full[s], (it / kS) & 1);
+          ok = wait.all(&row_empty[sr], ((it / kR) & 1) ^ 1) &&
+               wait.all(&q_full[sq], (it / kQ) & 1) && wait.all(&g_full[sg], (it / kG) & 1);
           if (!ok) break;
-          float *o = rows + s * 2 * kTile;
+          float *o = rows + sr * 2 * kTile;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             o[lane + 32 * e] = v[0][e];
@@ -657,14 +675,14 @@ attn_dkv_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wai
           }
           const int valid = x.len - q0;
           if (valid < kTile) {
-            zero_rows<DP>(sm + L::off_q + s * L::tile_bytes, valid, lane);
-            zero_rows<DP>(sm + L::off_g + s * L::tile_bytes, valid, lane);
+            zero_rows<DP>(sm + L::off_q + sq * L::tile_bytes, valid, lane);
+            zero_rows<DP>(sm + L::off_g + sg * L::tile_bytes, valid, lane);
           }
           __syncwarp();
           if (lane == 0) {
-            mbar_arrive(&t_ready[s]);
-            mbar_arrive(&q_empty[s]);
-            mbar_arrive(&g_empty[s]);
+            mbar_arrive(&s_full[sr]);
+            mbar_arrive(&q_empty[sq]);
+            mbar_arrive(&g_empty[sg]);
           }
           __syncwarp();
         }
@@ -685,11 +703,11 @@ attn_dkv_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wai
       if (nt == 0) continue;
       const int row = x.row0 + in_tile;  // key row within the sequence
       for (int j = 0; j < nt * G; ++j, ++it) {
-        const int s = it % kS, q0 = (f + j % nt) * kTile + 64 * half;
-        ok = wait.all(s_full, it & 1) && wait.all(&t_ready[s], (it / kS) & 1);
+        const int sr = it % kR, q0 = (f + j % nt) * kTile + 64 * half;
+        ok = wait.all(&s_full[sr], (it / kR) & 1);
         if (!ok) break;
         tc_fence_after();
-        const float4 *lse = reinterpret_cast<const float4 *>(rows + s * 2 * kTile + 64 * half);
+        const float4 *lse = reinterpret_cast<const float4 *>(rows + sr * 2 * kTile + 64 * half);
         const float4 *delta = lse + kTile / 4;
         // columns lo .. hi - 1 of this half are queries that see this key
         const int lo = a.causal ? row - q0 : 0, hi = x.len - q0;
@@ -704,8 +722,8 @@ attn_dkv_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wai
             const float4 l = lse[c];
             float2 x0 = make_float2(__uint_as_float(v[4 * c]), __uint_as_float(v[4 * c + 1]));
             float2 x1 = make_float2(__uint_as_float(v[4 * c + 2]), __uint_as_float(v[4 * c + 3]));
-            x0 = __ffma2_rn(x0, sc, make_float2(-l.x, -l.y));
-            x1 = __ffma2_rn(x1, sc, make_float2(-l.z, -l.w));
+            x0 = __ffma2_rn(x0, sc, make_float2(l.x, l.y));
+            x1 = __ffma2_rn(x1, sc, make_float2(l.z, l.w));
             pr[2 * c] = make_float2(ex2(x0.x), ex2(x0.y));
             pr[2 * c + 1] = make_float2(ex2(x1.x), ex2(x1.y));
           }
@@ -737,8 +755,8 @@ attn_dkv_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wai
             const float4 d = delta[c];
             float2 x0 = make_float2(__uint_as_float(v[4 * c]), __uint_as_float(v[4 * c + 1]));
             float2 x1 = make_float2(__uint_as_float(v[4 * c + 2]), __uint_as_float(v[4 * c + 3]));
-            pr[2 * c] = __fmul2_rn(pr[2 * c], __fadd2_rn(x0, make_float2(-d.x, -d.y)));
-            pr[2 * c + 1] = __fmul2_rn(pr[2 * c + 1], __fadd2_rn(x1, make_float2(-d.z, -d.w)));
+            pr[2 * c] = __fmul2_rn(pr[2 * c], __fadd2_rn(x0, make_float2(d.x, d.y)));
+            pr[2 * c + 1] = __fmul2_rn(pr[2 * c + 1], __fadd2_rn(x1, make_float2(d.z, d.w)));
           }
           if (masked) {  // selected again: 0 times what lies behind may be NaN
 #pragma unroll
@@ -757,7 +775,7 @@ attn_dkv_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wai
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(ds_ready);
-          mbar_arrive(&row_empty[s]);
+          mbar_arrive(&row_empty[sr]);
         }
       }
       if (!ok) break;
