@@ -12,10 +12,10 @@
 // instead of five: s and do v^T are made twice); in return the gradients are
 // bitwise reproducible and nothing but them is written.
 //
-// Both kernels are persistent, 12 warps (one idle): warp 0 issues the tile
+// Both kernels have 12 warps: warp 0 issues the tile
 // loads, warp 1 the MMAs, warps 2-9 turn scores into probabilities and score
 // gradients (thread = tile row, two groups of four warps take a half of the
-// columns each), warp 10 prepares tails.  p and ds go back to tensor memory
+// columns each), warp 10 prepares tails, warp 11 fetches work items.  p and ds go back to tensor memory
 // in bf16, over the fp32 values they came from (each half within its own 64
 // columns, so the halves need no barrier between them), and enter the next
 // product from there.  The MMAs are queued so that the tensor pipe always has
@@ -40,10 +40,6 @@ struct BwdParams {
   AttnArgs a;
   int slots;
 };
-
-__device__ __forceinline__ SeqTile uniform_tile(const SeqTile &x) {
-  return SeqTile{uniform(x.start), uniform(x.len), uniform(x.row0)};
-}
 
 // acc [128 x n] (+)= P B with P's bf16 halves in columns 0..31 and 64..95 of p.
 __device__ __forceinline__ void mma_halves(uint32_t acc, uint32_t p, uint32_t b, int n,
@@ -123,7 +119,8 @@ template <int DP> struct DqLayout {
   static constexpr uint32_t off_g = tile_bytes, off_k = 2 * tile_bytes;
   static constexpr uint32_t off_v = off_k + kK * tile_bytes;
   static constexpr uint32_t off_bar = off_v + kV * tile_bytes;
-  static constexpr uint32_t smem = off_bar + (3 * kK + 2 * kV + 11) * 8 + 16 + 1024;
+  static constexpr uint32_t off_items = (off_bar + (3 * kK + 2 * kV + 11) * 8 + 16 + 15) / 16 * 16;
+  static constexpr uint32_t smem = off_items + ItemRing::kBytes + 1024;
   static_assert(smem <= 227 * 1024, "shared memory per CTA");
 };
 
@@ -145,6 +142,7 @@ attn_dq_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wait
   uint64_t *drain = acc_empty + 1;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 2);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  const ItemRing ring(sm + L::off_items);
   const int warp = uniform((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -167,6 +165,7 @@ attn_dq_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wait
     mbar_init(acc_full, 1);
     mbar_init(acc_empty, kComputeWarps);
     mbar_init(drain, 1);
+    ring.init(11);  // loads, MMAs, eight compute warps, tails
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -181,15 +180,18 @@ attn_dq_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wait
   pdl_wait();
   pdl_trigger();
   const int G = a.Hq / a.Hkv;
-  const int items = attn_skipped(a.skip) ? 0 : p.slots * a.Hq;
-  // item of round r: head w % Hq (the heads of a group follow each other and share K and
+  const bool skipped = attn_skipped(a.skip);
+  // index w: head w % Hq (the heads of a group follow each other and share K and
   // V in L2), tiles from the last one back, whose rows see most keys
-  auto item = [&](int r, int &h) {
-    const int w = snake_item(r);
-    if (w >= items) return SeqTile{0, 0, 0};
-    h = uniform(w % a.Hq);
-    return uniform_tile(seq_tile(p.slots - 1 - w / a.Hq, a.cu, a.B, (int)a.T, kTile));
+  auto find = [&](int w, int (&v)[kItemWords]) {
+    const SeqTile x = seq_tile(p.slots - 1 - w / a.Hq, a.cu, a.B, (int)a.T, kTile);
+    v[0] = x.start;
+    v[1] = x.len;
+    v[2] = x.row0;
+    v[3] = w % a.Hq;
+    return x.len > 0;
   };
+  int item_no = 0, words[kItemWords] = {};
   auto tiles = [&](const SeqTile &x) {
     return x.len == 0 ? 0 : a.causal ? x.row0 / kTile + 1 : ceil_div(x.len, kTile);
   };
@@ -198,9 +200,9 @@ attn_dq_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wait
     // -------------------------------------------------------- tile loads
     int it = 0, nq = 0;
     bool ok = true;
-    for (int r = 0; ok && r * (int)gridDim.x < items; ++r) {
-      int h = 0;
-      const SeqTile x = item(r, h);
+    while (ok && next_item<true>(ring, wait, item_no, lane, words)) {
+      const SeqTile x{words[0], words[1], words[2]};
+      [[maybe_unused]] const int h = words[3];
       const int n = tiles(x);
       if (n == 0) continue;
       ok = wait.all(q_empty, (nq & 1) ^ 1);
@@ -245,9 +247,9 @@ attn_dq_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wait
     const int nk = (a.D + 15) / 16, no = nk * 16;
     int it = 0, nq = 0;  // key tiles and items so far
     bool ok = true;
-    for (int r = 0; ok && r * (int)gridDim.x < items; ++r) {
-      int h = 0;
-      const SeqTile x = item(r, h);
+    while (ok && next_item<false>(ring, wait, item_no, lane, words)) {
+      const SeqTile x{words[0], words[1], words[2]};
+      [[maybe_unused]] const int h = words[3];
       const int n = tiles(x);
       if (n == 0) continue;
       auto keys = [&](int i) {  // K of key tile i of this item has been loaded
@@ -319,9 +321,9 @@ attn_dq_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wait
     // -------------------------------------------------------- K tiles' tails
     int it = 0;
     bool ok = true;
-    for (int r = 0; ok && r * (int)gridDim.x < items; ++r) {
-      int h = 0;
-      const SeqTile x = item(r, h);
+    while (ok && next_item<false>(ring, wait, item_no, lane, words)) {
+      const SeqTile x{words[0], words[1], words[2]};
+      [[maybe_unused]] const int h = words[3];
       const int n = tiles(x);
       for (int i = 0; i < n; ++i, ++it) {
         const int s = it % kK;
@@ -344,9 +346,9 @@ attn_dq_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wait
     const float s2 = a.scale * kLog2E;
     int it = 0, nq = 0;
     bool ok = true;
-    for (int r = 0; ok && r * (int)gridDim.x < items; ++r) {
-      int h = 0;
-      const SeqTile x = item(r, h);
+    while (ok && next_item<false>(ring, wait, item_no, lane, words)) {
+      const SeqTile x{words[0], words[1], words[2]};
+      [[maybe_unused]] const int h = words[3];
       const int n = tiles(x);
       if (n == 0) continue;
       const int row = x.row0 + in_tile;
@@ -430,6 +432,13 @@ attn_dq_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wait
                    v, a.scale, min(kCols, a.D - half * kCols));
       __syncwarp();
     }
+  } else {
+    // -------------------------------------------------------- items
+    ItemSource<decltype(find)> source(ring, wait, find, skipped ? -1 : (int)blockIdx.x, lane);
+    bool ok = true;
+    do {
+      ok = source.publish(words);
+    } while (ok && words[0] >= 0);
   }
   tc_fence_before();
   __syncthreads();
@@ -455,7 +464,9 @@ template <int DP> struct DkvLayout {
   static constexpr uint32_t off_g = off_q + kQ * tile_bytes;
   static constexpr uint32_t off_row = off_g + kG * tile_bytes;  // [kR][-lse 128, -delta 128] floats
   static constexpr uint32_t off_bar = off_row + kR * 2 * kTile * 4;
-  static constexpr uint32_t smem = off_bar + (2 * kQ + 2 * kG + 2 * kR + 8) * 8 + 16;
+  static constexpr uint32_t off_items =
+      (off_bar + (2 * kQ + 2 * kG + 2 * kR + 8) * 8 + 16 + 15) / 16 * 16;
+  static constexpr uint32_t smem = off_items + ItemRing::kBytes;
   static_assert(smem <= 227 * 1024, "shared memory per CTA");
 };
 
@@ -477,6 +488,7 @@ attn_dkv_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wai
   uint64_t *acc_full = ds_ready + 1, *acc_empty = acc_full + 1, *drain = acc_empty + 1;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  const ItemRing ring(sm + L::off_items);
   const int warp = uniform((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -500,6 +512,7 @@ attn_dkv_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wai
     mbar_init(acc_full, 1);
     mbar_init(acc_empty, kComputeWarps);
     mbar_init(drain, 1);
+    ring.init(11);  // loads, MMAs, eight compute warps, tails
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -514,14 +527,17 @@ attn_dkv_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wai
   pdl_wait();
   pdl_trigger();
   const int G = a.Hq / a.Hkv;
-  const int items = attn_skipped(a.skip) ? 0 : p.slots * a.Hkv;
-  // item of round r: key head w % Hkv; tiles from the first one on, which most rows see
-  auto item = [&](int r, int &hk) {
-    const int w = snake_item(r);
-    if (w >= items) return SeqTile{0, 0, 0};
-    hk = uniform(w % a.Hkv);
-    return uniform_tile(seq_tile(w / a.Hkv, a.cu, a.B, (int)a.T, kTile));
+  const bool skipped = attn_skipped(a.skip);
+  // index w: key head w % Hkv; tiles from the first one on, which most rows see
+  auto find = [&](int w, int (&v)[kItemWords]) {
+    const SeqTile x = seq_tile(w / a.Hkv, a.cu, a.B, (int)a.T, kTile);
+    v[0] = x.start;
+    v[1] = x.len;
+    v[2] = x.row0;
+    v[3] = w % a.Hkv;
+    return x.len > 0;
   };
+  int item_no = 0, words[kItemWords] = {};
   // query tiles first .. first + count - 1 of every head; step j of the item is
   // query tile first + j % count of head hk G + j / count
   auto first_tile = [&](const SeqTile &x) { return a.causal ? x.row0 / kTile : 0; };
@@ -533,9 +549,9 @@ attn_dkv_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wai
     // -------------------------------------------------------- tile loads
     int it = 0, nkv = 0;
     bool ok = true, half_step = false;
-    for (int r = 0; ok && r * (int)gridDim.x < items; ++r) {
-      int hk = 0;
-      const SeqTile x = item(r, hk);
+    while (ok && next_item<true>(ring, wait, item_no, lane, words)) {
+      const SeqTile x{words[0], words[1], words[2]};
+      [[maybe_unused]] const int hk = words[3];
       const int nt = count(x), f = first_tile(x);
       if (nt == 0) continue;
       ok = wait.all(kv_empty, (nkv & 1) ^ 1);
@@ -577,9 +593,9 @@ attn_dkv_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wai
     const int nk = (a.D + 15) / 16, no = nk * 16;
     int it = 0, nkv = 0;
     bool ok = true;
-    for (int r = 0; ok && r * (int)gridDim.x < items; ++r) {
-      int hk = 0;
-      const SeqTile x = item(r, hk);
+    while (ok && next_item<false>(ring, wait, item_no, lane, words)) {
+      const SeqTile x{words[0], words[1], words[2]};
+      [[maybe_unused]] const int hk = words[3];
       const int n = count(x) * G;
       if (n == 0) continue;
       auto scores = [&](int j) {
@@ -648,9 +664,9 @@ attn_dkv_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wai
     // ---------------------------- lse, delta, and the tails of the Q, dO tiles
     int it = 0;
     bool ok = true;
-    for (int r = 0; ok && r * (int)gridDim.x < items; ++r) {
-      int hk = 0;
-      const SeqTile x = item(r, hk);
+    while (ok && next_item<false>(ring, wait, item_no, lane, words)) {
+      const SeqTile x{words[0], words[1], words[2]};
+      [[maybe_unused]] const int hk = words[3];
       const int nt = count(x), f = first_tile(x);
       for (int g = 0; ok && g < G; ++g)
         for (int i = 0; i < nt; ++i, ++it) {
@@ -696,9 +712,9 @@ attn_dkv_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wai
     const float s2 = a.scale * kLog2E;
     int it = 0, nkv = 0;
     bool ok = true;
-    for (int r = 0; ok && r * (int)gridDim.x < items; ++r) {
-      int hk = 0;
-      const SeqTile x = item(r, hk);
+    while (ok && next_item<false>(ring, wait, item_no, lane, words)) {
+      const SeqTile x{words[0], words[1], words[2]};
+      [[maybe_unused]] const int hk = words[3];
       const int nt = count(x), f = first_tile(x);
       if (nt == 0) continue;
       const int row = x.row0 + in_tile;  // key row within the sequence
@@ -802,6 +818,13 @@ attn_dkv_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wai
       }
       __syncwarp();
     }
+  } else {
+    // -------------------------------------------------------- items
+    ItemSource<decltype(find)> source(ring, wait, find, skipped ? -1 : (int)blockIdx.x, lane);
+    bool ok = true;
+    do {
+      ok = source.publish(words);
+    } while (ok && words[0] >= 0);
   }
   tc_fence_before();
   __syncthreads();
@@ -829,12 +852,12 @@ cudaError_t launch(const AttnArgs &a, const DeviceInfo &dev, cudaStream_t s) {
   constexpr size_t sq = DqLayout<DP>::smem, sk = DkvLayout<DP>::smem;
   blocks_per_sm((const void *)attn_dq_tc<DP>, kBwdThreads, sq, dev, 1);  // lifts the limits
   blocks_per_sm((const void *)attn_dkv_tc<DP>, kBwdThreads, sk, dev, 1);
-  auto grid = [&](int64_t items) { return dim3((unsigned)(items < dev.sms ? items : dev.sms)); };
-  e = launch_pdl(attn_dq_tc<DP>, grid((int64_t)p.slots * a.Hq), dim3(kBwdThreads), sq, s, p, status,
-                 kWaitLimitCycles);
+  // one CTA per item
+  e = launch_pdl(attn_dq_tc<DP>, dim3((unsigned)p.slots * (unsigned)a.Hq), dim3(kBwdThreads), sq, s,
+                 p, status, kWaitLimitCycles);
   if (e != cudaSuccess) return e;
-  return launch_pdl(attn_dkv_tc<DP>, grid((int64_t)p.slots * a.Hkv), dim3(kBwdThreads), sk, s, p,
-                    status, kWaitLimitCycles);
+  return launch_pdl(attn_dkv_tc<DP>, dim3((unsigned)p.slots * (unsigned)a.Hkv), dim3(kBwdThreads),
+                    sk, s, p, status, kWaitLimitCycles);
 }
 
 }  // namespace

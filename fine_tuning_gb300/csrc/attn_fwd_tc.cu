@@ -94,16 +94,27 @@ struct FwdItem {
   int start, len, hk;
   int h[2], row0[2], n[2];
   __device__ __forceinline__ int tiles() const { return max(n[0], n[1]); }
-  __device__ __forceinline__ void make_uniform() {
-    start = uniform(start);
-    len = uniform(len);
-    hk = uniform(hk);
+  __device__ __forceinline__ FwdItem() {}
+  __device__ __forceinline__ explicit FwdItem(const int (&v)[kItemWords])
+      : start(v[0]), len(v[1]), hk(v[2]) {
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      h[t] = uniform(h[t]);
-      row0[t] = uniform(row0[t]);
-      n[t] = uniform(n[t]);
+      h[t] = v[3 + t];
+      row0[t] = v[5 + t];
+      n[t] = v[7 + t];
     }
+  }
+  __device__ __forceinline__ void to(int (&v)[kItemWords]) const {
+    v[0] = start;
+    v[1] = len;
+    v[2] = hk;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      v[3 + t] = h[t];
+      v[5 + t] = row0[t];
+      v[7 + t] = n[t];
+    }
+    v[9] = v[10] = v[11] = 0;
   }
 };
 
@@ -118,12 +129,8 @@ __device__ __forceinline__ int pair_base(int c, int b, int G) {
   return ((max(c, 0) / kTile + b) * G + 1) / 2 + b;
 }
 
-__device__ __forceinline__ FwdItem fwd_item(const AttnArgs &a, int nslots, int item, int items) {
+__device__ __forceinline__ FwdItem fwd_item(const AttnArgs &a, int nslots, int item) {
   FwdItem w;
-  if (item >= items) {
-    w = FwdItem{};
-    return w;
-  }
   const int G = a.Hq / a.Hkv;
   w.hk = item % a.Hkv;
   // from the last slot back: in one long causal sequence the longest rows first
@@ -160,7 +167,8 @@ template <int DP> struct FwdLayout {
   static constexpr int kStages = DP == 128 ? 5 : 8;
   static constexpr uint32_t off_ring = 2 * tile_bytes;
   static constexpr uint32_t off_bar = off_ring + kStages * tile_bytes;
-  static constexpr uint32_t smem = off_bar + (3 * kStages + 20) * 8 + 16 + 1024;
+  static constexpr uint32_t off_items = (off_bar + (3 * kStages + 20) * 8 + 16 + 15) / 16 * 16;
+  static constexpr uint32_t smem = off_items + ItemRing::kBytes + 1024;
   static_assert(smem <= 227 * 1024, "shared memory per CTA");
 };
 
@@ -188,6 +196,7 @@ attn_fwd_tc(const __grid_constant__ FwdParams p, unsigned *status, long long wai
   uint64_t *drain = s_read + 2;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 2);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  const ItemRing ring(sm + L::off_items);
   const int warp = uniform((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -208,6 +217,7 @@ attn_fwd_tc(const __grid_constant__ FwdParams p, unsigned *status, long long wai
       mbar_init(&s_read[t], 4);
       mbar_init(&drain[t], 1);
     }
+    ring.init(11);  // loads, MMAs of both tiles, eight softmax warps
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -220,7 +230,8 @@ attn_fwd_tc(const __grid_constant__ FwdParams p, unsigned *status, long long wai
   const AttnArgs &a = p.a;
   pdl_wait();
   pdl_trigger();
-  const int items = attn_skipped(a.skip) ? 0 : p.nslots * a.Hkv;
+  const bool skipped = attn_skipped(a.skip);
+  int item_no = 0, words[kItemWords];
 
   if (warp == 0) {
     // -------------------------------------------------------- tile loads
@@ -235,9 +246,8 @@ attn_fwd_tc(const __grid_constant__ FwdParams p, unsigned *status, long long wai
       __syncwarp();
       ++it;
     };
-    for (int r = 0; ok && r * (int)gridDim.x < items; ++r) {
-      FwdItem x = fwd_item(a, p.nslots, snake_item(r), items);
-      x.make_uniform();
+    while (ok && next_item<true>(ring, wait, item_no, lane, words)) {
+      const FwdItem x(words);
       const int n = x.tiles();
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
@@ -269,9 +279,8 @@ attn_fwd_tc(const __grid_constant__ FwdParams p, unsigned *status, long long wai
     int it = 0, nq = 0, ns = 0;  // ring entries, items, score tiles so far
     int np0 = 0, np1 = 0;        // first and second halves so far
     bool ok = true;
-    for (int r = 0; ok && r * (int)gridDim.x < items; ++r) {
-      FwdItem x = fwd_item(a, p.nslots, snake_item(r), items);
-      x.make_uniform();
+    while (ok && next_item<false>(ring, wait, item_no, lane, words)) {
+      const FwdItem x(words);
       const int n = x.tiles(), mine = t ? x.n[1] : x.n[0];
       if (n == 0) continue;
       auto keys = [&](int e) {  // ring entry e has been loaded
@@ -361,14 +370,19 @@ attn_fwd_tc(const __grid_constant__ FwdParams p, unsigned *status, long long wai
       mbar_wait_bounded(&drain[t], 0, wait_limit, status);
     }
   } else if (warp == 10) {
-    // -------------------------------------------------------- V tiles' tails
+    // -------------------------------------------------------- items, V tiles' tails
+    auto find = [&](int index, int (&v)[kItemWords]) {
+      const FwdItem x = fwd_item(a, p.nslots, index);
+      x.to(v);
+      return x.tiles() > 0;
+    };
+    ItemSource<decltype(find)> source(ring, wait, find, skipped ? -1 : (int)blockIdx.x, lane);
     int it = 0;
-    bool ok = true;
-    for (int r = 0; ok && r * (int)gridDim.x < items; ++r) {
-      FwdItem x = fwd_item(a, p.nslots, snake_item(r), items);
-      x.make_uniform();
+    bool ok = source.publish(words);
+    while (ok && words[0] >= 0) {
+      const FwdItem x(words);
       const int n = x.tiles();
-      for (int i = 0; i < 2 * n; ++i, ++it) {  // K0 V0 K1 V1 ..., as loaded
+      for (int i = 0; ok && i < 2 * n; ++i, ++it) {  // K0 V0 K1 V1 ..., as loaded
         const int s = it % kStages;
         ok = wait.all(&kv_full[s], (it / kStages) & 1);
         if (!ok) break;
@@ -376,11 +390,12 @@ attn_fwd_tc(const __grid_constant__ FwdParams p, unsigned *status, long long wai
         if ((i & 1) && valid < kTile)
           zero_rows<DP>(sm + L::off_ring + s * L::tile_bytes, valid, lane);
         if (lane == 0) {
-          mbar_arrive(&v_ready[s]);  // before kv_empty: see the MMA warp's wait
+          mbar_arrive(&v_ready[s]);  // before kv_empty: see the MMA warps' wait
           mbar_arrive(&kv_empty[s]);
         }
         __syncwarp();
       }
+      if (ok) ok = source.publish(words);
     }
   } else if (warp < 10) {
     // -------------------------------------------------------- softmax
@@ -392,9 +407,8 @@ attn_fwd_tc(const __grid_constant__ FwdParams p, unsigned *status, long long wai
     const float2 sc = make_float2(s2, s2);
     int ns = 0, np0 = 0, np1 = 0;  // score tiles, first and second halves so far
     bool ok = true;
-    for (int r = 0; ok && r * (int)gridDim.x < items; ++r) {
-      FwdItem x = fwd_item(a, p.nslots, snake_item(r), items);
-      x.make_uniform();
+    while (ok && next_item<false>(ring, wait, item_no, lane, words)) {
+      const FwdItem x(words);
       // selected, not indexed: an index would put the item into local memory,
       // and beside this much shared memory L1 holds next to nothing of it
       const int n = t ? x.n[1] : x.n[0], row0 = t ? x.row0[1] : x.row0[0];
@@ -600,8 +614,7 @@ cudaError_t launch(const AttnArgs &a, const DeviceInfo &dev, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   constexpr size_t smem = FwdLayout<DP>::smem;
   blocks_per_sm((const void *)attn_fwd_tc<DP>, kFwdThreads, smem, dev, 1);  // lifts the limit
-  const int64_t items = (int64_t)p.nslots * a.Hkv;
-  const unsigned grid = (unsigned)(items < dev.sms ? items : dev.sms);
+  const unsigned grid = (unsigned)p.nslots * (unsigned)a.Hkv;  // one CTA per item
   return launch_pdl(attn_fwd_tc<DP>, dim3(grid), dim3(kFwdThreads), smem, s, p, status,
                     kWaitLimitCycles);
 }

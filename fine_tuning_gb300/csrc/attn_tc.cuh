@@ -142,14 +142,6 @@ __device__ __forceinline__ void mma_half(uint32_t acc, uint32_t p, uint32_t b, i
     mma_ts(acc, p + (uint32_t)kk * 8u, desc_mn(b, 4 * half + kk), id, accumulate || kk != 0);
 }
 
-// This CTA's item of round r: rounds run through the grid back
-// and forth, so that items sorted by cost even out.  May be >= the number of
-// items in the last round; the loop goes on while r * grid < items.
-__device__ __forceinline__ int snake_item(int r) {
-  const int g = (int)gridDim.x, b = (int)blockIdx.x;
-  return r * g + ((r & 1) ? g - 1 - b : b);
-}
-
 // The larger of three (one instruction).
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
@@ -293,6 +285,138 @@ struct Waits {
     return __all_sync(0xffffffffu, (*this)(bar, parity));
   }
 };
+
+// ------------------------------------------------------------- work items
+//
+// The grid has one CTA per item (a tile, or pair of tiles, and a head), but as
+// many run as fit, and each goes on to the items of CTAs that have not started
+// yet (cluster launch control: a running CTA cancels the launch of a waiting
+// one and takes its index over).  So items of very different lengths even out
+// without a counter in memory that calls on two streams would share.
+//
+// One warp of the CTA asks for the next item when the loading warp has no
+// more to load for the current one (an item asked for earlier would be tied to
+// this CTA while others run dry: with a few long items per SM that cost 19%),
+// finds its sequence and tile once for all roles, and hands it over in a ring
+// of two slots; empty items are dropped there.
+constexpr int kItemWords = 12;
+
+struct ItemRing {
+  uint64_t *want;   // the loading warp is done with the last item
+  uint64_t *asked;  // the answer has arrived (16 bytes)
+  uint64_t *full;   // [2]
+  uint64_t *empty;  // [2]
+  int *slots;       // [2][kItemWords]
+  uint4 *answer;
+  static constexpr uint32_t kBytes = 16 + 2 * kItemWords * 4 + 6 * 8;  // from a multiple of 16
+
+  __device__ __forceinline__ explicit ItemRing(unsigned char *at) {
+    answer = reinterpret_cast<uint4 *>(at);
+    slots = reinterpret_cast<int *>(at + 16);
+    asked = reinterpret_cast<uint64_t *>(at + 16 + 2 * kItemWords * 4);
+    full = asked + 1;
+    empty = full + 2;
+    want = empty + 2;
+  }
+  __device__ __forceinline__ void init(int readers) const {  // one thread
+    mbar_init(asked, 1);
+    mbar_init(want, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], readers);
+    }
+  }
+  // asks for another CTA's index (one lane; not again after an empty answer)
+  __device__ __forceinline__ void ask() const {
+    mbar_arrive_expect_tx(asked, 16);
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128"
+        " [%0], [%1];" ::"r"(smem_addr(answer)),
+        "r"(smem_addr(asked))
+        : "memory");
+  }
+  // the index, or -1 (every lane, after `asked`)
+  __device__ __forceinline__ int answered() const {
+    uint32_t got, x = 0;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t"
+        "ld.shared.b128 r, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+        "selp.u32 %1, 1, 0, p;\n\t"
+        "mov.u32 %0, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, r;\n\t}"
+        : "=r"(x), "=r"(got)
+        : "r"(smem_addr(answer))
+        : "memory");
+    fence_proxy_async_smem();  // read before the next answer is written
+    return got ? (int)x : -1;
+  }
+};
+
+// The asking warp's side.  find(index, words) fills in an item and says whether
+// it holds work; words[0] < 0 marks the end.
+template <class Find> struct ItemSource {
+  const ItemRing &ring;
+  const Waits &wait;
+  Find find;
+  int lane;
+  int index, count = 0, asks = 0;  // index: the CTA's own, -1 after the end
+  __device__ __forceinline__ ItemSource(const ItemRing &r, const Waits &w, Find f, int first,
+                                        int l)
+      : ring(r), wait(w), find(f), lane(l), index(first) {}
+  // Publishes the next item (or the end) into its slot; false when a wait gave
+  // up.  words: the item, in every lane.
+  __device__ __forceinline__ bool publish(int (&words)[kItemWords]) {
+    bool work = false;
+    if (count == 0) {
+      work = index >= 0 && find(index, words);
+    } else if (!wait.all(ring.want, (count - 1) & 1)) {
+      return false;
+    }
+    while (index >= 0 && !work) {
+      if (elect_one()) ring.ask();
+      __syncwarp();
+      if (!wait.all(ring.asked, asks & 1)) {  // the answer still comes: not after the CTA left
+        mbar_wait_bounded(ring.asked, asks & 1, wait.limit, wait.status);
+        return false;
+      }
+      ++asks;
+      index = uniform(ring.answered());
+      __syncwarp();
+      if (index >= 0) work = find(index, words);
+    }
+    if (!work) words[0] = -1;
+    const int s = count & 1;
+    if (!wait.all(&ring.empty[s], ((count >> 1) & 1) ^ 1)) return false;
+    if (lane == 0) {
+#pragma unroll
+      for (int i = 0; i < kItemWords; ++i) ring.slots[s * kItemWords + i] = words[i];
+      mbar_arrive(&ring.full[s]);
+    }
+    __syncwarp();
+    ++count;
+    return true;
+  }
+};
+
+// The reading side (a whole warp): item number `count`; false at the end or when
+// a wait gave up.  LOADS: this is the loading warp, whose request starts the
+// search for every item but the first.
+template <bool LOADS>
+__device__ __forceinline__ bool next_item(const ItemRing &ring, const Waits &wait, int &count,
+                                          int lane, int (&words)[kItemWords]) {
+  const int s = count & 1;
+  if (LOADS && count > 0 && lane == 0) mbar_arrive(ring.want);
+  if (!wait.all(&ring.full[s], (count >> 1) & 1)) return false;
+#pragma unroll
+  for (int i = 0; i < kItemWords; ++i) {
+    words[i] = uniform(ring.slots[s * kItemWords + i]);
+  }
+  __syncwarp();
+  if (lane == 0) mbar_arrive(&ring.empty[s]);
+  ++count;
+  return words[0] >= 0;
+}
 
 // Zeroes rows [from, 128) of a staged tile (whole warp): rows behind a
 // sequence's end hold another sequence's values, whose infinities would turn a
