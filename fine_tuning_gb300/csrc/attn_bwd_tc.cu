@@ -12,10 +12,10 @@
 // instead of five: s and do v^T are made twice); in return the gradients are
 // bitwise reproducible and nothing but them is written.
 //
-// Both kernels have 12 warps: warp 0 issues the tile
+// Both kernels have 12 warps (one idle): warp 0 issues the tile
 // loads, warp 1 the MMAs, warps 2-9 turn scores into probabilities and score
 // gradients (thread = tile row, two groups of four warps take a half of the
-// columns each), warp 10 prepares tails, warp 11 fetches work items.  p and ds go back to tensor memory
+// columns each), warp 10 prepares tails.  p and ds go back to tensor memory
 // in bf16, over the fp32 values they came from (each half within its own 64
 // columns, so the halves need no barrier between them), and enter the next
 // product from there.  The MMAs are queued so that the tensor pipe always has
@@ -39,7 +39,30 @@ struct BwdParams {
   CUtensorMap tq, tk, tv, tg;  // tg: do
   AttnArgs a;
   int slots;
+  int splits;  // CTAs that share a key tile's query heads (dk, dv)
+  float *part;  // splits > 1: [splits][dk, dv][T][Hkv][D] sums, unscaled
 };
+
+// How many CTAs share the query heads of a key tile.  dk and dv of a key head
+// are summed over its group's heads, so a call has T / 128 x Hkv of these sums,
+// and one of a long sequence's first tiles passes over all its queries, G
+// times.  Where that leaves fewer than two sums per SM (152), the heads are
+// dealt out to more CTAs, whose fp32 sums (8 bytes per element and share in the
+// workspace) a small kernel adds in order.  16,384 packed tokens x 14/2 x 64:
+// 256 sums, the longest of them 112 steps; three shares.
+int attn_bwd_splits(int64_t T, int32_t Hq, int32_t Hkv) {
+  const int64_t G = Hq / Hkv, sums = ceil_div(T, (int64_t)kTile) * Hkv, want = 2 * 152;
+  if (sums >= want) return 1;
+  const int64_t n = ceil_div(want, sums);
+  return (int)(n < G ? n : G);
+}
+
+size_t delta_bytes(int64_t T, int32_t Hq) {
+  return ((size_t)T * Hq * sizeof(float) + 15) / 16 * 16;
+}
+float *attn_bwd_part(const AttnArgs &a) {
+  return reinterpret_cast<float *>(reinterpret_cast<char *>(a.delta) + delta_bytes(a.T, a.Hq));
+}
 
 // acc [128 x n] (+)= P B with P's bf16 halves in columns 0..31 and 64..95 of p.
 __device__ __forceinline__ void mma_halves(uint32_t acc, uint32_t p, uint32_t b, int n,
@@ -64,6 +87,20 @@ __device__ __forceinline__ void store_half(bf16 *o, const uint32_t (&v)[64], flo
                      pack_bf16(x[6], x[7]));
     }
   }
+}
+
+// Tile of unit u of the whole batch (a SeqTile with len 0: none).  By length
+// where that order was made, else in the order of the slots; back: from a sequence's
+// last tile on instead of its first.
+__device__ __forceinline__ SeqTile tile_of(const AttnArgs &a, int slots, int u, bool back,
+                                           const SeqOrder &seqs, bool by_length) {
+  if (!by_length) return seq_tile(back ? slots - 1 - u : u, a.cu, a.B, (int)a.T, kTile);
+  if (u >= seqs.total) return SeqTile{0, 0, 0};
+  const int r = seqs.rank_of(u, a.B), b = seqs.order[r], i = u - seqs.base[r];
+  const int c0 = min(max(__ldg(a.cu + b), 0), (int)a.T);
+  const int len = min(max(__ldg(a.cu + b + 1), c0), (int)a.T) - c0;
+  const int tile = back ? ceil_div(len, kTile) - 1 - i : i;
+  return SeqTile{c0, tile >= 0 && tile * kTile < len ? len : 0, tile * kTile};
 }
 
 // ------------------------------------------------------------------- delta
@@ -120,7 +157,8 @@ template <int DP> struct DqLayout {
   static constexpr uint32_t off_v = off_k + kK * tile_bytes;
   static constexpr uint32_t off_bar = off_v + kV * tile_bytes;
   static constexpr uint32_t off_items = (off_bar + (3 * kK + 2 * kV + 11) * 8 + 16 + 15) / 16 * 16;
-  static constexpr uint32_t smem = off_items + ItemRing::kBytes + 1024;
+  static constexpr uint32_t off_order = off_items + ItemRing::kBytes;
+  static constexpr uint32_t smem = off_order + SeqOrder::kBytes;
   static_assert(smem <= 227 * 1024, "shared memory per CTA");
 };
 
@@ -129,8 +167,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 attn_dq_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wait_limit) {
   using L = DqLayout<DP>;
   constexpr int kK = L::kK, kV = L::kV;
-  extern __shared__ unsigned char smem_raw[];
-  unsigned char *sm = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
+  extern __shared__ __align__(1024) unsigned char smem_aligned[];
+  unsigned char *sm = smem_aligned;
   const uint32_t sbase = smem_addr(sm);
   uint64_t *k_full = reinterpret_cast<uint64_t *>(sm + L::off_bar);
   uint64_t *k_empty = k_full + kK, *k_ready = k_empty + kK;
@@ -165,7 +203,7 @@ attn_dq_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wait
     mbar_init(acc_full, 1);
     mbar_init(acc_empty, kComputeWarps);
     mbar_init(drain, 1);
-    ring.init(11);  // loads, MMAs, eight compute warps, tails
+    ring.init(10);  // MMAs, eight compute warps, tails
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -181,10 +219,14 @@ attn_dq_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wait
   pdl_trigger();
   const int G = a.Hq / a.Hkv;
   const bool skipped = attn_skipped(a.skip);
+  SeqOrder seqs(sm + L::off_order);
+  const bool by_length = a.B <= kSortMax;
+  if (by_length && !skipped)
+    seqs.make(a, reinterpret_cast<int *>(sm), [](int len) { return ceil_div(len, kTile); });
   // index w: head w % Hq (the heads of a group follow each other and share K and
   // V in L2), tiles from the last one back, whose rows see most keys
   auto find = [&](int w, int (&v)[kItemWords]) {
-    const SeqTile x = seq_tile(p.slots - 1 - w / a.Hq, a.cu, a.B, (int)a.T, kTile);
+    const SeqTile x = tile_of(a, p.slots, w / a.Hq, true, seqs, by_length);
     v[0] = x.start;
     v[1] = x.len;
     v[2] = x.row0;
@@ -200,11 +242,12 @@ attn_dq_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wait
     // -------------------------------------------------------- tile loads
     int it = 0, nq = 0;
     bool ok = true;
-    while (ok && next_item<true>(ring, wait, item_no, lane, words)) {
+    ItemSource<decltype(find)> source(ring, wait, find, skipped ? -1 : (int)blockIdx.x, lane);
+    while (ok && (ok = source.next(words)) && words[0] >= 0) {
       const SeqTile x{words[0], words[1], words[2]};
       [[maybe_unused]] const int h = words[3];
       const int n = tiles(x);
-      if (n == 0) continue;
+      if (n <= kShortItem) source.ask();
       ok = wait.all(q_empty, (nq & 1) ^ 1);
       if (!ok) break;
       if (elect_one()) {
@@ -232,6 +275,7 @@ attn_dq_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wait
         __syncwarp();
       }
     }
+    source.close();
     // every load has landed before the CTA may leave (after a wait that gave
     // up, a stage that was never filled may be waited for: bounded as well)
     if (nq) mbar_wait_bounded(q_full, (nq - 1) & 1, wait_limit, status);
@@ -247,7 +291,7 @@ attn_dq_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wait
     const int nk = (a.D + 15) / 16, no = nk * 16;
     int it = 0, nq = 0;  // key tiles and items so far
     bool ok = true;
-    while (ok && next_item<false>(ring, wait, item_no, lane, words)) {
+    while (ok && next_item(ring, wait, item_no, lane, words)) {
       const SeqTile x{words[0], words[1], words[2]};
       [[maybe_unused]] const int h = words[3];
       const int n = tiles(x);
@@ -321,7 +365,7 @@ attn_dq_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wait
     // -------------------------------------------------------- K tiles' tails
     int it = 0;
     bool ok = true;
-    while (ok && next_item<false>(ring, wait, item_no, lane, words)) {
+    while (ok && next_item(ring, wait, item_no, lane, words)) {
       const SeqTile x{words[0], words[1], words[2]};
       [[maybe_unused]] const int h = words[3];
       const int n = tiles(x);
@@ -346,7 +390,7 @@ attn_dq_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wait
     const float s2 = a.scale * kLog2E;
     int it = 0, nq = 0;
     bool ok = true;
-    while (ok && next_item<false>(ring, wait, item_no, lane, words)) {
+    while (ok && next_item(ring, wait, item_no, lane, words)) {
       const SeqTile x{words[0], words[1], words[2]};
       [[maybe_unused]] const int h = words[3];
       const int n = tiles(x);
@@ -432,13 +476,6 @@ attn_dq_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wait
                    v, a.scale, min(kCols, a.D - half * kCols));
       __syncwarp();
     }
-  } else {
-    // -------------------------------------------------------- items
-    ItemSource<decltype(find)> source(ring, wait, find, skipped ? -1 : (int)blockIdx.x, lane);
-    bool ok = true;
-    do {
-      ok = source.publish(words);
-    } while (ok && words[0] >= 0);
   }
   tc_fence_before();
   __syncthreads();
@@ -466,7 +503,8 @@ template <int DP> struct DkvLayout {
   static constexpr uint32_t off_bar = off_row + kR * 2 * kTile * 4;
   static constexpr uint32_t off_items =
       (off_bar + (2 * kQ + 2 * kG + 2 * kR + 8) * 8 + 16 + 15) / 16 * 16;
-  static constexpr uint32_t smem = off_items + ItemRing::kBytes;
+  static constexpr uint32_t off_order = off_items + ItemRing::kBytes;
+  static constexpr uint32_t smem = off_order + SeqOrder::kBytes;
   static_assert(smem <= 227 * 1024, "shared memory per CTA");
 };
 
@@ -512,7 +550,7 @@ attn_dkv_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wai
     mbar_init(acc_full, 1);
     mbar_init(acc_empty, kComputeWarps);
     mbar_init(drain, 1);
-    ring.init(11);  // loads, MMAs, eight compute warps, tails
+    ring.init(10);  // MMAs, eight compute warps, tails
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -528,18 +566,29 @@ attn_dkv_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wai
   pdl_trigger();
   const int G = a.Hq / a.Hkv;
   const bool skipped = attn_skipped(a.skip);
-  // index w: key head w % Hkv; tiles from the first one on, which most rows see
+  SeqOrder seqs(sm + L::off_order);
+  const bool by_length = a.B <= kSortMax;
+  if (by_length && !skipped)
+    seqs.make(a, reinterpret_cast<int *>(sm), [](int len) { return ceil_div(len, kTile); });
+  // index w: share w % splits of the query heads of key head (w / splits) % Hkv;
+  // tiles from the first one on, which most rows see
+  const int shares = p.splits;
   auto find = [&](int w, int (&v)[kItemWords]) {
-    const SeqTile x = seq_tile(w / a.Hkv, a.cu, a.B, (int)a.T, kTile);
+    const SeqTile x =
+        tile_of(a, p.slots, w / (a.Hkv * shares), false, seqs, by_length);
+    const int u = w % (a.Hkv * shares), c = u % shares;
     v[0] = x.start;
     v[1] = x.len;
     v[2] = x.row0;
-    v[3] = w % a.Hkv;
+    v[3] = u / shares;
+    v[4] = c;
+    v[5] = c * G / shares;        // its first head of the group, and how many
+    v[6] = (c + 1) * G / shares - v[5];
     return x.len > 0;
   };
   int item_no = 0, words[kItemWords] = {};
-  // query tiles first .. first + count - 1 of every head; step j of the item is
-  // query tile first + j % count of head hk G + j / count
+  // query tiles first .. first + count - 1 of every head of the share; step j of
+  // the item is query tile first + j % count of the share's head j / count
   auto first_tile = [&](const SeqTile &x) { return a.causal ? x.row0 / kTile : 0; };
   auto count = [&](const SeqTile &x) {
     return x.len == 0 ? 0 : ceil_div(x.len, kTile) - first_tile(x);
@@ -549,11 +598,12 @@ attn_dkv_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wai
     // -------------------------------------------------------- tile loads
     int it = 0, nkv = 0;
     bool ok = true, half_step = false;
-    while (ok && next_item<true>(ring, wait, item_no, lane, words)) {
+    ItemSource<decltype(find)> source(ring, wait, find, skipped ? -1 : (int)blockIdx.x, lane);
+    while (ok && (ok = source.next(words)) && words[0] >= 0) {
       const SeqTile x{words[0], words[1], words[2]};
-      [[maybe_unused]] const int hk = words[3];
+      [[maybe_unused]] const int hk = words[3], g0 = words[5], heads = words[6];
       const int nt = count(x), f = first_tile(x);
-      if (nt == 0) continue;
+      if (nt * heads <= kShortItem) source.ask();
       ok = wait.all(kv_empty, (nkv & 1) ^ 1);
       if (!ok) break;
       if (elect_one()) {
@@ -565,7 +615,7 @@ attn_dkv_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wai
       }
       __syncwarp();
       ++nkv;
-      for (int g = 0; ok && g < G; ++g)
+      for (int g = g0; ok && g < g0 + heads; ++g)
         for (int i = 0; i < nt; ++i, ++it) {
           const int sq = it % kQ, sg = it % kG, h = hk * G + g, row = x.start + (f + i) * kTile;
           ok = wait.all(&q_empty[sq], ((it / kQ) & 1) ^ 1);
@@ -581,6 +631,7 @@ attn_dkv_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wai
           __syncwarp();
         }
     }
+    source.close();
     // every load has landed before the CTA may leave
     if (nkv) mbar_wait_bounded(kv_full, (nkv - 1) & 1, wait_limit, status);
     for (int i = max(it - kQ, 0); i < it; ++i)
@@ -593,10 +644,10 @@ attn_dkv_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wai
     const int nk = (a.D + 15) / 16, no = nk * 16;
     int it = 0, nkv = 0;
     bool ok = true;
-    while (ok && next_item<false>(ring, wait, item_no, lane, words)) {
+    while (ok && next_item(ring, wait, item_no, lane, words)) {
       const SeqTile x{words[0], words[1], words[2]};
-      [[maybe_unused]] const int hk = words[3];
-      const int n = count(x) * G;
+      [[maybe_unused]] const int hk = words[3], g0 = words[5], heads = words[6];
+      const int n = count(x) * heads;
       if (n == 0) continue;
       auto scores = [&](int j) {
         const int u = it + j, s = u % kQ;
@@ -664,11 +715,11 @@ attn_dkv_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wai
     // ---------------------------- lse, delta, and the tails of the Q, dO tiles
     int it = 0;
     bool ok = true;
-    while (ok && next_item<false>(ring, wait, item_no, lane, words)) {
+    while (ok && next_item(ring, wait, item_no, lane, words)) {
       const SeqTile x{words[0], words[1], words[2]};
-      [[maybe_unused]] const int hk = words[3];
+      [[maybe_unused]] const int hk = words[3], g0 = words[5], heads = words[6];
       const int nt = count(x), f = first_tile(x);
-      for (int g = 0; ok && g < G; ++g)
+      for (int g = g0; ok && g < g0 + heads; ++g)
         for (int i = 0; i < nt; ++i, ++it) {
           const int sq = it % kQ, sg = it % kG, sr = it % kR, q0 = (f + i) * kTile;
           const int64_t at = (int64_t)(hk * G + g) * a.T + x.start + q0;
@@ -712,13 +763,13 @@ attn_dkv_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wai
     const float s2 = a.scale * kLog2E;
     int it = 0, nkv = 0;
     bool ok = true;
-    while (ok && next_item<false>(ring, wait, item_no, lane, words)) {
+    while (ok && next_item(ring, wait, item_no, lane, words)) {
       const SeqTile x{words[0], words[1], words[2]};
-      [[maybe_unused]] const int hk = words[3];
+      [[maybe_unused]] const int hk = words[3], g0 = words[5], heads = words[6];
       const int nt = count(x), f = first_tile(x);
       if (nt == 0) continue;
       const int row = x.row0 + in_tile;  // key row within the sequence
-      for (int j = 0; j < nt * G; ++j, ++it) {
+      for (int j = 0; j < nt * heads; ++j, ++it) {
         const int sr = it % kR, q0 = (f + j % nt) * kTile + 64 * half;
         ok = wait.all(&s_full[sr], (it / kR) & 1);
         if (!ok) break;
@@ -808,7 +859,17 @@ attn_dkv_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wai
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(acc_empty);
-      if (row < x.len) {
+      if (row < x.len && shares > 1) {
+        float *o = p.part + (((int64_t)words[4] * 2 + (half ? 0 : 1)) * a.T + x.start + row) *
+                                ((int64_t)a.Hkv * a.D) +
+                   (int64_t)hk * a.D;
+#pragma unroll
+        for (int c = 0; c < DP; c += 4)
+          if (c < a.D)
+            *reinterpret_cast<uint4 *>(o + c) =
+                make_uint4(v[c >> 6][c & 63], v[c >> 6][(c & 63) + 1], v[c >> 6][(c & 63) + 2],
+                           v[c >> 6][(c & 63) + 3]);
+      } else if (row < x.len) {
         bf16 *o = half ? (bf16 *)a.dk + (int64_t)(x.start + row) * a.ld_dk
                        : (bf16 *)a.dv + (int64_t)(x.start + row) * a.ld_dv;
         o += (int64_t)hk * a.D;
@@ -818,13 +879,6 @@ attn_dkv_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wai
       }
       __syncwarp();
     }
-  } else {
-    // -------------------------------------------------------- items
-    ItemSource<decltype(find)> source(ring, wait, find, skipped ? -1 : (int)blockIdx.x, lane);
-    bool ok = true;
-    do {
-      ok = source.publish(words);
-    } while (ok && words[0] >= 0);
   }
   tc_fence_before();
   __syncthreads();
@@ -834,11 +888,49 @@ attn_dkv_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wai
   }
 }
 
+// Adds the shares of dk and dv in order, scales dk and rounds: eight columns of
+// one row per thread.  Rows of no sequence have no sums and are left alone.
+__global__ void __launch_bounds__(256) attn_dkv_sum(const AttnArgs a, const float *part,
+                                                    int shares) {
+  pdl_wait();
+  pdl_trigger();
+  if (attn_skipped(a.skip)) return;
+  const int64_t row = (int64_t)a.Hkv * a.D, packs = row / 8;
+  const int64_t t0 = min(max(__ldg(a.cu), 0), (int)a.T), t1 = min(max(__ldg(a.cu + a.B), 0), (int)a.T);
+  const int64_t n = (t1 - t0) * packs * 2;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+    const int64_t u = i / packs, c = (i - u * packs) * 8;
+    const int dv = (int)(u & 1);
+    const int64_t t = t0 + (u >> 1);
+    float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int k = 0; k < shares; ++k) {
+      const float4 *p =
+          reinterpret_cast<const float4 *>(part + (((int64_t)k * 2 + dv) * a.T + t) * row + c);
+      const float4 x = __ldcs(p), y = __ldcs(p + 1);
+      s[0] += x.x;
+      s[1] += x.y;
+      s[2] += x.z;
+      s[3] += x.w;
+      s[4] += y.x;
+      s[5] += y.y;
+      s[6] += y.z;
+      s[7] += y.w;
+    }
+    const float f = dv ? 1.f : a.scale;
+    bf16 *o = (dv ? (bf16 *)a.dv + t * a.ld_dv : (bf16 *)a.dk + t * a.ld_dk) + c;
+    *reinterpret_cast<uint4 *>(o) =
+        make_uint4(pack_bf16(s[0] * f, s[1] * f), pack_bf16(s[2] * f, s[3] * f),
+                   pack_bf16(s[4] * f, s[5] * f), pack_bf16(s[6] * f, s[7] * f));
+  }
+}
+
 template <int DP>
 cudaError_t launch(const AttnArgs &a, const DeviceInfo &dev, cudaStream_t s) {
   BwdParams p;
   p.a = a;
   p.slots = (int)(a.T / kTile + a.B);
+  p.splits = attn_bwd_splits(a.T, a.Hq, a.Hkv);
+  p.part = attn_bwd_part(a);
   cudaError_t e = make_head_map(&p.tq, a.q, a.T, a.Hq, a.D, a.ld_q);
   if (e == cudaSuccess) e = make_head_map(&p.tk, a.k, a.T, a.Hkv, a.D, a.ld_k);
   if (e == cudaSuccess) e = make_head_map(&p.tv, a.v, a.T, a.Hkv, a.D, a.ld_v);
@@ -856,11 +948,22 @@ cudaError_t launch(const AttnArgs &a, const DeviceInfo &dev, cudaStream_t s) {
   e = launch_pdl(attn_dq_tc<DP>, dim3((unsigned)p.slots * (unsigned)a.Hq), dim3(kBwdThreads), sq, s,
                  p, status, kWaitLimitCycles);
   if (e != cudaSuccess) return e;
-  return launch_pdl(attn_dkv_tc<DP>, dim3((unsigned)p.slots * (unsigned)a.Hkv), dim3(kBwdThreads),
-                    sk, s, p, status, kWaitLimitCycles);
+  e = launch_pdl(attn_dkv_tc<DP>, dim3((unsigned)p.slots * (unsigned)(a.Hkv * p.splits)),
+                 dim3(kBwdThreads), sk, s, p, status, kWaitLimitCycles);
+  if (e != cudaSuccess || p.splits == 1) return e;
+  const int64_t want = ceil_div(a.T * a.Hkv * a.D * 2, (int64_t)(8 * 256));
+  const int64_t most = (int64_t)dev.sms * 16;
+  return launch_pdl(attn_dkv_sum, dim3((unsigned)(want < most ? want : most)), dim3(256), 0, s, a,
+                    (const float *)p.part, p.splits);
 }
 
 }  // namespace
+
+size_t attn_bwd_tc_workspace_bytes(int64_t T, int32_t Hq, int32_t Hkv, int32_t D) {
+  const int n = attn_bwd_splits(T, Hq, Hkv);
+  const size_t part = n > 1 ? (size_t)n * 2 * T * Hkv * D * sizeof(float) : 0;
+  return delta_bytes(T, Hq) + part;
+}
 
 cudaError_t launch_attn_bwd_tc(const AttnArgs &a, const DeviceInfo &dev, cudaStream_t s) {
   return a.D <= 64 ? launch<64>(a, dev, s) : launch<128>(a, dev, s);

@@ -129,27 +129,40 @@ __device__ __forceinline__ int pair_base(int c, int b, int G) {
   return ((max(c, 0) / kTile + b) * G + 1) / 2 + b;
 }
 
-__device__ __forceinline__ FwdItem fwd_item(const AttnArgs &a, int nslots, int item) {
+__device__ __forceinline__ int pairs_of(int len, int G) { return (ceil_div(len, kTile) * G + 1) / 2; }
+
+// Item `item` in the order of its slots or by length.  Within a
+// sequence from the last pair back, whose rows see most keys.
+__device__ __forceinline__ FwdItem fwd_item(const AttnArgs &a, int nslots, int item,
+                                            const SeqOrder &seqs, bool by_length) {
   FwdItem w;
   const int G = a.Hq / a.Hkv;
   w.hk = item % a.Hkv;
-  // from the last slot back: in one long causal sequence the longest rows first
-  const int slot = nslots - 1 - item / a.Hkv;
-  int lo = 1, hi = a.B;
-  while (lo <= hi) {
-    const int mid = (lo + hi) >> 1;
-    if (pair_base(__ldg(a.cu + mid), mid, G) <= slot)
-      lo = mid + 1;
-    else
-      hi = mid - 1;
+  int b, pair = 0;
+  if (by_length) {
+    const int u = item / a.Hkv, r = u < seqs.total ? seqs.rank_of(u, a.B) : 0;
+    b = seqs.order[r];
+    pair = u < seqs.total ? u - seqs.base[r] : 1 << 30;
+  } else {
+    const int slot = nslots - 1 - item / a.Hkv;
+    int lo = 1, hi = a.B;
+    while (lo <= hi) {
+      const int mid = (lo + hi) >> 1;
+      if (pair_base(__ldg(a.cu + mid), mid, G) <= slot)
+        lo = mid + 1;
+      else
+        hi = mid - 1;
+    }
+    b = min(lo - 1, a.B - 1);
+    pair = slot;
   }
-  const int b = min(lo - 1, a.B - 1);
   const int c0 = min(max(__ldg(a.cu + b), 0), (int)a.T);
   const int c1 = min(max(__ldg(a.cu + b + 1), c0), (int)a.T);
   w.start = c0;
   w.len = c1 - c0;
   const int nt = ceil_div(w.len, kTile);
-  const int64_t f0 = 2 * ((int64_t)slot - pair_base(c0, b, G));
+  const int64_t f0 = 2 * (by_length ? (int64_t)pairs_of(w.len, G) - 1 - pair
+                               : (int64_t)pair - pair_base(c0, b, G));
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     const int64_t f = f0 + t;
@@ -164,11 +177,13 @@ __device__ __forceinline__ FwdItem fwd_item(const AttnArgs &a, int nslots, int i
 
 template <int DP> struct FwdLayout {
   static constexpr uint32_t tile_bytes = (DP / 64) * kBoxBytes;
-  static constexpr int kStages = DP == 128 ? 5 : 8;
+  static constexpr int kStages = DP == 128 ? 4 : 8;
   static constexpr uint32_t off_ring = 2 * tile_bytes;
-  static constexpr uint32_t off_bar = off_ring + kStages * tile_bytes;
+  static constexpr uint32_t off_stage = off_ring + kStages * tile_bytes;  // 4 KB per softmax warp
+  static constexpr uint32_t off_bar = off_stage + 8 * 4096;
   static constexpr uint32_t off_items = (off_bar + (3 * kStages + 20) * 8 + 16 + 15) / 16 * 16;
-  static constexpr uint32_t smem = off_items + ItemRing::kBytes + 1024;
+  static constexpr uint32_t off_order = off_items + ItemRing::kBytes;
+  static constexpr uint32_t smem = off_order + SeqOrder::kBytes;
   static_assert(smem <= 227 * 1024, "shared memory per CTA");
 };
 
@@ -178,8 +193,8 @@ attn_fwd_tc(const __grid_constant__ FwdParams p, unsigned *status, long long wai
   using L = FwdLayout<DP>;
   constexpr int kStages = L::kStages;
   constexpr bool kApart = DP <= 64;  // P beside S in tensor memory, not over it
-  extern __shared__ unsigned char smem_raw[];
-  unsigned char *sm = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
+  extern __shared__ __align__(1024) unsigned char smem_aligned[];
+  unsigned char *sm = smem_aligned;
   const uint32_t sbase = smem_addr(sm);
   uint64_t *kv_full = reinterpret_cast<uint64_t *>(sm + L::off_bar);
   uint64_t *kv_empty = kv_full + kStages;
@@ -217,7 +232,7 @@ attn_fwd_tc(const __grid_constant__ FwdParams p, unsigned *status, long long wai
       mbar_init(&s_read[t], 4);
       mbar_init(&drain[t], 1);
     }
-    ring.init(11);  // loads, MMAs of both tiles, eight softmax warps
+    ring.init(11);  // MMAs of both tiles, eight softmax warps, tails
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -232,6 +247,10 @@ attn_fwd_tc(const __grid_constant__ FwdParams p, unsigned *status, long long wai
   pdl_trigger();
   const bool skipped = attn_skipped(a.skip);
   int item_no = 0, words[kItemWords];
+  SeqOrder seqs(sm + L::off_order);
+  const bool by_length = a.B <= kSortMax;
+  if (by_length && !skipped)
+    seqs.make(a, reinterpret_cast<int *>(sm), [&](int len) { return pairs_of(len, a.Hq / a.Hkv); });
 
   if (warp == 0) {
     // -------------------------------------------------------- tile loads
@@ -246,9 +265,16 @@ attn_fwd_tc(const __grid_constant__ FwdParams p, unsigned *status, long long wai
       __syncwarp();
       ++it;
     };
-    while (ok && next_item<true>(ring, wait, item_no, lane, words)) {
+    auto find = [&](int index, int (&v)[kItemWords]) {
+      const FwdItem y = fwd_item(a, p.nslots, index, seqs, by_length);
+      y.to(v);
+      return y.tiles() > 0;
+    };
+    ItemSource<decltype(find)> source(ring, wait, find, skipped ? -1 : (int)blockIdx.x, lane);
+    while (ok && (ok = source.next(words)) && words[0] >= 0) {
       const FwdItem x(words);
       const int n = x.tiles();
+      if (n <= kShortItem) source.ask();
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         if (!ok || x.n[t] == 0) continue;
@@ -264,6 +290,7 @@ attn_fwd_tc(const __grid_constant__ FwdParams p, unsigned *status, long long wai
         if (ok) load_kv(&p.tv, x.hk, x.start + i * kTile);
       }
     }
+    source.close();
     // every load has landed before the CTA may leave
 #pragma unroll
     for (int t = 0; t < 2; ++t)
@@ -279,7 +306,7 @@ attn_fwd_tc(const __grid_constant__ FwdParams p, unsigned *status, long long wai
     int it = 0, nq = 0, ns = 0;  // ring entries, items, score tiles so far
     int np0 = 0, np1 = 0;        // first and second halves so far
     bool ok = true;
-    while (ok && next_item<false>(ring, wait, item_no, lane, words)) {
+    while (ok && next_item(ring, wait, item_no, lane, words)) {
       const FwdItem x(words);
       const int n = x.tiles(), mine = t ? x.n[1] : x.n[0];
       if (n == 0) continue;
@@ -370,16 +397,10 @@ attn_fwd_tc(const __grid_constant__ FwdParams p, unsigned *status, long long wai
       mbar_wait_bounded(&drain[t], 0, wait_limit, status);
     }
   } else if (warp == 10) {
-    // -------------------------------------------------------- items, V tiles' tails
-    auto find = [&](int index, int (&v)[kItemWords]) {
-      const FwdItem x = fwd_item(a, p.nslots, index);
-      x.to(v);
-      return x.tiles() > 0;
-    };
-    ItemSource<decltype(find)> source(ring, wait, find, skipped ? -1 : (int)blockIdx.x, lane);
+    // -------------------------------------------------------- V tiles' tails
     int it = 0;
-    bool ok = source.publish(words);
-    while (ok && words[0] >= 0) {
+    bool ok = true;
+    while (ok && next_item(ring, wait, item_no, lane, words)) {
       const FwdItem x(words);
       const int n = x.tiles();
       for (int i = 0; ok && i < 2 * n; ++i, ++it) {  // K0 V0 K1 V1 ..., as loaded
@@ -395,7 +416,6 @@ attn_fwd_tc(const __grid_constant__ FwdParams p, unsigned *status, long long wai
         }
         __syncwarp();
       }
-      if (ok) ok = source.publish(words);
     }
   } else if (warp < 10) {
     // -------------------------------------------------------- softmax
@@ -407,7 +427,7 @@ attn_fwd_tc(const __grid_constant__ FwdParams p, unsigned *status, long long wai
     const float2 sc = make_float2(s2, s2);
     int ns = 0, np0 = 0, np1 = 0;  // score tiles, first and second halves so far
     bool ok = true;
-    while (ok && next_item<false>(ring, wait, item_no, lane, words)) {
+    while (ok && next_item(ring, wait, item_no, lane, words)) {
       const FwdItem x(words);
       // selected, not indexed: an index would put the item into local memory,
       // and beside this much shared memory L1 holds next to nothing of it
@@ -564,8 +584,9 @@ attn_fwd_tc(const __grid_constant__ FwdParams p, unsigned *status, long long wai
       tc_fence_after();
       const float l = l2.x + l2.y, inv = 1.f / l;
       const bool in = row < x.len;
-      bf16 *o = (bf16 *)a.o + (int64_t)(x.start + row) * a.ld_o + (int64_t)head * a.D;
-      // the whole row first, the warp converged, then the divergent stores: a
+      bf16 *o = (bf16 *)a.o + (int64_t)(x.start + row0 + quarter * 32) * a.ld_o +
+                (int64_t)head * a.D;
+      // all columns first, the warp converged, then the divergent stores: a
       // tensor-memory load must never sit behind a branch that lanes take apart
       uint32_t v[DP / 64][64];
       __syncwarp();
@@ -574,18 +595,14 @@ attn_fwd_tc(const __grid_constant__ FwdParams p, unsigned *status, long long wai
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&o_empty[t]);  // the next pair's O may be written
-      if (in) {
 #pragma unroll
-        for (int c = 0; c < DP; c += 8) {
-          if (c < a.D) {
-            float f[8];
+      for (int j = 0; j < DP / 64; ++j) {
+        uint32_t pk[32];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(v[c >> 6][(c & 63) + e]) * inv;
-            *reinterpret_cast<uint4 *>(o + c) =
-                make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
-                           pack_bf16(f[6], f[7]));
-          }
-        }
+        for (int c = 0; c < 32; ++c)
+          pk[c] = pack_bf16(__uint_as_float(v[j][2 * c]) * inv, __uint_as_float(v[j][2 * c + 1]) * inv);
+        store_rows64(sm + L::off_stage + (warp - 2) * 4096, pk, o + 64 * j, a.ld_o,
+                     x.len - row0 - quarter * 32, a.D - 64 * j, lane);
       }
       if (in && a.lse)
         a.lse[(int64_t)head * a.T + x.start + row] = ms * kLn2 + logf(l);

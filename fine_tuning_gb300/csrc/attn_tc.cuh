@@ -294,21 +294,23 @@ struct Waits {
 // one and takes its index over).  So items of very different lengths even out
 // without a counter in memory that calls on two streams would share.
 //
-// One warp of the CTA asks for the next item when the loading warp has no
-// more to load for the current one (an item asked for earlier would be tied to
-// this CTA while others run dry: with a few long items per SM that cost 19%),
+// The loading warp, which runs ahead of the others, asks for the next item,
 // finds its sequence and tile once for all roles, and hands it over in a ring
-// of two slots; empty items are dropped there.
+// of two slots; empty items are dropped there.  It asks when it has no more to
+// load for the current item: an item asked for earlier would be tied to this
+// CTA while others run dry (with a few long items per SM that cost 19%).  Only
+// when the current item is short (kShortItem tiles) does it ask before, since
+// the answer takes about as long as such an item.
 constexpr int kItemWords = 12;
+constexpr int kShortItem = 4;
 
 struct ItemRing {
-  uint64_t *want;   // the loading warp is done with the last item
   uint64_t *asked;  // the answer has arrived (16 bytes)
   uint64_t *full;   // [2]
   uint64_t *empty;  // [2]
   int *slots;       // [2][kItemWords]
   uint4 *answer;
-  static constexpr uint32_t kBytes = 16 + 2 * kItemWords * 4 + 6 * 8;  // from a multiple of 16
+  static constexpr uint32_t kBytes = 16 + 2 * kItemWords * 4 + 5 * 8 + 8;  // from a multiple of 16
 
   __device__ __forceinline__ explicit ItemRing(unsigned char *at) {
     answer = reinterpret_cast<uint4 *>(at);
@@ -316,11 +318,9 @@ struct ItemRing {
     asked = reinterpret_cast<uint64_t *>(at + 16 + 2 * kItemWords * 4);
     full = asked + 1;
     empty = full + 2;
-    want = empty + 2;
   }
   __device__ __forceinline__ void init(int readers) const {  // one thread
     mbar_init(asked, 1);
-    mbar_init(want, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], readers);
@@ -353,7 +353,7 @@ struct ItemRing {
   }
 };
 
-// The asking warp's side.  find(index, words) fills in an item and says whether
+// The loading warp's side.  find(index, words) fills in an item and says whether
 // it holds work; words[0] < 0 marks the end.
 template <class Find> struct ItemSource {
   const ItemRing &ring;
@@ -361,31 +361,33 @@ template <class Find> struct ItemSource {
   Find find;
   int lane;
   int index, count = 0, asks = 0;  // index: the CTA's own, -1 after the end
+  bool pending = false;
   __device__ __forceinline__ ItemSource(const ItemRing &r, const Waits &w, Find f, int first,
                                         int l)
       : ring(r), wait(w), find(f), lane(l), index(first) {}
-  // Publishes the next item (or the end) into its slot; false when a wait gave
-  // up.  words: the item, in every lane.
-  __device__ __forceinline__ bool publish(int (&words)[kItemWords]) {
-    bool work = false;
-    if (count == 0) {
-      work = index >= 0 && find(index, words);
-    } else if (!wait.all(ring.want, (count - 1) & 1)) {
-      return false;
-    }
+  __device__ __forceinline__ void ask() {
+    if (pending || index < 0) return;
+    if (elect_one()) ring.ask();
+    __syncwarp();
+    pending = true;
+  }
+  // The next item (or the end) into words, in every lane, and into its slot;
+  // false when a wait gave up.
+  __device__ __forceinline__ bool next(int (&words)[kItemWords]) {
+    bool work = count == 0 && index >= 0 && find(index, words);
     while (index >= 0 && !work) {
-      if (elect_one()) ring.ask();
-      __syncwarp();
-      if (!wait.all(ring.asked, asks & 1)) {  // the answer still comes: not after the CTA left
-        mbar_wait_bounded(ring.asked, asks & 1, wait.limit, wait.status);
-        return false;
-      }
+      ask();
+      const bool came = wait.all(ring.asked, asks & 1);
+      if (!came) return false;
       ++asks;
+      pending = false;
       index = uniform(ring.answered());
       __syncwarp();
       if (index >= 0) work = find(index, words);
     }
     if (!work) words[0] = -1;
+#pragma unroll
+    for (int i = 0; i < kItemWords; ++i) words[i] = uniform(words[i]);
     const int s = count & 1;
     if (!wait.all(&ring.empty[s], ((count >> 1) & 1) ^ 1)) return false;
     if (lane == 0) {
@@ -397,26 +399,127 @@ template <class Find> struct ItemSource {
     ++count;
     return true;
   }
+  // no answer may arrive after the CTA has left
+  __device__ __forceinline__ void close() const {
+    if (pending) mbar_wait_bounded(ring.asked, asks & 1, wait.limit, wait.status);
+  }
 };
 
 // The reading side (a whole warp): item number `count`; false at the end or when
-// a wait gave up.  LOADS: this is the loading warp, whose request starts the
-// search for every item but the first.
-template <bool LOADS>
+// a wait gave up.
 __device__ __forceinline__ bool next_item(const ItemRing &ring, const Waits &wait, int &count,
                                           int lane, int (&words)[kItemWords]) {
   const int s = count & 1;
-  if (LOADS && count > 0 && lane == 0) mbar_arrive(ring.want);
   if (!wait.all(&ring.full[s], (count >> 1) & 1)) return false;
 #pragma unroll
-  for (int i = 0; i < kItemWords; ++i) {
-    words[i] = uniform(ring.slots[s * kItemWords + i]);
-  }
+  for (int i = 0; i < kItemWords; ++i) words[i] = uniform(ring.slots[s * kItemWords + i]);
   __syncwarp();
   if (lane == 0) mbar_arrive(&ring.empty[s]);
   ++count;
   return words[0] >= 0;
 }
+
+// 32 rows x 64 columns of bf16 to global memory by a warp that holds a row per
+// lane (pk: its 32 words).  Stored straight from the lanes, every 16-byte piece
+// would be a transaction of its own (eight stores of 32 lines each, which also
+// hold up every later shared-memory access of the SM); through a 4 KB staging
+// tile (16-byte pieces swizzled by the row) eight lanes store a row's 128 bytes
+// together.  Rows at or past `rows`, columns at or past n: not stored.
+__device__ __forceinline__ void store_rows64(unsigned char *stage, const uint32_t (&pk)[32],
+                                             bf16 *base, int64_t ld, int rows, int n, int lane) {
+  uint4 *st = reinterpret_cast<uint4 *>(stage);
+#pragma unroll
+  for (int c = 0; c < 8; ++c)
+    st[lane * 8 + (c ^ (lane & 7))] =
+        make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+  __syncwarp();
+  const int c = lane & 7;
+  if (8 * c < n) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int r = 4 * k + (lane >> 3);
+      if (r < rows)
+        *reinterpret_cast<uint4 *>(base + (int64_t)r * ld + 8 * c) = st[r * 8 + (c ^ (r & 7))];
+    }
+  }
+  __syncwarp();
+}
+
+// Sequences by length, the longest first, for batches of up to kSortMax: with
+// items handed out in this order the long ones do not come last (16,384 packed
+// tokens in 85 sequences of 16 to 2,048: the tail of one long item is a third
+// of the call).  Larger batches keep the order of the slots, which needs no
+// table.  Every CTA makes the same table, from one look at cu.
+constexpr int kSortMax = 128;
+
+struct SeqOrder {
+  int *base;       // [kSortMax]: units of the sequences before rank r
+  uint8_t *order;  // [kSortMax]: the sequence of rank r
+  int total;       // units of all
+  static constexpr uint32_t kBytes = kSortMax * 5;
+
+  __device__ __forceinline__ explicit SeqOrder(unsigned char *at)
+      : base(reinterpret_cast<int *>(at)), order(at + kSortMax * 4), total(0) {}
+
+  // All threads of the CTA (at least kSortMax).  tmp: kSortMax ints of shared
+  // memory that tiles are loaded into later.  units(len): work units of a sequence.
+  template <class Units>
+  __device__ __forceinline__ void make(const AttnArgs &a, int *tmp, Units units) {
+    const int b = threadIdx.x;
+    int len = 0;
+    if (b < a.B) {
+      const int c0 = min(max(__ldg(a.cu + b), 0), (int)a.T);
+      len = min(max(__ldg(a.cu + b + 1), c0), (int)a.T) - c0;
+      tmp[b] = len;
+    }
+    __syncthreads();
+    if (b < a.B) {
+      int rank = 0;
+      for (int c = 0; c < a.B; ++c) rank += tmp[c] > len || (tmp[c] == len && c < b);
+      order[rank] = (uint8_t)b;
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) {  // running sum of the units, four ranks per lane
+      const int l = threadIdx.x;
+      int n[4], s = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = 4 * l + i;
+        n[i] = r < a.B ? units(tmp[order[r]]) : 0;
+        s += n[i];
+      }
+      int upto = s;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, upto, o);
+        if (l >= o) upto += v;
+      }
+      int at = upto - s;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        base[4 * l + i] = at;
+        at += n[i];
+      }
+      if (l == 31) tmp[kSortMax] = upto;
+    }
+    __syncthreads();
+    total = tmp[kSortMax];
+    fence_proxy_async_smem();  // tmp is written by tile loads next
+    __syncthreads();
+  }
+  // The rank that unit u (< total) belongs to.
+  __device__ __forceinline__ int rank_of(int u, int B) const {
+    int lo = 0, hi = B - 1;  // the last r with base[r] <= u
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (base[mid] <= u)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    return lo;
+  }
+};
 
 // Zeroes rows [from, 128) of a staged tile (whole warp): rows behind a
 // sequence's end hold another sequence's values, whose infinities would turn a

@@ -930,7 +930,8 @@ FTK_API ftk_status ftk_attn_fwd(const void *q, int64_t ld_q, const void *k, int6
 FTK_API size_t ftk_attn_bwd_workspace_bytes(int64_t T, int32_t Hq, int32_t Hkv, int32_t D,
                                             ftk_dtype dtype) {
   if (!valid_dtype(dtype) || T <= 0 || attn_shape(1, T, Hq, Hkv, D, 1.f) != FTK_OK) return 0;
-  return (size_t)T * (size_t)Hq * sizeof(float);
+  // the CUDA-core form, which a bf16 call may still take (alignment), needs none
+  return attn_tc_shape((DType)dtype, D) ? ftk::attn_bwd_tc_workspace_bytes(T, Hq, Hkv, D) : 16;
 }
 
 FTK_API ftk_status ftk_attn_bwd(const void *do_, int64_t ld_do, const void *q, int64_t ld_q,

@@ -274,6 +274,8 @@ cudaError_t launch_attn_bwd_generic(DType dt, const AttnArgs &a, const DeviceInf
                                     cudaStream_t s);
 // bf16, D % 8 == 0, D <= 128, 16-byte aligned tensors, row strides % 8 == 0.
 cudaError_t launch_attn_fwd_tc(const AttnArgs &a, const DeviceInfo &dev, cudaStream_t s);
+// bytes from AttnArgs::delta on that launch_attn_bwd_tc uses
+size_t attn_bwd_tc_workspace_bytes(int64_t T, int32_t Hq, int32_t Hkv, int32_t D);
 cudaError_t launch_attn_bwd_tc(const AttnArgs &a, const DeviceInfo &dev, cudaStream_t s);
 
 // Cross-entropy of the LM head (cce.cu).  bf16 h [T, ldh], W [V, ldw];
