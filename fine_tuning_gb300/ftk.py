@@ -548,31 +548,26 @@ def rope_llama3_inv_freq(D: int, theta: float, factor: float, low_freq_factor: f
 
 # ------------------------------------------------ QK-RoPE on several axes
 
-def _same_device(ref: torch.Tensor, *ts):
-    """Every tensor given lives on ref's CUDA device."""
-    if not ref.is_cuda:
+def _same_device(ref: torch.Tensor, *ts) -> int:
+    """The index of ref's CUDA device, on which every tensor given has to live."""
+    i = ref.get_device()  # -1: not a GPU's (an int, without the device objects)
+    if i < 0:
         raise ValueError("ftk ops take CUDA tensors (move inputs with .cuda())")
-    dev = ref.device
     for t in ts:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors on different devices: {t.device} and {dev}")
+        if t is not None and t.get_device() != i:
+            raise ValueError(f"tensors on different devices: {t.device} and {ref.device}")
+    return i
 
 
-def _call_on(ref: torch.Tensor, name: str, *args) -> None:
-    """_call on ref's device (made the current one for the launch) and that
-    device's current stream."""
-    i = ref.device.index
-    if i == torch.cuda.current_device():
-        _call(name, *args, _raw_stream(i))
+def _call_on(index: int, name: str, *args) -> None:
+    """_call on device `index` (made the current one for the launch) and its
+    current stream, as a raw handle: the Stream object that current_stream
+    builds costs 2 us of a small call's host time."""
+    if index == torch.cuda.current_device():
+        _call(name, *args, torch._C._cuda_getCurrentRawStream(index))
     else:
-        with torch.cuda.device(i):
-            _call(name, *args, _raw_stream(i))
-
-
-def _raw_stream(index: int) -> int:
-    """The handle of device `index`'s current stream (without the Stream object
-    that current_stream builds: 2 us of a small call's host time)."""
-    return torch._C._cuda_getCurrentRawStream(index)
+        with torch.cuda.device(index):
+            _call(name, *args, torch._C._cuda_getCurrentRawStream(index))
 
 
 def _head_rows(t: torch.Tensor, name: str) -> int:
@@ -599,7 +594,8 @@ def _mrope(name, q, k, pos, axis_of, theta, inv_freq, q_out, k_out):
     ref = q if q is not None else k
     if ref is None:
         raise ValueError("q or k is needed")
-    _same_device(ref, q, k, pos, q_out, k_out)
+    dev = _same_device(ref, q, k, pos, q_out, k_out)
+    given = q_out is not None or k_out is not None
     if q is not None and q_out is None:
         q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     if k is not None and k_out is None:
@@ -613,27 +609,29 @@ def _mrope(name, q, k, pos, axis_of, theta, inv_freq, q_out, k_out):
     if q is not None and k is not None and (k.shape[0] != T or k.shape[2] != D
                                             or k.dtype != q.dtype):
         raise ValueError("q and k must agree in tokens, head_dim and dtype")
-    for x, y in ((q, q_out), (k, k_out)):
-        if (x is None) != (y is None) or (x is not None and (y.shape != x.shape
-                                                             or y.dtype != x.dtype)):
-            raise ValueError("q_out and k_out must match q and k in shape and dtype")
+    if given:
+        for x, y in ((q, q_out), (k, k_out)):
+            if (x is None) != (y is None) or (x is not None and (y.shape != x.shape
+                                                                 or y.dtype != x.dtype)):
+                raise ValueError("q_out and k_out must match q and k in shape and dtype")
     if pos.dtype != torch.int32 or pos.dim() != 2 or pos.shape[1] != T \
             or (T > 1 and pos.stride(1) != 1):
         raise ValueError("pos must be int32 [axes, T] with unit stride along tokens")
     axes = pos.shape[0]
     ldp = max(pos.stride(0), T) if axes == 1 else pos.stride(0)
-    table = np.asarray(axis_of)
+    table = axis_of if type(axis_of) is np.ndarray else np.asarray(axis_of)
     if table.dtype != np.int32:
         if table.shape and not np.issubdtype(table.dtype, np.integer):
             raise ValueError("axis_of must hold integers")
         if table.size and (int(table.min()) < 0 or int(table.max()) >= axes):
             raise ValueError("axis_of must hold axes of pos")  # before the cast could wrap
-    table = np.ascontiguousarray(table, dtype=np.int32)
+    if table.dtype != np.int32 or not table.flags.c_contiguous:
+        table = np.ascontiguousarray(table, dtype=np.int32)
     if table.shape != (D // 2,):
         raise ValueError("axis_of must hold D/2 axes")
     freq, freq_p = (None, None) if inv_freq is None else _table(inv_freq, D)
-    _call_on(ref, name, _ptr(q), ldq, _ptr(k), ldk, _ptr(q_out), ldqo, _ptr(k_out), ldko,
-             _ptr(pos), ldp, axes, table.__array_interface__["data"][0], T, Hq, Hkv, D,
+    _call_on(dev, name, _ptr(q), ldq, _ptr(k), ldk, _ptr(q_out), ldqo, _ptr(k_out), ldko,
+             _ptr(pos), ldp, axes, table.ctypes.data, T, Hq, Hkv, D,
              float(theta or 0.0), freq_p, _code(ref))
     del table, freq
     return q_out, k_out
@@ -656,20 +654,23 @@ def qk_mrope_bwd(dq_out, dk_out, pos, axis_of, theta: float = 0.0, inv_freq=None
 
 # -------------------------------------------------------------- attention
 
-def _attn_check(q, k, v, cu_seqlens, seqlens_status, *rest):
-    _same_device(q, k, v, cu_seqlens, seqlens_status, *rest)
+def _attn_check(q, k, v, cu_seqlens, seqlens_status, *rest) -> int:
+    dev = _same_device(q, k, v, cu_seqlens, seqlens_status, *rest)
     _cu_check(cu_seqlens)
-    if cu_seqlens.numel() < 1:
+    if cu_seqlens.shape[0] < 1:
         raise ValueError("cu_seqlens must hold at least one boundary")
     if seqlens_status is not None:
         _status_check(seqlens_status)
-    if k.shape != v.shape or k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2] \
-            or k.dtype != q.dtype or v.dtype != q.dtype:
+    ks, qs, dt = k.shape, q.shape, q.dtype
+    if ks != v.shape or ks[0] != qs[0] or ks[2] != qs[2] or k.dtype != dt or v.dtype != dt:
         raise ValueError("q [T, Hq, D], k and v [T, Hkv, D] must agree in tokens, head_dim, dtype")
+    return dev
 
 
 def _like(x: torch.Tensor, y: Optional[torch.Tensor], name: str) -> torch.Tensor:
     if y is None:
+        if x.is_contiguous():  # then empty_like is contiguous too, and cheaper
+            return torch.empty_like(x)
         return torch.empty(x.shape, dtype=x.dtype, device=x.device)
     if y.shape != x.shape or y.dtype != x.dtype:
         raise ValueError(f"{name} must be {tuple(x.shape)} {x.dtype}")
@@ -687,17 +688,17 @@ def attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torc
     output allocated here).  seqlens_status: the word check_seqlens wrote; a
     non-zero word leaves every output untouched."""
     ldq, ldk, ldv = _head_rows(q, "q"), _head_rows(k, "k"), _head_rows(v, "v")
-    _attn_check(q, k, v, cu_seqlens, seqlens_status, o, lse)
+    dev = _attn_check(q, k, v, cu_seqlens, seqlens_status, o, lse)
     T, Hq, D = q.shape
     Hkv = k.shape[1]
     o = _like(q, o, "o")
-    if lse is None and save_lse:
-        lse = torch.empty((Hq, T), dtype=torch.float32, device=q.device)
-    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (Hq, T)
-                            or not lse.is_contiguous()):
+    if lse is None:
+        if save_lse:
+            lse = torch.empty((Hq, T), dtype=torch.float32, device=q.device)
+    elif lse.dtype != torch.float32 or lse.shape != (Hq, T) or not lse.is_contiguous():
         raise ValueError("lse must be a contiguous fp32 [Hq, T] tensor")
-    _call_on(q, "ftk_attn_fwd", _ptr(q), ldq, _ptr(k), ldk, _ptr(v), ldv, _ptr(o),
-             _head_rows(o, "o"), _ptr(lse), _ptr(cu_seqlens), cu_seqlens.numel() - 1, T, Hq, Hkv, D,
+    _call_on(dev, "ftk_attn_fwd", _ptr(q), ldq, _ptr(k), ldk, _ptr(v), ldv, _ptr(o),
+             _head_rows(o, "o"), _ptr(lse), _ptr(cu_seqlens), cu_seqlens.shape[0] - 1, T, Hq, Hkv, D,
              float(D ** -0.5 if scale is None else scale), int(bool(causal)),
              _ptr(seqlens_status), _code(q))
     return o, lse
@@ -718,7 +719,7 @@ def attn_bwd(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor
     probabilities are recomputed; the results are bitwise reproducible.
     dq, dk, dv may be slices of one fused [T, Hq + 2 Hkv, D] buffer."""
     ldq, ldk, ldv = _head_rows(q, "q"), _head_rows(k, "k"), _head_rows(v, "v")
-    _attn_check(q, k, v, cu_seqlens, seqlens_status, do, o, lse, dq, dk, dv, workspace)
+    dev = _attn_check(q, k, v, cu_seqlens, seqlens_status, do, o, lse, dq, dk, dv, workspace)
     T, Hq, D = q.shape
     Hkv = k.shape[1]
     for t, name in ((do, "do"), (o, "o")):
@@ -730,7 +731,7 @@ def attn_bwd(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor
     if workspace is None:
         workspace = torch.empty(max(16, attn_bwd_workspace_bytes(T, Hq, Hkv, D, q.dtype)),
                                 dtype=torch.uint8, device=q.device)
-    _call_on(q, "ftk_attn_bwd", _ptr(do), _head_rows(do, "do"), _ptr(q), ldq, _ptr(k), ldk, _ptr(v),
+    _call_on(dev, "ftk_attn_bwd", _ptr(do), _head_rows(do, "do"), _ptr(q), ldq, _ptr(k), ldk, _ptr(v),
              ldv, _ptr(o), _head_rows(o, "o"), _ptr(lse), _ptr(dq), _head_rows(dq, "dq"), _ptr(dk),
              _head_rows(dk, "dk"), _ptr(dv), _head_rows(dv, "dv"), _ptr(workspace),
              workspace.numel() * workspace.element_size(), _ptr(cu_seqlens),
