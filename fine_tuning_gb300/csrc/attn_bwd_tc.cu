@@ -12,12 +12,12 @@
 // instead of five: s and do v^T are made twice); in return the gradients are
 // bitwise reproducible and nothing but them is written.
 //
-// Both kernels have 12 warps (one idle): warp 0 issues the tile
-// loads, warp 1 the MMAs, warps 2-9 turn scores into probabilities and score
-// gradients (thread = tile row, two groups of four warps take a half of the
-// columns each), warp 10 prepares tails.  p and ds go back to tensor memory
-// in bf16, over the fp32 values they came from (each half within its own 64
-// columns, so the halves need no barrier between them), and enter the next
+// Both kernels have 12 warps: warp 0 issues the tile loads, warp 1 the MMAs,
+// warps 2-9 turn scores into probabilities and score gradients (thread = tile
+// row, two groups of four warps take a half of the columns each), warp 10
+// prepares tails, warp 11 finds the work items.  p and ds go back to tensor
+// memory in bf16, over the fp32 values they came from (each half within its own
+// 64 columns, so the halves need no barrier between them), and enter the next
 // product from there.  The MMAs are queued so that the tensor pipe always has
 // the next tile's scores to work on while p and ds are formed: both kernels
 // are bound by the MMAs of their tile pairs (dq: 3, dk/dv: 4, 512 cycles each
@@ -49,7 +49,7 @@ struct BwdParams {
 // times.  Where that leaves fewer than two sums per SM (152), the heads are
 // dealt out to more CTAs, whose fp32 sums (8 bytes per element and share in the
 // workspace) a small kernel adds in order.  16,384 packed tokens x 14/2 x 64:
-// 256 sums, the longest of them 112 steps; three shares.
+// 256 sums, the longest of them 112 steps; two shares.
 int attn_bwd_splits(int64_t T, int32_t Hq, int32_t Hkv) {
   const int64_t G = Hq / Hkv, sums = ceil_div(T, (int64_t)kTile) * Hkv, want = 2 * 152;
   if (sums >= want) return 1;
@@ -158,7 +158,7 @@ template <int DP> struct DqLayout {
   static constexpr uint32_t off_bar = off_v + kV * tile_bytes;
   static constexpr uint32_t off_items = (off_bar + (3 * kK + 2 * kV + 11) * 8 + 16 + 15) / 16 * 16;
   static constexpr uint32_t off_order = off_items + ItemRing::kBytes;
-  static constexpr uint32_t smem = off_order + SeqOrder::kBytes;
+  static constexpr uint32_t smem = off_order + SeqOrder::kBytes + 1024;
   static_assert(smem <= 227 * 1024, "shared memory per CTA");
 };
 
@@ -167,8 +167,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 attn_dq_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wait_limit) {
   using L = DqLayout<DP>;
   constexpr int kK = L::kK, kV = L::kV;
-  extern __shared__ __align__(1024) unsigned char smem_aligned[];
-  unsigned char *sm = smem_aligned;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char *sm = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
   const uint32_t sbase = smem_addr(sm);
   uint64_t *k_full = reinterpret_cast<uint64_t *>(sm + L::off_bar);
   uint64_t *k_empty = k_full + kK, *k_ready = k_empty + kK;
@@ -203,7 +203,7 @@ attn_dq_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wait
     mbar_init(acc_full, 1);
     mbar_init(acc_empty, kComputeWarps);
     mbar_init(drain, 1);
-    ring.init(10);  // MMAs, eight compute warps, tails
+    ring.init(11);  // MMAs, eight compute warps, tails
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -220,7 +220,7 @@ attn_dq_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wait
   const int G = a.Hq / a.Hkv;
   const bool skipped = attn_skipped(a.skip);
   SeqOrder seqs(sm + L::off_order);
-  const bool by_length = a.B <= kSortMax;
+  const bool by_length = a.B > 1 && a.B <= kSortMax;
   if (by_length && !skipped)
     seqs.make(a, reinterpret_cast<int *>(sm), [](int len) { return ceil_div(len, kTile); });
   // index w: head w % Hq (the heads of a group follow each other and share K and
@@ -242,12 +242,10 @@ attn_dq_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wait
     // -------------------------------------------------------- tile loads
     int it = 0, nq = 0;
     bool ok = true;
-    ItemSource<decltype(find)> source(ring, wait, find, skipped ? -1 : (int)blockIdx.x, lane);
-    while (ok && (ok = source.next(words)) && words[0] >= 0) {
+    while (ok && next_item<true>(ring, wait, item_no, lane, words)) {
       const SeqTile x{words[0], words[1], words[2]};
       [[maybe_unused]] const int h = words[3];
       const int n = tiles(x);
-      if (n <= kShortItem) source.ask();
       ok = wait.all(q_empty, (nq & 1) ^ 1);
       if (!ok) break;
       if (elect_one()) {
@@ -275,7 +273,6 @@ attn_dq_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wait
         __syncwarp();
       }
     }
-    source.close();
     // every load has landed before the CTA may leave (after a wait that gave
     // up, a stage that was never filled may be waited for: bounded as well)
     if (nq) mbar_wait_bounded(q_full, (nq - 1) & 1, wait_limit, status);
@@ -291,7 +288,7 @@ attn_dq_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wait
     const int nk = (a.D + 15) / 16, no = nk * 16;
     int it = 0, nq = 0;  // key tiles and items so far
     bool ok = true;
-    while (ok && next_item(ring, wait, item_no, lane, words)) {
+    while (ok && next_item<false>(ring, wait, item_no, lane, words)) {
       const SeqTile x{words[0], words[1], words[2]};
       [[maybe_unused]] const int h = words[3];
       const int n = tiles(x);
@@ -365,7 +362,7 @@ attn_dq_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wait
     // -------------------------------------------------------- K tiles' tails
     int it = 0;
     bool ok = true;
-    while (ok && next_item(ring, wait, item_no, lane, words)) {
+    while (ok && next_item<false>(ring, wait, item_no, lane, words)) {
       const SeqTile x{words[0], words[1], words[2]};
       [[maybe_unused]] const int h = words[3];
       const int n = tiles(x);
@@ -390,7 +387,7 @@ attn_dq_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wait
     const float s2 = a.scale * kLog2E;
     int it = 0, nq = 0;
     bool ok = true;
-    while (ok && next_item(ring, wait, item_no, lane, words)) {
+    while (ok && next_item<false>(ring, wait, item_no, lane, words)) {
       const SeqTile x{words[0], words[1], words[2]};
       [[maybe_unused]] const int h = words[3];
       const int n = tiles(x);
@@ -476,6 +473,13 @@ attn_dq_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wait
                    v, a.scale, min(kCols, a.D - half * kCols));
       __syncwarp();
     }
+  } else {
+    // -------------------------------------------------------- items
+    ItemSource<decltype(find)> source(ring, wait, find, skipped ? -1 : (int)blockIdx.x, lane);
+    bool ok = true;
+    do {
+      ok = source.publish(words);
+    } while (ok && words[0] >= 0);
   }
   tc_fence_before();
   __syncthreads();
@@ -550,7 +554,7 @@ attn_dkv_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wai
     mbar_init(acc_full, 1);
     mbar_init(acc_empty, kComputeWarps);
     mbar_init(drain, 1);
-    ring.init(10);  // MMAs, eight compute warps, tails
+    ring.init(11);  // MMAs, eight compute warps, tails
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -567,7 +571,7 @@ attn_dkv_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wai
   const int G = a.Hq / a.Hkv;
   const bool skipped = attn_skipped(a.skip);
   SeqOrder seqs(sm + L::off_order);
-  const bool by_length = a.B <= kSortMax;
+  const bool by_length = a.B > 1 && a.B <= kSortMax;
   if (by_length && !skipped)
     seqs.make(a, reinterpret_cast<int *>(sm), [](int len) { return ceil_div(len, kTile); });
   // index w: share w % splits of the query heads of key head (w / splits) % Hkv;
@@ -598,12 +602,10 @@ attn_dkv_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wai
     // -------------------------------------------------------- tile loads
     int it = 0, nkv = 0;
     bool ok = true, half_step = false;
-    ItemSource<decltype(find)> source(ring, wait, find, skipped ? -1 : (int)blockIdx.x, lane);
-    while (ok && (ok = source.next(words)) && words[0] >= 0) {
+    while (ok && next_item<true>(ring, wait, item_no, lane, words)) {
       const SeqTile x{words[0], words[1], words[2]};
       [[maybe_unused]] const int hk = words[3], g0 = words[5], heads = words[6];
       const int nt = count(x), f = first_tile(x);
-      if (nt * heads <= kShortItem) source.ask();
       ok = wait.all(kv_empty, (nkv & 1) ^ 1);
       if (!ok) break;
       if (elect_one()) {
@@ -631,7 +633,6 @@ attn_dkv_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wai
           __syncwarp();
         }
     }
-    source.close();
     // every load has landed before the CTA may leave
     if (nkv) mbar_wait_bounded(kv_full, (nkv - 1) & 1, wait_limit, status);
     for (int i = max(it - kQ, 0); i < it; ++i)
@@ -644,7 +645,7 @@ attn_dkv_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wai
     const int nk = (a.D + 15) / 16, no = nk * 16;
     int it = 0, nkv = 0;
     bool ok = true;
-    while (ok && next_item(ring, wait, item_no, lane, words)) {
+    while (ok && next_item<false>(ring, wait, item_no, lane, words)) {
       const SeqTile x{words[0], words[1], words[2]};
       [[maybe_unused]] const int hk = words[3], g0 = words[5], heads = words[6];
       const int n = count(x) * heads;
@@ -715,7 +716,7 @@ attn_dkv_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wai
     // ---------------------------- lse, delta, and the tails of the Q, dO tiles
     int it = 0;
     bool ok = true;
-    while (ok && next_item(ring, wait, item_no, lane, words)) {
+    while (ok && next_item<false>(ring, wait, item_no, lane, words)) {
       const SeqTile x{words[0], words[1], words[2]};
       [[maybe_unused]] const int hk = words[3], g0 = words[5], heads = words[6];
       const int nt = count(x), f = first_tile(x);
@@ -763,7 +764,7 @@ attn_dkv_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wai
     const float s2 = a.scale * kLog2E;
     int it = 0, nkv = 0;
     bool ok = true;
-    while (ok && next_item(ring, wait, item_no, lane, words)) {
+    while (ok && next_item<false>(ring, wait, item_no, lane, words)) {
       const SeqTile x{words[0], words[1], words[2]};
       [[maybe_unused]] const int hk = words[3], g0 = words[5], heads = words[6];
       const int nt = count(x), f = first_tile(x);
@@ -879,6 +880,13 @@ attn_dkv_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wai
       }
       __syncwarp();
     }
+  } else {
+    // -------------------------------------------------------- items
+    ItemSource<decltype(find)> source(ring, wait, find, skipped ? -1 : (int)blockIdx.x, lane);
+    bool ok = true;
+    do {
+      ok = source.publish(words);
+    } while (ok && words[0] >= 0);
   }
   tc_fence_before();
   __syncthreads();
@@ -896,7 +904,8 @@ __global__ void __launch_bounds__(256) attn_dkv_sum(const AttnArgs a, const floa
   pdl_trigger();
   if (attn_skipped(a.skip)) return;
   const int64_t row = (int64_t)a.Hkv * a.D, packs = row / 8;
-  const int64_t t0 = min(max(__ldg(a.cu), 0), (int)a.T), t1 = min(max(__ldg(a.cu + a.B), 0), (int)a.T);
+  const int64_t t0 = min(max(__ldg(a.cu), 0), (int)a.T);
+  const int64_t t1 = min(max(__ldg(a.cu + a.B), 0), (int)a.T);
   const int64_t n = (t1 - t0) * packs * 2;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
     const int64_t u = i / packs, c = (i - u * packs) * 8;

@@ -15,16 +15,17 @@
 //               shared memory; O += P V with P read from tensor memory);
 //   warps 2-5   softmax of tile 0, one query row per thread (no shuffles),
 //   warps 6-9   and of tile 1;
-//   warp 10     zeroes the rows of a V tile that lie behind its sequence's end
-//               before the MMAs may read them.
+//   warp 10     finds the work items, and zeroes the rows of a V tile that lie
+//               behind its sequence's end before the MMAs may read them.
 // A key tile's 128 scores are taken as two halves of 64, each a step of the
 // running softmax of its own: the first half's P V runs while the second
 // half's exponentials are formed.  Within a half the exponentials do not wait
 // for the maximum: they are formed against the one that stands, the half's own
 // maximum beside them, and only if some row passes the standing one by more
 // than 2^kRaise are they formed again (after O and l were brought to the new
-// maximum).  Keeping a lower maximum changes nothing in exact arithmetic (o
-// and l carry the same factor) and keeps p <= 2^kRaise.  Rounding p to bf16
+// maximum): 350 against 374 us with the maximum first (one causal sequence of
+// 8,192 tokens, 32/8 x 128).  Keeping a lower maximum changes nothing in exact
+// arithmetic (o and l carry the same factor) and keeps p <= 2^kRaise.  Rounding p to bf16
 // (2^-8 relative at most, per term) is the price of the tensor cores' second
 // product.
 // Tensor memory: S0 S1 (128 columns each), O0 O1.  P, in bf16, replaces the
@@ -129,10 +130,13 @@ __device__ __forceinline__ int pair_base(int c, int b, int G) {
   return ((max(c, 0) / kTile + b) * G + 1) / 2 + b;
 }
 
-__device__ __forceinline__ int pairs_of(int len, int G) { return (ceil_div(len, kTile) * G + 1) / 2; }
+__device__ __forceinline__ int pairs_of(int len, int G) {
+  return (ceil_div(len, kTile) * G + 1) / 2;
+}
 
-// Item `item` in the order of its slots or by length.  Within a
-// sequence from the last pair back, whose rows see most keys.
+// Item `item`: key heads fastest, then the pairs in the order of their slots or
+// by the length of their sequence.  Within a sequence from the last pair back,
+// whose rows see most keys.
 __device__ __forceinline__ FwdItem fwd_item(const AttnArgs &a, int nslots, int item,
                                             const SeqOrder &seqs, bool by_length) {
   FwdItem w;
@@ -162,7 +166,7 @@ __device__ __forceinline__ FwdItem fwd_item(const AttnArgs &a, int nslots, int i
   w.len = c1 - c0;
   const int nt = ceil_div(w.len, kTile);
   const int64_t f0 = 2 * (by_length ? (int64_t)pairs_of(w.len, G) - 1 - pair
-                               : (int64_t)pair - pair_base(c0, b, G));
+                                    : (int64_t)pair - pair_base(c0, b, G));
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     const int64_t f = f0 + t;
@@ -183,7 +187,7 @@ template <int DP> struct FwdLayout {
   static constexpr uint32_t off_bar = off_stage + 8 * 4096;
   static constexpr uint32_t off_items = (off_bar + (3 * kStages + 20) * 8 + 16 + 15) / 16 * 16;
   static constexpr uint32_t off_order = off_items + ItemRing::kBytes;
-  static constexpr uint32_t smem = off_order + SeqOrder::kBytes;
+  static constexpr uint32_t smem = off_order + SeqOrder::kBytes + 1024;
   static_assert(smem <= 227 * 1024, "shared memory per CTA");
 };
 
@@ -193,8 +197,8 @@ attn_fwd_tc(const __grid_constant__ FwdParams p, unsigned *status, long long wai
   using L = FwdLayout<DP>;
   constexpr int kStages = L::kStages;
   constexpr bool kApart = DP <= 64;  // P beside S in tensor memory, not over it
-  extern __shared__ __align__(1024) unsigned char smem_aligned[];
-  unsigned char *sm = smem_aligned;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char *sm = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
   const uint32_t sbase = smem_addr(sm);
   uint64_t *kv_full = reinterpret_cast<uint64_t *>(sm + L::off_bar);
   uint64_t *kv_empty = kv_full + kStages;
@@ -232,7 +236,7 @@ attn_fwd_tc(const __grid_constant__ FwdParams p, unsigned *status, long long wai
       mbar_init(&s_read[t], 4);
       mbar_init(&drain[t], 1);
     }
-    ring.init(11);  // MMAs of both tiles, eight softmax warps, tails
+    ring.init(11);  // loads, MMAs of both tiles, eight softmax warps
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -248,7 +252,7 @@ attn_fwd_tc(const __grid_constant__ FwdParams p, unsigned *status, long long wai
   const bool skipped = attn_skipped(a.skip);
   int item_no = 0, words[kItemWords];
   SeqOrder seqs(sm + L::off_order);
-  const bool by_length = a.B <= kSortMax;
+  const bool by_length = a.B > 1 && a.B <= kSortMax;
   if (by_length && !skipped)
     seqs.make(a, reinterpret_cast<int *>(sm), [&](int len) { return pairs_of(len, a.Hq / a.Hkv); });
 
@@ -265,16 +269,9 @@ attn_fwd_tc(const __grid_constant__ FwdParams p, unsigned *status, long long wai
       __syncwarp();
       ++it;
     };
-    auto find = [&](int index, int (&v)[kItemWords]) {
-      const FwdItem y = fwd_item(a, p.nslots, index, seqs, by_length);
-      y.to(v);
-      return y.tiles() > 0;
-    };
-    ItemSource<decltype(find)> source(ring, wait, find, skipped ? -1 : (int)blockIdx.x, lane);
-    while (ok && (ok = source.next(words)) && words[0] >= 0) {
+    while (ok && next_item<true>(ring, wait, item_no, lane, words)) {
       const FwdItem x(words);
       const int n = x.tiles();
-      if (n <= kShortItem) source.ask();
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         if (!ok || x.n[t] == 0) continue;
@@ -290,7 +287,6 @@ attn_fwd_tc(const __grid_constant__ FwdParams p, unsigned *status, long long wai
         if (ok) load_kv(&p.tv, x.hk, x.start + i * kTile);
       }
     }
-    source.close();
     // every load has landed before the CTA may leave
 #pragma unroll
     for (int t = 0; t < 2; ++t)
@@ -306,7 +302,7 @@ attn_fwd_tc(const __grid_constant__ FwdParams p, unsigned *status, long long wai
     int it = 0, nq = 0, ns = 0;  // ring entries, items, score tiles so far
     int np0 = 0, np1 = 0;        // first and second halves so far
     bool ok = true;
-    while (ok && next_item(ring, wait, item_no, lane, words)) {
+    while (ok && next_item<false>(ring, wait, item_no, lane, words)) {
       const FwdItem x(words);
       const int n = x.tiles(), mine = t ? x.n[1] : x.n[0];
       if (n == 0) continue;
@@ -397,10 +393,16 @@ attn_fwd_tc(const __grid_constant__ FwdParams p, unsigned *status, long long wai
       mbar_wait_bounded(&drain[t], 0, wait_limit, status);
     }
   } else if (warp == 10) {
-    // -------------------------------------------------------- V tiles' tails
+    // -------------------------------------------------------- items, V tiles' tails
+    auto find = [&](int index, int (&v)[kItemWords]) {
+      const FwdItem x = fwd_item(a, p.nslots, index, seqs, by_length);
+      x.to(v);
+      return x.tiles() > 0;
+    };
+    ItemSource<decltype(find)> source(ring, wait, find, skipped ? -1 : (int)blockIdx.x, lane);
     int it = 0;
-    bool ok = true;
-    while (ok && next_item(ring, wait, item_no, lane, words)) {
+    bool ok = source.publish(words);
+    while (ok && words[0] >= 0) {
       const FwdItem x(words);
       const int n = x.tiles();
       for (int i = 0; ok && i < 2 * n; ++i, ++it) {  // K0 V0 K1 V1 ..., as loaded
@@ -416,6 +418,7 @@ attn_fwd_tc(const __grid_constant__ FwdParams p, unsigned *status, long long wai
         }
         __syncwarp();
       }
+      if (ok) ok = source.publish(words);
     }
   } else if (warp < 10) {
     // -------------------------------------------------------- softmax
@@ -427,7 +430,7 @@ attn_fwd_tc(const __grid_constant__ FwdParams p, unsigned *status, long long wai
     const float2 sc = make_float2(s2, s2);
     int ns = 0, np0 = 0, np1 = 0;  // score tiles, first and second halves so far
     bool ok = true;
-    while (ok && next_item(ring, wait, item_no, lane, words)) {
+    while (ok && next_item<false>(ring, wait, item_no, lane, words)) {
       const FwdItem x(words);
       // selected, not indexed: an index would put the item into local memory,
       // and beside this much shared memory L1 holds next to nothing of it
@@ -600,7 +603,8 @@ attn_fwd_tc(const __grid_constant__ FwdParams p, unsigned *status, long long wai
         uint32_t pk[32];
 #pragma unroll
         for (int c = 0; c < 32; ++c)
-          pk[c] = pack_bf16(__uint_as_float(v[j][2 * c]) * inv, __uint_as_float(v[j][2 * c + 1]) * inv);
+          pk[c] = pack_bf16(__uint_as_float(v[j][2 * c]) * inv,
+                            __uint_as_float(v[j][2 * c + 1]) * inv);
         store_rows64(sm + L::off_stage + (warp - 2) * 4096, pk, o + 64 * j, a.ld_o,
                      x.len - row0 - quarter * 32, a.D - 64 * j, lane);
       }

@@ -149,13 +149,7 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
-// 8, 16 or 32 columns of this thread's lane from registers.
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
-      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-      : "memory");
-}
+// 16 or 32 columns of this thread's lane from registers.
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
@@ -187,44 +181,6 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
         "=r"(v[14]), "=r"(v[15])
       : "r"(taddr)
       : "memory");
-}
-// tmem_ld64 in two steps: the load, and the wait that makes the values usable
-// (the values pass through it, so no use can be placed before it).
-__device__ __forceinline__ void tmem_ld64_start(uint32_t taddr, uint32_t (&v)[64]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-      "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
-      "%28, %29, %30, %31, %32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, "
-      "%45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, "
-      "%62, %63}, [%64];"
-      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
-        "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
-        "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]),
-        "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]),
-        "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31]), "=r"(v[32]), "=r"(v[33]), "=r"(v[34]),
-        "=r"(v[35]), "=r"(v[36]), "=r"(v[37]), "=r"(v[38]), "=r"(v[39]), "=r"(v[40]), "=r"(v[41]),
-        "=r"(v[42]), "=r"(v[43]), "=r"(v[44]), "=r"(v[45]), "=r"(v[46]), "=r"(v[47]), "=r"(v[48]),
-        "=r"(v[49]), "=r"(v[50]), "=r"(v[51]), "=r"(v[52]), "=r"(v[53]), "=r"(v[54]), "=r"(v[55]),
-        "=r"(v[56]), "=r"(v[57]), "=r"(v[58]), "=r"(v[59]), "=r"(v[60]), "=r"(v[61]), "=r"(v[62]),
-        "=r"(v[63])
-      : "r"(taddr)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_ld64_finish(uint32_t (&v)[64]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]),
-                 "+r"(v[6]), "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]),
-                 "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]), "+r"(v[16]), "+r"(v[17]),
-                 "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]),
-                 "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]),
-                 "+r"(v[30]), "+r"(v[31]), "+r"(v[32]), "+r"(v[33]), "+r"(v[34]), "+r"(v[35]),
-                 "+r"(v[36]), "+r"(v[37]), "+r"(v[38]), "+r"(v[39]), "+r"(v[40]), "+r"(v[41]),
-                 "+r"(v[42]), "+r"(v[43]), "+r"(v[44]), "+r"(v[45]), "+r"(v[46]), "+r"(v[47]),
-                 "+r"(v[48]), "+r"(v[49]), "+r"(v[50]), "+r"(v[51]), "+r"(v[52]), "+r"(v[53]),
-                 "+r"(v[54]), "+r"(v[55]), "+r"(v[56]), "+r"(v[57]), "+r"(v[58]), "+r"(v[59]),
-                 "+r"(v[60]), "+r"(v[61]), "+r"(v[62]), "+r"(v[63])
-               :
-               : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -294,23 +250,21 @@ struct Waits {
 // one and takes its index over).  So items of very different lengths even out
 // without a counter in memory that calls on two streams would share.
 //
-// The loading warp, which runs ahead of the others, asks for the next item,
+// One warp of the CTA asks for the next item when the loading warp has no
+// more to load for the current one (an item asked for earlier would be tied to
+// this CTA while others run dry: with a few long items per SM that cost 19%),
 // finds its sequence and tile once for all roles, and hands it over in a ring
-// of two slots; empty items are dropped there.  It asks when it has no more to
-// load for the current item: an item asked for earlier would be tied to this
-// CTA while others run dry (with a few long items per SM that cost 19%).  Only
-// when the current item is short (kShortItem tiles) does it ask before, since
-// the answer takes about as long as such an item.
+// of two slots; empty items are dropped there.
 constexpr int kItemWords = 12;
-constexpr int kShortItem = 4;
 
 struct ItemRing {
+  uint64_t *want;   // the loading warp is done with the last item
   uint64_t *asked;  // the answer has arrived (16 bytes)
   uint64_t *full;   // [2]
   uint64_t *empty;  // [2]
   int *slots;       // [2][kItemWords]
   uint4 *answer;
-  static constexpr uint32_t kBytes = 16 + 2 * kItemWords * 4 + 5 * 8 + 8;  // from a multiple of 16
+  static constexpr uint32_t kBytes = 16 + 2 * kItemWords * 4 + 6 * 8;  // from a multiple of 16
 
   __device__ __forceinline__ explicit ItemRing(unsigned char *at) {
     answer = reinterpret_cast<uint4 *>(at);
@@ -318,9 +272,11 @@ struct ItemRing {
     asked = reinterpret_cast<uint64_t *>(at + 16 + 2 * kItemWords * 4);
     full = asked + 1;
     empty = full + 2;
+    want = empty + 2;
   }
   __device__ __forceinline__ void init(int readers) const {  // one thread
     mbar_init(asked, 1);
+    mbar_init(want, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], readers);
@@ -353,7 +309,7 @@ struct ItemRing {
   }
 };
 
-// The loading warp's side.  find(index, words) fills in an item and says whether
+// The asking warp's side.  find(index, words) fills in an item and says whether
 // it holds work; words[0] < 0 marks the end.
 template <class Find> struct ItemSource {
   const ItemRing &ring;
@@ -361,33 +317,31 @@ template <class Find> struct ItemSource {
   Find find;
   int lane;
   int index, count = 0, asks = 0;  // index: the CTA's own, -1 after the end
-  bool pending = false;
   __device__ __forceinline__ ItemSource(const ItemRing &r, const Waits &w, Find f, int first,
                                         int l)
       : ring(r), wait(w), find(f), lane(l), index(first) {}
-  __device__ __forceinline__ void ask() {
-    if (pending || index < 0) return;
-    if (elect_one()) ring.ask();
-    __syncwarp();
-    pending = true;
-  }
-  // The next item (or the end) into words, in every lane, and into its slot;
-  // false when a wait gave up.
-  __device__ __forceinline__ bool next(int (&words)[kItemWords]) {
-    bool work = count == 0 && index >= 0 && find(index, words);
+  // Publishes the next item (or the end) into its slot; false when a wait gave
+  // up.  words: the item, in every lane.
+  __device__ __forceinline__ bool publish(int (&words)[kItemWords]) {
+    bool work = false;
+    if (count == 0) {
+      work = index >= 0 && find(index, words);
+    } else if (!wait.all(ring.want, (count - 1) & 1)) {
+      return false;
+    }
     while (index >= 0 && !work) {
-      ask();
-      const bool came = wait.all(ring.asked, asks & 1);
-      if (!came) return false;
+      if (elect_one()) ring.ask();
+      __syncwarp();
+      if (!wait.all(ring.asked, asks & 1)) {  // the answer still comes: not after the CTA left
+        mbar_wait_bounded(ring.asked, asks & 1, wait.limit, wait.status);
+        return false;
+      }
       ++asks;
-      pending = false;
       index = uniform(ring.answered());
       __syncwarp();
       if (index >= 0) work = find(index, words);
     }
     if (!work) words[0] = -1;
-#pragma unroll
-    for (int i = 0; i < kItemWords; ++i) words[i] = uniform(words[i]);
     const int s = count & 1;
     if (!wait.all(&ring.empty[s], ((count >> 1) & 1) ^ 1)) return false;
     if (lane == 0) {
@@ -399,20 +353,21 @@ template <class Find> struct ItemSource {
     ++count;
     return true;
   }
-  // no answer may arrive after the CTA has left
-  __device__ __forceinline__ void close() const {
-    if (pending) mbar_wait_bounded(ring.asked, asks & 1, wait.limit, wait.status);
-  }
 };
 
 // The reading side (a whole warp): item number `count`; false at the end or when
-// a wait gave up.
+// a wait gave up.  LOADS: this is the loading warp, whose request starts the
+// search for every item but the first.
+template <bool LOADS>
 __device__ __forceinline__ bool next_item(const ItemRing &ring, const Waits &wait, int &count,
                                           int lane, int (&words)[kItemWords]) {
   const int s = count & 1;
+  if (LOADS && count > 0 && lane == 0) mbar_arrive(ring.want);
   if (!wait.all(&ring.full[s], (count >> 1) & 1)) return false;
 #pragma unroll
-  for (int i = 0; i < kItemWords; ++i) words[i] = uniform(ring.slots[s * kItemWords + i]);
+  for (int i = 0; i < kItemWords; ++i) {
+    words[i] = uniform(ring.slots[s * kItemWords + i]);
+  }
   __syncwarp();
   if (lane == 0) mbar_arrive(&ring.empty[s]);
   ++count;
@@ -445,11 +400,13 @@ __device__ __forceinline__ void store_rows64(unsigned char *stage, const uint32_
   __syncwarp();
 }
 
-// Sequences by length, the longest first, for batches of up to kSortMax: with
-// items handed out in this order the long ones do not come last (16,384 packed
-// tokens in 85 sequences of 16 to 2,048: the tail of one long item is a third
-// of the call).  Larger batches keep the order of the slots, which needs no
-// table.  Every CTA makes the same table, from one look at cu.
+// Sequences by length, the longest first, for batches of 2 to kSortMax: with
+// items handed out in this order the long ones do not come last.  Measured
+// against the order of the slots: forward 32,768 tokens of 16 to 8,192 x 32/8 x
+// 128 1,070 against 1,108 us, 16,384 tokens of 16 to 2,048 x 14/2 x 64 50 against
+// 53, backward of the latter 165 against 171.  Larger batches keep the order of
+// the slots, which needs no table.  Every CTA makes the same table, from one
+// look at cu.
 constexpr int kSortMax = 128;
 
 struct SeqOrder {
