@@ -4,7 +4,10 @@ rule for building optimizer parameter groups.
 Each Function runs the library's forward kernel, saves what the backward
 kernel needs, and calls the backward kernel: argument marshalling only, no
 arithmetic of its own (weight gradients, which the kernels produce in fp32,
-are cast to the weight's dtype as autograd requires).
+are cast to the weight's dtype as autograd requires).  A step may be captured
+into a CUDA graph, gradients included (torch.autograd.grad, or backward with no
+earlier eager graph of the same leaves alive: torch ties a leaf's accumulation
+to the stream that first used it, and a capture may not wait for another).
 
 LoRA+ ("Chronicals", arXiv 2601.02609, abstract, optimisation (3)): the
 adapter matrix B of every LoRA pair learns at 16 times the rate of A.
@@ -131,13 +134,20 @@ class QKMrope(torch.autograd.Function):
         return dq, dk, None, None, None, None
 
 
+def _zeros(x):
+    return torch.zeros(x.shape, dtype=x.dtype, device=x.device)
+
+
 class Attention(torch.autograd.Function):
-    """Attention inside every sequence of a packed batch (ftk.attn_fwd).  Every
-    token must belong to a sequence (cu_seqlens from 0 to T)."""
+    """Attention inside every sequence of a packed batch (ftk.attn_fwd).  Tokens
+    of no sequence (a batch padded past cu_seqlens[B]) get a zero output and
+    zero gradients: where the sequences end is known on the device alone, so
+    every result starts as zeros (4% of the forward pass of 32,768 mixed tokens
+    with 32/8 bf16 heads of 128; ftk.attn_fwd itself leaves such rows alone)."""
 
     @staticmethod
     def forward(ctx, q, k, v, cu_seqlens, scale=None, causal: bool = True):
-        o, lse = ftk.attn_fwd(q, k, v, cu_seqlens, scale=scale, causal=causal)
+        o, lse = ftk.attn_fwd(q, k, v, cu_seqlens, scale=scale, causal=causal, o=_zeros(q))
         ctx.save_for_backward(q, k, v, o, lse, cu_seqlens)
         ctx.scale, ctx.causal = scale, causal
         return o
@@ -146,7 +156,7 @@ class Attention(torch.autograd.Function):
     def backward(ctx, do):
         q, k, v, o, lse, cu = ctx.saved_tensors
         dq, dk, dv = ftk.attn_bwd(do.contiguous(), q, k, v, o, lse, cu, scale=ctx.scale,
-                                  causal=ctx.causal)
+                                  causal=ctx.causal, dq=_zeros(q), dk=_zeros(k), dv=_zeros(v))
         return dq, dk, dv, None, None, None
 
 

@@ -505,7 +505,9 @@ FTK_API size_t ftk_attn_bwd_workspace_bytes(int64_t T, int32_t Hq, int32_t Hkv, 
  * are left as they were.  workspace: >= ftk_attn_bwd_workspace_bytes(...)
  * bytes, 16-byte aligned, contents ignored and clobbered; calls that overlap
  * on the GPU need one each.  Every sum has a fixed order (no atomics): the
- * gradients are bitwise reproducible run to run.  Other rules as above. */
+ * gradients are bitwise reproducible run to run (the order depends on T, B,
+ * Hq, Hkv and D, so the same sequence in another batch may differ in the last
+ * bits of dk and dv).  Other rules as above. */
 FTK_API ftk_status ftk_attn_bwd(const void *do_, int64_t ld_do, const void *q, int64_t ld_q,
                                 const void *k, int64_t ld_k, const void *v, int64_t ld_v,
                                 const void *o, int64_t ld_o, const float *lse, void *dq,

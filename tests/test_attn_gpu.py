@@ -434,3 +434,76 @@ def test_autograd_equals_the_direct_calls():
         o, lse = ftk.attn_fwd(q0, k0, v0, cu, scale=0.2, causal=causal)
         for a, b in zip(leaves, ftk.attn_bwd(do, q0, k0, v0, o, lse, cu, scale=0.2, causal=causal)):
             assert torch.equal(a.grad, b)
+
+
+def test_autograd_on_a_padded_batch():
+    """Rows of no sequence: whatever stands there, zero output and gradients."""
+    q0, k0, v0, cu = inputs((60, 70), 4, 2, 64, torch.bfloat16, lead=3, tail=50)
+    pad = torch.ones(183, dtype=torch.bool, device=DEV)
+    pad[3:133] = False
+    do = rnd(q0.shape, 6, q0.dtype)
+    for t in (q0, k0, v0, do):
+        t[pad] = math.nan
+    leaves = [t.clone().requires_grad_(True) for t in (q0, k0, v0)]
+    o = autograd.attention(*leaves, cu)
+    o.backward(do)
+    assert bool((o[pad] == 0).all())
+    one = [t[3:133].clone().requires_grad_(True) for t in (q0, k0, v0)]
+    p = autograd.attention(*one, cu - 3)
+    p.backward(do[3:133])
+    assert torch.equal(o[3:133], p)
+    for a, b in zip(leaves, one):
+        assert bool((a.grad[pad] == 0).all())
+        assert torch.equal(a.grad[3:133], b.grad)
+
+
+def test_autograd_captured_with_its_gradients():
+    q0, k0, v0, cu = inputs((60, 70), 4, 2, 64, torch.bfloat16)
+    pos, axis = positions(130, 5), ftk.mrope_axis_of((8, 12, 12))
+    do = rnd(q0.shape, 6, q0.dtype)
+    leaves = [t.clone().requires_grad_(True) for t in (q0, k0, v0)]
+
+    def step():
+        q, k = autograd.qk_mrope(leaves[0], leaves[1], pos, axis, 1e6)
+        o = autograd.attention(q, k, leaves[2], cu)
+        return (o.detach(), *torch.autograd.grad(o, leaves, do))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for seed in (11, 12):
+        with torch.no_grad():
+            for i, t in enumerate(leaves):
+                t.copy_(rnd(t.shape, seed + 10 * i, t.dtype))
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, step()):
+            assert torch.equal(a, b)
+
+
+# ------------------------------------------------------------------ rules by size
+
+@pytest.mark.parametrize("Hq,Hkv,D,lens", [
+    # 32 key tiles or more of 16 key heads: a group's heads stay in one CTA
+    (32, 16, 64, (1500, 700, 232, 100)), (32, 16, 128, (1500, 700, 232, 100)),
+    # some 50 tiles of 2 key heads: seven heads dealt to four CTAs, unevenly
+    (14, 2, 64, (900, 1, 700) * 4), (14, 2, 128, (900, 1, 700) * 4)])
+def test_shared_heads_by_the_number_of_key_tiles(Hq, Hkv, D, lens):
+    check(*inputs(lens, Hq, Hkv, D, torch.bfloat16, fused=True), True)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("B", [2, 127, 128, 129])
+def test_batches_around_the_length_order(B, D):
+    """Up to 128 sequences are taken by length, more by position; empty ones,
+    equal ones and a long one among them."""
+    lens = np.random.default_rng(B).integers(0, 40, B)
+    lens[B // 2] = 600
+    lens[-1] = 0 if B > 2 else 17
+    check(*inputs(tuple(int(n) for n in lens), 4, 2, D, torch.bfloat16, lead=5, tail=9), True)
