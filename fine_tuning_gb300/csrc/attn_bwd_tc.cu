@@ -19,9 +19,15 @@
 // memory in bf16, over the fp32 values they came from (each half within its own
 // 64 columns, so the halves need no barrier between them), and enter the next
 // product from there.  The MMAs are queued so that the tensor pipe always has
-// the next tile's scores to work on while p and ds are formed: both kernels
-// are bound by the MMAs of their tile pairs (dq: 3, dk/dv: 4, 512 cycles each
-// for 128 x 128 x 128).
+// the next tile's scores to work on while p and ds are formed: with heads of
+// 128 both kernels are bound by the MMAs of their tile pairs (dq: 3, dk/dv: 4,
+// 512 cycles each for 128 x 128 x 128; the pipe is busy 69 and 79% of the time),
+// with heads of 64 by the exponentials and conversions of the 8 warps (44 and
+// 47%).  Measured, one causal sequence of 8,192 tokens, 32/8 heads: 517 us (dq)
+// and 634 (dk, dv) with heads of 128, 402 and 527 with heads of 64; 16,384 tokens,
+// 32/8 x 128, everything: 4.8 ms.  16 warps on the scores instead of 8: 4% slower;
+// the two halves of a tile on barriers and 64-column products of their own, so
+// that one half's exponentials run under the other's gradients: 25% slower (64).
 #include <cmath>
 
 #include "attn_tc.cuh"
@@ -45,15 +51,19 @@ struct BwdParams {
 
 // How many CTAs share the query heads of a key tile.  dk and dv of a key head
 // are summed over its group's heads, so a call has T / 128 x Hkv of these sums,
-// and one of a long sequence's first tiles passes over all its queries, G
-// times.  Where that leaves fewer than two sums per SM (152), the heads are
-// dealt out to more CTAs, whose fp32 sums (8 bytes per element and share in the
-// workspace) a small kernel adds in order.  16,384 packed tokens x 14/2 x 64:
-// 256 sums, the longest of them 112 steps; two shares.
+// and the one of a long sequence's first tile passes over all its queries, G
+// times: 304 / sums as long as an SM's part of the work (152 SMs, half of the
+// tiles masked) if the batch is one sequence.  So many CTAs are given its heads,
+// and their fp32 sums (8 bytes per element and share in the workspace) are added
+// in order by a small kernel.  Fractions round up by G / 8: the more heads, the
+// longer the sum against the fixed cost of a share.  Measured, one CTA per sum
+// against this rule, us: one sequence of 8,192, 8/1 x 128: 801, 336; of 2,048,
+// 32/8 x 128: 149, 125 (141 always rounded up); 16,384 tokens in 85 sequences,
+// 14/2 x 64: 174, 165; 4,096 in 4, 32/8 x 128: 296, 296 (313 rounded up).
 int attn_bwd_splits(int64_t T, int32_t Hq, int32_t Hkv) {
   const int64_t G = Hq / Hkv, sums = ceil_div(T, (int64_t)kTile) * Hkv, want = 2 * 152;
   if (sums >= want) return 1;
-  const int64_t n = ceil_div(want, sums);
+  const int64_t n = (8 * want + sums * G) / (8 * sums);
   return (int)(n < G ? n : G);
 }
 
@@ -107,7 +117,7 @@ __device__ __forceinline__ SeqTile tile_of(const AttnArgs &a, int slots, int u, 
 
 // delta[h, t] = sum_d do[t, h, d] o[t, h, d]: 16 lanes per row, one 16-byte
 // packet each; a warp walks pairs of consecutive tokens of one head, so delta
-// is written in runs.  Bound by HBM (do and o read once).
+// is written in runs.  Bound by HBM (do and o read once): 23 us for 134 MB.
 constexpr int kDeltaTokens = 64;  // per CTA of 8 warps
 __global__ void __launch_bounds__(256) attn_delta_packed(const AttnArgs a) {
   pdl_wait();
@@ -897,7 +907,8 @@ attn_dkv_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wai
 }
 
 // Adds the shares of dk and dv in order, scales dk and rounds: eight columns of
-// one row per thread.  Rows of no sequence have no sums and are left alone.
+// one row per thread, bound by L2, where the sums still are.  Rows of no
+// sequence have no sums and are left alone.
 __global__ void __launch_bounds__(256) attn_dkv_sum(const AttnArgs a, const float *part,
                                                     int shares) {
   pdl_wait();

@@ -18,6 +18,9 @@
 // 8 lanes' reads fall into different banks), so that the multiply-adds, not
 // the shared-memory reads, are the bound: 12 (20) wavefronts of LDS for 64
 // (128) warp instructions of FFMA in the two products of a 64 x 64 tile.
+// Measured, one causal fp32 sequence of 4,096 tokens, 32/8 heads of 128: 5.5 ms
+// (25 TFLOP/s over the unmasked scores) forward, 17.2 ms (20, and 28 with the
+// scores and do v^T that dq and dk/dv each make) backward.
 #include <cmath>
 
 #include "attn_common.cuh"
@@ -398,7 +401,10 @@ template <typename T, int BT, int DMAX> struct Generic {
 
 // 64-row tiles while four of them fit beside the score tiles (D <= 128), 32-row
 // tiles for the larger heads, and for calls whose 64-row tiles would leave SMs
-// without one.
+// without one.  Measured, fp32, 4/2 heads of 64, one sequence, 64 rows against 32,
+// us: 300 tokens 44, 40 forward and 132, 117 backward; 1,200 tokens 144, 135 and
+// 484, 456; 2,400 tokens 281, 310 and 961, 1,014; 4,096 tokens, 32/8 x 128: 5,460,
+// 5,920 and 17,230, 21,280.
 bool small_tiles(const AttnArgs &a, const DeviceInfo &dev) {
   return a.D > 128 || (a.T / 64 + a.B) * a.Hq < dev.sms;
 }
