@@ -19,6 +19,7 @@ from __future__ import annotations
 from typing import Iterable, List, Optional, Tuple
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import ftk
 
@@ -127,6 +128,7 @@ class QKMrope(torch.autograd.Function):
         return ftk.qk_mrope_fwd(q, k, pos, axis_of, theta=theta, inv_freq=inv_freq)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dq, dk):
         (pos,) = ctx.saved_tensors
         dq, dk = ftk.qk_mrope_bwd(dq.contiguous(), dk.contiguous(), pos, ctx.axis_of,
@@ -153,6 +155,7 @@ class Attention(torch.autograd.Function):
         return o
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, do):
         q, k, v, o, lse, cu = ctx.saved_tensors
         dq, dk, dv = ftk.attn_bwd(do.contiguous(), q, k, v, o, lse, cu, scale=ctx.scale,

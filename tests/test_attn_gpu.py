@@ -487,6 +487,25 @@ def test_autograd_captured_with_its_gradients():
             assert torch.equal(a, b)
 
 
+def test_second_derivatives_are_refused():
+    q, k, v, cu = inputs((20, 30), 4, 2, 64, torch.bfloat16)
+    pos, axis = positions(50, 5), ftk.mrope_axis_of((8, 12, 12))
+    q, k = q.requires_grad_(True), k.requires_grad_(True)
+    for out in (autograd.attention(q, k, v, cu), autograd.qk_mrope(q, k, pos, axis, 1e6)[0]):
+        (g,) = torch.autograd.grad(out.float().square().sum(), q, create_graph=True)
+        with pytest.raises(RuntimeError):
+            torch.autograd.grad(g.float().sum(), q)
+
+
+def test_expanded_heads_and_tokens_are_refused():
+    """Broadcast views have no row per token and head to read."""
+    q, k, v, cu = inputs((20, 30), 4, 2, 64, torch.bfloat16)
+    with pytest.raises(ValueError):
+        ftk.attn_fwd(q, k[:, :1].expand(50, 2, 64), v, cu)
+    with pytest.raises((ValueError, ftk.FtkError)):
+        ftk.attn_fwd(q, k[:1].expand(50, 2, 64), v, cu)
+
+
 # ------------------------------------------------------------------ rules by size
 
 @pytest.mark.parametrize("Hq,Hkv,D,lens", [
