@@ -19,6 +19,7 @@ from .build import LIB as _LIB_PATH
 
 F32, BF16 = 0, 1
 _DTYPES = {torch.float32: F32, torch.bfloat16: BF16}
+_INT32 = np.dtype(np.int32)
 
 STATUS = {0: "FTK_OK", 1: "FTK_ERR_NULL", 2: "FTK_ERR_SHAPE", 3: "FTK_ERR_ALIGN",
           4: "FTK_ERR_DTYPE", 5: "FTK_ERR_WORKSPACE", 6: "FTK_ERR_CUDA", 7: "FTK_ERR_ALIAS"}
@@ -563,7 +564,7 @@ def _call_on(index: int, name: str, *args) -> None:
     """_call on device `index` (made the current one for the launch) and its
     current stream, as a raw handle: the Stream object that current_stream
     builds costs 2 us of a small call's host time."""
-    if index == torch.cuda.current_device():
+    if index == torch._C._cuda_getDevice():
         _call(name, *args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(index):
@@ -590,48 +591,59 @@ def mrope_axis_of(sections) -> np.ndarray:
     return np.repeat(np.arange(sec.size), sec).astype(np.int32)
 
 
+def _out(x: torch.Tensor, y: Optional[torch.Tensor], name: str) -> Tuple[torch.Tensor, int]:
+    """The output that goes with x [T, heads, D] (y, or a new contiguous one) and
+    its row stride."""
+    if y is None:
+        s = x.shape
+        return torch.empty_like(x, memory_format=torch.contiguous_format), s[1] * s[2]
+    if y.shape != x.shape or y.dtype != x.dtype:
+        raise ValueError(f"{name} must be {tuple(x.shape)} {x.dtype}")
+    return y, _head_rows(y, name)
+
+
 def _mrope(name, q, k, pos, axis_of, theta, inv_freq, q_out, k_out):
     ref = q if q is not None else k
     if ref is None:
         raise ValueError("q or k is needed")
     dev = _same_device(ref, q, k, pos, q_out, k_out)
-    given = q_out is not None or k_out is not None
-    if q is not None and q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    if k is not None and k_out is None:
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    if (q is None and q_out is not None) or (k is None and k_out is not None):
+        raise ValueError("q_out and k_out need q and k")
     ldq = ldk = ldqo = ldko = Hq = Hkv = 0
-    T, D = ref.shape[0], ref.shape[-1]
     if q is not None:
-        ldq, ldqo, Hq = _head_rows(q, "q"), _head_rows(q_out, "q_out"), q.shape[1]
+        ldq = _head_rows(q, "q")
+        T, Hq, D = q.shape
+        q_out, ldqo = _out(q, q_out, "q_out")
     if k is not None:
-        ldk, ldko, Hkv = _head_rows(k, "k"), _head_rows(k_out, "k_out"), k.shape[1]
-    if q is not None and k is not None and (k.shape[0] != T or k.shape[2] != D
-                                            or k.dtype != q.dtype):
-        raise ValueError("q and k must agree in tokens, head_dim and dtype")
-    if given:
-        for x, y in ((q, q_out), (k, k_out)):
-            if (x is None) != (y is None) or (x is not None and (y.shape != x.shape
-                                                                 or y.dtype != x.dtype)):
-                raise ValueError("q_out and k_out must match q and k in shape and dtype")
-    if pos.dtype != torch.int32 or pos.dim() != 2 or pos.shape[1] != T \
-            or (T > 1 and pos.stride(1) != 1):
+        ldk = _head_rows(k, "k")
+        Tk, Hkv, Dk = k.shape
+        if q is None:
+            T, D = Tk, Dk
+        elif Tk != T or Dk != D or k.dtype != q.dtype:
+            raise ValueError("q and k must agree in tokens, head_dim and dtype")
+        k_out, ldko = _out(k, k_out, "k_out")
+    if pos.dtype != torch.int32 or pos.dim() != 2:
         raise ValueError("pos must be int32 [axes, T] with unit stride along tokens")
-    axes = pos.shape[0]
-    ldp = max(pos.stride(0), T) if axes == 1 else pos.stride(0)
+    axes, Tp = pos.shape
+    ldp, step = pos.stride()
+    if Tp != T or (T > 1 and step != 1):
+        raise ValueError("pos must be int32 [axes, T] with unit stride along tokens")
+    if axes == 1:
+        ldp = max(ldp, T)
     table = axis_of if type(axis_of) is np.ndarray else np.asarray(axis_of)
-    if table.dtype != np.int32:
+    if table.dtype != _INT32:
         if table.shape and not np.issubdtype(table.dtype, np.integer):
             raise ValueError("axis_of must hold integers")
         if table.size and (int(table.min()) < 0 or int(table.max()) >= axes):
             raise ValueError("axis_of must hold axes of pos")  # before the cast could wrap
-    if table.dtype != np.int32 or not table.flags.c_contiguous:
         table = np.ascontiguousarray(table, dtype=np.int32)
+    elif not table.flags.c_contiguous:
+        table = np.ascontiguousarray(table)
     if table.shape != (D // 2,):
         raise ValueError("axis_of must hold D/2 axes")
     freq, freq_p = (None, None) if inv_freq is None else _table(inv_freq, D)
     _call_on(dev, name, _ptr(q), ldq, _ptr(k), ldk, _ptr(q_out), ldqo, _ptr(k_out), ldko,
-             _ptr(pos), ldp, axes, table.ctypes.data, T, Hq, Hkv, D,
+             pos.data_ptr(), ldp, axes, table.ctypes.data, T, Hq, Hkv, D,
              float(theta or 0.0), freq_p, _code(ref))
     del table, freq
     return q_out, k_out
@@ -667,16 +679,6 @@ def _attn_check(q, k, v, cu_seqlens, seqlens_status, *rest) -> int:
     return dev
 
 
-def _like(x: torch.Tensor, y: Optional[torch.Tensor], name: str) -> torch.Tensor:
-    if y is None:
-        if x.is_contiguous():  # then empty_like is contiguous too, and cheaper
-            return torch.empty_like(x)
-        return torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    if y.shape != x.shape or y.dtype != x.dtype:
-        raise ValueError(f"{name} must be {tuple(x.shape)} {x.dtype}")
-    return y
-
-
 def attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
              scale: Optional[float] = None, causal: bool = True,
              o: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
@@ -690,16 +692,15 @@ def attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torc
     ldq, ldk, ldv = _head_rows(q, "q"), _head_rows(k, "k"), _head_rows(v, "v")
     dev = _attn_check(q, k, v, cu_seqlens, seqlens_status, o, lse)
     T, Hq, D = q.shape
-    Hkv = k.shape[1]
-    o = _like(q, o, "o")
+    o, ldo = _out(q, o, "o")
     if lse is None:
         if save_lse:
             lse = torch.empty((Hq, T), dtype=torch.float32, device=q.device)
     elif lse.dtype != torch.float32 or lse.shape != (Hq, T) or not lse.is_contiguous():
         raise ValueError("lse must be a contiguous fp32 [Hq, T] tensor")
-    _call_on(dev, "ftk_attn_fwd", _ptr(q), ldq, _ptr(k), ldk, _ptr(v), ldv, _ptr(o),
-             _head_rows(o, "o"), _ptr(lse), _ptr(cu_seqlens), cu_seqlens.shape[0] - 1, T, Hq, Hkv, D,
-             float(D ** -0.5 if scale is None else scale), int(bool(causal)),
+    _call_on(dev, "ftk_attn_fwd", q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv,
+             o.data_ptr(), ldo, _ptr(lse), cu_seqlens.data_ptr(), cu_seqlens.shape[0] - 1, T, Hq,
+             k.shape[1], D, D ** -0.5 if scale is None else float(scale), 1 if causal else 0,
              _ptr(seqlens_status), _code(q))
     return o, lse
 
@@ -720,23 +721,22 @@ def attn_bwd(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor
     dq, dk, dv may be slices of one fused [T, Hq + 2 Hkv, D] buffer."""
     ldq, ldk, ldv = _head_rows(q, "q"), _head_rows(k, "k"), _head_rows(v, "v")
     dev = _attn_check(q, k, v, cu_seqlens, seqlens_status, do, o, lse, dq, dk, dv, workspace)
-    T, Hq, D = q.shape
+    T, Hq, D = qs = q.shape
     Hkv = k.shape[1]
-    for t, name in ((do, "do"), (o, "o")):
-        if t.shape != q.shape or t.dtype != q.dtype:
-            raise ValueError(f"{name} must match q in shape and dtype")
+    if do.shape != qs or o.shape != qs or do.dtype != q.dtype or o.dtype != q.dtype:
+        raise ValueError("do and o must match q in shape and dtype")
     if lse.dtype != torch.float32 or lse.shape != (Hq, T) or not lse.is_contiguous():
         raise ValueError("lse must be a contiguous fp32 [Hq, T] tensor")
-    dq, dk, dv = _like(q, dq, "dq"), _like(k, dk, "dk"), _like(v, dv, "dv")
+    (dq, lddq), (dk, lddk), (dv, lddv) = _out(q, dq, "dq"), _out(k, dk, "dk"), _out(v, dv, "dv")
     if workspace is None:
         workspace = torch.empty(max(16, attn_bwd_workspace_bytes(T, Hq, Hkv, D, q.dtype)),
                                 dtype=torch.uint8, device=q.device)
-    _call_on(dev, "ftk_attn_bwd", _ptr(do), _head_rows(do, "do"), _ptr(q), ldq, _ptr(k), ldk, _ptr(v),
-             ldv, _ptr(o), _head_rows(o, "o"), _ptr(lse), _ptr(dq), _head_rows(dq, "dq"), _ptr(dk),
-             _head_rows(dk, "dk"), _ptr(dv), _head_rows(dv, "dv"), _ptr(workspace),
-             workspace.numel() * workspace.element_size(), _ptr(cu_seqlens),
-             cu_seqlens.numel() - 1, T, Hq, Hkv, D,
-             float(D ** -0.5 if scale is None else scale), int(bool(causal)),
+    _call_on(dev, "ftk_attn_bwd", do.data_ptr(), _head_rows(do, "do"), q.data_ptr(), ldq,
+             k.data_ptr(), ldk, v.data_ptr(), ldv, o.data_ptr(), _head_rows(o, "o"),
+             lse.data_ptr(), dq.data_ptr(), lddq, dk.data_ptr(), lddk, dv.data_ptr(), lddv,
+             workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+             cu_seqlens.data_ptr(), cu_seqlens.shape[0] - 1, T, Hq, Hkv, D,
+             D ** -0.5 if scale is None else float(scale), 1 if causal else 0,
              _ptr(seqlens_status), _code(q))
     return dq, dk, dv
 
