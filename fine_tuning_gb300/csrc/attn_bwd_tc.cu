@@ -407,7 +407,8 @@ attn_dq_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wait
       const int64_t at = (int64_t)h * a.T + x.start + row;
       const float lse2 = in ? a.lse[at] * kLog2E : 0.f, delta = in ? a.delta[at] : 0.f;
       const int last = a.causal ? min(row, x.len - 1) : x.len - 1;
-      const int last_all = a.causal ? min(x.row0, x.len - 1) : x.len - 1;
+      // by every row of this warp
+      const int last_all = a.causal ? min(x.row0 + quarter * 32, x.len - 1) : x.len - 1;
       for (int i = 0; i < n; ++i, ++it) {
         const uint32_t ts = tmem + (it & 1) * 128 + 64 * half + lanes;
         ok = wait.all(&s_full[it & 1], (it >> 1) & 1);
@@ -425,7 +426,7 @@ attn_dq_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wait
             pr[c] = make_float2(ex2(v.x), ex2(v.y));
           }
         }
-        const bool masked = i * kTile + kTile - 1 > last_all;
+        const bool masked = i * kTile + 64 * half + 63 > last_all;
         ok = wait.all(dp_full, it & 1);
         if (!ok) break;
         tc_fence_after();
@@ -789,7 +790,7 @@ attn_dkv_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wai
         const float4 *delta = lse + kTile / 4;
         // columns lo .. hi - 1 of this half are queries that see this key
         const int lo = a.causal ? row - q0 : 0, hi = x.len - q0;
-        const bool masked = (a.causal && q0 < x.row0 + kTile) || hi < 64;
+        const bool masked = (a.causal && q0 < x.row0 + quarter * 32 + 31) || hi < 64;
         float2 pr[32];
         {
           uint32_t v[64];

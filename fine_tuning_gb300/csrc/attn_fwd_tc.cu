@@ -23,7 +23,7 @@
 // for the maximum: they are formed against the one that stands, the half's own
 // maximum beside them, and only if some row passes the standing one by more
 // than 2^kRaise are they formed again (after O and l were brought to the new
-// maximum): 350 against 374 us with the maximum first (one causal sequence of
+// maximum): 347 against 374 us with the maximum first (one causal sequence of
 // 8,192 tokens, 32/8 x 128).  Keeping a lower maximum changes nothing in exact
 // arithmetic (o and l carry the same factor) and keeps p <= 2^kRaise.  Rounding p to bf16
 // (2^-8 relative at most, per term) is the price of the tensor cores' second
@@ -33,10 +33,11 @@
 // and the next scores are formed while the current ones are still worked on.
 // Measured, one causal sequence of 32,768 tokens, 64/8 heads of 128: 11.5 ms, 1.53
 // PFLOP/s over the unmasked scores (0.89 of what a library GEMM sustains); of
-// 8,192, 32/8: 350 us with heads of 128 (tensor pipe busy 69% of the cycles, the
-// bound), 252 with heads of 64 (46%; the exponentials' unit 46%, issue 53%);
-// 16,384 tokens in 85 sequences, 14/2 x 64: 50 us, mostly the start and end of
-// items of one or two key tiles.
+// 8,192, 32/8: 347 us with heads of 128 (tensor pipe busy 69% of the cycles, the
+// bound), 237 with heads of 64 (46%; the exponentials' unit 46%, issue 53%);
+// 16,384 tokens in 85 sequences, 14/2 x 64: 48 us, mostly the start and end of
+// items of one or two key tiles.  Masks are looked at by each warp's own rows and
+// O leaves by tile stores: together 252 -> 237 and 50 -> 48 us of these.
 #include <cudaTypedefs.h>
 
 #include <cmath>
@@ -48,7 +49,7 @@ namespace ftk {
 namespace attn {
 
 cudaError_t make_head_map(CUtensorMap *map, const void *base, int64_t T, int64_t H, int64_t D,
-                          int64_t ld) {
+                          int64_t ld, uint32_t rows) {
   static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
   if (!encode) {
     void *fn = nullptr;
@@ -60,7 +61,7 @@ cudaError_t make_head_map(CUtensorMap *map, const void *base, int64_t T, int64_t
   }
   const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)T};
   const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)ld * 2};
-  const cuuint32_t box[3] = {64, 1, kTile};
+  const cuuint32_t box[3] = {64, 1, rows};
   const cuuint32_t elem[3] = {1, 1, 1};
   auto make = [&] {
     return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides,
@@ -90,7 +91,7 @@ constexpr int kFwdThreads = 384;
 constexpr float kRaise = 8.f;
 
 struct FwdParams {
-  CUtensorMap tq, tk, tv;
+  CUtensorMap tq, tk, tv, to;
   AttnArgs a;
   int nslots;  // pair slots per key head
 };
@@ -445,7 +446,9 @@ attn_fwd_tc(const __grid_constant__ FwdParams p, unsigned *status, long long wai
       if (n == 0) continue;
       const int row = row0 + quarter * 32 + lane;                   // within the sequence
       const int last = a.causal ? min(row, x.len - 1) : x.len - 1;  // the last key seen
-      const int last_all = a.causal ? min(row0, x.len - 1) : x.len - 1;  // by every row
+      // by every row of this warp, and by any
+      const int last_all = a.causal ? min(row0 + quarter * 32, x.len - 1) : x.len - 1;
+      const int last_any = a.causal ? row0 + quarter * 32 + 31 : x.len - 1;
       float m = -INFINITY, ms = 0.f;
       float2 l2 = make_float2(0.f, 0.f);
       for (int i = 0; ok && i < n; ++i, ++ns) {
@@ -453,6 +456,10 @@ attn_fwd_tc(const __grid_constant__ FwdParams p, unsigned *status, long long wai
         if (!ok) break;
         tc_fence_after();
         const int halves = halves_of(x, i);
+        // of a tile on the diagonal the first two warps see nothing of its second half
+        // (left out with heads of up to 64; with the steps of half a tile the branch
+        // costs more than it saves, 371 against 347 us)
+        [[maybe_unused]] const bool two = halves == 2 && i * kTile + 64 <= last_any;
         // 64 columns from column 64 h on, masked
         auto load = [&](int h, uint32_t (&s)[64]) {
           __syncwarp();
@@ -523,7 +530,7 @@ attn_fwd_tc(const __grid_constant__ FwdParams p, unsigned *status, long long wai
             ms = m == -INFINITY ? 0.f : m * s2;
           }
           float2 sum = probs(s, p0);
-          if (halves == 2) {
+          if (two) {
             load(1, s);
             top = fmaxf(top, highest(s));
           }
@@ -537,12 +544,17 @@ attn_fwd_tc(const __grid_constant__ FwdParams p, unsigned *status, long long wai
             }
             load(0, s);
             sum = probs(s, p0);
-            if (halves == 2) load(1, s);
+            if (two) load(1, s);
           }
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&s_read[t]);  // the next scores may replace these
-          if (halves == 2) sum = __fadd2_rn(sum, probs(s, p1));
+          if (two) {
+            sum = __fadd2_rn(sum, probs(s, p1));
+          } else {
+#pragma unroll
+            for (int c = 0; c < 32; ++c) p1[c] = 0u;
+          }
           l2 = __fadd2_rn(l2, sum);
           if (np0 > 0) {  // the last P V has read P's columns
             ok = wait.all(&o_full[2 * t], (np0 - 1) & 1);
@@ -612,12 +624,14 @@ attn_fwd_tc(const __grid_constant__ FwdParams p, unsigned *status, long long wai
           pk[c] = pack_bf16(__uint_as_float(v[j][2 * c]) * inv,
                             __uint_as_float(v[j][2 * c + 1]) * inv);
         store_rows64(sm + L::off_stage + (warp - 2) * 4096, pk, o + 64 * j, a.ld_o,
-                     x.len - row0 - quarter * 32, a.D - 64 * j, lane);
+                     x.len - row0 - quarter * 32, a.D - 64 * j, lane, &p.to, 64 * j, head,
+                     x.start + row0 + quarter * 32);
       }
       if (in && a.lse)
         a.lse[(int64_t)head * a.T + x.start + row] = ms * kLn2 + logf(l);
       __syncwarp();
     }
+    bulk_stores_done();
   }
   tc_fence_before();
   __syncthreads();
@@ -636,6 +650,7 @@ cudaError_t launch(const AttnArgs &a, const DeviceInfo &dev, cudaStream_t s) {
   cudaError_t e = make_head_map(&p.tq, a.q, a.T, a.Hq, a.D, a.ld_q);
   if (e == cudaSuccess) e = make_head_map(&p.tk, a.k, a.T, a.Hkv, a.D, a.ld_k);
   if (e == cudaSuccess) e = make_head_map(&p.tv, a.v, a.T, a.Hkv, a.D, a.ld_v);
+  if (e == cudaSuccess) e = make_head_map(&p.to, a.o, a.T, a.Hq, a.D, a.ld_o, 32);
   unsigned *status = nullptr;
   if (e == cudaSuccess) e = device_status_ptr(dev, &status);
   if (e != cudaSuccess) return e;

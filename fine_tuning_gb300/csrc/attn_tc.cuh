@@ -24,9 +24,9 @@ constexpr int kTile = 128;
 constexpr uint32_t kBoxBytes = kTile * 128;  // 64 bf16 columns of a tile
 
 // One tensor [T, H, D] read in boxes of 128 tokens x one head x 64 columns;
-// columns past D and tokens past T read as zeros.
+// columns past D and tokens past T read as zeros (rows: tokens of a box).
 cudaError_t make_head_map(CUtensorMap *map, const void *base, int64_t T, int64_t H, int64_t D,
-                          int64_t ld);
+                          int64_t ld, uint32_t rows = kTile);
 
 __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *map, int col, int head,
                                          int row, uint64_t *bar) {
@@ -374,19 +374,47 @@ __device__ __forceinline__ bool next_item(const ItemRing &ring, const Waits &wai
   return words[0] >= 0;
 }
 
+// The copies of this thread's stores out of shared memory have been read from
+// there, or have arrived.
+__device__ __forceinline__ void bulk_stores_read() {
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+__device__ __forceinline__ void bulk_stores_done() {
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+
 // 32 rows x 64 columns of bf16 to global memory by a warp that holds a row per
-// lane (pk: its 32 words).  Stored straight from the lanes, every 16-byte piece
-// would be a transaction of its own (eight stores of 32 lines each, which also
-// hold up every later shared-memory access of the SM); through a 4 KB staging
-// tile (16-byte pieces swizzled by the row) eight lanes store a row's 128 bytes
-// together.  Rows at or past `rows`, columns at or past n: not stored.
+// lane (pk: its 32 words), through a staging tile of 4 KB (1024-byte aligned,
+// 16-byte pieces swizzled by the row as the tensor map has it).  A whole group of
+// rows leaves by one tile store, which the warp does not wait for; of a group that
+// a sequence ends in, eight lanes store a row's 128 bytes together (straight from
+// the lanes, every 16-byte piece would be a transaction of its own).  Rows at or
+// past `rows`, columns at or past n: not stored.  map: the output in boxes of 32
+// tokens x one head x 64 columns; (col, head, row) in it is `base`.
 __device__ __forceinline__ void store_rows64(unsigned char *stage, const uint32_t (&pk)[32],
-                                             bf16 *base, int64_t ld, int rows, int n, int lane) {
+                                             bf16 *base, int64_t ld, int rows, int n, int lane,
+                                             const CUtensorMap *map, int col, int head, int row) {
   uint4 *st = reinterpret_cast<uint4 *>(stage);
+  bulk_stores_read();  // the last tile has left the staging
+  __syncwarp();
 #pragma unroll
   for (int c = 0; c < 8; ++c)
     st[lane * 8 + (c ^ (lane & 7))] =
         make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+  if (rows >= 32) {
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (n > 0 && elect_one()) {
+      asm volatile(
+          "cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];"
+          ::"l"(reinterpret_cast<uint64_t>(map)),
+          "r"(col), "r"(head), "r"(row), "r"(smem_addr(stage))
+          : "memory");
+      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    }
+    __syncwarp();
+    return;
+  }
   __syncwarp();
   const int c = lane & 7;
   if (8 * c < n) {
@@ -418,21 +446,29 @@ struct SeqOrder {
   __device__ __forceinline__ explicit SeqOrder(unsigned char *at)
       : base(reinterpret_cast<int *>(at)), order(at + kSortMax * 4), total(0) {}
 
-  // All threads of the CTA (at least kSortMax).  tmp: kSortMax ints of shared
-  // memory that tiles are loaded into later.  units(len): work units of a sequence.
+  // All threads of the CTA (at least kSortMax).  tmp: kSortMax + 1 ints of shared
+  // memory (16-byte aligned) that tiles are loaded into later.  units(len): work
+  // units of a sequence.
   template <class Units>
   __device__ __forceinline__ void make(const AttnArgs &a, int *tmp, Units units) {
     const int b = threadIdx.x;
-    int len = 0;
+    int len = -1;
     if (b < a.B) {
       const int c0 = min(max(__ldg(a.cu + b), 0), (int)a.T);
       len = min(max(__ldg(a.cu + b + 1), c0), (int)a.T) - c0;
-      tmp[b] = len;
     }
+    if (b < kSortMax) tmp[b] = len;
     __syncthreads();
     if (b < a.B) {
       int rank = 0;
-      for (int c = 0; c < a.B; ++c) rank += tmp[c] > len || (tmp[c] == len && c < b);
+#pragma unroll 8
+      for (int c = 0; c < a.B; c += 4) {
+        const int4 v = reinterpret_cast<const int4 *>(tmp)[c >> 2];
+        rank += v.x > len || (v.x == len && c < b);
+        rank += v.y > len || (v.y == len && c + 1 < b);
+        rank += v.z > len || (v.z == len && c + 2 < b);
+        rank += v.w > len || (v.w == len && c + 3 < b);
+      }
       order[rank] = (uint8_t)b;
     }
     __syncthreads();
