@@ -42,7 +42,7 @@ constexpr int kBwdThreads = 384;
 constexpr int kComputeWarps = 8;
 
 struct BwdParams {
-  CUtensorMap tq, tk, tv, tg;  // tg: do
+  CUtensorMap tq, tk, tv, tg, tdq;  // tg: do; tdq: boxes of 32 columns to store
   AttnArgs a;
   int slots;
   int splits;  // CTAs that share a key tile's query heads (dk, dv)
@@ -165,7 +165,9 @@ template <int DP> struct DqLayout {
   static constexpr int kK = DP == 128 ? 3 : 5, kV = DP == 128 ? 2 : 4;
   static constexpr uint32_t off_g = tile_bytes, off_k = 2 * tile_bytes;
   static constexpr uint32_t off_v = off_k + kK * tile_bytes;
-  static constexpr uint32_t off_bar = off_v + kV * tile_bytes;
+  // 2 KB per compute warp; with heads of 128 nothing is left for it
+  static constexpr uint32_t off_stage = off_v + kV * tile_bytes;
+  static constexpr uint32_t off_bar = off_stage + (DP == 64 ? kComputeWarps * 2048 : 0);
   static constexpr uint32_t off_items = (off_bar + (3 * kK + 2 * kV + 11) * 8 + 16 + 15) / 16 * 16;
   static constexpr uint32_t off_order = off_items + ItemRing::kBytes;
   static constexpr uint32_t smem = off_order + SeqOrder::kBytes + 1024;
@@ -465,25 +467,36 @@ attn_dq_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wait
       tc_fence_after();
       // this half's columns of dq
       constexpr int kCols = DP / 2;
-      uint32_t v[64];
+      uint32_t v[kCols];
       __syncwarp();
-      if constexpr (kCols == 64) {
+      if constexpr (kCols == 64)
         tmem_ld64(t_dq + half * kCols + lanes, v);
-      } else {
-        uint32_t u[32];
-        tmem_ld32(t_dq + half * kCols + lanes, u);
-#pragma unroll
-        for (int e = 0; e < 64; ++e) v[e] = e < 32 ? u[e & 31] : 0u;
-      }
+      else
+        tmem_ld32(t_dq + half * kCols + lanes, v);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(acc_empty);
-      if (in)
-        store_half((bf16 *)a.dq + (int64_t)(x.start + row) * a.ld_dq + (int64_t)h * a.D +
-                       half * kCols,
-                   v, a.scale, min(kCols, a.D - half * kCols));
-      __syncwarp();
+      if constexpr (kCols == 32) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int c = 0; c < 16; ++c)
+          pk[c] = pack_bf16(__uint_as_float(v[2 * c]) * a.scale,
+                            __uint_as_float(v[2 * c + 1]) * a.scale);
+        const int r0 = x.row0 + quarter * 32;
+        store_rows<32>(sm + L::off_stage + (warp - 2) * 2048, pk,
+                       (bf16 *)a.dq + (int64_t)(x.start + r0) * a.ld_dq + (int64_t)h * a.D +
+                           half * kCols,
+                       a.ld_dq, x.len - r0, a.D - half * kCols, lane, &p.tdq, half * kCols, h,
+                       x.start + r0);
+      } else {
+        if (in)
+          store_half((bf16 *)a.dq + (int64_t)(x.start + row) * a.ld_dq + (int64_t)h * a.D +
+                         half * kCols,
+                     v, a.scale, min(kCols, a.D - half * kCols));
+        __syncwarp();
+      }
     }
+    bulk_stores_done();
   } else {
     // -------------------------------------------------------- items
     ItemSource<decltype(find)> source(ring, wait, find, skipped ? -1 : (int)blockIdx.x, lane);
@@ -956,6 +969,8 @@ cudaError_t launch(const AttnArgs &a, const DeviceInfo &dev, cudaStream_t s) {
   if (e == cudaSuccess) e = make_head_map(&p.tk, a.k, a.T, a.Hkv, a.D, a.ld_k);
   if (e == cudaSuccess) e = make_head_map(&p.tv, a.v, a.T, a.Hkv, a.D, a.ld_v);
   if (e == cudaSuccess) e = make_head_map(&p.tg, a.do_, a.T, a.Hq, a.D, a.ld_do);
+  if (e == cudaSuccess && DP == 64)
+    e = make_head_map(&p.tdq, a.dq, a.T, a.Hq, a.D, a.ld_dq, 32, 32);
   unsigned *status = nullptr;
   if (e == cudaSuccess) e = device_status_ptr(dev, &status);
   if (e != cudaSuccess) return e;

@@ -49,7 +49,7 @@ namespace ftk {
 namespace attn {
 
 cudaError_t make_head_map(CUtensorMap *map, const void *base, int64_t T, int64_t H, int64_t D,
-                          int64_t ld, uint32_t rows) {
+                          int64_t ld, uint32_t rows, uint32_t cols) {
   static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
   if (!encode) {
     void *fn = nullptr;
@@ -61,11 +61,12 @@ cudaError_t make_head_map(CUtensorMap *map, const void *base, int64_t T, int64_t
   }
   const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)T};
   const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)ld * 2};
-  const cuuint32_t box[3] = {64, 1, rows};
+  const cuuint32_t box[3] = {cols, 1, rows};
   const cuuint32_t elem[3] = {1, 1, 1};
   auto make = [&] {
     return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides,
-                  box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   };
   CUresult r = make();
@@ -623,9 +624,9 @@ attn_fwd_tc(const __grid_constant__ FwdParams p, unsigned *status, long long wai
         for (int c = 0; c < 32; ++c)
           pk[c] = pack_bf16(__uint_as_float(v[j][2 * c]) * inv,
                             __uint_as_float(v[j][2 * c + 1]) * inv);
-        store_rows64(sm + L::off_stage + (warp - 2) * 4096, pk, o + 64 * j, a.ld_o,
-                     x.len - row0 - quarter * 32, a.D - 64 * j, lane, &p.to, 64 * j, head,
-                     x.start + row0 + quarter * 32);
+        store_rows<64>(sm + L::off_stage + (warp - 2) * 4096, pk, o + 64 * j, a.ld_o,
+                       x.len - row0 - quarter * 32, a.D - 64 * j, lane, &p.to, 64 * j, head,
+                       x.start + row0 + quarter * 32);
       }
       if (in && a.lse)
         a.lse[(int64_t)head * a.T + x.start + row] = ms * kLn2 + logf(l);

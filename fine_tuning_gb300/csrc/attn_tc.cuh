@@ -24,9 +24,10 @@ constexpr int kTile = 128;
 constexpr uint32_t kBoxBytes = kTile * 128;  // 64 bf16 columns of a tile
 
 // One tensor [T, H, D] read in boxes of 128 tokens x one head x 64 columns;
-// columns past D and tokens past T read as zeros (rows: tokens of a box).
+// columns past D and tokens past T read as zeros.  rows, cols: tokens and columns
+// of a box (64 columns with the 128-byte swizzle, 32 with the 64-byte one).
 cudaError_t make_head_map(CUtensorMap *map, const void *base, int64_t T, int64_t H, int64_t D,
-                          int64_t ld, uint32_t rows = kTile);
+                          int64_t ld, uint32_t rows = kTile, uint32_t cols = 64);
 
 __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *map, int col, int head,
                                          int row, uint64_t *bar) {
@@ -383,23 +384,27 @@ __device__ __forceinline__ void bulk_stores_done() {
   asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
-// 32 rows x 64 columns of bf16 to global memory by a warp that holds a row per
-// lane (pk: its 32 words), through a staging tile of 4 KB (1024-byte aligned,
-// 16-byte pieces swizzled by the row as the tensor map has it).  A whole group of
-// rows leaves by one tile store, which the warp does not wait for; of a group that
-// a sequence ends in, eight lanes store a row's 128 bytes together (straight from
+// 32 rows x W columns (64 or 32) of bf16 to global memory by a warp that holds a
+// row per lane (pk: its W / 2 words), through a staging tile of 64 W bytes
+// (16-byte pieces swizzled by the row as the tensor map has it: 128-byte rows by
+// 8, aligned to 1024; 64-byte rows by 4 in pairs, aligned to 512).  A whole group
+// of rows leaves by one tile store, which the warp does not wait for; of a group
+// that a sequence ends in, W / 8 lanes store a row's bytes together (straight from
 // the lanes, every 16-byte piece would be a transaction of its own).  Rows at or
 // past `rows`, columns at or past n: not stored.  map: the output in boxes of 32
-// tokens x one head x 64 columns; (col, head, row) in it is `base`.
-__device__ __forceinline__ void store_rows64(unsigned char *stage, const uint32_t (&pk)[32],
-                                             bf16 *base, int64_t ld, int rows, int n, int lane,
-                                             const CUtensorMap *map, int col, int head, int row) {
+// tokens x one head x W columns; (col, head, row) in it is `base`.
+template <int W>
+__device__ __forceinline__ void store_rows(unsigned char *stage, const uint32_t (&pk)[W / 2],
+                                           bf16 *base, int64_t ld, int rows, int n, int lane,
+                                           const CUtensorMap *map, int col, int head, int row) {
+  constexpr int kPieces = W / 8;  // per row
   uint4 *st = reinterpret_cast<uint4 *>(stage);
+  auto swizzle = [](int r) { return W == 64 ? r & 7 : (r >> 1) & 3; };
   bulk_stores_read();  // the last tile has left the staging
   __syncwarp();
 #pragma unroll
-  for (int c = 0; c < 8; ++c)
-    st[lane * 8 + (c ^ (lane & 7))] =
+  for (int c = 0; c < kPieces; ++c)
+    st[lane * kPieces + (c ^ swizzle(lane))] =
         make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
   if (rows >= 32) {
     fence_proxy_async_smem();
@@ -416,13 +421,14 @@ __device__ __forceinline__ void store_rows64(unsigned char *stage, const uint32_
     return;
   }
   __syncwarp();
-  const int c = lane & 7;
+  const int c = lane % kPieces;
   if (8 * c < n) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int r = 4 * k + (lane >> 3);
+    for (int k = 0; k < kPieces; ++k) {
+      const int r = 32 / kPieces * k + lane / kPieces;
       if (r < rows)
-        *reinterpret_cast<uint4 *>(base + (int64_t)r * ld + 8 * c) = st[r * 8 + (c ^ (r & 7))];
+        *reinterpret_cast<uint4 *>(base + (int64_t)r * ld + 8 * c) =
+            st[r * kPieces + (c ^ swizzle(r))];
     }
   }
   __syncwarp();
