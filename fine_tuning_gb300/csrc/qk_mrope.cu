@@ -27,7 +27,9 @@ constexpr int kMropeThreads = 256;
 // beside 16 cosines and sines) four CTAs fit an SM; with four, two
 template <int N> constexpr int kMropeUnroll = N == 8 ? 2 : 4;
 
-// What varies by frequency: read by index, so it stays in the constant bank.
+// What varies by frequency.  A CTA copies it to shared memory first: lanes that
+// read 32 different entries of the constant bank are served one by one, which
+// for every angle anew costs more than the angles.
 struct MropeFreqs {
   RopeFreqs f;
   uint8_t axis[kRopeMaxHalf];
@@ -76,17 +78,24 @@ __global__ void __launch_bounds__(kMropeThreads, 4)
 qk_mrope_kernel(const __grid_constant__ MropeFreqs fr, MropeView q, MropeView k,
                 const int32_t *__restrict__ pos, int64_t ld_pos, int64_t tokens, int Hq, int H,
                 int half, int nv, int S, int tok, float sign) {
-  extern __shared__ __align__(16) float tab[];  // cos [tok][half], then sin
+  extern __shared__ __align__(16) float tab[];  // cos, sin [tok][half]; hi, lo, axis [half]
   pdl_wait();
   pdl_trigger();
   const int64_t t0 = (int64_t)blockIdx.x * tok;
   const int nt = (int)(tokens - t0 < tok ? tokens - t0 : tok);
-  float *cs = tab, *sn = tab + tok * half;
+  float *cs = tab, *sn = tab + tok * half, *hi = sn + tok * half, *lo = hi + half;
+  int *axis = reinterpret_cast<int *>(lo + half);
+  for (int i = threadIdx.x; i < half; i += kMropeThreads) {
+    hi[i] = fr.f.hi[i];
+    lo[i] = fr.f.lo[i];
+    axis[i] = fr.axis[i];
+  }
+  __syncthreads();
   for (int e = threadIdx.x; e < nt * half; e += kMropeThreads) {
     const int t = e / half, i = e - t * half;
-    const int p = __ldg(pos + (int64_t)fr.axis[i] * ld_pos + t0 + t);
+    const int p = __ldg(pos + (int64_t)axis[i] * ld_pos + t0 + t);
     float c, s;
-    rope_cos_sin(p, fr.f.hi[i], fr.f.lo[i], &c, &s);
+    rope_cos_sin(p, hi[i], lo[i], &c, &s);
     cs[e] = c;
     sn[e] = sign * s;
   }
@@ -159,7 +168,7 @@ cudaError_t launch(const QkMropeArgs &a, const DeviceInfo &dev, cudaStream_t s) 
   const int64_t grid = ceil_div(a.T, tok);
   const MropeView q{a.q, a.oq, a.ld_q, a.ld_oq}, k{a.k, a.ok, a.ld_k, a.ld_ok};
   return launch_pdl(qk_mrope_kernel<T, N>, dim3((unsigned)grid), dim3(kMropeThreads),
-                    (size_t)tok * half * 2 * sizeof(float), s, fr, q, k, a.pos, a.ld_pos, a.T, a.Hq,
+                    (size_t)(2 * tok + 3) * half * sizeof(float), s, fr, q, k, a.pos, a.ld_pos, a.T, a.Hq,
                     H, half, nv, S, (int)tok, a.backward ? -1.f : 1.f);
 }
 
