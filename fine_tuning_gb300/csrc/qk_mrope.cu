@@ -9,12 +9,14 @@
 // one (token, packet) in registers and walks every S-th head of Q and K: one
 // 16-byte packet of each half per head, kMropeUnroll heads' loads issued
 // before the first store.  Bound by HBM, 4 bytes per element (bf16 in and out):
-// 215 us on 65,536 tokens x 32/8 bf16 heads of 128 (6.25 TB/s, 0.92 of the copy
-// rate), 100 us on 32,767 tokens x 32/8 fp32 heads of 64 (6.7 TB/s).  Measured
-// on the way, same bf16 call: the table read from shared memory for every head,
+// 207 us on 65,536 tokens x 32/8 bf16 heads of 128 (6.48 TB/s, 0.96 of the copy
+// rate), 100 us on 32,767 tokens x 32/8 fp32 heads of 64 (6.7 TB/s); with few heads
+// by the angles: 23 us on 68,158 tokens x 1/1 bf16 heads of 96 (2.3 TB/s).  Measured
+// on the way, first call: the table read from shared memory for every head,
 // 346 us; in registers with four heads in flight but two CTAs per SM, 345; two
 // heads and four CTAs, 266 (bf16 values converted one by one, spilling); pairs,
-// 215.
+// 215; frequencies from shared memory instead of the constant bank, 207 (the last
+// call: 74 before, 23 after).
 #include "pair_math.cuh"
 #include "rope_common.cuh"
 
