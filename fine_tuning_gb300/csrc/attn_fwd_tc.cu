@@ -541,7 +541,7 @@ attn_fwd_tc(const __grid_constant__ FwdParams p, unsigned *status, long long wai
               if (!ok) break;
             } else {  // nothing in O yet: the first half's maximum was too low
               m = fmaxf(m, top);
-              ms = m * s2;
+              ms = m == -INFINITY ? 0.f : m * s2;
             }
             load(0, s);
             sum = probs(s, p0);

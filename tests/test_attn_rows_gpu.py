@@ -1,0 +1,88 @@
+"""Attention rows on their own: keys whose scores are all -inf, rows whose
+neighbours hold large values, against the 64-bit form and bit for bit."""
+import math
+
+import pytest
+import torch
+
+from fine_tuning_gb300 import build, ftk
+from oracle import attention as A
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+CODE = {torch.float32: "f32", torch.bfloat16: "bf16"}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    build.build()
+    ftk.library()
+    yield
+    assert ftk.device_status(clear=True) == 0
+
+
+def rnd(shape, seed, dtype):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    return torch.randn(shape, generator=g, device=DEV).to(dtype)
+
+
+def seen_fwd(q, k, v, scale, seen, code):
+    """(o, lse, their bars) of one sequence in 64 bits where row i attends to
+    the keys of seen[i] alone: the bars of the oracle's forward, from the scores
+    that are seen (one that is -inf has a weight of zero exactly)."""
+    q, k, v = q.double(), k.double(), v.double()
+    n, Hq, D = q.shape
+    G, u, r = Hq // k.shape[1], A.U, A.R[code]
+    o, ob = torch.empty_like(q), torch.empty_like(q)
+    lse = torch.empty((Hq, n), dtype=torch.float64, device=q.device)
+    lb = lse.clone()
+    for h in range(Hq):
+        qs, ks, vs = q[:, h], k[:, h // G], v[:, h // G]
+        ks = torch.where(torch.isfinite(ks), ks, 0.0)  # components of keys that are not seen
+        z = (scale * (qs @ ks.T)).masked_fill(~seen, -math.inf)
+        mag = (scale * (qs.abs() @ ks.abs().T)).masked_fill(~seen, 0.0)
+        norm = torch.logsumexp(z, 1)
+        p = torch.exp(z - norm[:, None])
+        far = (norm[:, None] - z).masked_fill(p == 0, 0.0).amax(1)
+        es = (D + 3) * 2 * u * mag.amax(1) + u * z.amax(1).abs()
+        e = 2 * es + (8 + 3 * far) * u + (n + 3) * 2 * u
+        o[:, h] = p @ vs
+        ob[:, h] = (r + 2 * e[:, None] + (n + 3) * 2 * u) * (p @ vs.abs()) + r * o[:, h].abs()
+        lse[h] = norm
+        lb[h] = e + 4 * u * (norm.abs() + math.log(n + 1))
+    return o, lse, ob, lb
+
+
+def within(name, got, ref, bar):
+    off = (got.double() - ref).abs()
+    assert bool(torch.isfinite(got).all()), name
+    assert bool((off <= bar).all()), f"{name}: {float((off / bar).max()):.2f} of its bar"
+
+
+@pytest.mark.parametrize("dtype,D", [(torch.bfloat16, 16), (torch.bfloat16, 64),
+                                     (torch.bfloat16, 80), (torch.bfloat16, 128)])
+def test_rows_with_overflowing_scores_beside_rows_without(dtype, D):
+    """Even rows score -2.4e39 / sqrt(D), -inf in 32 bits, with the first 128 keys
+    and see the rest; odd rows see all, and the second half of the first key tile
+    scores far above their first half."""
+    n, Hq, Hkv = 300, 4, 2
+    q, k, v = (rnd((n, h, D), i, dtype) for i, h in enumerate((Hq, Hkv, Hkv)))
+    q[0::2, :, 0], q[1::2, :, 0] = 8.0, 0.0
+    k[:128, :, 0], k[128:, :, 0] = -3e38, 0.0
+    q[:, :, 1] = 8.0
+    k[:64, :, 1], k[64:128, :, 1], k[128:, :, 1] = 0.0, 20.0, -1.0
+    scale = D ** -0.5
+    seen = torch.ones(n, n, dtype=torch.bool, device=DEV)
+    seen[0::2, :128] = False
+    cu = torch.tensor([0, n], dtype=torch.int32, device=DEV)
+    o, lse = ftk.attn_fwd(q, k, v, cu, causal=False)
+    ro, rl, bo, bl = seen_fwd(q, k, v, scale, seen, CODE[dtype])
+    within("o", o, ro, bo)
+    within("lse", lse, rl, bl)
+    # dk and dv (dq holds sums of the 3e38)
+    do = rnd(q.shape, 9, dtype)
+    grads = ftk.attn_bwd(do, q, k, v, o, lse, cu, causal=False)
+    ref, bar = A.attn_bwd(do, q, k, v, o, lse, cu, scale, False, CODE[dtype])
+    for name, g, r, b in list(zip(("dq", "dk", "dv"), grads, ref, bar))[1:]:
+        within(name, g, r, b)
