@@ -213,13 +213,15 @@ attn_fwd_generic(const AttnArgs a, int slots) {
         s[i][j] = see ? s[i][j] * a.scale : -INFINITY;
         mx = fmaxf(mx, s[i][j]);
       }
-      mx = row_max(mx);  // key 0 is seen by every row: finite from the first tile on
-      const float f = expf(m[i] - mx);
+      mx = row_max(mx);
+      // -inf while every key so far scored -inf (infinite keys, an overflow)
+      const float off = mx == -INFINITY ? 0.f : mx;
+      const float f = expf(m[i] - off);
       m[i] = mx;
       float sum = 0.f;
 #pragma unroll
       for (int j = 0; j < TM; ++j) {
-        const float p = expf(s[i][j] - mx);
+        const float p = expf(s[i][j] - off);
         sum += p;
         Ps[(ty * TM + i) * LDP + tx + 16 * j] = p;
       }

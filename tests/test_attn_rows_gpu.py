@@ -86,3 +86,32 @@ def test_rows_with_overflowing_scores_beside_rows_without(dtype, D):
     ref, bar = A.attn_bwd(do, q, k, v, o, lse, cu, scale, False, CODE[dtype])
     for name, g, r, b in list(zip(("dq", "dk", "dv"), grads, ref, bar))[1:]:
         within(name, g, r, b)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("dtype,D,first", [
+    (torch.float32, 16, 40), (torch.float32, 64, 70), (torch.float32, 128, 130),
+    (torch.float32, 256, 33), (torch.bfloat16, 33, 70), (torch.bfloat16, 160, 33),
+    (torch.bfloat16, 64, 130), (torch.bfloat16, 128, 130), (torch.bfloat16, 128, 70)])
+@pytest.mark.parametrize("n", [330, 1500])
+def test_first_keys_with_infinite_components(dtype, D, first, causal, n):
+    """Every key of the first tile scores -inf with every query, later ones are
+    finite: they alone count.  (1,500 tokens take the 64-row tiles of the
+    CUDA-core form, 330 its 32-row ones.)  With the causal mask the rows of the
+    first keys themselves have nothing but -inf, and no value by the definition."""
+    Hq, Hkv = 8, 4
+    q, k, v = (rnd((n, h, D), i, dtype) for i, h in enumerate((Hq, Hkv, Hkv)))
+    q[:, :, 0] = q[:, :, 0].abs() + 0.25
+    k[:first, :, 0] = -math.inf
+    seen = torch.ones(n, n, dtype=torch.bool, device=DEV)
+    if causal:
+        seen = seen.tril()
+    seen[:, :first] = False
+    cu = torch.tensor([0, n], dtype=torch.int32, device=DEV)
+    o, lse = ftk.attn_fwd(q, k, v, cu, causal=causal)
+    ro, rl, bo, bl = seen_fwd(q, k, v, D ** -0.5, seen, CODE[dtype])
+    rows = slice(first if causal else 0, n)
+    within("o", o[rows], ro[rows], bo[rows])
+    within("lse", lse[:, rows], rl[:, rows], bl[:, rows])
+    if causal:
+        assert bool(torch.isnan(o[:first]).all()) and bool((lse[:, :first] == -math.inf).all())
