@@ -22,12 +22,14 @@
 // half's exponentials are formed.  Within a half the exponentials do not wait
 // for the maximum: they are formed against the one that stands, the half's own
 // maximum beside them, and only if some row passes the standing one by more
-// than 2^kRaise are they formed again (after O and l were brought to the new
-// maximum): 347 against 374 us with the maximum first (one causal sequence of
-// 8,192 tokens, 32/8 x 128).  Keeping a lower maximum changes nothing in exact
-// arithmetic (o and l carry the same factor) and keeps p <= 2^kRaise.  Rounding p to bf16
-// (2^-8 relative at most, per term) is the price of the tensor cores' second
-// product.
+// than 2^kRaise are they formed again, after O and l of the rows that passed
+// were brought to the new maximum: 347 against 374 us with the maximum first
+// (one causal sequence of 8,192 tokens, 32/8 x 128).  Each row goes by its own
+// scores alone, so its bits do not depend on its neighbours in the tile, and
+// rows behind a sequence's end start nothing.  Keeping a lower maximum changes
+// nothing in exact arithmetic (o and l carry the same factor) and keeps p <=
+// 2^kRaise.  Rounding p to bf16 (2^-8 relative at most, per term) is the price
+// of the tensor cores' second product.
 // Tensor memory: S0 S1 (128 columns each), O0 O1.  P, in bf16, replaces the
 // scores it came from; with head sizes up to 64 there is room for P beside S,
 // and the next scores are formed while the current ones are still worked on.
@@ -446,6 +448,10 @@ attn_fwd_tc(const __grid_constant__ FwdParams p, unsigned *status, long long wai
       const int head = t ? x.h[1] : x.h[0];
       if (n == 0) continue;
       const int row = row0 + quarter * 32 + lane;                   // within the sequence
+      const bool in = row < x.len;  // behind it: rows of another sequence, or of none
+      // rows behind the end start no raise (a limit in a register: as a term of the vote,
+      // `in` cost 3% with heads of 128)
+      const float limit = in ? kRaise : INFINITY;
       const int last = a.causal ? min(row, x.len - 1) : x.len - 1;  // the last key seen
       // by every row of this warp, and by any
       const int last_all = a.causal ? min(row0 + quarter * 32, x.len - 1) : x.len - 1;
@@ -501,10 +507,10 @@ attn_fwd_tc(const __grid_constant__ FwdParams p, unsigned *status, long long wai
           return __fadd2_rn(sum[0], sum[1]);
         };
         // brings O and l from the standing maximum to `to_m`, once the P V that
-        // `bar` counts is in O
+        // `bar` counts is in O; f is 1 exactly in the rows that keep theirs
         auto raise = [&](float to_m, uint64_t *bar, int count) {
           const float nm = to_m == -INFINITY ? 0.f : to_m * s2;
-          const float f = ex2(m * s2 - nm);
+          const float f = to_m == m ? 1.f : ex2(m * s2 - nm);
           ok = wait.all(bar, (count - 1) & 1);
           if (!ok) return;
           tc_fence_after();
@@ -535,12 +541,13 @@ attn_fwd_tc(const __grid_constant__ FwdParams p, unsigned *status, long long wai
             load(1, s);
             top = fmaxf(top, highest(s));
           }
-          if (__any_sync(0xffffffffu, (top - m) * s2 > kRaise)) {
+          const bool passed = (top - m) * s2 > limit;
+          if (__any_sync(0xffffffffu, passed)) {
             if (i > 0) {
-              raise(fmaxf(m, top), &o_full[2 * t], np0);
+              raise(passed ? top : m, &o_full[2 * t], np0);
               if (!ok) break;
             } else {  // nothing in O yet: the first half's maximum was too low
-              m = fmaxf(m, top);
+              m = passed ? top : m;
               ms = m == -INFINITY ? 0.f : m * s2;
             }
             load(0, s);
@@ -581,9 +588,10 @@ attn_fwd_tc(const __grid_constant__ FwdParams p, unsigned *status, long long wai
               ms = m == -INFINITY ? 0.f : m * s2;
             }
             float2 sum = probs(s, pk);
-            if (__any_sync(0xffffffffu, (top - m) * s2 > kRaise)) {
+            const float to_m = (top - m) * s2 > limit ? top : m;
+            if (__any_sync(0xffffffffu, to_m > m)) {
               // (never the first half of the first tile, which set the maximum)
-              raise(fmaxf(m, top), &o_full[2 * t + 1 - h], h ? np0 : np1);
+              raise(to_m, &o_full[2 * t + 1 - h], h ? np0 : np1);
               if (!ok) break;
               sum = probs(s, pk);
             }
@@ -605,7 +613,6 @@ attn_fwd_tc(const __grid_constant__ FwdParams p, unsigned *status, long long wai
       if (!ok) break;
       tc_fence_after();
       const float l = l2.x + l2.y, inv = 1.f / l;
-      const bool in = row < x.len;
       bf16 *o = (bf16 *)a.o + (int64_t)(x.start + row0 + quarter * 32) * a.ld_o +
                 (int64_t)head * a.D;
       // all columns first, the warp converged, then the divergent stores: a

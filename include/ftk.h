@@ -475,9 +475,11 @@ FTK_API ftk_status ftk_qk_mrope_bwd(const void *dq_out, int64_t ld_gq, const voi
  * [0, T] give unspecified results, every access inside the tensors;
  * seqlens_status (DEVICE uint32, nullable) is the word ftk_check_seqlens
  * wrote: when it is non-zero the kernels return without writing anything.
- * A sequence never sees another's values, infinities and NaN included; inside
- * a sequence a masked infinity or NaN may reach the rows of its own tile
- * (0 * inf), as in any product with masked probabilities.
+ * A sequence never sees another's values, infinities and NaN included: its o
+ * and lse are the same bits whatever the other rows hold.  Inside a sequence a
+ * masked infinity or NaN may reach the rows of its own tile (0 * inf), as in
+ * any product with masked probabilities.  Keys that score -inf have a weight of
+ * 0; a row with no other keys gets lse = -inf and NaN in o.
  * bf16 with D a multiple of 8 up to 128, 16-byte aligned pointers and row
  * strides that are multiples of 8 runs on the tensor cores (probabilities
  * rounded to bf16 for the second product); anything else on the CUDA cores in

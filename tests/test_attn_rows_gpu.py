@@ -115,3 +115,55 @@ def test_first_keys_with_infinite_components(dtype, D, first, causal, n):
     within("lse", lse[:, rows], rl[:, rows], bl[:, rows])
     if causal:
         assert bool(torch.isnan(o[:first]).all()) and bool((lse[:, :first] == -math.inf).all())
+
+
+def everything(q, k, v, do, cu, causal):
+    o, lse = ftk.attn_fwd(q, k, v, cu, causal=causal)
+    return [o, lse.T, *ftk.attn_bwd(do, q, k, v, o, lse, cu, causal=causal)]
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("dtype,D", [(torch.bfloat16, 64), (torch.bfloat16, 128),
+                                     (torch.bfloat16, 24), (torch.bfloat16, 80),
+                                     (torch.float32, 64)])
+@pytest.mark.parametrize("n", [20, 100, 200, 330])
+def test_large_values_of_other_sequences_change_no_bit(dtype, D, causal, n):
+    """Rows behind a sequence's end hold large finite queries, keys and values, as
+    another sequence or as padding; its own rows stay as they are."""
+    T, Hq, Hkv = n + 230, 4, 2
+    x = [rnd((T, h, D), i, dtype) for i, h in enumerate((Hq, Hkv, Hkv, Hq))]
+    cu = torch.tensor([0, n], dtype=torch.int32, device=DEV)
+    clean = [t[:n] for t in everything(*x, cu, causal)]
+    for t in x:
+        t[n:] *= 50
+    both = torch.tensor([0, n, T], dtype=torch.int32, device=DEV)
+    for c in (cu, both):
+        for name, a, b in zip(("o", "lse", "dq", "dk", "dv"), clean, everything(*x, c, causal)):
+            assert torch.equal(a, b[:n]), name
+
+
+@pytest.mark.parametrize("dtype,D", [(torch.bfloat16, 64), (torch.bfloat16, 128),
+                                     (torch.float32, 64)])
+@pytest.mark.parametrize("cut", [10, 150, 205])
+def test_later_tokens_of_a_causal_sequence_change_no_bit(dtype, D, cut):
+    n, Hq, Hkv = 330, 4, 2
+    x = [rnd((n, h, D), i, dtype) for i, h in enumerate((Hq, Hkv, Hkv, Hq))]
+    cu = torch.tensor([0, n], dtype=torch.int32, device=DEV)
+    clean = [t[:cut].clone() for t in everything(*x, cu, True)[:3]]
+    for t in x[:3]:
+        t[cut:] *= 50
+    for name, a, b in zip(("o", "lse", "dq"), clean, everything(*x, cu, True)):
+        assert torch.equal(a, b[:cut]), name
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_a_row_does_not_depend_on_its_neighbours_queries(D):
+    """Full mask: every second query grows until it raises its maximum in every
+    tile; the others, and their gradients of q, stay as they are."""
+    n = 400
+    q, k, v, do = (rnd((n, 2, D), i, torch.bfloat16) for i in range(4))
+    cu = torch.tensor([0, n], dtype=torch.int32, device=DEV)
+    clean = [t[::2].clone() for t in everything(q, k, v, do, cu, False)[:3]]
+    q[1::2] *= 60
+    for name, a, b in zip(("o", "lse", "dq"), clean, everything(q, k, v, do, cu, False)):
+        assert torch.equal(a, b[::2]), name
