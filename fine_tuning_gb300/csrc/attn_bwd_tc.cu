@@ -56,14 +56,19 @@ struct BwdParams {
 // tiles masked) if the batch is one sequence.  So many CTAs are given its heads,
 // and their fp32 sums (8 bytes per element and share in the workspace) are added
 // in order by a small kernel.  Fractions round up by G / 8: the more heads, the
-// longer the sum against the fixed cost of a share.  Measured, one CTA per sum
-// against this rule, us: one sequence of 8,192, 8/1 x 128: 801, 336; of 2,048,
-// 32/8 x 128: 149, 125 (141 always rounded up); 16,384 tokens in 85 sequences,
-// 14/2 x 64: 174, 165; 4,096 in 4, 32/8 x 128: 296, 296 (313 rounded up).
+// longer the sum against the fixed cost of a share; by two whole shares at most,
+// so that the workspace does not grow with the group.  152 and not the device's
+// count: the workspace and the order of the sums follow from the call alone.
+// Measured, one CTA per sum against this rule, us: one sequence of 8,192, 8/1 x
+// 128: 801, 336; of 2,048, 32/8 x 128: 149, 125 (141 always rounded up); 16,384
+// tokens in 85 sequences, 14/2 x 64: 174, 165; 4,096 in 4, 32/8 x 128: 296, 296
+// (313 rounded up).  G / 8 without the bound, one share at most, this rule, 38,784
+// tokens 64/1: sequences of 4,000 x 128 6,281, 6,580, 6,290; of 200 x 128 1,540,
+// 1,434, 1,430; one x 64 37,400, 37,530, 37,660 (9, 2 and 3 shares).
 int attn_bwd_splits(int64_t T, int32_t Hq, int32_t Hkv) {
   const int64_t G = Hq / Hkv, sums = ceil_div(T, (int64_t)kTile) * Hkv, want = 2 * 152;
   if (sums >= want) return 1;
-  const int64_t n = (8 * want + sums * G) / (8 * sums);
+  const int64_t n = (8 * want + sums * (G < 16 ? G : 16)) / (8 * sums);
   return (int)(n < G ? n : G);
 }
 

@@ -155,3 +155,17 @@ def test_binding_checks():
         ftk.qk_mrope_fwd(x, x, torch.zeros(3, 4, dtype=torch.int32), np.zeros(4, np.int32), 1e4)
     with pytest.raises(ValueError):
         ftk.qk_mrope_fwd(None, None, torch.zeros(3, 4, dtype=torch.int32), np.zeros(4), 1e4)
+
+
+def test_attn_workspace_does_not_grow_with_the_group(lib):
+    """The fp32 sums of dk and dv that the workspace holds beside delta: at most
+    two shares more than 304 tasks over the key tiles' sums give."""
+    f = lib.ftk_attn_bwd_workspace_bytes
+    for T, Hkv, G, D in ((38784, 1, 64, 128), (38784, 1, 128, 128), (38912, 1, 128, 64),
+                         (19400, 2, 32, 64), (8192, 1, 8, 128), (2048, 8, 4, 128),
+                         (16384, 2, 7, 64), (100, 1, 256, 8), (1, 1, 1, 8)):
+        sums = -(-T // 128) * Hkv
+        delta = -(-T * Hkv * G * 4 // 16) * 16
+        shares, rest = divmod(f(T, Hkv * G, Hkv, D, BF16) - delta, 2 * T * Hkv * D * 4)
+        assert rest == 0 and shares != 1
+        assert shares <= min(G, 304 // sums + 2), (T, Hkv, G, D)
