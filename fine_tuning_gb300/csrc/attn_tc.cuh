@@ -224,12 +224,12 @@ struct Waits {
   volatile int *abort;
   unsigned *status;
   long long limit;
-  __device__ __forceinline__ bool operator()(uint64_t *bar, uint32_t parity) const {
+  __device__ __forceinline__ bool within(uint64_t *bar, uint32_t parity, long long cycles) const {
     if (mbar_try_wait_long(bar, parity)) return true;
     const long long t0 = clock64();
     while (!mbar_try_wait_long(bar, parity)) {
       if (*abort) return false;
-      if (clock64() - t0 > limit) {
+      if (clock64() - t0 > cycles) {
         atomicOr(status, kStatusWaitTimeout);
         *abort = 1;
         return false;
@@ -239,7 +239,15 @@ struct Waits {
   }
   // for a whole warp that goes on together or stops together
   __device__ __forceinline__ bool all(uint64_t *bar, uint32_t parity) const {
-    return __all_sync(0xffffffffu, (*this)(bar, parity));
+    return __all_sync(0xffffffffu, within(bar, parity, limit));
+  }
+  // The same for a wait that lasts as long as another role of this CTA works on a
+  // whole item, or searches for one: dk and dv of 128 heads that share one, over 1M
+  // tokens, are 1M tile steps of some 2,260 cycles.  What that role waits for is
+  // bounded by `limit`, tile by tile, and its giving up ends this wait too; the
+  // bound here (a quarter of an hour) is only the last resort.
+  __device__ __forceinline__ bool all_item(uint64_t *bar, uint32_t parity) const {
+    return __all_sync(0xffffffffu, within(bar, parity, limit << 10));
   }
 };
 
@@ -327,7 +335,7 @@ template <class Find> struct ItemSource {
     bool work = false;
     if (count == 0) {
       work = index >= 0 && find(index, words);
-    } else if (!wait.all(ring.want, (count - 1) & 1)) {
+    } else if (!wait.all_item(ring.want, (count - 1) & 1)) {
       return false;
     }
     while (index >= 0 && !work) {
@@ -364,7 +372,7 @@ __device__ __forceinline__ bool next_item(const ItemRing &ring, const Waits &wai
                                           int lane, int (&words)[kItemWords]) {
   const int s = count & 1;
   if (LOADS && count > 0 && lane == 0) mbar_arrive(ring.want);
-  if (!wait.all(&ring.full[s], (count >> 1) & 1)) return false;
+  if (!wait.all_item(&ring.full[s], (count >> 1) & 1)) return false;
 #pragma unroll
   for (int i = 0; i < kItemWords; ++i) {
     words[i] = uniform(ring.slots[s * kItemWords + i]);

@@ -33,3 +33,32 @@ def test_odd_groups_over_many_sequences(B, Hq, Hkv, D):
                                            (64, 2, 16, (150, 0, 129))])
 def test_large_groups(Hq, Hkv, D, lens, causal):
     check(*inputs(lens, Hq, Hkv, D, torch.bfloat16, fused=True), causal)
+
+
+@pytest.mark.slow
+def test_an_item_of_more_than_a_second():
+    """One CTA passes over 6,144 query heads of 38,912 tokens for the first key
+    tile: 1.9M tile steps, some 3e9 cycles, where a single wait may take 2e9.  Only
+    the first and the last head have a gradient: the others add exact zeros, so
+    every result is that of a call with these two heads."""
+    T, H, D = 38912, 6144, 8
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    q2, k, v, do2 = (torch.randn((T, h, D), generator=g, device="cuda").bfloat16()
+                     for h in (2, 1, 1, 2))
+    cu = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    o2, lse2 = ftk.attn_fwd(q2, k, v, cu)
+    dq2, dk2, dv2 = ftk.attn_bwd(do2, q2, k, v, o2, lse2, cu)
+    q = q2[:, :1].repeat(1, H, 1)
+    q[:, -1] = q2[:, 1]
+    lse = lse2[:1].repeat(H, 1)
+    lse[-1] = lse2[1]
+    do, o = torch.zeros_like(q), torch.zeros_like(q)
+    for x, x2 in ((do, do2), (o, o2)):
+        x[:, 0], x[:, -1] = x2[:, 0], x2[:, 1]
+    dq, dk, dv = (torch.full_like(x, float("nan")) for x in (q, k, v))
+    ftk.attn_bwd(do, q, k, v, o, lse, cu, dq=dq, dk=dk, dv=dv)
+    assert ftk.device_status() == 0
+    assert torch.equal(dk, dk2) and torch.equal(dv, dv2)
+    assert torch.equal(dq[:, 0], dq2[:, 0]) and torch.equal(dq[:, -1], dq2[:, 1])
+    assert not bool(dq[:, 1:-1].any())
