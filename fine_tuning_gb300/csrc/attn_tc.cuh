@@ -15,6 +15,7 @@
 namespace ftk {
 namespace attn {
 
+using tc::elect_one;
 using tc::tc_fence_after;
 using tc::tc_fence_before;
 using tc::tmem_ld32;
@@ -66,21 +67,6 @@ __device__ __forceinline__ void tmem_dealloc1(uint32_t taddr, uint32_t ncols) {
 __device__ __forceinline__ int uniform(int v) { return __reduce_max_sync(0xffffffffu, v); }
 __device__ __forceinline__ uint32_t uniform(uint32_t v) {
   return __reduce_max_sync(0xffffffffu, v);
-}
-
-// One lane of a converged warp.  The instructions below read their operands
-// from the warp's uniform registers; with elect.sync the compiler knows that
-// one lane runs them and keeps those registers right.  Under a plain test of
-// the lane number inside a loop, MMAs were measured to run with another MMA's
-// descriptor (wrong scores at best, an illegal address at worst), so every
-// tensor-core and tile-load instruction of the attention kernels is issued by
-// a whole warp's control flow under this election.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(r)::"memory");
-  return r != 0;
 }
 
 // D [128 x N] (+)= A B^T, A and B in shared memory.

@@ -165,6 +165,21 @@ template <int BN> __device__ __forceinline__ uint32_t idesc_bf16(int maj) {
          ((uint32_t)((2 * BM) >> 4) << 24);
 }
 
+// One lane of a converged warp.  The MMAs, their commits and the tile loads read
+// their operands from the warp's uniform registers; with elect.sync the compiler
+// knows that one lane runs them and keeps those registers right.  Under a plain
+// test of the lane number inside a loop, MMAs of the attention kernels were measured
+// to run with another MMA's descriptor (wrong scores at best, an illegal address
+// at worst), so every such instruction is issued under this election: here by one
+// lane for its whole role, in the attention kernels one by one.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r)::"memory");
+  return r != 0;
+}
+
 // D [256 x BN] (+)= A B^T for the pair, issued by one thread of the leader
 // (rank 0): A rows 0..127 from the leader's shared memory, 128..255 from
 // the peer's, both at descriptor a; B rows (N) 0..BN/2-1 from the leader's,
@@ -413,7 +428,7 @@ tc_gemm(const __grid_constant__ Group<Epi> g, unsigned *status, long long wait_l
 
   if (warp == 0) {
     // ------------------------------------------------------ TMA producer
-    if (lane == 0) {
+    if (elect_one()) {
       const uint32_t full0 = cluster_addr(full, 0);  // the leader's full[0]
       Seq q[G];
       load_seqs<G>(g, q);
@@ -480,7 +495,7 @@ tc_gemm(const __grid_constant__ Group<Epi> g, unsigned *status, long long wait_l
     }
   } else if (warp == 1) {
     // ------------------------------------------------------ MMA issuer
-    if (lane == 0 && leader) {
+    if (leader && elect_one()) {
       Seq q[G];
       load_seqs<G>(g, q);
       int it = 0, tcount = 0;
