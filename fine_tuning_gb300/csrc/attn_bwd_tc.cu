@@ -548,10 +548,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 attn_dkv_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wait_limit) {
   using L = DkvLayout<DP>;
   constexpr int kQ = L::kQ, kG = L::kG, kR = L::kR;
-  // all of the 227 KB are spoken for, none is left to align the tiles by hand
+  // all of the 227 KB are spoken for, none is left to align the tiles by hand: the
+  // declared alignment has to hold, and a kernel that finds it broken does nothing
   extern __shared__ __align__(1024) unsigned char smem_aligned[];
   unsigned char *sm = smem_aligned;
   const uint32_t sbase = smem_addr(sm);
+  if ((sbase & 1023) != 0) {
+    if (threadIdx.x == 0) atomicOr(status, kStatusSmemBase);
+    return;
+  }
   float *rows = reinterpret_cast<float *>(sm + L::off_row);
   uint64_t *q_full = reinterpret_cast<uint64_t *>(sm + L::off_bar);
   uint64_t *q_empty = q_full + kQ, *g_full = q_empty + kQ, *g_empty = g_full + kG;

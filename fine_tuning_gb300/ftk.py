@@ -852,7 +852,8 @@ WAIT_TIMEOUT = 1  # FTK_DEVSTAT_WAIT_TIMEOUT
 
 def device_status(clear: bool = True) -> int:
     """Status word of the current device (bit WAIT_TIMEOUT: a kernel's
-    bounded pipeline wait ran out, so some launch's results are invalid)."""
+    bounded pipeline wait ran out; SMEM_BASE: a kernel's shared memory began
+    off its tiles' alignment; either way some launch's results are invalid)."""
     v = ctypes.c_uint32(0)
     _call("ftk_device_status", ctypes.byref(v), 1 if clear else 0)
     return int(v.value)

@@ -617,12 +617,16 @@ FTK_API ftk_status ftk_bfd_pack(const int32_t *lengths, int64_t n, int32_t capac
 
 /* Bits of the device status word. */
 #define FTK_DEVSTAT_WAIT_TIMEOUT 1u /* a kernel's pipeline wait ran out */
+#define FTK_DEVSTAT_SMEM_BASE 2u    /* a kernel's shared memory began off its tiles' alignment */
 
 /* The device status word of the current device, into *flags (host
  * pointer); cleared afterwards when clear != 0.  Kernels that stream data
  * through shared memory wait on barriers for bulk copies; every such wait
  * gives up after ~1 s of SM clock, sets FTK_DEVSTAT_WAIT_TIMEOUT and lets
- * the kernel finish instead of hanging.  A set bit means some launch since
+ * the kernel finish instead of hanging (a wait that lasts as long as another
+ * part of the CTA works on a whole item ends when that part gives up).
+ * FTK_DEVSTAT_SMEM_BASE: the kernel did nothing, rather than read tiles that
+ * lie elsewhere than it takes them to.  A set bit means some launch since
  * the last clear produced invalid results.  This call synchronises with
  * the device (it reads device memory). */
 FTK_API ftk_status ftk_device_status(uint32_t *flags, int clear);

@@ -169,3 +169,18 @@ def test_attn_workspace_does_not_grow_with_the_group(lib):
         shares, rest = divmod(f(T, Hkv * G, Hkv, D, BF16) - delta, 2 * T * Hkv * D * 4)
         assert rest == 0 and shares != 1
         assert shares <= min(G, 304 // sums + 2), (T, Hkv, G, D)
+
+
+def test_status_bits_of_the_header_and_the_kernels_agree():
+    import os
+    import re
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    header = open(os.path.join(root, "include", "ftk.h")).read()
+    kernels = open(os.path.join(root, "fine_tuning_gb300", "csrc", "common.cuh")).read()
+    for a, b in (("WAIT_TIMEOUT", "WaitTimeout"), ("SMEM_BASE", "SmemBase")):
+        x = re.search(rf"#define FTK_DEVSTAT_{a} (\d)u", header).group(1)
+        assert x == re.search(rf"kStatus{b} = (\d)u", kernels).group(1)
+    # the one kernel that cannot align its tiles by hand looks before it uses them
+    bwd = open(os.path.join(root, "fine_tuning_gb300", "csrc", "attn_bwd_tc.cu")).read()
+    at = bwd.index("__align__(1024) unsigned char smem_aligned[]")
+    assert 0 < bwd.index("kStatusSmemBase", at) < bwd.index("mbar_init", at)
