@@ -869,7 +869,8 @@ namespace {
 
 // Sizes shared by the forward and the backward; row strides are the caller's.
 ftk_status attn_shape(int32_t B, int64_t T, int32_t Hq, int32_t Hkv, int32_t D, float scale) {
-  if (T < 0 || T >= (int64_t(1) << 31) || B < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || D < 1 ||
+  // rows are counted in 32 bits, up to the end of the last tile
+  if (T < 0 || T > ftk::kAttnMaxT || B < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || D < 1 ||
       D > ftk::kAttnMaxD || !(scale > 0.f) || !std::isfinite(scale))
     return FTK_ERR_SHAPE;
   if (T > 0 && B < 1) return FTK_ERR_SHAPE;

@@ -483,7 +483,8 @@ FTK_API ftk_status ftk_qk_mrope_bwd(const void *dq_out, int64_t ld_gq, const voi
  * bf16 with D a multiple of 8 up to 128, 16-byte aligned pointers and row
  * strides that are multiples of 8 runs on the tensor cores (probabilities
  * rounded to bf16 for the second product); anything else on the CUDA cores in
- * fp32.  (T / 32 + B) * (Hq + Hkv) must stay below 2^31, else FTK_ERR_SHAPE. */
+ * fp32.  T <= 2^31 - 1024, and (T / 32 + B) * (Hq + Hkv) must stay below 2^31,
+ * else FTK_ERR_SHAPE. */
 FTK_API ftk_status ftk_attn_fwd(const void *q, int64_t ld_q, const void *k, int64_t ld_k,
                                 const void *v, int64_t ld_v, void *o, int64_t ld_o, float *lse,
                                 const int32_t *cu_seqlens, int32_t B, int64_t T, int32_t Hq,

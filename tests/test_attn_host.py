@@ -184,3 +184,15 @@ def test_status_bits_of_the_header_and_the_kernels_agree():
     bwd = open(os.path.join(root, "fine_tuning_gb300", "csrc", "attn_bwd_tc.cu")).read()
     at = bwd.index("__align__(1024) unsigned char smem_aligned[]")
     assert 0 < bwd.index("kStatusSmemBase", at) < bwd.index("mbar_init", at)
+
+
+def test_attn_refuses_rows_that_32_bits_do_not_count(lib):
+    """The last tile's rows reach up to 127 past the last token."""
+    big = dict(Hq=1, Hkv=1, D=8, B=1, ldq=8, ldk=8, ldv=8, ldo=8)
+    call, (back, _) = fwd(lib), bwd(lib)
+    for T in ((1 << 31) - 1, (1 << 31) - 128, (1 << 31) - 1023):
+        assert call(T=T, **big) == SHAPE, T
+        assert back(T=T, lddo=8, lddq=8, lddk=8, lddv=8, **big) == SHAPE, T
+        assert lib.ftk_attn_bwd_workspace_bytes(T, 1, 1, 8, BF16) == 0
+    # refused for the overlap of the pointers below, so not for the size
+    assert call(T=(1 << 31) - 1024, **big) == ALIAS
