@@ -871,7 +871,7 @@ namespace {
 ftk_status attn_shape(int32_t B, int64_t T, int32_t Hq, int32_t Hkv, int32_t D, float scale) {
   // rows are counted in 32 bits, up to the end of the last tile
   if (T < 0 || T > ftk::kAttnMaxT || B < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || D < 1 ||
-      D > ftk::kAttnMaxD || !(scale > 0.f) || !std::isfinite(scale))
+      D > ftk::kAttnMaxD || !(scale > 0.f && scale <= ftk::kAttnMaxScale))  // NaN fails too
     return FTK_ERR_SHAPE;
   if (T > 0 && B < 1) return FTK_ERR_SHAPE;
   // one block per (tile, head), of queries and of keys: the count must fit a grid

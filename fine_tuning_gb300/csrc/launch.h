@@ -267,6 +267,7 @@ struct AttnArgs {
   float *delta;
 };
 constexpr int kAttnMaxD = 256;
+constexpr float kAttnMaxScale = 0x1p127f;  // log2(e) times it is finite
 constexpr int64_t kAttnMaxT = (int64_t(1) << 31) - 1024;
 constexpr int kAttnMinTile = 32;  // rows of the smallest tile any attention kernel uses
 cudaError_t launch_attn_fwd_generic(DType dt, const AttnArgs &a, const DeviceInfo &dev,

@@ -468,7 +468,7 @@ FTK_API ftk_status ftk_qk_mrope_bwd(const void *dq_out, int64_t ld_gq, const voi
  * v [T, ld_v] with Hkv heads, o [T, ld_o] with Hq; Hq a multiple of Hkv; q, k
  * and v may be interleaved slices of one fused QKV buffer, o must overlap no
  * input.  lse: fp32 [Hq, T] contiguous (head-major), nullable; the backward
- * needs it.  1 <= D <= 256; scale > 0 and finite.
+ * needs it.  1 <= D <= 256; 0 < scale <= 2^127.
  * cu_seqlens: DEVICE int32 [B+1], non-decreasing within [0, T]; read on the
  * device.  Rows of o and lse that belong to no sequence (before cu[0], at or
  * past cu[B]) are left as they were.  Boundaries that decrease or leave

@@ -196,3 +196,11 @@ def test_attn_refuses_rows_that_32_bits_do_not_count(lib):
         assert lib.ftk_attn_bwd_workspace_bytes(T, 1, 1, 8, BF16) == 0
     # refused for the overlap of the pointers below, so not for the size
     assert call(T=(1 << 31) - 1024, **big) == ALIAS
+
+
+def test_attn_refuses_scales_whose_exponent_base_two_overflows(lib):
+    """The exponentials are powers of two, of scores times scale * log2(e)."""
+    call, (back, _) = fwd(lib), bwd(lib)
+    for scale in (2.5e38, 3.4e38):
+        assert call(scale=scale) == SHAPE and back(scale=scale) == SHAPE
+    assert call(scale=2.0 ** 127, o=A) == ALIAS  # refused for the overlap alone
