@@ -18,12 +18,19 @@ from __future__ import annotations
 
 from typing import Iterable, List, Optional, Tuple
 
+import numpy as np
 import torch
 from torch.autograd.function import once_differentiable
 
 from . import ftk
 
 LORA_PLUS_RATIO = 16.0
+
+
+def _kept(table):
+    """A copy of a host table for the backward pass: the caller's may change
+    before it runs, and the angles have to be those of the forward."""
+    return None if table is None else np.asarray(table).copy()
 
 
 class RMSNorm(torch.autograd.Function):
@@ -85,7 +92,7 @@ class QKRope(torch.autograd.Function):
         else:
             ftk.qk_rope_freq_fwd(q, k, cu_seqlens, inv_freq)
         ctx.save_for_backward(cu_seqlens)
-        ctx.theta, ctx.inv_freq = theta, inv_freq
+        ctx.theta, ctx.inv_freq = theta, _kept(inv_freq)
         return q, k
 
     @staticmethod
@@ -105,7 +112,7 @@ class QKNormRope(torch.autograd.Function):
         qo, ko, rq, rk = ftk.qk_norm_rope_fwd(q, k, wq, wk, cu_seqlens, eps, theta=theta,
                                               inv_freq=inv_freq)
         ctx.save_for_backward(q, k, wq, wk, rq, rk, cu_seqlens)
-        ctx.eps, ctx.theta, ctx.inv_freq = eps, theta, inv_freq
+        ctx.eps, ctx.theta, ctx.inv_freq = eps, theta, _kept(inv_freq)
         return qo, ko
 
     @staticmethod
@@ -124,7 +131,7 @@ class QKMrope(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, pos, axis_of, theta: float, inv_freq=None):
         ctx.save_for_backward(pos)
-        ctx.axis_of, ctx.theta, ctx.inv_freq = axis_of, theta, inv_freq
+        ctx.axis_of, ctx.theta, ctx.inv_freq = _kept(axis_of), theta, _kept(inv_freq)
         return ftk.qk_mrope_fwd(q, k, pos, axis_of, theta=theta, inv_freq=inv_freq)
 
     @staticmethod
