@@ -731,6 +731,8 @@ def attn_bwd(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor
     if workspace is None:
         workspace = torch.empty(max(16, attn_bwd_workspace_bytes(T, Hq, Hkv, D, q.dtype)),
                                 dtype=torch.uint8, device=q.device)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous: all of its bytes are written")
     _call_on(dev, "ftk_attn_bwd", do.data_ptr(), _head_rows(do, "do"), q.data_ptr(), ldq,
              k.data_ptr(), ldk, v.data_ptr(), ldv, o.data_ptr(), _head_rows(o, "o"),
              lse.data_ptr(), dq.data_ptr(), lddq, dk.data_ptr(), lddk, dv.data_ptr(), lddv,

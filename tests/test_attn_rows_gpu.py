@@ -167,3 +167,44 @@ def test_a_row_does_not_depend_on_its_neighbours_queries(D):
     q[1::2] *= 60
     for name, a, b in zip(("o", "lse", "dq"), clean, everything(q, k, v, do, cu, False)):
         assert torch.equal(a, b[::2]), name
+
+
+def test_a_workspace_with_gaps_is_refused():
+    """Its elements' count says nothing about the bytes from its first one on."""
+    q, k, v, do = (rnd((50, 2, 64), i, torch.bfloat16) for i in range(4))
+    cu = torch.tensor([0, 50], dtype=torch.int32, device=DEV)
+    o, lse = ftk.attn_fwd(q, k, v, cu)
+    n = ftk.attn_bwd_workspace_bytes(50, 2, 2, 64, q.dtype)
+    both = torch.zeros(n, 2, dtype=torch.uint8, device=DEV)
+    with pytest.raises(ValueError):
+        ftk.attn_bwd(do, q, k, v, o, lse, cu, workspace=both[:, 0])
+    ftk.attn_bwd(do, q, k, v, o, lse, cu, workspace=both)
+    with pytest.raises(ftk.FtkError):
+        ftk.attn_bwd(do, q, k, v, o, lse, cu, workspace=both.view(-1)[:n - 1])
+
+
+def test_two_threads_at_once_from_their_first_call_on():
+    """The binding leaves the interpreter's lock during a call: each thread on its own
+    stream gets the bits of a lone call."""
+    import threading
+    cases = []
+    for i, D in enumerate((64, 128, 24, 96)):
+        x = [rnd((700, h, D), i, torch.bfloat16) for h in (4, 2, 2, 4)]
+        cases.append((x, torch.tensor([0, 300, 700], dtype=torch.int32, device=DEV)))
+    torch.cuda.synchronize()
+    got = [None] * len(cases)
+
+    def work(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(5):
+                got[i] = everything(*cases[i][0], cases[i][1], True)
+            torch.cuda.current_stream().synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(cases))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for (x, cu), g in zip(cases, got):
+        for a, b in zip(g, everything(*x, cu, True)):
+            assert torch.equal(a, b)
