@@ -40,8 +40,6 @@
 // 16,384 tokens in 85 sequences, 14/2 x 64: 48 us, mostly the start and end of
 // items of one or two key tiles.  Masks are looked at by each warp's own rows and
 // O leaves by tile stores: together 252 -> 237 and 50 -> 48 us of these.
-#include <cudaTypedefs.h>
-
 #include <cmath>
 
 #include "attn_tc.cuh"
@@ -52,36 +50,11 @@ namespace attn {
 
 cudaError_t make_head_map(CUtensorMap *map, const void *base, int64_t T, int64_t H, int64_t D,
                           int64_t ld, uint32_t rows, uint32_t cols) {
-  static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
-  if (!encode) {
-    void *fn = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000,
-                                                     cudaEnableDefault, &q);
-    if (e != cudaSuccess || q != cudaDriverEntryPointSuccess || !fn) return cudaErrorNotSupported;
-    encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-  }
   const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)T};
   const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)ld * 2};
   const cuuint32_t box[3] = {cols, 1, rows};
-  const cuuint32_t elem[3] = {1, 1, 1};
-  auto make = [&] {
-    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides,
-                  box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  };
-  CUresult r = make();
-  if (r != CUDA_SUCCESS) {
-    // a thread that has made no CUDA call of its own yet (autograd's worker, say)
-    // has no current context, which this driver call needs
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaSetDevice(dev);
-    if (e != cudaSuccess) return e;
-    r = make();
-  }
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+  return tc::encode_bf16_map(map, base, 3, dims, strides, box,
+                             cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 }  // namespace attn

@@ -622,6 +622,12 @@ tc_gemm(const __grid_constant__ Group<Epi> g, unsigned *status, long long wait_l
 
 // ---------------------------------------------------------------- host
 
+// The map of a bf16 tensor (dims and box innermost first, strides in bytes from the
+// second dimension on); reads past its ends return zeros.  From any thread.
+cudaError_t encode_bf16_map(CUtensorMap *map, const void *base, int rank, const cuuint64_t *dims,
+                            const cuuint64_t *strides, const cuuint32_t *box,
+                            CUtensorMapSwizzle swizzle);
+
 // A row-major bf16 matrix [rows, cols] with a row stride of ld elements
 // (ld % 8 == 0, base 16-byte aligned), read in boxes of box_rows x 64 with
 // the 128-byte swizzle; reads past rows / cols return zeros.  A K-major
