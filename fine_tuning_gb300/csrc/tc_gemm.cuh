@@ -37,6 +37,8 @@
 
 #include <cuda.h>
 
+#include <atomic>
+
 #include "common.cuh"
 #include "launch.h"
 
@@ -669,7 +671,7 @@ cudaError_t launch_tc_gemm(Group<Epi> &g, const DeviceInfo &dev, cudaStream_t s)
   static_assert(G == 1 || G == 2, "one or two problems");
   using L = Layout<BN, Epi::kScratch>;
   auto kern = tc_gemm<BN, G, Epi>;
-  static int max_clusters[64] = {};
+  static std::atomic<int> max_clusters[64] = {};  // calls may come from several threads
   if (dev.device < 0 || dev.device >= 64) return cudaErrorInvalidDevice;
   if (g.count != G) return cudaErrorInvalidValue;
   g.units = 0;
@@ -686,21 +688,21 @@ cudaError_t launch_tc_gemm(Group<Epi> &g, const DeviceInfo &dev, cudaStream_t s)
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (!max_clusters[dev.device]) {
+  int fit = max_clusters[dev.device];
+  if (!fit) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)L::smem_bytes);
     if (e != cudaSuccess) return e;
     cfg.gridDim = dim3((unsigned)(dev.sms & ~1));
-    int n = 0;
-    e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
+    e = cudaOccupancyMaxActiveClusters(&fit, kern, &cfg);
     if (e != cudaSuccess) return e;
-    if (n < 1) return cudaErrorInvalidConfiguration;  // no pair of CTAs fits at all
-    max_clusters[dev.device] = n;
+    if (fit < 1) return cudaErrorInvalidConfiguration;  // no pair of CTAs fits at all
+    max_clusters[dev.device] = fit;
   }
   unsigned *status = nullptr;
   cudaError_t e = device_status_ptr(dev, &status);
   if (e != cudaSuccess) return e;
-  const int ncl = g.units < max_clusters[dev.device] ? g.units : max_clusters[dev.device];
+  const int ncl = g.units < fit ? g.units : fit;
   cfg.gridDim = dim3((unsigned)(2 * ncl));
   long long limit = kWaitLimitCycles;
   return cudaLaunchKernelEx(&cfg, kern, g, status, limit);

@@ -79,3 +79,24 @@ def test_attention(D):
                                            dv=out[2], workspace=ws))
     for a, b in zip((o2, lse2, *out), (o, lse, *ref)):
         assert torch.equal(a, b)
+
+
+def test_several_threads_at_once():
+    xs = [(rnd(200 + 64 * i, 64, seed=i), rnd(256, 64, seed=9)) for i in range(4)]
+    ref = [ftk.gemm_bf16(a, b) for a, b in xs]
+    got = [None] * len(xs)
+
+    def work(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(10):
+                got[i] = ftk.gemm_bf16(*xs[i])
+            torch.cuda.current_stream().synchronize()
+
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(xs))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for a, b in zip(got, ref):
+        assert torch.equal(a, b)
