@@ -11,7 +11,7 @@
 #pragma once
 
 #include "common.cuh"
-#include "launch.h"
+#include "launch_attn.h"
 
 namespace ftk {
 

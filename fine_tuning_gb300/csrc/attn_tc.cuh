@@ -21,6 +21,10 @@ using tc::tc_fence_before;
 using tc::tmem_ld32;
 using tc::tmem_ld64;
 
+// Bit of the device status word beside kStatusWaitTimeout: shared memory began off
+// the tiles' alignment.
+constexpr unsigned kStatusSmemBase = 2u;
+
 constexpr int kTile = 128;
 constexpr uint32_t kBoxBytes = kTile * 128;  // 64 bf16 columns of a tile
 

@@ -106,7 +106,6 @@ template <typename T, typename U> __host__ __device__ constexpr T ceil_div(T a, 
 
 // Bits of the library's device status word.
 constexpr unsigned kStatusWaitTimeout = 1u;  // a pipeline wait gave up
-constexpr unsigned kStatusSmemBase = 2u;     // shared memory began off the tiles' alignment
 
 __device__ __forceinline__ uint32_t smem_addr(const void *p) {
   return (uint32_t)__cvta_generic_to_shared(p);

@@ -11,6 +11,7 @@
 
 #include "ftk.h"
 #include "launch.h"
+#include "launch_attn.h"
 
 namespace {
 

@@ -17,6 +17,7 @@
 // heads and four CTAs, 266 (bf16 values converted one by one, spilling); pairs,
 // 215; frequencies from shared memory instead of the constant bank, 207 (the last
 // call: 74 before, 23 after).
+#include "launch_attn.h"
 #include "pair_math.cuh"
 #include "rope_common.cuh"
 

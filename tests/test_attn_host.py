@@ -176,7 +176,8 @@ def test_status_bits_of_the_header_and_the_kernels_agree():
     import re
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     header = open(os.path.join(root, "include", "ftk.h")).read()
-    kernels = open(os.path.join(root, "fine_tuning_gb300", "csrc", "common.cuh")).read()
+    csrc = os.path.join(root, "fine_tuning_gb300", "csrc")
+    kernels = "".join(open(os.path.join(csrc, f)).read() for f in ("common.cuh", "attn_tc.cuh"))
     for a, b in (("WAIT_TIMEOUT", "WaitTimeout"), ("SMEM_BASE", "SmemBase")):
         x = re.search(rf"#define FTK_DEVSTAT_{a} (\d)u", header).group(1)
         assert x == re.search(rf"kStatus{b} = (\d)u", kernels).group(1)
@@ -204,3 +205,16 @@ def test_attn_refuses_scales_whose_exponent_base_two_overflows(lib):
     for scale in (2.5e38, 3.4e38):
         assert call(scale=scale) == SHAPE and back(scale=scale) == SHAPE
     assert call(scale=2.0 ** 127, o=A) == ALIAS  # refused for the overlap alone
+
+
+def test_attention_is_no_part_of_the_sources_that_measured_traffic_is_filed_under():
+    """The DRAM traffic on file counts while an op's sources and the shared headers are
+    those of its capture; what only attention needs must not touch them."""
+    import os
+    import bench
+    csrc = os.path.join(bench.ROOT, "fine_tuning_gb300", "csrc")
+    names = {n for names in bench.KERNEL_SOURCES.values() for n in names}
+    for name in sorted(names | {"common.cuh", "launch.h"}):
+        text = open(os.path.join(csrc, name)).read()
+        for word in ("Attn", "attn_", "Mrope", "mrope"):
+            assert word not in text, f"{name}: {word}"
