@@ -5,7 +5,7 @@ import math
 import pytest
 import torch
 
-from fine_tuning_gb300 import build, ftk
+from fine_tuning_gb300 import autograd, build, ftk
 from oracle import attention as A
 
 pytestmark = pytest.mark.gpu
@@ -208,3 +208,75 @@ def test_two_threads_at_once_from_their_first_call_on():
     for (x, cu), g in zip(cases, got):
         for a, b in zip(g, everything(*x, cu, True)):
             assert torch.equal(a, b)
+
+
+FORMS = [(torch.float32, 16), (torch.bfloat16, 64), (torch.bfloat16, 128), (torch.bfloat16, 33)]
+
+
+@pytest.mark.parametrize("dtype,D", FORMS)
+@pytest.mark.parametrize("bounds", [[3, 3], [0, 0, 0], [40, 40], [5] * 200])
+def test_batches_whose_sequences_are_all_empty(dtype, D, bounds):
+    q, k, v, do = (rnd((40, h, D), i, dtype) for i, h in enumerate((4, 2, 2, 4)))
+    cu = torch.tensor(bounds, dtype=torch.int32, device=DEV)
+    o, lse = torch.full_like(q, 7.0), torch.full((4, 40), 7.0, device=DEV)
+    outs = [torch.full_like(t, 7.0) for t in (q, k, v)]
+    ftk.attn_fwd(q, k, v, cu, o=o, lse=lse)
+    ftk.attn_bwd(do, q, k, v, o, lse, cu, dq=outs[0], dk=outs[1], dv=outs[2])
+    for t in (o, lse, *outs):
+        assert bool((t == 7).all())
+    leaves = [t.clone().requires_grad_(True) for t in (q, k, v)]
+    out = autograd.attention(*leaves, cu)
+    out.backward(do)
+    assert not bool(out.any()) and not any(bool(t.grad.any()) for t in leaves)
+
+
+@pytest.mark.parametrize("dtype,D", FORMS)
+def test_one_tensor_as_queries_keys_and_values(dtype, D):
+    x, do = rnd((150, 2, D), 0, dtype), rnd((150, 2, D), 1, dtype)
+    cu = torch.tensor([0, 20, 150], dtype=torch.int32, device=DEV)
+    apart = everything(x, x.clone(), x.clone(), do, cu, True)
+    for a, b in zip(apart, everything(x, x, x, do, cu, True)):
+        assert torch.equal(a, b)
+    leaf = x.clone().requires_grad_(True)
+    autograd.attention(leaf, leaf, leaf, cu).backward(do)
+    ref = sum(t.double() for t in apart[2:])
+    # two sums of rounded tensors: half a step of each operand and of each sum
+    bar = 4 * A.R[CODE[dtype]] * sum(t.double().abs() for t in apart[2:])
+    assert bool(((leaf.grad.double() - ref).abs() <= bar).all())
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_one_sequence_among_many_empty_ones(D):
+    """The items of 100,000 empty sequences are dropped on the device."""
+    q, k, v, do = (rnd((300, h, D), i, torch.bfloat16) for i, h in enumerate((4, 2, 2, 4)))
+    one = torch.tensor([0, 300], dtype=torch.int32, device=DEV)
+    many = torch.cat([torch.zeros(50000, dtype=torch.int32), torch.full((50001,), 300)]).int().to(DEV)
+    for name, a, b in zip(("o", "lse", "dq", "dk", "dv"), everything(q, k, v, do, one, True),
+                          everything(q, k, v, do, many, True)):
+        assert torch.equal(a, b), name
+
+
+def test_two_graphs_that_share_a_workspace():
+    """Replayed one after the other, each clobbers it and needs nothing of it."""
+    sets, ref, graphs, outs = [], [], [], []
+    ws = torch.empty(ftk.attn_bwd_workspace_bytes(300, 8, 2, 64, torch.bfloat16),
+                     dtype=torch.uint8, device=DEV)
+    for s in range(2):
+        q, k, v, do = (rnd((300, h, 64), 10 * s + i, torch.bfloat16)
+                       for i, h in enumerate((8, 2, 2, 8)))
+        cu = torch.tensor([0, 50 + 100 * s, 300], dtype=torch.int32, device=DEV)
+        o, lse = ftk.attn_fwd(q, k, v, cu)
+        ref.append(ftk.attn_bwd(do, q, k, v, o, lse, cu))
+        sets.append((do, q, k, v, o, lse, cu))
+    torch.cuda.synchronize()
+    for x in sets:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(ftk.attn_bwd(*x, workspace=ws))
+        graphs.append(g)
+    for _ in range(3):
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(outs, ref):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
