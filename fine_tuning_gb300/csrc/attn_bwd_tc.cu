@@ -23,9 +23,9 @@
 // 128 both kernels are bound by the MMAs of their tile pairs (dq: 3, dk/dv: 4,
 // 512 cycles each for 128 x 128 x 128; the pipe is busy 69 and 79% of the time),
 // with heads of 64 by the exponentials and conversions of the 8 warps (44 and
-// 47%).  Measured, one causal sequence of 8,192 tokens, 32/8 heads: 510 us (dq)
-// and 632 (dk, dv) with heads of 128, 392 and 523 with heads of 64; 16,384 tokens,
-// 32/8 x 128, everything: 4.7 ms.  16 warps on the scores instead of 8: 4% slower;
+// 47%).  Measured, one causal sequence of 8,192 tokens, 32/8 heads: 517 us (dq)
+// and 637 (dk, dv) with heads of 128, 397 and 523 with heads of 64; 16,384 tokens,
+// 32/8 x 128, everything: 4.8 ms.  16 warps on the scores instead of 8: 4% slower;
 // the two halves of a tile on barriers and 64-column products of their own, so
 // that one half's exponentials run under the other's gradients: 25% slower (64).
 #include <cmath>

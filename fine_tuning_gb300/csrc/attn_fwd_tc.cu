@@ -33,13 +33,13 @@
 // Tensor memory: S0 S1 (128 columns each), O0 O1.  P, in bf16, replaces the
 // scores it came from; with head sizes up to 64 there is room for P beside S,
 // and the next scores are formed while the current ones are still worked on.
-// Measured, one causal sequence of 32,768 tokens, 64/8 heads of 128: 11.5 ms, 1.53
-// PFLOP/s over the unmasked scores (0.89 of what a library GEMM sustains); of
+// Measured, one causal sequence of 32,768 tokens, 64/8 heads of 128: 11.7 ms, 1.51
+// PFLOP/s over the unmasked scores (0.87 of what a library GEMM sustains); of
 // 8,192, 32/8: 347 us with heads of 128 (tensor pipe busy 69% of the cycles, the
-// bound), 237 with heads of 64 (46%; the exponentials' unit 46%, issue 53%);
-// 16,384 tokens in 85 sequences, 14/2 x 64: 48 us, mostly the start and end of
-// items of one or two key tiles.  Masks are looked at by each warp's own rows and
-// O leaves by tile stores: together 252 -> 237 and 50 -> 48 us of these.
+// bound), 242 with heads of 64 (49%; the exponentials' unit 49%, issue 56%);
+// 16,384 tokens in 85 sequences, 14/2 x 64: 47 us, mostly the start and end of
+// items of one or two key tiles.  Masks looked at by each warp's own rows and O
+// leaving by tile stores were worth 15 and 2 us of the last two.
 #include <cmath>
 
 #include "attn_tc.cuh"

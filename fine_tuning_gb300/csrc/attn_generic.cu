@@ -15,12 +15,16 @@
 // Thread (ty, tx) of 16 x 16 holds BT/16 rows x BT/16 columns of the score
 // tile and, of the outputs, BT/16 rows x groups of 4 columns 64 apart.  Every
 // operand is read from shared memory as float4 (rows padded by 4 words so that
-// 8 lanes' reads fall into different banks), so that the multiply-adds, not
-// the shared-memory reads, are the bound: 12 (20) wavefronts of LDS for 64
+// 8 lanes' reads fall into different banks): 12 (20) wavefronts of LDS for 64
 // (128) warp instructions of FFMA in the two products of a 64 x 64 tile.
-// Measured, one causal fp32 sequence of 4,096 tokens, 32/8 heads of 128: 5.5 ms
+// Measured, one causal fp32 sequence of 4,096 tokens, 32/8 heads of 128: 5.6 ms
 // (25 TFLOP/s over the unmasked scores) forward, 17.2 ms (20, and 28 with the
-// scores and do v^T that dq and dk/dv each make) backward.
+// scores and do v^T that dq and dk/dv each make) backward, of some 80 that the
+// multiply-add units give.  Nothing is saturated: the multiply-add pipe is busy
+// 35% (backward 41) of the cycles, shared memory 48 (53), the issue slots 49 (55).
+// The bound is latency: the tiles' shared memory (119 and 170 KB) leaves one CTA
+// per SM, two warps to a scheduler, and they wait for the scalar loads of a tile,
+// which nothing overlaps, for shared memory and for each other's barriers.
 #include <cmath>
 
 #include "attn_common.cuh"
