@@ -555,6 +555,7 @@ attn_dkv_tc(const __grid_constant__ BwdParams p, unsigned *status, long long wai
   const uint32_t sbase = smem_addr(sm);
   if ((sbase & 1023) != 0) {
     if (threadIdx.x == 0) atomicOr(status, kStatusSmemBase);
+    pdl_wait();  // or the next kernel could start under the ones before this
     return;
   }
   float *rows = reinterpret_cast<float *>(sm + L::off_row);

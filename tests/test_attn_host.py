@@ -184,7 +184,8 @@ def test_status_bits_of_the_header_and_the_kernels_agree():
     # the one kernel that cannot align its tiles by hand looks before it uses them
     bwd = open(os.path.join(root, "fine_tuning_gb300", "csrc", "attn_bwd_tc.cu")).read()
     at = bwd.index("__align__(1024) unsigned char smem_aligned[]")
-    assert 0 < bwd.index("kStatusSmemBase", at) < bwd.index("mbar_init", at)
+    look, wait = bwd.index("kStatusSmemBase", at), bwd.index("pdl_wait();", at)
+    assert look < wait < bwd.index("return;", at) < bwd.index("mbar_init", at)
 
 
 def test_attn_refuses_rows_that_32_bits_do_not_count(lib):
