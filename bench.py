@@ -20,7 +20,8 @@ run, with the same per-kernel method, in a compact `per_workload` block.
 row shapes, for profiler captures that must stay small).
 
 Under torchrun each rank runs its own batch (weak scaling, no collective on
-the data path); rank 0 prints one JSON line.
+the data path); rank 0 prints one JSON line of a few KB, which a reader of the
+output's end gets whole.  `--full FILE` writes everything the run measured.
 """
 from __future__ import annotations
 
@@ -71,7 +72,51 @@ def parse_args(argv=None):
                    help="total CPU time budget of the --impl reference run")
     p.add_argument("--records", default="",
                    help="also write one JSON record per (workload, op) to this .jsonl file")
+    p.add_argument("--full", default="",
+                   help="also write the whole result, which the line shortens, to this .json file")
     return p.parse_args(argv)
+
+
+def line_of(out):
+    """The printed line: the result with its per-op and per-workload parts cut down
+    to times, rates and fractions, and without the prose."""
+    frac = "frac_of_measured_hbm" if out.get("hbm_peak_source") == "measured" \
+        else "frac_of_fallback_hbm"
+
+    def ops(entries, keys):
+        return {n: {f: e[f] for f in keys if f in e} for n, e in entries.items()
+                if isinstance(e, dict) and "us" in e}
+
+    short = dict(out)
+    for k in ("kernels", "extensions"):
+        if k in out:
+            short[k] = ops(out[k], ("us", "GB_s", frac))
+    if "parity" in out:
+        short["parity"] = {k: v for k, v in out["parity"].items()
+                           if k not in ("literal", "literal_note", "rows")}
+    if "per_workload" in out:
+        short["per_workload"] = {
+            n: {**{k: w[k] for k in ("step_ms", "step_GB_s", "step_frac_of_hbm") if k in w},
+                frac: {op: e[frac] for op, e in w.get("kernels", {}).items() if frac in e}}
+            for n, w in out["per_workload"].items()}
+    if "cce" in out:
+        c = out["cce"]
+        short["cce"] = {"workload": c["workload"]["name"], **{
+            k: {"ms": c[k]["ms"], "TFLOP_s": c[k]["TFLOP_s"], "frac": c[k]["roofline"]["frac"]}
+            for k in ("cce_fwd", "cce_bwd") if k in c}}
+    if "packing" in out:
+        short["packing"] = {k: out["packing"][k] for k in
+                            ("sequences_per_s", "oracle_sequences_per_s", "fill")
+                            if k in out["packing"]}
+    if "cpu_baseline" in out:
+        short["cpu_baseline"] = {k: v for k, v in out["cpu_baseline"].items()
+                                 if k not in ("per_op_s", "one_thread")}
+    if "e2e" in out:
+        short["e2e"] = {k: v for k, v in out["e2e"].items()
+                        if k not in ("overlap", "host_buffers")}
+    if "timing" in out:
+        short["timing"] = out["timing"].split(";")[0]
+    return short
 
 
 def records_from(out):
@@ -911,7 +956,10 @@ def run_ours(args):
         out["cpu_baseline"] = cpu_leg(wl, batch.cu_host, cut, args.cpu_seconds)
         out["packing"] = packing_leg(wl)
     if rank == 0:
-        print(json.dumps(out), flush=True)
+        print(json.dumps(line_of(out)), flush=True)
+        if args.full:
+            with open(args.full, "w") as f:
+                json.dump(out, f)
         if args.records:
             with open(args.records, "w") as f:
                 for rec in records_from(out):

@@ -129,3 +129,60 @@ def test_records_flatten_every_workload_and_op():
         ("qwen3-32b-524k", "swiglu_h", "bwd"), ("qwen2.5-0.5b", "swiglu", "fwd")]
     assert recs[0]["shapes"] == {"T": 524288, "H": 5120} and recs[0]["frac_of_hbm"] == 0.75
     assert recs[-1]["parity_max_err_over_bound"] == 0.1 and recs[-1]["shapes"]["H"] == 896
+
+
+def test_the_line_is_short_and_keeps_what_a_reader_needs():
+    """With every leg on, as the default run has it: a few KB instead of 25, the
+    headline, the end-to-end figure, the clocks and the launches whole."""
+    ib = {k: 10 ** 9 for k in bench.OPS}
+    kernels = {k: bench.kernel_entry(k, 1.234567, ib[k], 524288, 6782.4, "measured")
+               for k in bench.OPS}
+    bench.add_references(kernels, {"launch_gap_ms": 1e-3, "copy_ms": [1.0] * 6}, ib)
+    literal = {o: {"elements": 983040, "max_rel": 0.003890401, "max_ulp": 0.500013245,
+                   "ulp_hist": {"0": 0, "<=0.5": 983029, "<=1": 11, "<=2": 0, ">2": 0},
+                   "needed_floor": 0} for op in bench.OPS for o in bench.OUTPUTS_OF[op]}
+    parity = {"tokens_checked": 192, "swiglu_tokens_checked": 192, "outputs": 10,
+              "max_err_over_bound": 0.25, "literal": literal, "literal_note": "n" * 150,
+              "rows": "r" * 150}
+    clocks = {"sm_mhz": 2070.0, "sm_max_mhz": 2070.0, "reasons": [], "samples": 20,
+              "samples_inside_timed_region": 20}
+    tensor = {"ms": 1.1379, "TFLOP_s": 1960.2, "algorithmic_flops": 2230430203904,
+              "tokens_per_s": 7199403.8, "roofline": {"bound": "tensor", "frac": 1.0158}}
+    ext = {n: dict(kernels["rmsnorm_fwd"], launches=2) for n in bench.EXT_OPS}
+    wl = W.WORKLOADS["qwen3-32b-524k"]
+    out = {"metric": bench.METRIC, "value": 6789.4, "unit": "GB/s", "n_gpus": 1, "steps": 20,
+           "warmup": 5, "ms_per_step": 13.5955, "higher_is_better": True, "scaling": "weak",
+           "vs_baseline": None, "dtype": "bf16", "data": "synthetic",
+           "config": bench.workload_config(wl, 1, 1), "hbm_peak_source": "measured",
+           "parity": parity, "kernels": kernels, "roofline": {"kernel": "qk_rope_fwd",
+                                                              "frac": 0.97, "traffic": 1.8e10},
+           "gpu_launches": 140, "timing": "step: replays; " + "t" * 700, "clocks": clocks,
+           "clocks_kernel_leg": clocks, "extensions": {**ext, "clocks": clocks},
+           "per_workload": {n: {"T": 65536, "step_ms": 2.6786, "step_GB_s": 6814.9,
+                                "step_frac_of_hbm": 1.0048, "kernels": kernels, "parity": parity,
+                                "extensions": ext, "clocks_kernel_leg": clocks}
+                            for n in ("qwen2.5-0.5b", "llama-3.2-1b", "qwen3-8b")},
+           "cce": {"workload": {"name": "qwen2.5-0.5b-head"}, "cce_fwd": tensor,
+                   "cce_bwd": tensor, "timing": "t" * 200, "clocks": clocks},
+           "device_status": 0,
+           "e2e": {"value": 283.5, "unit": "GB/s", "ms_per_step": 325.756, "steps": 20,
+                   "h2d_bytes_per_step": 40131110920, "d2h_bytes_per_step": 40133218304,
+                   "overlap": "o" * 200, "host_buffers": "h" * 50},
+           "cpu_baseline": {"value": 20.68, "unit": "GB/s", "cores": 16, "kind": "oracle",
+                            "sample": "s" * 160, "per_op_s": {o: 0.005508 for o in bench.OPS}},
+           "packing": {"sequences_per_s": 2.6e7, "oracle_sequences_per_s": 2.2e5, "fill": 0.9998,
+                       "vs": "v" * 60}}
+    assert len(json.dumps(out)) > 15000
+    line = bench.line_of(out)
+    assert len(json.dumps(line)) < 5000
+    same = ("metric", "value", "unit", "n_gpus", "steps", "warmup", "ms_per_step",
+            "higher_is_better", "scaling", "vs_baseline", "dtype", "data", "config", "roofline",
+            "gpu_launches", "clocks", "device_status")
+    assert all(line[k] == out[k] for k in same)
+    assert {k: line["e2e"][k] for k in ("value", "unit", "h2d_bytes_per_step",
+                                        "d2h_bytes_per_step")}.items() <= out["e2e"].items()
+    assert set(line["kernels"]) == set(bench.OPS) and set(line["extensions"]) == set(bench.EXT_OPS)
+    assert line["per_workload"]["qwen3-8b"]["frac_of_measured_hbm"]["swiglu_bwd"] > 0
+    assert line["cce"]["cce_bwd"] == {"ms": 1.1379, "TFLOP_s": 1960.2, "frac": 1.0158}
+    # the records come from the whole result, which is left as it was
+    assert any("parity_literal" in r for r in bench.records_from(out))
