@@ -193,6 +193,69 @@ class CrossEntropyHead(torch.autograd.Function):
         return dh, dW.to(W.dtype), None
 
 
+class Dropout(torch.autograd.Function):
+    """ftk.dropout_fwd; the mask is made again in the backward pass, from the same
+    step (torch refuses the backward when step was changed in between)."""
+
+    @staticmethod
+    def forward(ctx, x, p: float, seed: int, offset: int = 0, step=None):
+        ctx.save_for_backward(step)
+        ctx.numbers = p, seed, offset
+        return ftk.dropout_fwd(x, p, seed, offset, step)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        (step,) = ctx.saved_tensors
+        return ftk.dropout_bwd(dy.contiguous(), *ctx.numbers, step), None, None, None, None
+
+
+class Embedding(torch.autograd.Function):
+    """scale * W[ids] (ids int32; rows of zeros outside [0, V)).  The gradient is
+    the whole table's, summed in fp32; a step that adds it to a tied head's calls
+    ftk.embed_bwd with accumulate instead."""
+
+    @staticmethod
+    def forward(ctx, W, ids, scale: float = 1.0):
+        ctx.save_for_backward(ids)
+        ctx.scale, ctx.V, ctx.dtype = scale, W.shape[0], W.dtype
+        return ftk.embed_fwd(W, ids, scale)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dx):
+        (ids,) = ctx.saved_tensors
+        return ftk.embed_bwd(dx.contiguous(), ids, ctx.V, ctx.scale).to(ctx.dtype), None, None
+
+
+class BlockRMSNorm(torch.autograd.Function):
+    """(h, y) of ftk.rmsnorm_block_fwd: a block's output x joins the stream res."""
+
+    @staticmethod
+    def forward(ctx, x, res, w, eps: float, w_post=None, gate=None, gate_tok=None,
+                res_scale: float = 1.0, x_scale: float = 1.0, p: float = 0.0, seed: int = 0,
+                offset: int = 0, step=None):
+        ctx.numbers = res_scale, x_scale, p, seed, offset
+        h, y, rstd, rstd_post = ftk.rmsnorm_block_fwd(x, res, w, eps, w_post, gate, gate_tok,
+                                                      *ctx.numbers, step)
+        ctx.save_for_backward(x, h, w, rstd, rstd_post, w_post, gate, gate_tok, step)
+        return h, y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dh, dy):
+        *saved, step = ctx.saved_tensors
+        w_post, gate = saved[5:7]
+        dx, dres, dw, dw_post, dgate, dgate_tok = ftk.rmsnorm_block_bwd(
+            dy.contiguous(), dh.contiguous(), *saved, *ctx.numbers, step)
+        dw = dw.to(saved[2].dtype)
+        if dw_post is not None:
+            dw_post = dw_post.to(w_post.dtype)
+        if dgate is not None:
+            dgate = dgate.to(gate.dtype)
+        return dx, dres, dw, None, dw_post, dgate, dgate_tok, *([None] * 6)
+
+
 def rmsnorm(x, w, eps: float):
     return RMSNorm.apply(x, w, eps)
 
@@ -219,6 +282,21 @@ def qk_mrope(q, k, pos, axis_of, theta: float, inv_freq=None):
 
 def attention(q, k, v, cu_seqlens, scale=None, causal: bool = True):
     return Attention.apply(q, k, v, cu_seqlens, scale, causal)
+
+
+def dropout(x, p: float, seed: int, offset: int = 0, step=None):
+    return Dropout.apply(x, p, seed, offset, step)
+
+
+def embedding(W, ids, scale: float = 1.0):
+    return Embedding.apply(W, ids, scale)
+
+
+def rmsnorm_block(x, res, w, eps: float, w_post=None, gate=None, gate_tok=None,
+                  res_scale: float = 1.0, x_scale: float = 1.0, p: float = 0.0, seed: int = 0,
+                  offset: int = 0, step=None):
+    return BlockRMSNorm.apply(x, res, w, eps, w_post, gate, gate_tok, res_scale, x_scale, p, seed,
+                              offset, step)
 
 
 def cross_entropy_head(h, W, y):

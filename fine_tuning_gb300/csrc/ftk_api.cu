@@ -6,12 +6,14 @@
 
 #include <cmath>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 #include <string>
 
 #include "ftk.h"
 #include "launch.h"
 #include "launch_attn.h"
+#include "launch_residual.h"
 
 namespace {
 
@@ -991,6 +993,279 @@ FTK_API ftk_status ftk_attn_bwd(const void *do_, int64_t ld_do, const void *q, i
                   attn_tc_tensor(dv, ld_dv);
   return finish(tc ? ftk::launch_attn_bwd_tc(a, dev, (cudaStream_t)stream)
                    : ftk::launch_attn_bwd_generic(dt, a, dev, (cudaStream_t)stream));
+}
+
+// ------------------------------- dropout, embedding, a block's joint
+
+}  // extern "C"
+
+namespace {
+
+// Rows and columns are counted in 32 bits inside the kernels, columns with room for
+// the last step of a CTA.
+constexpr int64_t kMaxRows = int64_t(1) << 31;
+constexpr int64_t kMaxCols = int64_t(1) << 24;
+
+bool residual_sizes(int64_t T, int64_t H) {
+  return T >= 0 && T < kMaxRows && H >= 1 && H < kMaxCols;
+}
+
+// False for a probability outside [0, 1] (NaN too).
+bool drop_args(double p, uint64_t seed, uint64_t offset, const int64_t *step,
+               ftk::DropArgs *out) {
+  if (!(p >= 0.0 && p <= 1.0)) return false;
+  out->k0 = (uint32_t)seed;
+  out->k1 = (uint32_t)(seed >> 32);
+  out->offset = offset;
+  out->thr = (int)std::floor(65536.0 * p + 0.5);
+  out->step = out->thr > 0 ? step : nullptr;
+  out->scale = out->thr < 65536 ? (float)(65536.0 / (double)(65536 - out->thr)) : 0.f;
+  return true;
+}
+
+// A contiguous array of n elements of es bytes; empty when p is null.
+View array(const void *p, int64_t n, int64_t es) { return view(p, p ? 1 : 0, n, n, es); }
+
+bool any_overlap(const View &a, std::initializer_list<View> others) {
+  for (const View &o : others)
+    if (may_overlap(a, o)) return true;
+  return false;
+}
+
+// Overlap other than being exactly the same view.
+bool bad_alias(const View &out, const View &in) {
+  return !same_view(out, in) && may_overlap(out, in);
+}
+
+bool all_aligned(std::initializer_list<const void *> ps, size_t n) {
+  for (const void *p : ps)
+    if (!aligned(p, n)) return false;
+  return true;
+}
+
+// Row strides that are whole 16-byte packets.
+bool packets(std::initializer_list<int64_t> lds, int64_t n) {
+  for (int64_t ld : lds)
+    if (ld % n != 0) return false;
+  return true;
+}
+
+ftk_status dropout(const void *x, int64_t ldx, void *y, int64_t ldy, int64_t T, int64_t H,
+                   double p, uint64_t seed, uint64_t offset, const int64_t *step,
+                   ftk_dtype dtype, ftk_stream_t stream) {
+  if (!valid_dtype(dtype)) return FTK_ERR_DTYPE;
+  if (!residual_sizes(T, H) || ldx < H || ldy < H) return FTK_ERR_SHAPE;
+  ftk::DropoutArgs a{x, ldx, y, ldy, T, H, {}};
+  if (!drop_args(p, seed, offset, step, &a.drop)) return FTK_ERR_SHAPE;
+  if (T == 0) return FTK_OK;
+  if (!x || !y) return FTK_ERR_NULL;
+  const DType dt = (DType)dtype;
+  const int64_t es = ftk::dtype_bytes(dt);
+  if (!all_aligned({x, y}, es) || !aligned(step, 8)) return FTK_ERR_ALIGN;
+  const View vx = view(x, T, ldx, H, es), vy = view(y, T, ldy, H, es), vs = array(step, 1, 8);
+  if (bad_alias(vy, vx) || may_overlap(vy, vs)) return FTK_ERR_ALIAS;
+  const int64_t n = 16 / es;
+  const bool vec = all_aligned({x, y}, 16) && packets({H, ldx, ldy}, n);
+  ftk::DeviceInfo dev;
+  cudaError_t e = device_info(&dev);
+  if (e != cudaSuccess) return cuda_fail(e);
+  return finish(ftk::launch_dropout(dt, vec, a, dev, (cudaStream_t)stream));
+}
+
+}  // namespace
+
+extern "C" {
+
+FTK_API ftk_status ftk_dropout_fwd(const void *x, int64_t ldx, void *y, int64_t ldy, int64_t T,
+                                   int64_t H, double p, uint64_t seed, uint64_t offset,
+                                   const int64_t *step, ftk_dtype dtype, ftk_stream_t stream) {
+  return dropout(x, ldx, y, ldy, T, H, p, seed, offset, step, dtype, stream);
+}
+
+FTK_API ftk_status ftk_dropout_bwd(const void *dy, int64_t lddy, void *dx, int64_t lddx,
+                                   int64_t T, int64_t H, double p, uint64_t seed,
+                                   uint64_t offset, const int64_t *step, ftk_dtype dtype,
+                                   ftk_stream_t stream) {
+  return dropout(dy, lddy, dx, lddx, T, H, p, seed, offset, step, dtype, stream);
+}
+
+FTK_API ftk_status ftk_embed_fwd(const void *w, int64_t ldw, int64_t V, const int32_t *ids,
+                                 void *x, int64_t ldx, int64_t T, int64_t H, float scale,
+                                 ftk_dtype dtype, ftk_stream_t stream) {
+  if (!valid_dtype(dtype)) return FTK_ERR_DTYPE;
+  if (!residual_sizes(T, H) || V < 1 || V >= kMaxRows || ldw < H || ldx < H ||
+      !std::isfinite(scale))
+    return FTK_ERR_SHAPE;
+  if (T == 0) return FTK_OK;
+  if (!w || !ids || !x) return FTK_ERR_NULL;
+  const DType dt = (DType)dtype;
+  const int64_t es = ftk::dtype_bytes(dt);
+  if (!all_aligned({w, x}, es) || !aligned(ids, 4)) return FTK_ERR_ALIGN;
+  if (any_overlap(view(x, T, ldx, H, es), {view(w, V, ldw, H, es), array(ids, T, 4)}))
+    return FTK_ERR_ALIAS;
+  const bool vec = all_aligned({w, x}, 16) && packets({H, ldw, ldx}, 16 / es);
+  ftk::DeviceInfo dev;
+  cudaError_t e = device_info(&dev);
+  if (e != cudaSuccess) return cuda_fail(e);
+  const ftk::EmbedFwdArgs a{w, ldw, V, ids, x, ldx, T, H, scale};
+  return finish(ftk::launch_embed_fwd(dt, vec, a, dev, (cudaStream_t)stream));
+}
+
+FTK_API size_t ftk_embed_bwd_workspace_bytes(int64_t T, int64_t H, int64_t V) {
+  if (!residual_sizes(T, H) || V < 1 || V >= kMaxRows) return 0;
+  return ftk::embed_bwd_workspace_bytes(T, H, V);
+}
+
+FTK_API ftk_status ftk_embed_bwd(const void *dx, int64_t lddx, const int32_t *ids, float *dw,
+                                 int64_t lddw, int64_t V, int64_t T, int64_t H, float scale,
+                                 int32_t accumulate, void *workspace, size_t workspace_bytes,
+                                 ftk_dtype dtype, ftk_stream_t stream) {
+  if (!valid_dtype(dtype)) return FTK_ERR_DTYPE;
+  if (!residual_sizes(T, H) || V < 1 || V >= kMaxRows || lddx < H || lddw < H ||
+      !std::isfinite(scale))
+    return FTK_ERR_SHAPE;
+  if (T == 0 && accumulate) return FTK_OK;
+  if (!dw || (T > 0 && (!dx || !ids))) return FTK_ERR_NULL;
+  const size_t need = ftk::embed_bwd_workspace_bytes(T, H, V);
+  if (T > 0 && (!workspace || workspace_bytes < need)) return FTK_ERR_WORKSPACE;
+  const DType dt = (DType)dtype;
+  const int64_t es = ftk::dtype_bytes(dt);
+  if (!aligned(dx, es) || !aligned(ids, 4) || !aligned(dw, 4) || !aligned(workspace, 16))
+    return FTK_ERR_ALIGN;
+  if (T > 0) {
+    const View vdw = view(dw, V, lddw, H, 4), vws = array(workspace, (int64_t)need, 1);
+    const View vdx = view(dx, T, lddx, H, es), vi = array(ids, T, 4);
+    if (any_overlap(vdw, {vdx, vi, vws}) || any_overlap(vws, {vdx, vi})) return FTK_ERR_ALIAS;
+  }
+  const bool vec = all_aligned({dx, dw}, 16) && packets({H, lddx}, 16 / es) && lddw % 4 == 0;
+  ftk::DeviceInfo dev;
+  cudaError_t e = device_info(&dev);
+  if (e != cudaSuccess) return cuda_fail(e);
+  const ftk::EmbedBwdArgs a{dx, lddx, ids, dw, lddw, V, T, H, scale, accumulate != 0, workspace};
+  return finish(ftk::launch_embed_bwd(dt, vec, a, dev, (cudaStream_t)stream));
+}
+
+FTK_API ftk_status ftk_rmsnorm_block_fwd(const void *x, int64_t ldx, const void *res,
+                                         int64_t ldr, const void *w_post, const void *gate,
+                                         const float *gate_tok, const void *w, void *h,
+                                         int64_t ldh, void *y, int64_t ldy, float *rstd_post,
+                                         float *rstd, int64_t T, int64_t H, float eps,
+                                         float res_scale, float x_scale, double p,
+                                         uint64_t seed, uint64_t offset, const int64_t *step,
+                                         ftk_dtype dtype, ftk_stream_t stream) {
+  if (!valid_dtype(dtype)) return FTK_ERR_DTYPE;
+  if (!residual_sizes(T, H) || ldx < H || ldr < H || ldh < H || ldy < H || !(eps >= 0.f) ||
+      !std::isfinite(eps) || !std::isfinite(res_scale) || !std::isfinite(x_scale))
+    return FTK_ERR_SHAPE;
+  ftk::BlockNormArgs a{};
+  if (!drop_args(p, seed, offset, step, &a.drop)) return FTK_ERR_SHAPE;
+  if (T == 0) return FTK_OK;
+  if (!x || !res || !w || !h || !y) return FTK_ERR_NULL;
+  const DType dt = (DType)dtype;
+  const int64_t es = ftk::dtype_bytes(dt);
+  if (!all_aligned({x, res, w_post, gate, w, h, y}, es) ||
+      !all_aligned({gate_tok, rstd_post, rstd}, 4) || !aligned(step, 8))
+    return FTK_ERR_ALIGN;
+  const View vx = view(x, T, ldx, H, es), vres = view(res, T, ldr, H, es);
+  const View vh = view(h, T, ldh, H, es), vy = view(y, T, ldy, H, es);
+  const View v1 = array(rstd_post, T, 4), v2 = array(rstd, T, 4);
+  const View wp = array(w_post, H, es), vg = array(gate, H, es), vw = array(w, H, es);
+  const View vt = array(gate_tok, T, 4), vs = array(step, 1, 8);
+  if (bad_alias(vh, vx) || bad_alias(vh, vres)) return FTK_ERR_ALIAS;
+  for (const View &o : {vh, vy, v1, v2})
+    if (any_overlap(o, {wp, vg, vw, vt, vs})) return FTK_ERR_ALIAS;
+  for (const View &o : {vy, v1, v2})
+    if (any_overlap(o, {vx, vres, vh})) return FTK_ERR_ALIAS;
+  if (any_overlap(vy, {v1, v2}) || may_overlap(v1, v2)) return FTK_ERR_ALIAS;
+  a.x = x, a.ldx = ldx, a.res = res, a.ldr = ldr;
+  a.w_post = w_post, a.gate = gate, a.w = w, a.gate_tok = gate_tok;
+  a.h = h, a.ldh = ldh, a.y = y, a.ldy = ldy;
+  a.rstd_post = rstd_post, a.rstd = rstd;
+  a.T = T, a.H = H, a.eps = eps, a.res_scale = res_scale, a.x_scale = x_scale;
+  const bool vec = all_aligned({x, res, w_post, gate, w, h, y}, 16) &&
+                   packets({H, ldx, ldr, ldh, ldy}, 16 / es);
+  ftk::DeviceInfo dev;
+  cudaError_t e = device_info(&dev);
+  if (e != cudaSuccess) return cuda_fail(e);
+  return finish(ftk::launch_block_norm_fwd(dt, vec, a, dev, (cudaStream_t)stream));
+}
+
+FTK_API size_t ftk_rmsnorm_block_bwd_workspace_bytes(int64_t T, int64_t H, ftk_dtype dtype) {
+  if (!valid_dtype(dtype) || !residual_sizes(T, H) || T == 0) return 0;
+  ftk::DeviceInfo dev;
+  if (device_info(&dev) != cudaSuccess) return 0;
+  return (size_t)ftk::block_norm_partial_rows(T, dev) * 2 * (size_t)H * sizeof(float);
+}
+
+FTK_API ftk_status ftk_rmsnorm_block_bwd(
+    const void *dy, int64_t lddy, const void *dh, int64_t lddh, const void *x, int64_t ldx,
+    const void *h, int64_t ldh, const void *w_post, const void *gate, const float *gate_tok,
+    const void *w, const float *rstd_post, const float *rstd, void *dx, int64_t lddx, void *dres,
+    int64_t lddr, float *dw_post, float *dgate, float *dgate_tok, float *dw, void *workspace,
+    size_t workspace_bytes, int64_t T, int64_t H, float res_scale, float x_scale, double p,
+    uint64_t seed, uint64_t offset, const int64_t *step, ftk_dtype dtype, ftk_stream_t stream) {
+  if (!valid_dtype(dtype)) return FTK_ERR_DTYPE;
+  if (!residual_sizes(T, H) || lddy < H || lddh < H || ldx < H || ldh < H || lddx < H ||
+      lddr < H || !std::isfinite(res_scale) || !std::isfinite(x_scale))
+    return FTK_ERR_SHAPE;
+  ftk::BlockNormArgs a{};
+  if (!drop_args(p, seed, offset, step, &a.drop)) return FTK_ERR_SHAPE;
+  if (!dw || (w_post && !dw_post) || (gate && !dgate)) return FTK_ERR_NULL;
+  if (T > 0 && (!dy || !dh || !x || !h || !w || !rstd || !dx || !dres || (w_post && !rstd_post) ||
+                (gate_tok && !dgate_tok)))
+    return FTK_ERR_NULL;
+  ftk::DeviceInfo dev;
+  cudaError_t e = cudaSuccess;
+  const DType dt = (DType)dtype;
+  const int64_t es = ftk::dtype_bytes(dt);
+  if (!all_aligned({dy, dh, x, h, w_post, gate, w, dx, dres}, es) ||
+      !all_aligned({gate_tok, rstd_post, rstd, dw_post, dgate, dgate_tok, dw}, 4) ||
+      !aligned(step, 8) || !aligned(workspace, 16))
+    return FTK_ERR_ALIGN;
+  if (T > 0 && !workspace) return FTK_ERR_WORKSPACE;
+  const View vdy = view(dy, T, lddy, H, es), vdh = view(dh, T, lddh, H, es);
+  const View vx = view(x, T, ldx, H, es), vh = view(h, T, ldh, H, es);
+  const View vdx = view(dx, T, lddx, H, es), vdr = view(dres, T, lddr, H, es);
+  const View wp = array(w_post, H, es), vg = array(gate, H, es), vw = array(w, H, es);
+  const View vt = array(gate_tok, T, 4), vs = array(step, 1, 8);
+  const View v1 = array(rstd_post, T, 4), v2 = array(rstd, T, 4);
+  // outputs that are asked for without their input are not written
+  const View sums[4] = {array(dw, H, 4), array(w_post ? dw_post : nullptr, H, 4),
+                        array(gate ? dgate : nullptr, H, 4),
+                        array(gate_tok ? dgate_tok : nullptr, T, 4)};
+  if (may_overlap(vdx, vdr)) return FTK_ERR_ALIAS;
+  for (const View &o : {vdx, vdr}) {
+    if (bad_alias(o, vdy) || bad_alias(o, vdh)) return FTK_ERR_ALIAS;
+    if (any_overlap(o, {vx, vh, wp, vg, vw, vt, vs, v1, v2})) return FTK_ERR_ALIAS;
+  }
+  for (int i = 0; i < 4; ++i) {
+    if (any_overlap(sums[i], {vdy, vdh, vx, vh, vdx, vdr, wp, vg, vw, vt, vs, v1, v2}))
+      return FTK_ERR_ALIAS;
+    for (int k = i + 1; k < 4; ++k)
+      if (may_overlap(sums[i], sums[k])) return FTK_ERR_ALIAS;
+  }
+  e = device_info(&dev);
+  if (e != cudaSuccess) return cuda_fail(e);
+  if (T > 0) {
+    const size_t need = (size_t)ftk::block_norm_partial_rows(T, dev) * 2 * (size_t)H * 4;
+    if (workspace_bytes < need) return FTK_ERR_WORKSPACE;
+    const View vws = array(workspace, (int64_t)need, 1);
+    if (any_overlap(vws, {vdy, vdh, vx, vh, vdx, vdr, wp, vg, vw, vt, vs, v1, v2, sums[0],
+                          sums[1], sums[2], sums[3]}))
+      return FTK_ERR_ALIAS;
+  }
+  a.dy = dy, a.lddy = lddy, a.dh = dh, a.lddh = lddh;
+  a.x = x, a.ldx = ldx, a.h = (void *)h, a.ldh = ldh;
+  a.w_post = w_post, a.gate = gate, a.w = w, a.gate_tok = gate_tok;
+  a.rstd_post = (float *)rstd_post, a.rstd = (float *)rstd;
+  a.dx = dx, a.lddx = lddx, a.dres = dres, a.lddr = lddr;
+  a.dw = dw, a.dw_post = w_post ? dw_post : nullptr, a.dgate = gate ? dgate : nullptr;
+  a.dgate_tok = gate_tok ? dgate_tok : nullptr;
+  a.ws = (float *)workspace;
+  a.T = T, a.H = H, a.res_scale = res_scale, a.x_scale = x_scale;
+  const bool vec = all_aligned({dy, dh, x, h, w_post, gate, w, dx, dres}, 16) &&
+                   packets({H, lddy, lddh, ldx, ldh, lddx, lddr}, 16 / es);
+  return finish(ftk::launch_block_norm_bwd(dt, vec, a, dev, (cudaStream_t)stream));
 }
 
 // ------------------------------------------------------ tensor-core GEMM

@@ -1,0 +1,65 @@
+// The random numbers of dropout: Philox4x32-10, a counter-based generator (Salmon,
+// Moraes, Dror and Shaw, "Parallel random numbers: as easy as 1, 2, 3", SC 2011).
+// The bits are a function of a key and a 128-bit counter alone, so that a mask is
+// made again wherever it is needed and never stored.
+//
+// key = the caller's seed; counter = (j / 8, t, offset + step): one call gives the
+// eight 16-bit numbers of columns 8 (j / 8) .. + 7 of row t, column j taking number
+// j % 8 (the low half of a word first).  Sixteen bits an element halve the integer
+// work of the usual 32 (a bf16 stream would otherwise be bound by it); the
+// probability then counts in steps of 2^-16, and the scale is the reciprocal of the
+// probability as counted, so that the mean is kept.
+#pragma once
+
+#include "common.cuh"
+#include "launch_residual.h"
+
+namespace ftk {
+
+namespace {
+
+struct Philox {
+  uint32_t k0, k1, c2, c3;  // the key, and the counter's part that a launch shares
+};
+
+// After pdl_wait(): *step may be the previous kernel's output.
+__device__ __forceinline__ Philox philox_of(const DropArgs &d) {
+  uint64_t at = d.offset;
+  if (d.step != nullptr) at += (uint64_t)*d.step;
+  return Philox{d.k0, d.k1, (uint32_t)at, (uint32_t)(at >> 32)};
+}
+
+__device__ __forceinline__ uint4 philox4x32(const Philox &g, uint32_t c0, uint32_t c1) {
+  uint32_t c2 = g.c2, c3 = g.c3, k0 = g.k0, k1 = g.k1;
+#pragma unroll
+  for (int i = 0; i < 10; ++i) {
+    const uint64_t a = (uint64_t)c0 * 0xD2511F53u, b = (uint64_t)c2 * 0xCD9E8D57u;
+    c0 = (uint32_t)(b >> 32) ^ c1 ^ k0;
+    c1 = (uint32_t)b;
+    c2 = (uint32_t)(a >> 32) ^ c3 ^ k1;
+    c3 = (uint32_t)a;
+    k0 += 0x9E3779B9u;
+    k1 += 0xBB67AE85u;
+  }
+  return make_uint4(c0, c1, c2, c3);
+}
+
+// Number e (0..7) of a call's bits.
+__device__ __forceinline__ int philox_u16(const uint4 &u, int e) {
+  const uint32_t w = e < 2 ? u.x : e < 4 ? u.y : e < 6 ? u.z : u.w;
+  return (int)(e & 1 ? w >> 16 : w & 0xffffu);
+}
+
+// Bit e: column 8 block + e of row t is kept.
+__device__ __forceinline__ uint32_t keep_bits(const Philox &g, int thr, uint32_t block,
+                                              uint32_t t) {
+  const uint4 u = philox4x32(g, block, t);
+  uint32_t m = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) m |= philox_u16(u, e) >= thr ? 1u << e : 0u;
+  return m;
+}
+
+}  // namespace
+
+}  // namespace ftk

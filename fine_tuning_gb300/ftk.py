@@ -49,7 +49,7 @@ def library() -> ctypes.CDLL:
     lib = ctypes.CDLL(_LIB_PATH)
     vp, i64, i32, f32, f64 = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32,
                               ctypes.c_float, ctypes.c_double)
-    st, dt, sz = ctypes.c_int, ctypes.c_int, ctypes.c_size_t
+    st, dt, sz, u64 = ctypes.c_int, ctypes.c_int, ctypes.c_size_t, ctypes.c_uint64
     sig = {
         "ftk_rmsnorm_fwd": (st, [vp, i64, vp, vp, i64, vp, i64, i64, f32, dt, vp]),
         "ftk_rmsnorm_bwd_workspace_bytes": (sz, [i64, i64, dt]),
@@ -105,6 +105,17 @@ def library() -> ctypes.CDLL:
         "ftk_attn_bwd": (st, [vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, i64, vp, i64,
                               vp, i64, vp, sz, vp, i32, i64, i32, i32, i32, f32, i32, vp, dt,
                               vp]),
+        "ftk_dropout_fwd": (st, [vp, i64, vp, i64, i64, i64, f64, u64, u64, vp, dt, vp]),
+        "ftk_dropout_bwd": (st, [vp, i64, vp, i64, i64, i64, f64, u64, u64, vp, dt, vp]),
+        "ftk_embed_fwd": (st, [vp, i64, i64, vp, vp, i64, i64, i64, f32, dt, vp]),
+        "ftk_embed_bwd_workspace_bytes": (sz, [i64, i64, i64]),
+        "ftk_embed_bwd": (st, [vp, i64, vp, vp, i64, i64, i64, i64, f32, i32, vp, sz, dt, vp]),
+        "ftk_rmsnorm_block_fwd": (st, [vp, i64, vp, i64, vp, vp, vp, vp, vp, i64, vp, i64, vp, vp,
+                                       i64, i64, f32, f32, f32, f64, u64, u64, vp, dt, vp]),
+        "ftk_rmsnorm_block_bwd_workspace_bytes": (sz, [i64, i64, dt]),
+        "ftk_rmsnorm_block_bwd": (st, [vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, vp, vp,
+                                       vp, i64, vp, i64, vp, vp, vp, vp, vp, sz, i64, i64, f32,
+                                       f32, f64, u64, u64, vp, dt, vp]),
         "ftk_bfd_pack": (st, [vp, i64, i32, vp, vp, vp, vp]),
         "ftk_device_status": (st, [ctypes.POINTER(ctypes.c_uint32), ctypes.c_int]),
         "ftk_selftest_wait_timeout": (st, [i64, vp]),
@@ -741,6 +752,216 @@ def attn_bwd(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor
              D ** -0.5 if scale is None else float(scale), 1 if causal else 0,
              _ptr(seqlens_status), _code(q))
     return dq, dk, dv
+
+
+# ---------------------------------------------------------------- dropout
+
+def _ld(t: torch.Tensor, name: str) -> int:
+    """_rows, for batches without a row too (whose strides may be anything)."""
+    return _rows(t, name) if t.dim() != 2 or t.shape[0] > 0 else max(1, t.shape[1])
+
+
+def _rows_like(x: torch.Tensor, t: torch.Tensor, name: str) -> int:
+    """Row stride of t, which has x's [T, H] shape and dtype."""
+    if t.shape != x.shape or t.dtype != x.dtype:
+        raise ValueError(f"{name} must be {tuple(x.shape)} {x.dtype}")
+    return _ld(t, name)
+
+
+def _new_rows(x: torch.Tensor, t: Optional[torch.Tensor], name: str) -> Tuple[torch.Tensor, int]:
+    """The output that goes with x [T, H] (t, or a new contiguous one) and its row stride."""
+    if t is None:
+        return torch.empty_like(x, memory_format=torch.contiguous_format), x.shape[1]
+    return t, _rows_like(x, t, name)
+
+
+def _vector(t: Optional[torch.Tensor], n: int, dtype: torch.dtype, name: str):
+    """The address of a contiguous [n] tensor of dtype, or None."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} values")
+    return t.data_ptr()
+
+
+def _random(p: float, seed: int, offset: int, step: Optional[torch.Tensor]):
+    """A dropout's arguments of a C call."""
+    if not (0 <= seed < 2 ** 64 and 0 <= offset < 2 ** 64):
+        raise ValueError("seed and offset must lie in [0, 2^64)")
+    return float(p), int(seed), int(offset), _vector(step, 1, torch.int64, "step")
+
+
+def _dropout(name, x, p, seed, offset, step, y, out):
+    ldx = _ld(x, "x")
+    dev = _same_device(x, y, step)
+    y, ldy = _new_rows(x, y, out)
+    T, H = x.shape
+    _call_on(dev, name, x.data_ptr(), ldx, y.data_ptr(), ldy, T, H,
+             *_random(p, seed, offset, step), _code(x))
+    return y
+
+
+def dropout_fwd(x: torch.Tensor, p: float, seed: int, offset: int = 0,
+                step: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None
+                ) -> torch.Tensor:
+    """y = x / (1 - p) where a counter-based generator keeps x [T, H], else 0.
+    The mask is a function of seed, offset + step, row and column, and is
+    never stored; p counts in steps of 2^-16.  step: int64 [1] on the device,
+    read when the kernel runs (advance it between replays of a captured
+    graph; the backward needs the same value).  y=x drops in place."""
+    return _dropout("ftk_dropout_fwd", x, p, seed, offset, step, y, "y")
+
+
+def dropout_bwd(dy: torch.Tensor, p: float, seed: int, offset: int = 0,
+                step: Optional[torch.Tensor] = None, dx: Optional[torch.Tensor] = None
+                ) -> torch.Tensor:
+    """Backward of dropout_fwd: dx, the mask made again from the same numbers."""
+    return _dropout("ftk_dropout_bwd", dy, p, seed, offset, step, dx, "dx")
+
+
+# -------------------------------------------------------------- embedding
+
+def _ids(ids: torch.Tensor) -> int:
+    if ids.dtype != torch.int32 or ids.dim() != 1 or not ids.is_contiguous():
+        raise ValueError("ids must be a contiguous int32 [T] tensor")
+    return ids.shape[0]
+
+
+def embed_fwd(W: torch.Tensor, ids: torch.Tensor, scale: float = 1.0,
+              x: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """x [T, H] = scale * W[ids] (ids int32; a row of zeros where an id lies
+    outside [0, V))."""
+    ldw, T = _ld(W, "W"), _ids(ids)
+    dev = _same_device(W, ids, x)
+    V, H = W.shape
+    if x is None:
+        x, ldx = torch.empty((T, H), dtype=W.dtype, device=W.device), H
+    elif x.shape != (T, H) or x.dtype != W.dtype:
+        raise ValueError(f"x must be {(T, H)} {W.dtype}")
+    else:
+        ldx = _ld(x, "x")
+    _call_on(dev, "ftk_embed_fwd", W.data_ptr(), ldw, V, ids.data_ptr(), x.data_ptr(), ldx, T, H,
+             float(scale), _code(W))
+    return x
+
+
+def embed_bwd_workspace_bytes(T: int, H: int, V: int) -> int:
+    return int(library().ftk_embed_bwd_workspace_bytes(T, H, V))
+
+
+def embed_bwd(dx: torch.Tensor, ids: torch.Tensor, V: int, scale: float = 1.0,
+              dW: Optional[torch.Tensor] = None, accumulate: bool = False,
+              workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """dW fp32 [V, H]: scale * the sum of dx [T, H] over each id's tokens, in
+    their order (bitwise reproducible).  Overwrites dW, zeros in the rows of no
+    token; with accumulate it adds to the rows that tokens name (of an earlier
+    batch, or of a tied head's cce_bwd)."""
+    lddx, T = _ld(dx, "dx"), _ids(ids)
+    dev = _same_device(dx, ids, dW, workspace)
+    V, H = int(V), dx.shape[1]
+    if dx.shape[0] != T:
+        raise ValueError("dx and ids must agree in tokens")
+    if dW is None:
+        if accumulate:
+            raise ValueError("accumulate needs a dW to add to")
+        dW, lddw = torch.empty((V, H), dtype=torch.float32, device=dx.device), H
+    elif dW.shape != (V, H) or dW.dtype != torch.float32:
+        raise ValueError(f"dW must be {(V, H)} fp32")
+    else:
+        lddw = _ld(dW, "dW")
+    if workspace is None:
+        workspace = torch.empty(max(16, embed_bwd_workspace_bytes(T, H, V)), dtype=torch.uint8,
+                                device=dx.device)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous: all of its bytes are written")
+    _call_on(dev, "ftk_embed_bwd", dx.data_ptr(), lddx, ids.data_ptr(), dW.data_ptr(), lddw, V, T,
+             H, float(scale), 1 if accumulate else 0, workspace.data_ptr(),
+             workspace.numel() * workspace.element_size(), _code(dx))
+    return dW
+
+
+# ------------------------- a block's output joins the residual stream
+
+def rmsnorm_block_fwd(x: torch.Tensor, res: torch.Tensor, w: torch.Tensor, eps: float,
+                      w_post: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
+                      gate_tok: Optional[torch.Tensor] = None, res_scale: float = 1.0,
+                      x_scale: float = 1.0, p: float = 0.0, seed: int = 0, offset: int = 0,
+                      step: Optional[torch.Tensor] = None, h: Optional[torch.Tensor] = None,
+                      y: Optional[torch.Tensor] = None, save_rstd: bool = True):
+    """h = res_scale * res + x_scale * dropout(rmsnorm(x) * w_post * gate *
+    gate_tok), stored; y = rmsnorm(h) * w.  x, res [T, H]; w, w_post, gate
+    [H]; gate_tok fp32 [T].  Factors left out are 1, and without w_post x is
+    not normalised.  p, seed, offset, step: dropout_fwd's (the same mask).
+    Returns (h, y, rstd, rstd_post); h=res (or h=x) updates the stream in
+    place."""
+    ldx, ldr = _ld(x, "x"), _rows_like(x, res, "res")
+    dev = _same_device(x, res, w, w_post, gate, gate_tok, step, h, y)
+    T, H = x.shape
+    h, ldh = _new_rows(x, h, "h")
+    y, ldy = _new_rows(x, y, "y")
+    rstd = rstd_post = None
+    if save_rstd:
+        rstd = torch.empty(T, dtype=torch.float32, device=x.device)
+        if w_post is not None:
+            rstd_post = torch.empty(T, dtype=torch.float32, device=x.device)
+    _call_on(dev, "ftk_rmsnorm_block_fwd", x.data_ptr(), ldx, res.data_ptr(), ldr,
+             _vector(w_post, H, x.dtype, "w_post"), _vector(gate, H, x.dtype, "gate"),
+             _vector(gate_tok, T, torch.float32, "gate_tok"), _vector(w, H, x.dtype, "w"),
+             h.data_ptr(), ldh, y.data_ptr(), ldy, _ptr(rstd_post), _ptr(rstd), T, H, float(eps),
+             float(res_scale), float(x_scale), *_random(p, seed, offset, step), _code(x))
+    return h, y, rstd, rstd_post
+
+
+def rmsnorm_block_bwd_workspace_bytes(T: int, H: int, dtype: torch.dtype) -> int:
+    """For the current device."""
+    return int(library().ftk_rmsnorm_block_bwd_workspace_bytes(T, H, _DTYPES[dtype]))
+
+
+def rmsnorm_block_bwd(dy: torch.Tensor, dh: torch.Tensor, x: torch.Tensor, h: torch.Tensor,
+                      w: torch.Tensor, rstd: torch.Tensor,
+                      rstd_post: Optional[torch.Tensor] = None,
+                      w_post: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
+                      gate_tok: Optional[torch.Tensor] = None, res_scale: float = 1.0,
+                      x_scale: float = 1.0, p: float = 0.0, seed: int = 0, offset: int = 0,
+                      step: Optional[torch.Tensor] = None, dx: Optional[torch.Tensor] = None,
+                      dres: Optional[torch.Tensor] = None,
+                      workspace: Optional[torch.Tensor] = None):
+    """Backward of rmsnorm_block_fwd from dy and dh (the gradient the stream
+    carries back into h), the block's output x, the stored h and the saved
+    rstd: (dx, dres, dw, dw_post, dgate, dgate_tok), the last four fp32, None
+    where the factor is.  dx and dres may each be dy or dh."""
+    ldx, ldh = _ld(x, "x"), _rows_like(x, h, "h")
+    lddy, lddh = _rows_like(x, dy, "dy"), _rows_like(x, dh, "dh")
+    dev = _same_device(x, dy, dh, h, w, rstd, rstd_post, w_post, gate, gate_tok, step, dx, dres,
+                       workspace)
+    T, H = x.shape
+    if w_post is not None and rstd_post is None:
+        raise ValueError("w_post needs the forward's rstd_post")
+    dx, lddx = _new_rows(x, dx, "dx")
+    dres, lddr = _new_rows(x, dres, "dres")
+
+    def sums(factor, n):
+        return None if factor is None else torch.empty(n, dtype=torch.float32, device=x.device)
+
+    dw, dw_post, dgate, dgate_tok = sums(w, H), sums(w_post, H), sums(gate, H), sums(gate_tok, T)
+    if workspace is None:
+        if dev == torch._C._cuda_getDevice():
+            n = rmsnorm_block_bwd_workspace_bytes(T, H, x.dtype)
+        else:
+            with torch.cuda.device(dev):
+                n = rmsnorm_block_bwd_workspace_bytes(T, H, x.dtype)
+        workspace = torch.empty(max(16, n), dtype=torch.uint8, device=x.device)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous: all of its bytes are written")
+    _call_on(dev, "ftk_rmsnorm_block_bwd", dy.data_ptr(), lddy, dh.data_ptr(), lddh, x.data_ptr(),
+             ldx, h.data_ptr(), ldh, _vector(w_post, H, x.dtype, "w_post"),
+             _vector(gate, H, x.dtype, "gate"), _vector(gate_tok, T, torch.float32, "gate_tok"),
+             _vector(w, H, x.dtype, "w"), _vector(rstd_post, T, torch.float32, "rstd_post"),
+             _vector(rstd, T, torch.float32, "rstd"), dx.data_ptr(), lddx, dres.data_ptr(), lddr,
+             _ptr(dw_post), _ptr(dgate), _ptr(dgate_tok), dw.data_ptr(), workspace.data_ptr(),
+             workspace.numel() * workspace.element_size(), T, H, float(res_scale), float(x_scale),
+             *_random(p, seed, offset, step), _code(x))
+    return dx, dres, dw, dw_post, dgate, dgate_tok
 
 
 # ------------------------------------------------------ Cut Cross-Entropy

@@ -521,6 +521,124 @@ FTK_API ftk_status ftk_attn_bwd(const void *do_, int64_t ld_do, const void *q, i
                                 const uint32_t *seqlens_status, ftk_dtype dtype,
                                 ftk_stream_t stream);
 
+/* ---------------------------------------------------------------- dropout */
+
+/* Dropout of T rows of H features, with a mask that is never stored (the pages
+ * fine-tune adapters, whose input is dropped out; they print no formula):
+ *   y[t,j] = keep[t,j] ? x[t,j] * 65536 / (65536 - thr) : 0
+ *   keep[t,j] = u[t,j] >= thr,   thr = floor(65536 p + 1/2)
+ * u[t,j] is the 16-bit number j % 8 (the low half of a word first) of the 128
+ * bits that Philox4x32-10 (Salmon, Moraes, Dror and Shaw, "Parallel random
+ * numbers: as easy as 1, 2, 3", SC 2011) makes of the key `seed` and the counter
+ * (j / 8, t, low word, high word of offset + *step), words in this order.  The
+ * mask depends on seed, offset + *step, t and j alone: not on strides, dtype, H,
+ * T or the device.  A dropped element is 0 whatever x holds there (inf and NaN
+ * included).  Probabilities count in steps of 2^-16 (p below 2^-17 drops
+ * nothing), and the scale is that of the probability as counted.
+ * offset: tells the dropouts of one seed apart (a layer's number, say);
+ * step: DEVICE int64, nullable, 8-byte aligned, read when the kernel runs: a
+ * captured graph makes new masks when the value is advanced between replays.
+ * The backward needs the same value.
+ * x [T, ldx], y [T, ldy]; y may be x exactly (same pointer and stride), otherwise
+ * they must not overlap; step overlaps neither.  0 <= p <= 1, T < 2^31,
+ * H < 2^24, else FTK_ERR_SHAPE. */
+FTK_API ftk_status ftk_dropout_fwd(const void *x, int64_t ldx, void *y, int64_t ldy, int64_t T,
+                                   int64_t H, double p, uint64_t seed, uint64_t offset,
+                                   const int64_t *step, ftk_dtype dtype, ftk_stream_t stream);
+
+/* Backward: dx[t,j] = keep[t,j] ? dy[t,j] * 65536 / (65536 - thr) : 0, the mask
+ * made again from the forward's p, seed, offset and *step.  Rules as above. */
+FTK_API ftk_status ftk_dropout_bwd(const void *dy, int64_t lddy, void *dx, int64_t lddx,
+                                   int64_t T, int64_t H, double p, uint64_t seed,
+                                   uint64_t offset, const int64_t *step, ftk_dtype dtype,
+                                   ftk_stream_t stream);
+
+/* -------------------------------------------------------------- embedding */
+
+/* Embedding lookup with scaling, the start of the residual stream (the pages
+ * feed a packed 1-D token tensor; they print no formula):
+ *   x[t,j] = scale * W[ids[t], j]   (0 when ids[t] lies outside [0, V))
+ * so that -100, or any negative value, marks padding, as in ftk_cce_fwd.
+ * W [V, ldw], x [T, ldx] (dtype); ids: DEVICE int32 [T].  x overlaps neither.
+ * 1 <= V < 2^31, T < 2^31, 1 <= H < 2^24, scale finite, else FTK_ERR_SHAPE. */
+FTK_API ftk_status ftk_embed_fwd(const void *w, int64_t ldw, int64_t V, const int32_t *ids,
+                                 void *x, int64_t ldx, int64_t T, int64_t H, float scale,
+                                 ftk_dtype dtype, ftk_stream_t stream);
+
+/* Bytes of device workspace ftk_embed_bwd needs; 0 for invalid arguments. */
+FTK_API size_t ftk_embed_bwd_workspace_bytes(int64_t T, int64_t H, int64_t V);
+
+/* The table's gradient, from dx [T, lddx] (dtype):
+ *   g[v,j] = scale * sum over t with ids[t] = v, in the order of t, of dx[t,j]
+ * dW fp32 [V, lddw]: accumulate == 0 overwrites every row (zeros in the rows that
+ * no token names, T = 0 included); accumulate != 0 adds g to the rows that a token
+ * names and leaves the others as they are, so that several batches, or a tied LM
+ * head (ftk_cce_bwd's dW), share one gradient.  Sums are fp32 in a fixed order
+ * (no atomics): bitwise reproducible.  Columns past H of a row are left as they
+ * were.  workspace: >= ftk_embed_bwd_workspace_bytes(T, H, V) bytes, 16-byte
+ * aligned, contents ignored and clobbered; calls that overlap on the GPU need one
+ * each.  dW, workspace and the inputs must not overlap.  Limits as above. */
+FTK_API ftk_status ftk_embed_bwd(const void *dx, int64_t lddx, const int32_t *ids, float *dw,
+                                 int64_t lddw, int64_t V, int64_t T, int64_t H, float scale,
+                                 int32_t accumulate, void *workspace, size_t workspace_bytes,
+                                 ftk_dtype dtype, ftk_stream_t stream);
+
+/* --------------------------- a block's output joins the residual stream */
+
+/* RMSNorm behind a block, its gate, dropout and scales, the residual add and
+ * RMSNorm before the next block, in one pass (ftk_rmsnorm_add_fwd's variant for
+ * models with norms on both sides of a block, learned gates or residual
+ * dropout; the pages print no formula):
+ *   r1[t]  = 1 / sqrt( (1/H) sum_j x[t,j]^2 + eps )         (with w_post)
+ *   b[t,j] = x[t,j] r1[t] w_post[j] gate[j] gate_tok[t]
+ *   h[t,j] = res_scale res[t,j] + x_scale dropout(b)[t,j]   rounded to dtype, STORED
+ *   r[t]   = 1 / sqrt( (1/H) sum_j h[t,j]^2 + eps )
+ *   y[t,j] = h[t,j] r[t] w[j]
+ * x [T, ldx]: the block's output; res [T, ldr]: the stream; h, y as in
+ * ftk_rmsnorm_add_fwd.  w [H] (dtype).  Nullable factors, left out when NULL:
+ * w_post [H] (dtype; without it r1 = w_post = 1), gate [H] (dtype), gate_tok [T]
+ * (fp32).  dropout: ftk_dropout_fwd's, of the [T, H] values b with the same p,
+ * seed, offset and step (the same mask; p = 0: none), not rounded in between.
+ * rstd_post, rstd [T] fp32, nullable: r1 (untouched without w_post) and r.
+ * h may be x or res exactly (same pointer and stride), y overlaps nothing, rstd
+ * outputs nothing either.  eps >= 0, res_scale and x_scale finite; T < 2^31,
+ * 1 <= H < 2^24, else FTK_ERR_SHAPE. */
+FTK_API ftk_status ftk_rmsnorm_block_fwd(const void *x, int64_t ldx, const void *res,
+                                         int64_t ldr, const void *w_post, const void *gate,
+                                         const float *gate_tok, const void *w, void *h,
+                                         int64_t ldh, void *y, int64_t ldy, float *rstd_post,
+                                         float *rstd, int64_t T, int64_t H, float eps,
+                                         float res_scale, float x_scale, double p,
+                                         uint64_t seed, uint64_t offset, const int64_t *step,
+                                         ftk_dtype dtype, ftk_stream_t stream);
+
+/* Bytes of device workspace ftk_rmsnorm_block_bwd needs on the CURRENT device;
+ * 0 for T = 0 or invalid arguments. */
+FTK_API size_t ftk_rmsnorm_block_bwd_workspace_bytes(int64_t T, int64_t H, ftk_dtype dtype);
+
+/* Backward of ftk_rmsnorm_block_fwd from dy, dh (the gradient the stream carries
+ * back into h), the block's output x, the stored h, and the saved r1 and r:
+ *   G    = dh + r w dy - r^3 h (1/H) sum_j w dy h,       dres = res_scale G
+ *   g    = x_scale dropout(G)  (the forward's mask),     e = g gate gate_tok
+ *   dx   = r1 w_post e - r1^3 x (1/H) sum_j w_post e x   (without w_post: e)
+ *   dw[j]      = sum_t dy h r
+ *   S[j]       = sum_t g gate_tok x r1,  dw_post[j] = gate S,  dgate[j] = w_post S
+ *   dgate_tok[t] = sum_j g gate w_post x r1
+ * dx, dres (dtype) may each be dy or dh exactly, not both the same; dw, dw_post,
+ * dgate [H], dgate_tok [T]: fp32, OVERWRITTEN (T = 0: zeros), needed where their
+ * input is given; no other output may overlap anything.  workspace: >=
+ * ftk_rmsnorm_block_bwd_workspace_bytes(T, H, dtype) bytes, 16-byte aligned,
+ * contents ignored and clobbered.  Column sums are fp32 in a fixed order: bitwise
+ * reproducible run to run on the same device.  The factors, p, seed, offset and
+ * *step have to be the forward's. */
+FTK_API ftk_status ftk_rmsnorm_block_bwd(
+    const void *dy, int64_t lddy, const void *dh, int64_t lddh, const void *x, int64_t ldx,
+    const void *h, int64_t ldh, const void *w_post, const void *gate, const float *gate_tok,
+    const void *w, const float *rstd_post, const float *rstd, void *dx, int64_t lddx, void *dres,
+    int64_t lddr, float *dw_post, float *dgate, float *dgate_tok, float *dw, void *workspace,
+    size_t workspace_bytes, int64_t T, int64_t H, float res_scale, float x_scale, double p,
+    uint64_t seed, uint64_t offset, const int64_t *step, ftk_dtype dtype, ftk_stream_t stream);
+
 /* ------------------------------------------------------ tensor-core GEMM */
 
 /* C = A B^T on the 5th-generation tensor cores: A bf16 [M, lda], B bf16
