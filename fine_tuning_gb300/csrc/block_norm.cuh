@@ -8,6 +8,7 @@
 
 #include "common.cuh"
 #include "launch_residual.h"
+#include "pair_math.cuh"
 #include "philox.cuh"
 
 namespace ftk {
@@ -111,6 +112,253 @@ __device__ __forceinline__ void for_columns(const Philox &g, int thr, int64_t t,
     }
   }
 }
+
+// ------------------------------------------------------------------ row groups
+
+// How the register kernels spread rows: W warps a row, V packets of N columns a
+// thread (column (gi + k 32W) N + e of thread gi), R rows a CTA.  W = 0: the row does
+// not fit, the kernels for any length take it.
+struct BlockPlan {
+  int V, W, R;
+  int threads() const { return 32 * W * R; }
+};
+
+constexpr int kMaxWarps = 20;  // of a row group
+
+inline BlockPlan plan_block_row(int64_t hp, int vmax) {
+  for (int v = 1; v <= vmax; v *= 2) {
+    const int64_t W = ceil_div(hp, (int64_t)32 * v);
+    if (W > kMaxWarps) continue;
+    // rows of one warp need no barrier; of the others at most four groups have one each
+    const int R = W == 1 ? 8 : kMaxWarps / (int)W < 4 ? kMaxWarps / (int)W : 4;
+    return BlockPlan{v, (int)W, R};
+  }
+  return BlockPlan{0, 0, 0};
+}
+
+// The row group's sum of v, to all of its threads, in a fixed order.  slots: room for
+// kMaxWarps floats, 16-byte aligned, unused ones zero; not written again before every
+// thread has passed the next barrier of the group.
+__device__ __forceinline__ float group_sum(float v, float *slots, int W, int wig, int grp) {
+  v = warp_sum(v);
+  if (W == 1) return v;
+  if ((threadIdx.x & 31) == 0) slots[wig] = v;
+  group_barrier(grp, 32 * W);
+  float s = 0.f;
+  for (int i = 0; i < W; i += 4) {
+    const float4 f = *reinterpret_cast<const float4 *>(slots + i);
+    s += (f.x + f.y) + (f.z + f.w);
+  }
+  return s;
+}
+
+// Three sums at once.  In the warp the values are dealt out while they are added
+// (lanes 0-7 end with the first, 8-15 with the second, 16-23 with the third: 6
+// shuffles instead of 15); slots: [3][kMaxWarps + 4] floats.
+__device__ __forceinline__ float3 group_sum3(float a, float b, float c, float *slots, int W,
+                                             int wig, int grp) {
+  const int lane = threadIdx.x & 31;
+  constexpr unsigned kAll = 0xffffffffu;
+  const bool up = lane & 16, up2 = lane & 8;
+  // lanes 0-15 keep a, b; lanes 16-31 keep c (and a zero)
+  const float s0 = up ? a : c, s1 = up ? b : 0.f;
+  float k0 = up ? c : a, k1 = up ? 0.f : b;
+  k0 += __shfl_xor_sync(kAll, s0, 16);
+  k1 += __shfl_xor_sync(kAll, s1, 16);
+  float v = up2 ? k1 : k0;
+  v += __shfl_xor_sync(kAll, up2 ? k0 : k1, 8);
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+  if (W > 1) {
+    constexpr int kRow = kMaxWarps + 4;
+    if ((lane & 7) == 0 && lane < 24) slots[(lane >> 3) * kRow + wig] = v;
+    group_barrier(grp, 32 * W);
+    v = 0.f;
+    if (lane < 24)
+      for (int i = lane & 7; i < W; i += 8) v += slots[(lane >> 3) * kRow + i];
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+  }
+  return make_float3(__shfl_sync(kAll, v, 0), __shfl_sync(kAll, v, 8), __shfl_sync(kAll, v, 16));
+}
+
+// The dropout bits of a thread's packets: bit e of m[k] is column e of packet k.  A
+// bf16 packet is one call's eight columns, an fp32 packet half of them; single
+// columns come from the lanes that make the warp's blocks, 4 for each k.
+template <int N, int V>
+__device__ __forceinline__ void packet_bits(const Philox &g, int thr, uint32_t t, int gi, int G,
+                                            uint32_t (&m)[V]) {
+  const int lane = threadIdx.x & 31;
+  if constexpr (N == 1) {
+    static_assert(V <= 8, "a warp makes 32 blocks");
+    const int mine = (gi - lane + (lane >> 2) * G) / 8 + (lane & 3);
+    const uint32_t b = keep_bits(g, thr, (uint32_t)mine, t);
+#pragma unroll
+    for (int k = 0; k < V; ++k)
+      m[k] = __shfl_sync(0xffffffffu, b, k * 4 + (lane >> 3)) >> (lane & 7);
+  } else {
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      const int c = gi + k * G;
+      const uint32_t b = keep_bits(g, thr, (uint32_t)(c * N / 8), t);
+      m[k] = N == 4 ? b >> (c & 1) * 4 : b;
+    }
+  }
+}
+
+// A packet of N columns as fp32 values: pairs (Blackwell's two-wide fp32 operations,
+// each half rounded like the scalar one), or one float where columns are single.
+template <int N> struct Values {
+  using V = float2;
+  static constexpr int kCount = N / 2;
+};
+template <> struct Values<1> {
+  using V = float;
+  static constexpr int kCount = 1;
+};
+
+__device__ __forceinline__ float vmul(float a, float b) { return a * b; }
+__device__ __forceinline__ float2 vmul(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float vfma(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ float2 vfma(float2 a, float2 b, float2 c) {
+  return __ffma2_rn(a, b, c);
+}
+__device__ __forceinline__ float vsum(float a) { return a; }
+__device__ __forceinline__ float vsum(float2 a) { return a.x + a.y; }
+// value i of a packet, where its bits of m are set, else 0
+__device__ __forceinline__ float vkeep(uint32_t m, int, float a) { return m & 1 ? a : 0.f; }
+__device__ __forceinline__ float2 vkeep(uint32_t m, int i, float2 a) {
+  return make_float2(m >> (2 * i) & 1 ? a.x : 0.f, m >> (2 * i + 1) & 1 ? a.y : 0.f);
+}
+template <typename VT> __device__ __forceinline__ VT vall(float a);
+template <> __device__ __forceinline__ float vall<float>(float a) { return a; }
+template <> __device__ __forceinline__ float2 vall<float2>(float a) { return make_float2(a, a); }
+
+// What a packet is held and moved as: 16 bytes, or one value.
+template <typename T, int N> struct Raw {
+  using type = uint4;
+};
+template <typename T> struct Raw<T, 1> {
+  using type = T;
+};
+
+__device__ __forceinline__ void unpack(const uint4 &u, float2 (&f)[4]) { unpack8(u, f); }
+__device__ __forceinline__ void unpack(const uint4 &u, float2 (&f)[2]) {
+  f[0] = make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
+  f[1] = make_float2(__uint_as_float(u.z), __uint_as_float(u.w));
+}
+__device__ __forceinline__ void unpack(float u, float (&f)[1]) { f[0] = u; }
+__device__ __forceinline__ void unpack(bf16 u, float (&f)[1]) { f[0] = to_float(u); }
+__device__ __forceinline__ void pack(const float2 (&f)[4], uint4 &u) { u = pack8(f); }
+__device__ __forceinline__ void pack(const float2 (&f)[2], uint4 &u) {
+  u = make_uint4(__float_as_uint(f[0].x), __float_as_uint(f[0].y), __float_as_uint(f[1].x),
+                 __float_as_uint(f[1].y));
+}
+__device__ __forceinline__ void pack(const float (&f)[1], float &u) { u = f[0]; }
+__device__ __forceinline__ void pack(const float (&f)[1], bf16 &u) { u = from_float<bf16>(f[0]); }
+
+template <typename R, typename T> __device__ __forceinline__ R load_raw(const T *p) {
+  return *reinterpret_cast<const R *>(p);
+}
+// for data read once
+template <typename R, typename T> __device__ __forceinline__ R load_raw_stream(const T *p) {
+  if constexpr (sizeof(R) == 16) {
+    R u;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
+                 : "l"(p));
+    return u;
+  } else {
+    return *p;
+  }
+}
+template <typename R, typename T> __device__ __forceinline__ void store_raw(T *p, const R &u) {
+  *reinterpret_cast<R *>(p) = u;
+}
+
+// w_post gate of the packet at column c, as far as they are there.
+template <typename T, int N, typename VT>
+__device__ __forceinline__ void column_factors(const BlockNorm<T> &a, int64_t c,
+                                               VT (&f)[Values<N>::kCount]) {
+  using R = typename Raw<T, N>::type;
+#pragma unroll
+  for (int i = 0; i < Values<N>::kCount; ++i) f[i] = vall<VT>(1.f);
+  if (a.w_post != nullptr) unpack(load_raw<R>(a.w_post + c), f);
+  if (a.gate != nullptr) {
+    VT g[Values<N>::kCount];
+    unpack(load_raw<R>(a.gate + c), g);
+#pragma unroll
+    for (int i = 0; i < Values<N>::kCount; ++i) f[i] = vmul(f[i], g[i]);
+  }
+}
+
+// A thread's packets of the rows ahead.  Packets of 16 bytes are copied into a ring in
+// shared memory (cp.async: each thread reads back what it copied itself, so that the
+// ring needs no barrier), kDepth - 1 rows ahead; single columns, which are too small
+// for such copies, wait in registers, one row ahead.
+template <typename T, int N, int V, int B, int kDepth> struct Ahead {
+  uint4 *slot;  // this thread's place in the ring
+  int at;       // the slot of the current row
+  static constexpr size_t bytes(int threads) {
+    return (size_t)threads * kDepth * B * V * sizeof(uint4);
+  }
+  __device__ __forceinline__ uint4 *place(int s, int b, int k) const {
+    return slot + ((s * B + b) * V + k) * (int)blockDim.x;
+  }
+  __device__ __forceinline__ void init(uint4 *ring) { slot = ring + threadIdx.x, at = 0; }
+  // the packets of the row `ahead` slots after the current one; col(k) < 0: none
+  template <typename F, typename C>
+  __device__ __forceinline__ void fetch(int ahead, bool on, F row, C col) {
+    const int s = at + ahead < kDepth ? at + ahead : at + ahead - kDepth;
+    if (on)
+#pragma unroll
+      for (int b = 0; b < B; ++b)
+#pragma unroll
+        for (int k = 0; k < V; ++k)
+          if (col(k) >= 0) cp_async16(place(s, b, k), row(b) + col(k));
+    cp_async_commit();  // a group for each row, empty or not
+  }
+  template <typename F, typename C>
+  __device__ __forceinline__ void start(int64_t t, int64_t step, int64_t rows, F row, C col) {
+#pragma unroll
+    for (int i = 0; i < kDepth - 1; ++i)
+      fetch(i, t + i * step < rows, [&](int b) { return row(b, t + i * step); }, col);
+  }
+  // the current row is there; the one kDepth - 1 rows on is on its way
+  template <typename F, typename C>
+  __device__ __forceinline__ void arrive(int64_t t, int64_t step, int64_t rows, F row, C col) {
+    const int64_t n = t + (kDepth - 1) * step;
+    fetch(kDepth - 1, n < rows, [&](int b) { return row(b, n); }, col);
+    cp_async_wait<kDepth - 1>();
+  }
+  __device__ __forceinline__ uint4 get(int b, int k) const { return *place(at, b, k); }
+  __device__ __forceinline__ void next() { at = at + 1 == kDepth ? 0 : at + 1; }
+};
+
+template <typename T, int V, int B, int kDepth> struct Ahead<T, 1, V, B, kDepth> {
+  T now[B][V], then[B][V];
+  static constexpr size_t bytes(int) { return 0; }
+  __device__ __forceinline__ void init(uint4 *) {}
+  template <typename F, typename C>
+  __device__ __forceinline__ void start(int64_t t, int64_t, int64_t rows, F row, C col) {
+    if (t < rows)
+#pragma unroll
+      for (int b = 0; b < B; ++b)
+#pragma unroll
+        for (int k = 0; k < V; ++k)
+          if (col(k) >= 0) then[b][k] = row(b, t)[col(k)];
+  }
+  template <typename F, typename C>
+  __device__ __forceinline__ void arrive(int64_t t, int64_t step, int64_t rows, F row, C col) {
+#pragma unroll
+    for (int b = 0; b < B; ++b)
+#pragma unroll
+      for (int k = 0; k < V; ++k) now[b][k] = then[b][k];
+    start(t + step, step, rows, row, col);
+  }
+  __device__ __forceinline__ T get(int b, int k) const { return now[b][k]; }
+  __device__ __forceinline__ void next() {}
+};
 
 }  // namespace
 

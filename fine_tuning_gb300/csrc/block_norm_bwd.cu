@@ -66,6 +66,143 @@ __global__ void __launch_bounds__(kThreads) block_norm_bwd_any(const BlockNorm<T
   }
 }
 
+// Rows of up to kMaxWarps warps: a persistent grid, W warps a row, the rows ahead on
+// their way while the group works on the current one.  Each thread keeps its columns'
+// sums for the whole kernel; at the end the CTA's row groups are added in their order.
+// rows in the ring, the current one among them: what 227 KB hold
+template <int V> constexpr int kBwdDepth = V == 1 ? 3 : V == 2 ? 2 : 1;
+
+template <typename T, int N, int V, bool DROP>
+__global__ void __launch_bounds__(32 * kMaxWarps)
+block_norm_bwd_rows(const BlockNorm<T> a, int W, int R) {
+  using VT = typename Values<N>::V;
+  using Rw = typename Raw<T, N>::type;
+  constexpr int P = Values<N>::kCount;
+  constexpr bool kHold = V * N <= 8;  // the weights in registers; else read for each row
+  extern __shared__ uint4 ring[];     // the rows ahead, then [R][2 H] sums when R > 1
+  __shared__ float slots[8][2][3 * (kMaxWarps + 4)];  // group, parity
+  pdl_wait();
+  pdl_trigger();
+  const Philox g = philox_of(a.drop);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int grp = warp / W, wig = warp - grp * W, gi = wig * 32 + lane, G = W * 32;
+  const int hp = a.H / N;
+  auto col = [&](int k) { return gi + k * G < hp ? (gi + k * G) * N : -1; };
+  VT wg[kHold ? V : 1][P], sw[V][P], sx[V][P];
+  Rw w[kHold ? V : 1];
+#pragma unroll
+  for (int k = 0; k < V; ++k) {
+    if constexpr (kHold)
+      if (col(k) >= 0) {
+        column_factors<T, N>(a, col(k), wg[k]);
+        w[k] = load_raw<Rw>(a.w + col(k));
+      }
+#pragma unroll
+    for (int i = 0; i < P; ++i) sw[k][i] = sx[k][i] = vall<VT>(0.f);
+  }
+  const int64_t step = (int64_t)gridDim.x * R;
+  const float beta = a.x_scale * a.drop.scale;
+  auto row = [&](int b, int64_t t) {
+    return b == 0 ? a.x + t * a.ldx : b == 1 ? (const T *)a.h + t * a.ldh
+           : b == 2 ? a.dy + t * a.lddy : a.dh + t * a.lddh;
+  };
+  Ahead<T, N, V, 4, kBwdDepth<V>> in;
+  in.init(ring);
+  int64_t t = (int64_t)blockIdx.x * R + grp;
+  in.start(t, step, a.rows, row, col);
+  float r1_next = 1.f, r2_next = 0.f, tok_next = 1.f;
+  auto scalars = [&](int64_t n) {
+    if (n >= a.rows) return;
+    if (a.w_post != nullptr) r1_next = a.rstd_post[n];
+    r2_next = a.rstd[n];
+    if (a.gate_tok != nullptr) tok_next = a.gate_tok[n];
+  };
+  scalars(t);
+  for (int parity = 0; t < a.rows; t += step, parity ^= 1, in.next()) {  // uniform in the group
+    const float r1 = r1_next, r2 = r2_next, gt = tok_next;
+    scalars(t + step);
+    uint32_t m[V];
+    if (DROP) packet_bits<N, V>(g, a.drop.thr, (uint32_t)t, gi, G, m);
+    in.arrive(t, step, a.rows, row, col);
+    const VT r1v = vall<VT>(r1), r2v = vall<VT>(r2);
+    VT s_h = vall<VT>(0.f), s_g = s_h, s_c = s_h;  // w dy hn, q (dh + r2 w dy), q hn
+#pragma unroll
+    for (int k = 0; k < V; ++k)
+      if (col(k) >= 0) {
+        VT x[P], h[P], dy[P], dh[P], f[P], wf[P];
+        unpack(in.get(0, k), x);
+        unpack(in.get(1, k), h);
+        unpack(in.get(2, k), dy);
+        unpack(in.get(3, k), dh);
+        unpack(kHold ? w[kHold ? k : 0] : load_raw<Rw>(a.w + col(k)), wf);
+        if constexpr (!kHold) column_factors<T, N>(a, col(k), f);
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+          const VT wd = vmul(wf[i], dy[i]), hn = vmul(h[i], r2v);
+          VT q = vmul(kHold ? wg[kHold ? k : 0][i] : f[i], vmul(x[i], r1v));
+          if (DROP) q = vkeep(m[k], i, q);
+          s_h = vfma(wd, hn, s_h);
+          s_g = vfma(q, vfma(r2v, wd, dh[i]), s_g);
+          s_c = vfma(q, hn, s_c);
+        }
+      }
+    const float3 s =
+        group_sum3(vsum(s_h), vsum(s_g), vsum(s_c), slots[grp][parity], W, wig, grp);
+    const float kk = r2 * (s.x * a.inv_h);
+    const float c1 = beta * fmaf(-kk, s.z, s.y);
+    if (a.dgate_tok != nullptr && gi == 0) a.dgate_tok[t] = c1;
+    const VT nkk = vall<VT>(-kk), bg = vall<VT>(beta * gt), rs = vall<VT>(a.res_scale);
+    const VT nam = vall<VT>(a.w_post != nullptr ? -r1 * (gt * c1 * a.inv_h) : 0.f);
+#pragma unroll
+    for (int k = 0; k < V; ++k)
+      if (col(k) >= 0) {
+        VT x[P], h[P], dy[P], dh[P], f[P], wf[P];
+        unpack(in.get(0, k), x);
+        unpack(in.get(1, k), h);
+        unpack(in.get(2, k), dy);
+        unpack(in.get(3, k), dh);
+        unpack(kHold ? w[kHold ? k : 0] : load_raw<Rw>(a.w + col(k)), wf);
+        if constexpr (!kHold) column_factors<T, N>(a, col(k), f);
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+          const VT hn = vmul(h[i], r2v), xn = vmul(x[i], r1v);
+          const VT Gv = vfma(nkk, hn, vfma(r2v, vmul(wf[i], dy[i]), dh[i]));
+          VT gm = vmul(bg, Gv);
+          if (DROP) gm = vkeep(m[k], i, gm);
+          sw[k][i] = vfma(dy[i], hn, sw[k][i]);
+          sx[k][i] = vfma(gm, xn, sx[k][i]);
+          dh[i] = vmul(rs, Gv);
+          x[i] = vfma(nam, xn, vmul(r1v, vmul(gm, kHold ? wg[kHold ? k : 0][i] : f[i])));
+        }
+        Rw o;
+        pack(dh, o);
+        store_raw(a.dres + t * a.lddr + col(k), o);
+        pack(x, o);
+        store_raw(a.dx + t * a.lddx + col(k), o);
+      }
+  }
+  cp_async_wait<0>();
+  if (R > 1) __syncthreads();  // the ring becomes the row groups' sums
+  float *const dst = a.ws + (int64_t)blockIdx.x * 2 * a.H;
+  float *const comb = reinterpret_cast<float *>(ring);
+  float *const mine = R > 1 ? comb + grp * 2 * a.H : dst;
+#pragma unroll
+  for (int k = 0; k < V; ++k)
+    if (col(k) >= 0)
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        reinterpret_cast<VT *>(mine + col(k))[i] = sw[k][i];
+        reinterpret_cast<VT *>(mine + a.H + col(k))[i] = sx[k][i];
+      }
+  if (R == 1) return;
+  __syncthreads();
+  for (int j = threadIdx.x; j < 2 * a.H; j += blockDim.x) {
+    float v = comb[j];
+    for (int i = 1; i < R; ++i) v += comb[i * 2 * a.H + j];
+    dst[j] = v;
+  }
+}
+
 constexpr int kReduceWarps = 32;
 
 // dw[j] = sum_p ws[p][j]; S[j] = sum_p ws[p][H + j], dw_post = gate S, dgate = w_post S.
@@ -109,13 +246,43 @@ cudaError_t reduce(const BlockNormArgs &a, int64_t P, cudaStream_t s) {
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-template <typename T>
-cudaError_t bwd_typed(bool, const BlockNormArgs &a, const DeviceInfo &dev, cudaStream_t s) {
-  if (a.T == 0) return reduce<T>(a, 0, s);
+template <typename T, int N, int V>
+cudaError_t bwd_rows(const BlockPlan &p, const BlockNormArgs &a, const DeviceInfo &dev,
+                     cudaStream_t s) {
+  auto kern = a.drop.thr > 0 ? block_norm_bwd_rows<T, N, V, true>
+                             : block_norm_bwd_rows<T, N, V, false>;
+  size_t smem = Ahead<T, N, V, 4, kBwdDepth<V>>::bytes(p.threads());
+  const size_t sums = p.R > 1 ? (size_t)p.R * 2 * (size_t)a.H * sizeof(float) : 0;
+  if (sums > smem) smem = sums;
+  const int occ = blocks_per_sm((const void *)kern, p.threads(), smem, dev, kMaxBlocksPerSm);
+  int64_t P = ceil_div(a.T, (int64_t)p.R);
+  if (P > (int64_t)dev.sms * occ) P = (int64_t)dev.sms * occ;
+  cudaError_t e = launch_pdl(kern, dim3((unsigned)P), dim3(p.threads()), smem, s,
+                             block_norm_params<T>(a), p.W, p.R);
+  return e != cudaSuccess ? e : reduce<T>(a, P, s);
+}
+
+template <typename T, int N>
+cudaError_t bwd_packets(const BlockNormArgs &a, const DeviceInfo &dev, cudaStream_t s) {
+  const BlockPlan p = plan_block_row(a.H / N, N == 1 ? 8 : 4);
+  switch (p.V) {
+    case 1: return bwd_rows<T, N, 1>(p, a, dev, s);
+    case 2: return bwd_rows<T, N, 2>(p, a, dev, s);
+    case 4: return bwd_rows<T, N, 4>(p, a, dev, s);
+    case 8:
+      if constexpr (N == 1) return bwd_rows<T, N, 8>(p, a, dev, s);
+    default: break;
+  }
   const int64_t P = a.T < (int64_t)dev.sms * 4 ? a.T : (int64_t)dev.sms * 4;
   cudaError_t e = launch_pdl(block_norm_bwd_any<T>, dim3((unsigned)P), dim3(kThreads), 0, s,
                              block_norm_params<T>(a));
   return e != cudaSuccess ? e : reduce<T>(a, P, s);
+}
+
+template <typename T>
+cudaError_t bwd_typed(bool vec, const BlockNormArgs &a, const DeviceInfo &dev, cudaStream_t s) {
+  if (a.T == 0) return reduce<T>(a, 0, s);
+  return vec ? bwd_packets<T, VecWidth<T>::value>(a, dev, s) : bwd_packets<T, 1>(a, dev, s);
 }
 
 }  // namespace
