@@ -125,12 +125,13 @@ struct BlockPlan {
 
 constexpr int kMaxWarps = 20;  // of a row group
 
-inline BlockPlan plan_block_row(int64_t hp, int vmax) {
+// `first`: the warps up to which a thread takes one packet; `warps`: those of a CTA.
+inline BlockPlan plan_block_row(int64_t hp, int vmax, int first, int warps) {
   for (int v = 1; v <= vmax; v *= 2) {
     const int64_t W = ceil_div(hp, (int64_t)32 * v);
-    if (W > kMaxWarps) continue;
+    if (W > (v == 1 ? first : warps)) continue;
     // rows of one warp need no barrier; of the others at most four groups have one each
-    const int R = W == 1 ? 8 : kMaxWarps / (int)W < 4 ? kMaxWarps / (int)W : 4;
+    const int R = W == 1 ? 8 : warps / (int)W < 4 ? warps / (int)W : 4;
     return BlockPlan{v, (int)W, R};
   }
   return BlockPlan{0, 0, 0};
@@ -182,29 +183,50 @@ __device__ __forceinline__ float3 group_sum3(float a, float b, float c, float *s
   return make_float3(__shfl_sync(kAll, v, 0), __shfl_sync(kAll, v, 8), __shfl_sync(kAll, v, 16));
 }
 
-// The dropout bits of a thread's packets: bit e of m[k] is column e of packet k.  A
-// bf16 packet is one call's eight columns, an fp32 packet half of them; single
-// columns come from the lanes that make the warp's blocks, 4 for each k.
-template <int N, int V>
-__device__ __forceinline__ void packet_bits(const Philox &g, int thr, uint32_t t, int gi, int G,
-                                            uint32_t (&m)[V]) {
-  const int lane = threadIdx.x & 31;
-  if constexpr (N == 1) {
-    static_assert(V <= 8, "a warp makes 32 blocks");
+// The random words of a thread's packets.  A bf16 packet is one call's eight columns,
+// an fp32 packet half of them; single columns (N = 1) get their bit from the lanes that
+// make the warp's blocks, 4 for each k.
+template <int N, int V> struct Mask {
+  PhiloxBlock p[V];
+  uint32_t cut, m[V][N / 2];
+  __device__ __forceinline__ void init(const Philox &g, int thr, int gi, int G) {
+    cut = keep_cut(thr);
+#pragma unroll
+    for (int k = 0; k < V; ++k) p[k] = philox_block(g, (uint32_t)((gi + k * G) * N / 8));
+  }
+  __device__ __forceinline__ void row(const Philox &g, uint32_t t, int gi, int G) {
+    const uint64_t r = philox_row(g, t);
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      const uint4 u = philox4x32(g, p[k], r);
+      if constexpr (N == 8) {
+        m[k][0] = u.x, m[k][1] = u.y, m[k][2] = u.z, m[k][3] = u.w;
+      } else {
+        const bool odd = (gi + k * G) & 1;
+        m[k][0] = odd ? u.z : u.x, m[k][1] = odd ? u.w : u.y;
+      }
+    }
+  }
+  // value i of packet k where it is kept, else 0
+  __device__ __forceinline__ float2 keep(int k, int i, float2 a) const {
+    return make_float2(keep_low(m[k][i], cut) ? a.x : 0.f, keep_high(m[k][i], cut) ? a.y : 0.f);
+  }
+};
+template <int V> struct Mask<1, V> {
+  static_assert(V <= 8, "a warp makes 32 blocks");
+  int thr;
+  uint32_t m[V];
+  __device__ __forceinline__ void init(const Philox &, int t, int, int) { thr = t; }
+  __device__ __forceinline__ void row(const Philox &g, uint32_t t, int gi, int G) {
+    const int lane = threadIdx.x & 31;
     const int mine = (gi - lane + (lane >> 2) * G) / 8 + (lane & 3);
     const uint32_t b = keep_bits(g, thr, (uint32_t)mine, t);
 #pragma unroll
     for (int k = 0; k < V; ++k)
       m[k] = __shfl_sync(0xffffffffu, b, k * 4 + (lane >> 3)) >> (lane & 7);
-  } else {
-#pragma unroll
-    for (int k = 0; k < V; ++k) {
-      const int c = gi + k * G;
-      const uint32_t b = keep_bits(g, thr, (uint32_t)(c * N / 8), t);
-      m[k] = N == 4 ? b >> (c & 1) * 4 : b;
-    }
   }
-}
+  __device__ __forceinline__ float keep(int k, int, float a) const { return m[k] & 1 ? a : 0.f; }
+};
 
 // A packet of N columns as fp32 values: pairs (Blackwell's two-wide fp32 operations,
 // each half rounded like the scalar one), or one float where columns are single.
@@ -225,11 +247,6 @@ __device__ __forceinline__ float2 vfma(float2 a, float2 b, float2 c) {
 }
 __device__ __forceinline__ float vsum(float a) { return a; }
 __device__ __forceinline__ float vsum(float2 a) { return a.x + a.y; }
-// value i of a packet, where its bits of m are set, else 0
-__device__ __forceinline__ float vkeep(uint32_t m, int, float a) { return m & 1 ? a : 0.f; }
-__device__ __forceinline__ float2 vkeep(uint32_t m, int i, float2 a) {
-  return make_float2(m >> (2 * i) & 1 ? a.x : 0.f, m >> (2 * i + 1) & 1 ? a.y : 0.f);
-}
 template <typename VT> __device__ __forceinline__ VT vall(float a);
 template <> __device__ __forceinline__ float vall<float>(float a) { return a; }
 template <> __device__ __forceinline__ float2 vall<float2>(float a) { return make_float2(a, a); }

@@ -72,6 +72,8 @@ __global__ void __launch_bounds__(kThreads) block_norm_bwd_any(const BlockNorm<T
 // rows in the ring, the current one among them: what 227 KB hold
 template <int V> constexpr int kBwdDepth = V == 1 ? 3 : V == 2 ? 2 : 1;
 
+constexpr int kBwdFirst = 20;
+
 template <typename T, int N, int V, bool DROP>
 __global__ void __launch_bounds__(32 * kMaxWarps)
 block_norm_bwd_rows(const BlockNorm<T> a, int W, int R) {
@@ -100,6 +102,8 @@ block_norm_bwd_rows(const BlockNorm<T> a, int W, int R) {
 #pragma unroll
     for (int i = 0; i < P; ++i) sw[k][i] = sx[k][i] = vall<VT>(0.f);
   }
+  Mask<N, V> mask;
+  if (DROP) mask.init(g, a.drop.thr, gi, G);
   const int64_t step = (int64_t)gridDim.x * R;
   const float beta = a.x_scale * a.drop.scale;
   auto row = [&](int b, int64_t t) {
@@ -121,8 +125,7 @@ block_norm_bwd_rows(const BlockNorm<T> a, int W, int R) {
   for (int parity = 0; t < a.rows; t += step, parity ^= 1, in.next()) {  // uniform in the group
     const float r1 = r1_next, r2 = r2_next, gt = tok_next;
     scalars(t + step);
-    uint32_t m[V];
-    if (DROP) packet_bits<N, V>(g, a.drop.thr, (uint32_t)t, gi, G, m);
+    if (DROP) mask.row(g, (uint32_t)t, gi, G);
     in.arrive(t, step, a.rows, row, col);
     const VT r1v = vall<VT>(r1), r2v = vall<VT>(r2);
     VT s_h = vall<VT>(0.f), s_g = s_h, s_c = s_h;  // w dy hn, q (dh + r2 w dy), q hn
@@ -140,7 +143,7 @@ block_norm_bwd_rows(const BlockNorm<T> a, int W, int R) {
         for (int i = 0; i < P; ++i) {
           const VT wd = vmul(wf[i], dy[i]), hn = vmul(h[i], r2v);
           VT q = vmul(kHold ? wg[kHold ? k : 0][i] : f[i], vmul(x[i], r1v));
-          if (DROP) q = vkeep(m[k], i, q);
+          if (DROP) q = mask.keep(k, i, q);
           s_h = vfma(wd, hn, s_h);
           s_g = vfma(q, vfma(r2v, wd, dh[i]), s_g);
           s_c = vfma(q, hn, s_c);
@@ -168,7 +171,7 @@ block_norm_bwd_rows(const BlockNorm<T> a, int W, int R) {
           const VT hn = vmul(h[i], r2v), xn = vmul(x[i], r1v);
           const VT Gv = vfma(nkk, hn, vfma(r2v, vmul(wf[i], dy[i]), dh[i]));
           VT gm = vmul(bg, Gv);
-          if (DROP) gm = vkeep(m[k], i, gm);
+          if (DROP) gm = mask.keep(k, i, gm);
           sw[k][i] = vfma(dy[i], hn, sw[k][i]);
           sx[k][i] = vfma(gm, xn, sx[k][i]);
           dh[i] = vmul(rs, Gv);
@@ -264,7 +267,7 @@ cudaError_t bwd_rows(const BlockPlan &p, const BlockNormArgs &a, const DeviceInf
 
 template <typename T, int N>
 cudaError_t bwd_packets(const BlockNormArgs &a, const DeviceInfo &dev, cudaStream_t s) {
-  const BlockPlan p = plan_block_row(a.H / N, N == 1 ? 8 : 4);
+  const BlockPlan p = plan_block_row(a.H / N, N == 1 ? 8 : 4, kBwdFirst, kMaxWarps);
   switch (p.V) {
     case 1: return bwd_rows<T, N, 1>(p, a, dev, s);
     case 2: return bwd_rows<T, N, 2>(p, a, dev, s);

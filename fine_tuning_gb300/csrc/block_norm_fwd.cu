@@ -48,8 +48,10 @@ __global__ void __launch_bounds__(kThreads) block_norm_fwd_any(const BlockNorm<T
 // rows in the ring, the current one among them (four packets a thread leave room for two)
 template <int V> constexpr int kFwdDepth = V > 2 ? 2 : 3;
 
+constexpr int kFwdWarps = 16, kFwdFirst = 8;
+
 template <typename T, int N, int V, bool DROP>
-__global__ void __launch_bounds__(32 * kMaxWarps)
+__global__ void __launch_bounds__(32 * kFwdWarps, 2)
 block_norm_fwd_rows(const BlockNorm<T> a, int W, int R) {
   using VT = typename Values<N>::V;
   using Rw = typename Raw<T, N>::type;
@@ -76,6 +78,8 @@ block_norm_fwd_rows(const BlockNorm<T> a, int W, int R) {
         column_factors<T, N>(a, col(k), wg[k]);
         w[k] = load_raw<Rw>(a.w + col(k));
       }
+  Mask<N, V> mask;
+  if (DROP) mask.init(g, a.drop.thr, gi, G);
   const int64_t step = (int64_t)gridDim.x * R;
   auto row = [&](int b, int64_t t) { return b == 0 ? a.x + t * a.ldx : a.res + t * a.ldr; };
   Ahead<T, N, V, 2, kFwdDepth<V>> in;
@@ -87,8 +91,7 @@ block_norm_fwd_rows(const BlockNorm<T> a, int W, int R) {
   for (int parity = 0; t < a.rows; t += step, parity ^= 1, in.next()) {  // uniform in the group
     const float c0 = tok_next * a.x_scale * a.drop.scale;
     if (a.gate_tok != nullptr && t + step < a.rows) tok_next = a.gate_tok[t + step];
-    uint32_t m[V];
-    if (DROP) packet_bits<N, V>(g, a.drop.thr, (uint32_t)t, gi, G, m);
+    if (DROP) mask.row(g, (uint32_t)t, gi, G);
     in.arrive(t, step, a.rows, row, col);
     float r1 = 1.f;
     if (a.w_post != nullptr) {
@@ -117,7 +120,7 @@ block_norm_fwd_rows(const BlockNorm<T> a, int W, int R) {
 #pragma unroll
         for (int i = 0; i < P; ++i) {
           VT b = vmul(vmul(vmul(x[i], r1v), kHold ? wg[kHold ? k : 0][i] : f[i]), c0v);
-          if (DROP) b = vkeep(m[k], i, b);
+          if (DROP) b = mask.keep(k, i, b);
           o[i] = vfma(rs, o[i], b);
         }
         pack(o, h[k]);
@@ -160,7 +163,7 @@ cudaError_t fwd_rows(const BlockPlan &p, const BlockNormArgs &a, const DeviceInf
 
 template <typename T, int N>
 cudaError_t fwd_packets(const BlockNormArgs &a, const DeviceInfo &dev, cudaStream_t s) {
-  const BlockPlan p = plan_block_row(a.H / N, N == 1 ? 8 : 4);
+  const BlockPlan p = plan_block_row(a.H / N, N == 1 ? 8 : 4, kFwdFirst, kFwdWarps);
   switch (p.V) {
     case 1: return fwd_rows<T, N, 1>(p, a, dev, s);
     case 2: return fwd_rows<T, N, 2>(p, a, dev, s);

@@ -3,6 +3,7 @@
 // Elementwise: 2 es bytes an element, one Philox call for eight.
 #include "common.cuh"
 #include "launch_residual.h"
+#include "pair_math.cuh"
 #include "philox.cuh"
 
 namespace ftk {
@@ -10,6 +11,35 @@ namespace ftk {
 namespace {
 
 constexpr int kThreads = 256;
+
+__device__ __forceinline__ uint4 ld_stream(const uint4 *p) {
+  uint4 u;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
+               : "l"(p));
+  return u;
+}
+
+// Eight columns: one packet of bf16, two of fp32.
+__device__ __forceinline__ void unpack_block(const uint4 (&u)[1], float2 (&f)[4]) {
+  unpack8(u[0], f);
+}
+__device__ __forceinline__ void unpack_block(const uint4 (&u)[2], float2 (&f)[4]) {
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    f[2 * k] = make_float2(__uint_as_float(u[k].x), __uint_as_float(u[k].y));
+    f[2 * k + 1] = make_float2(__uint_as_float(u[k].z), __uint_as_float(u[k].w));
+  }
+}
+__device__ __forceinline__ void pack_block(const float2 (&f)[4], uint4 (&u)[1]) {
+  u[0] = pack8(f);
+}
+__device__ __forceinline__ void pack_block(const float2 (&f)[4], uint4 (&u)[2]) {
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    u[k] = make_uint4(__float_as_uint(f[2 * k].x), __float_as_uint(f[2 * k].y),
+                      __float_as_uint(f[2 * k + 1].x), __float_as_uint(f[2 * k + 1].y));
+}
 
 // A warp takes 256 columns of a row: each lane makes the eight bits of its own
 // block, then the warp walks the columns 32 at a time, so that accesses of any
@@ -38,8 +68,73 @@ dropout_cols(const T *x, int64_t ldx, T *y, int64_t ldy, int64_t rows, int64_t H
   }
 }
 
+// Rows of whole 16-byte packets: a thread stays with one block of eight columns and
+// walks the rows, kRows of them at a time, all loads first.  `cols` threads lie along a
+// row (gridDim.y such parts make it up), blockDim.x / cols rows side by side.
+constexpr int kRows = 4;
+
+template <typename T, bool DROP>
+__global__ void __launch_bounds__(kThreads)
+dropout_blocks(const T *x, int64_t ldx, T *y, int64_t ldy, int64_t rows, int blocks, int cols,
+               DropArgs d) {
+  constexpr int kPackets = 8 / VecWidth<T>::value;  // of a block
+  pdl_wait();
+  pdl_trigger();
+  const int r = threadIdx.x / cols, b = blockIdx.y * cols + threadIdx.x - r * cols;
+  const int side = blockDim.x / cols;
+  if (r >= side || b >= blocks) return;
+  const Philox g = philox_of(d);
+  const PhiloxBlock p = philox_block(g, (uint32_t)b);
+  const uint32_t cut = keep_cut(d.thr);
+  const int64_t step = (int64_t)gridDim.x * side;
+  for (int64_t t0 = (int64_t)blockIdx.x * side + r; t0 < rows; t0 += kRows * step) {
+    uint4 v[kRows][kPackets];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i)
+      if (t0 + i * step < rows)
+#pragma unroll
+        for (int k = 0; k < kPackets; ++k)
+          v[i][k] = ld_stream(reinterpret_cast<const uint4 *>(x + (t0 + i * step) * ldx +
+                                                              (int64_t)b * 8) + k);
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const int64_t t = t0 + i * step;
+      if (t < rows) {
+        if (DROP) {
+          const uint4 u = philox4x32(g, p, philox_row(g, (uint32_t)t));
+          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+          float2 f[4];
+          unpack_block(v[i], f);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            f[e] = __fmul2_rn(f[e], make_float2(d.scale, d.scale));
+            if (!keep_low(w[e], cut)) f[e].x = 0.f;
+            if (!keep_high(w[e], cut)) f[e].y = 0.f;
+          }
+          pack_block(f, v[i]);
+        }
+#pragma unroll
+        for (int k = 0; k < kPackets; ++k)
+          reinterpret_cast<uint4 *>(y + t * ldy + (int64_t)b * 8)[k] = v[i][k];
+      }
+    }
+  }
+}
+
 template <typename T>
-cudaError_t launch_typed(bool, const DropoutArgs &a, const DeviceInfo &dev, cudaStream_t s) {
+cudaError_t launch_typed(bool vec, const DropoutArgs &a, const DeviceInfo &dev, cudaStream_t s) {
+  if (vec && a.H % 8 == 0) {
+    const int blocks = (int)(a.H / 8);
+    const int parts = ceil_div(blocks, kThreads), cols = ceil_div(blocks, parts);
+    const int side = kThreads / cols;
+    int64_t grid = ceil_div(a.T, (int64_t)side);
+    const int64_t most = ceil_div((int64_t)dev.sms * 8, (int64_t)parts);
+    if (grid > most) grid = most;
+    auto kern = a.drop.thr > 0 ? dropout_blocks<T, true> : dropout_blocks<T, false>;
+    return launch_pdl(kern, dim3((unsigned)grid, (unsigned)parts),
+                      dim3((unsigned)(side * cols)), 0, s, (const T *)a.x, a.ldx, (T *)a.y, a.ldy,
+                      a.T, blocks, cols, a.drop);
+  }
   const int64_t segs = ceil_div(a.H, (int64_t)256);
   int64_t grid = ceil_div(a.T * segs, (int64_t)(kThreads / 32));
   if (grid > (int64_t)dev.sms * 32) grid = (int64_t)dev.sms * 32;

@@ -44,6 +44,53 @@ __device__ __forceinline__ uint4 philox4x32(const Philox &g, uint32_t c0, uint32
   return make_uint4(c0, c1, c2, c3);
 }
 
+// The same for a thread that stays with one block of columns while it walks rows.  Of
+// the first three rounds' six products four depend on the block (or on nothing) alone
+// and one on the row alone: they are made once, and a call's 20 wide products become 15
+// and one for the row.
+struct PhiloxBlock {
+  uint32_t x, y, z, w;
+};
+
+__device__ __forceinline__ PhiloxBlock philox_block(const Philox &g, uint32_t c0) {
+  const uint64_t a1 = (uint64_t)c0 * 0xD2511F53u, b1 = (uint64_t)g.c2 * 0xCD9E8D57u;
+  const uint64_t b2 = (uint64_t)((uint32_t)(a1 >> 32) ^ g.c3 ^ g.k1) * 0xCD9E8D57u;
+  const uint32_t c0r2 = (uint32_t)(b2 >> 32) ^ (uint32_t)b1 ^ (g.k0 + 0x9E3779B9u);
+  const uint64_t a3 = (uint64_t)c0r2 * 0xD2511F53u;
+  return PhiloxBlock{(uint32_t)a1 ^ (g.k1 + 0xBB67AE85u), (uint32_t)b2 ^ (g.k0 + 2 * 0x9E3779B9u),
+                     (uint32_t)(a3 >> 32) ^ (g.k1 + 2 * 0xBB67AE85u), (uint32_t)a3};
+}
+
+// The row's own product, the same for every block of it.
+__device__ __forceinline__ uint64_t philox_row(const Philox &g, uint32_t t) {
+  return (uint64_t)(__umulhi(g.c2, 0xCD9E8D57u) ^ t ^ g.k0) * 0xD2511F53u;
+}
+
+__device__ __forceinline__ uint4 philox4x32(const Philox &g, const PhiloxBlock &p, uint64_t row) {
+  const uint64_t b3 = (uint64_t)((uint32_t)(row >> 32) ^ p.x) * 0xCD9E8D57u;
+  uint32_t c0 = (uint32_t)(b3 >> 32) ^ p.y, c1 = (uint32_t)b3, c2 = p.z ^ (uint32_t)row, c3 = p.w;
+  uint32_t k0 = g.k0 + 3 * 0x9E3779B9u, k1 = g.k1 + 3 * 0xBB67AE85u;
+#pragma unroll
+  for (int i = 3; i < 10; ++i) {
+    const uint64_t a = (uint64_t)c0 * 0xD2511F53u, b = (uint64_t)c2 * 0xCD9E8D57u;
+    c0 = (uint32_t)(b >> 32) ^ c1 ^ k0;
+    c1 = (uint32_t)b;
+    c2 = (uint32_t)(a >> 32) ^ c3 ^ k1;
+    c3 = (uint32_t)a;
+    k0 += 0x9E3779B9u;
+    k1 += 0xBB67AE85u;
+  }
+  return make_uint4(c0, c1, c2, c3);
+}
+
+// A word's two numbers against thr >= 1 as keep_cut(thr): the high half by comparing
+// the word, whose lower bits do not matter then, the low half shifted up.
+__device__ __forceinline__ uint32_t keep_cut(int thr) {
+  return (uint32_t)(((uint64_t)thr << 16) - 1);
+}
+__device__ __forceinline__ bool keep_low(uint32_t word, uint32_t cut) { return word << 16 > cut; }
+__device__ __forceinline__ bool keep_high(uint32_t word, uint32_t cut) { return word > cut; }
+
 // Number e (0..7) of a call's bits.
 __device__ __forceinline__ int philox_u16(const uint4 &u, int e) {
   const uint32_t w = e < 2 ? u.x : e < 4 ? u.y : e < 6 ? u.z : u.w;
