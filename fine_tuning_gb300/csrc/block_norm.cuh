@@ -137,64 +137,65 @@ inline BlockPlan plan_block_row(int64_t hp, int vmax, int first, int warps) {
   return BlockPlan{0, 0, 0};
 }
 
-// The row group's sum of v, to all of its threads, in a fixed order.  slots: room for
-// kMaxWarps floats, 16-byte aligned, unused ones zero; not written again before every
-// thread has passed the next barrier of the group.
-__device__ __forceinline__ float group_sum(float v, float *slots, int W, int wig, int grp) {
-  v = warp_sum(v);
-  if (W == 1) return v;
-  if ((threadIdx.x & 31) == 0) slots[wig] = v;
-  group_barrier(grp, 32 * W);
-  float s = 0.f;
-  for (int i = 0; i < W; i += 4) {
-    const float4 f = *reinterpret_cast<const float4 *>(slots + i);
-    s += (f.x + f.y) + (f.z + f.w);
-  }
-  return s;
-}
+// The row group's sums of n values of each thread, to all of them, in a fixed order.
+// The values are dealt out while a warp adds its lanes: each step hands half of the
+// values to half of the lanes (n = 2 takes 5 shuffles instead of 10, n = 3 6 instead of
+// 15, n = 6 9 instead of 30), so that lanes [i L, (i + 1) L) end with value i.  The warps'
+// sums meet in slots ([n][kMaxWarps]), which may be written again once every thread has
+// passed the group's next barrier.
+template <int n> struct Deal {
+  static constexpr int kPow = n <= 1 ? 1 : n <= 2 ? 2 : n <= 4 ? 4 : 8;
+  static constexpr int L = 32 / kPow;
+};
 
-// Three sums at once.  In the warp the values are dealt out while they are added
-// (lanes 0-7 end with the first, 8-15 with the second, 16-23 with the third: 6
-// shuffles instead of 15); slots: [3][kMaxWarps + 4] floats.
-__device__ __forceinline__ float3 group_sum3(float a, float b, float c, float *slots, int W,
-                                             int wig, int grp) {
-  const int lane = threadIdx.x & 31;
+template <int n>
+__device__ __forceinline__ void group_sums(float (&v)[n], float *slots, int W, int wig, int grp) {
   constexpr unsigned kAll = 0xffffffffu;
-  const bool up = lane & 16, up2 = lane & 8;
-  // lanes 0-15 keep a, b; lanes 16-31 keep c (and a zero)
-  const float s0 = up ? a : c, s1 = up ? b : 0.f;
-  float k0 = up ? c : a, k1 = up ? 0.f : b;
-  k0 += __shfl_xor_sync(kAll, s0, 16);
-  k1 += __shfl_xor_sync(kAll, s1, 16);
-  float v = up2 ? k1 : k0;
-  v += __shfl_xor_sync(kAll, up2 ? k0 : k1, 8);
+  constexpr int kPow = Deal<n>::kPow, L = Deal<n>::L;
+  const int lane = threadIdx.x & 31;
+  float d[kPow];
 #pragma unroll
-  for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
-  if (W > 1) {
-    constexpr int kRow = kMaxWarps + 4;
-    if ((lane & 7) == 0 && lane < 24) slots[(lane >> 3) * kRow + wig] = v;
-    group_barrier(grp, 32 * W);
-    v = 0.f;
-    if (lane < 24)
-      for (int i = lane & 7; i < W; i += 8) v += slots[(lane >> 3) * kRow + i];
+  for (int i = 0; i < kPow; ++i) d[i] = i < n ? v[i] : 0.f;
 #pragma unroll
-    for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+  for (int m = kPow / 2, o = 16; m > 0; m /= 2, o /= 2) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int i = 0; i < kPow / 2; ++i)
+      if (i < m) {
+        const float out = up ? d[i] : d[i + m];
+        d[i] = (up ? d[i + m] : d[i]) + __shfl_xor_sync(kAll, out, o);
+      }
   }
-  return make_float3(__shfl_sync(kAll, v, 0), __shfl_sync(kAll, v, 8), __shfl_sync(kAll, v, 16));
+#pragma unroll
+  for (int o = L / 2; o > 0; o /= 2) d[0] += __shfl_xor_sync(kAll, d[0], o);
+  if (W > 1) {
+    const int i = lane / L, sub = lane % L;
+    if (sub == 0 && i < n) slots[i * kMaxWarps + wig] = d[0];
+    group_barrier(grp, 32 * W);
+    d[0] = 0.f;
+#pragma unroll
+    for (int k = 0; k < (kMaxWarps + L - 1) / L; ++k)
+      if (i < n && sub + k * L < W) d[0] += slots[i * kMaxWarps + sub + k * L];
+#pragma unroll
+    for (int o = L / 2; o > 0; o /= 2) d[0] += __shfl_xor_sync(kAll, d[0], o);
+  }
+#pragma unroll
+  for (int i = 0; i < n; ++i) v[i] = n == 1 ? d[0] : __shfl_sync(kAll, d[0], i * L);
 }
 
-// The random words of a thread's packets.  A bf16 packet is one call's eight columns,
+// The random numbers of a thread's packets.  A bf16 packet is one call's eight columns,
 // an fp32 packet half of them; single columns (N = 1) get their bit from the lanes that
 // make the warp's blocks, 4 for each k.
 template <int N, int V> struct Mask {
   PhiloxBlock p[V];
-  uint32_t cut, m[V][N / 2];
+  uint32_t cut;
+  using Row = uint32_t[V][N / 2];
   __device__ __forceinline__ void init(const Philox &g, int thr, int gi, int G) {
     cut = keep_cut(thr);
 #pragma unroll
     for (int k = 0; k < V; ++k) p[k] = philox_block(g, (uint32_t)((gi + k * G) * N / 8));
   }
-  __device__ __forceinline__ void row(const Philox &g, uint32_t t, int gi, int G) {
+  __device__ __forceinline__ void row(const Philox &g, uint32_t t, int gi, int G, Row &m) const {
     const uint64_t r = philox_row(g, t);
 #pragma unroll
     for (int k = 0; k < V; ++k) {
@@ -208,16 +209,16 @@ template <int N, int V> struct Mask {
     }
   }
   // value i of packet k where it is kept, else 0
-  __device__ __forceinline__ float2 keep(int k, int i, float2 a) const {
+  __device__ __forceinline__ float2 keep(const Row &m, int k, int i, float2 a) const {
     return make_float2(keep_low(m[k][i], cut) ? a.x : 0.f, keep_high(m[k][i], cut) ? a.y : 0.f);
   }
 };
 template <int V> struct Mask<1, V> {
   static_assert(V <= 8, "a warp makes 32 blocks");
   int thr;
-  uint32_t m[V];
+  using Row = uint32_t[V];
   __device__ __forceinline__ void init(const Philox &, int t, int, int) { thr = t; }
-  __device__ __forceinline__ void row(const Philox &g, uint32_t t, int gi, int G) {
+  __device__ __forceinline__ void row(const Philox &g, uint32_t t, int gi, int G, Row &m) const {
     const int lane = threadIdx.x & 31;
     const int mine = (gi - lane + (lane >> 2) * G) / 8 + (lane & 3);
     const uint32_t b = keep_bits(g, thr, (uint32_t)mine, t);
@@ -225,7 +226,9 @@ template <int V> struct Mask<1, V> {
     for (int k = 0; k < V; ++k)
       m[k] = __shfl_sync(0xffffffffu, b, k * 4 + (lane >> 3)) >> (lane & 7);
   }
-  __device__ __forceinline__ float keep(int k, int, float a) const { return m[k] & 1 ? a : 0.f; }
+  __device__ __forceinline__ float keep(const Row &m, int k, int, float a) const {
+    return m[k] & 1 ? a : 0.f;
+  }
 };
 
 // A packet of N columns as fp32 values: pairs (Blackwell's two-wide fp32 operations,
@@ -309,73 +312,98 @@ __device__ __forceinline__ void column_factors(const BlockNorm<T> &a, int64_t c,
   }
 }
 
-// A thread's packets of the rows ahead.  Packets of 16 bytes are copied into a ring in
-// shared memory (cp.async: each thread reads back what it copied itself, so that the
-// ring needs no barrier), kDepth - 1 rows ahead; single columns, which are too small
-// for such copies, wait in registers, one row ahead.
-template <typename T, int N, int V, int B, int kDepth> struct Ahead {
-  uint4 *slot;  // this thread's place in the ring
-  int at;       // the slot of the current row
-  static constexpr size_t bytes(int threads) {
-    return (size_t)threads * kDepth * B * V * sizeof(uint4);
-  }
-  __device__ __forceinline__ uint4 *place(int s, int b, int k) const {
-    return slot + ((s * B + b) * V + k) * (int)blockDim.x;
-  }
-  __device__ __forceinline__ void init(uint4 *ring) { slot = ring + threadIdx.x, at = 0; }
-  // the packets of the row `ahead` slots after the current one; col(k) < 0: none
-  template <typename F, typename C>
-  __device__ __forceinline__ void fetch(int ahead, bool on, F row, C col) {
-    const int s = at + ahead < kDepth ? at + ahead : at + ahead - kDepth;
-    if (on)
-#pragma unroll
-      for (int b = 0; b < B; ++b)
-#pragma unroll
-        for (int k = 0; k < V; ++k)
-          if (col(k) >= 0) cp_async16(place(s, b, k), row(b) + col(k));
-    cp_async_commit();  // a group for each row, empty or not
-  }
-  template <typename F, typename C>
-  __device__ __forceinline__ void start(int64_t t, int64_t step, int64_t rows, F row, C col) {
-#pragma unroll
-    for (int i = 0; i < kDepth - 1; ++i)
-      fetch(i, t + i * step < rows, [&](int b) { return row(b, t + i * step); }, col);
-  }
-  // the current row is there; the one kDepth - 1 rows on is on its way
-  template <typename F, typename C>
-  __device__ __forceinline__ void arrive(int64_t t, int64_t step, int64_t rows, F row, C col) {
-    const int64_t n = t + (kDepth - 1) * step;
-    fetch(kDepth - 1, n < rows, [&](int b) { return row(b, n); }, col);
-    cp_async_wait<kDepth - 1>();
-  }
-  __device__ __forceinline__ uint4 get(int b, int k) const { return *place(at, b, k); }
-  __device__ __forceinline__ void next() { at = at + 1 == kDepth ? 0 : at + 1; }
+// A thread's packets (V of each of S source tensors, B rows at a time) of the rows ahead.
+// Packets of 16 bytes are copied into a ring in shared memory (cp.async: each thread
+// reads back what it copied itself, so that the ring needs no barrier), kDepth - 1 turns
+// ahead; single columns, which are too small for such copies, wait in registers, one
+// turn ahead.
+template <typename T, int S> struct Sources {
+  const T *at[S];   // at the next row to fetch, this thread's first column
+  int64_t row[S];   // elements from one row of the group to its next
+  int64_t t, step, rows;
 };
 
-template <typename T, int V, int B, int kDepth> struct Ahead<T, 1, V, B, kDepth> {
-  T now[B][V], then[B][V];
+template <typename T, int N, int V, int S, int B, int kDepth> struct Ahead {
+  using R = uint4;
+  uint4 *slot;  // this thread's place in the ring
+  int turn;
+  static constexpr size_t bytes(int threads) {
+    return (size_t)threads * kDepth * S * B * V * sizeof(uint4);
+  }
+  __device__ __forceinline__ uint4 *place(int d, int s, int b, int k) const {
+    return slot + (((d * S + s) * B + b) * V + k) * (int)blockDim.x;
+  }
+  // on: bit k of the packets that this thread has
+  __device__ __forceinline__ void fetch(int d, Sources<T, S> &src, int G, uint32_t on) {
+#pragma unroll
+    for (int b = 0; b < B; ++b)
+      if (src.t + b * src.step < src.rows)
+#pragma unroll
+        for (int s = 0; s < S; ++s)
+#pragma unroll
+          for (int k = 0; k < V; ++k)
+            if (on >> k & 1) cp_async16(place(d, s, b, k), src.at[s] + b * src.row[s] + k * G * N);
+    cp_async_commit();  // a group for each turn, empty or not
+    src.t += B * src.step;
+#pragma unroll
+    for (int s = 0; s < S; ++s) src.at[s] += B * src.row[s];
+  }
+  __device__ __forceinline__ void start(uint4 *ring, Sources<T, S> &src, int G, uint32_t on) {
+    slot = ring + threadIdx.x;
+    turn = 0;
+#pragma unroll
+    for (int i = 0; i < kDepth - 1; ++i) fetch(i, src, G, on);
+  }
+  // the current turn's rows are there, the last of the ring's on their way
+  __device__ __forceinline__ void arrive(Sources<T, S> &src, int G, uint32_t on) {
+    fetch(turn == 0 ? kDepth - 1 : turn - 1, src, G, on);
+    cp_async_wait<kDepth - 1>();
+  }
+  __device__ __forceinline__ uint4 get(int s, int b, int k) const { return *place(turn, s, b, k); }
+  __device__ __forceinline__ void next() { turn = turn + 1 == kDepth ? 0 : turn + 1; }
+};
+
+template <typename T, int V, int S, int B, int kDepth> struct Ahead<T, 1, V, S, B, kDepth> {
+  using R = T;
+  T now[S][B][V], then[S][B][V];
   static constexpr size_t bytes(int) { return 0; }
-  __device__ __forceinline__ void init(uint4 *) {}
-  template <typename F, typename C>
-  __device__ __forceinline__ void start(int64_t t, int64_t, int64_t rows, F row, C col) {
-    if (t < rows)
+  __device__ __forceinline__ void start(uint4 *, Sources<T, S> &src, int G, uint32_t on) {
+#pragma unroll
+    for (int b = 0; b < B; ++b)
+      if (src.t + b * src.step < src.rows)
+#pragma unroll
+        for (int s = 0; s < S; ++s)
+#pragma unroll
+          for (int k = 0; k < V; ++k)
+            if (on >> k & 1) then[s][b][k] = src.at[s][b * src.row[s] + k * G];
+    src.t += B * src.step;
+#pragma unroll
+    for (int s = 0; s < S; ++s) src.at[s] += B * src.row[s];
+  }
+  __device__ __forceinline__ void arrive(Sources<T, S> &src, int G, uint32_t on) {
+#pragma unroll
+    for (int s = 0; s < S; ++s)
 #pragma unroll
       for (int b = 0; b < B; ++b)
 #pragma unroll
-        for (int k = 0; k < V; ++k)
-          if (col(k) >= 0) then[b][k] = row(b, t)[col(k)];
+        for (int k = 0; k < V; ++k) now[s][b][k] = then[s][b][k];
+    start(nullptr, src, G, on);
   }
-  template <typename F, typename C>
-  __device__ __forceinline__ void arrive(int64_t t, int64_t step, int64_t rows, F row, C col) {
-#pragma unroll
-    for (int b = 0; b < B; ++b)
-#pragma unroll
-      for (int k = 0; k < V; ++k) now[b][k] = then[b][k];
-    start(t + step, step, rows, row, col);
-  }
-  __device__ __forceinline__ T get(int b, int k) const { return now[b][k]; }
+  __device__ __forceinline__ T get(int s, int b, int k) const { return now[s][b][k]; }
   __device__ __forceinline__ void next() {}
 };
+
+// Where a thread stands: its row group and its place in it.
+struct Place {
+  int grp, wig, gi, G;
+};
+__device__ __forceinline__ Place place_of(int W) {
+  // from lane 0, so that the compiler knows it to be the same in the whole warp and
+  // keeps the row's addresses in uniform registers
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0);
+  const int grp = warp / W, wig = warp - grp * W;
+  return Place{grp, wig, wig * 32 + (int)(threadIdx.x & 31), W * 32};
+}
 
 }  // namespace
 

@@ -66,38 +66,40 @@ __global__ void __launch_bounds__(kThreads) block_norm_bwd_any(const BlockNorm<T
   }
 }
 
-// Rows of up to kMaxWarps warps: a persistent grid, W warps a row, the rows ahead on
-// their way while the group works on the current one.  Each thread keeps its columns'
-// sums for the whole kernel; at the end the CTA's row groups are added in their order.
-// rows in the ring, the current one among them: what 227 KB hold
-template <int V> constexpr int kBwdDepth = V == 1 ? 3 : V == 2 ? 2 : 1;
-
+// Rows of up to kMaxWarps warps: a persistent grid, W warps a row, B rows at a time (which
+// share the weights in registers, the barrier and the shuffles), the rows ahead on their
+// way while the group works on the current ones.  Each thread keeps its columns' sums
+// for the whole kernel; at the end the CTA's row groups are added in their order.
 constexpr int kBwdFirst = 20;
+template <int N, int V> constexpr int kBwdRows = N > 1 && V == 1 ? 2 : 1;
+// turns in the ring, the current one among them: what 227 KB hold
+template <int V> constexpr int kBwdDepth = V <= 2 ? 2 : 1;
 
 template <typename T, int N, int V, bool DROP>
 __global__ void __launch_bounds__(32 * kMaxWarps)
 block_norm_bwd_rows(const BlockNorm<T> a, int W, int R) {
   using VT = typename Values<N>::V;
   using Rw = typename Raw<T, N>::type;
-  constexpr int P = Values<N>::kCount;
+  constexpr int P = Values<N>::kCount, B = kBwdRows<N, V>;
   constexpr bool kHold = V * N <= 8;  // the weights in registers; else read for each row
   extern __shared__ uint4 ring[];     // the rows ahead, then [R][2 H] sums when R > 1
-  __shared__ float slots[8][2][3 * (kMaxWarps + 4)];  // group, parity
+  __shared__ float slots[8][2][3 * B * kMaxWarps];  // group, parity
   pdl_wait();
   pdl_trigger();
   const Philox g = philox_of(a.drop);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int grp = warp / W, wig = warp - grp * W, gi = wig * 32 + lane, G = W * 32;
-  const int hp = a.H / N;
-  auto col = [&](int k) { return gi + k * G < hp ? (gi + k * G) * N : -1; };
+  const auto [grp, wig, gi, G] = place_of(W);
+  const int c0 = gi * N;
+  uint32_t on = 0;
+#pragma unroll
+  for (int k = 0; k < V; ++k) on |= (gi + k * G) * N < a.H ? 1u << k : 0u;
   VT wg[kHold ? V : 1][P], sw[V][P], sx[V][P];
   Rw w[kHold ? V : 1];
 #pragma unroll
   for (int k = 0; k < V; ++k) {
     if constexpr (kHold)
-      if (col(k) >= 0) {
-        column_factors<T, N>(a, col(k), wg[k]);
-        w[k] = load_raw<Rw>(a.w + col(k));
+      if (on >> k & 1) {
+        column_factors<T, N>(a, c0 + k * G * N, wg[k]);
+        w[k] = load_raw<Rw>(a.w + c0 + k * G * N);
       }
 #pragma unroll
     for (int i = 0; i < P; ++i) sw[k][i] = sx[k][i] = vall<VT>(0.f);
@@ -106,96 +108,114 @@ block_norm_bwd_rows(const BlockNorm<T> a, int W, int R) {
   if (DROP) mask.init(g, a.drop.thr, gi, G);
   const int64_t step = (int64_t)gridDim.x * R;
   const float beta = a.x_scale * a.drop.scale;
-  auto row = [&](int b, int64_t t) {
-    return b == 0 ? a.x + t * a.ldx : b == 1 ? (const T *)a.h + t * a.ldh
-           : b == 2 ? a.dy + t * a.lddy : a.dh + t * a.lddh;
-  };
-  Ahead<T, N, V, 4, kBwdDepth<V>> in;
-  in.init(ring);
   int64_t t = (int64_t)blockIdx.x * R + grp;
-  in.start(t, step, a.rows, row, col);
-  float r1_next = 1.f, r2_next = 0.f, tok_next = 1.f;
+  Sources<T, 4> src{{a.x + t * a.ldx + c0, a.h + t * a.ldh + c0, a.dy + t * a.lddy + c0,
+                     a.dh + t * a.lddh + c0},
+                    {step * a.ldx, step * a.ldh, step * a.lddy, step * a.lddh}, t, step, a.rows};
+  Ahead<T, N, V, 4, B, kBwdDepth<V>> in;
+  in.start(ring, src, G, on);
+  T *dxr = a.dx + t * a.lddx + c0, *drr = a.dres + t * a.lddr + c0;
+  float r1_next[B], r2_next[B], tok_next[B];
   auto scalars = [&](int64_t n) {
-    if (n >= a.rows) return;
-    if (a.w_post != nullptr) r1_next = a.rstd_post[n];
-    r2_next = a.rstd[n];
-    if (a.gate_tok != nullptr) tok_next = a.gate_tok[n];
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+      const bool there = n + b * step < a.rows;
+      r1_next[b] = there && a.w_post != nullptr ? a.rstd_post[n + b * step] : 1.f;
+      r2_next[b] = there ? a.rstd[n + b * step] : 0.f;
+      tok_next[b] = there && a.gate_tok != nullptr ? a.gate_tok[n + b * step] : 1.f;
+    }
   };
   scalars(t);
-  for (int parity = 0; t < a.rows; t += step, parity ^= 1, in.next()) {  // uniform in the group
-    const float r1 = r1_next, r2 = r2_next, gt = tok_next;
-    scalars(t + step);
-    if (DROP) mask.row(g, (uint32_t)t, gi, G);
-    in.arrive(t, step, a.rows, row, col);
-    const VT r1v = vall<VT>(r1), r2v = vall<VT>(r2);
-    VT s_h = vall<VT>(0.f), s_g = s_h, s_c = s_h;  // w dy hn, q (dh + r2 w dy), q hn
+  for (int parity = 0; t < a.rows; t += B * step, parity ^= 1, in.next()) {  // group-uniform
+    float r1[B], r2[B], gt[B], s[3 * B];
 #pragma unroll
-    for (int k = 0; k < V; ++k)
-      if (col(k) >= 0) {
-        VT x[P], h[P], dy[P], dh[P], f[P], wf[P];
-        unpack(in.get(0, k), x);
-        unpack(in.get(1, k), h);
-        unpack(in.get(2, k), dy);
-        unpack(in.get(3, k), dh);
-        unpack(kHold ? w[kHold ? k : 0] : load_raw<Rw>(a.w + col(k)), wf);
-        if constexpr (!kHold) column_factors<T, N>(a, col(k), f);
+    for (int b = 0; b < B; ++b) r1[b] = r1_next[b], r2[b] = r2_next[b], gt[b] = tok_next[b];
+    scalars(t + B * step);
+    typename Mask<N, V>::Row m[B];
+    if (DROP)
 #pragma unroll
-        for (int i = 0; i < P; ++i) {
-          const VT wd = vmul(wf[i], dy[i]), hn = vmul(h[i], r2v);
-          VT q = vmul(kHold ? wg[kHold ? k : 0][i] : f[i], vmul(x[i], r1v));
-          if (DROP) q = mask.keep(k, i, q);
-          s_h = vfma(wd, hn, s_h);
-          s_g = vfma(q, vfma(r2v, wd, dh[i]), s_g);
-          s_c = vfma(q, hn, s_c);
+      for (int b = 0; b < B; ++b) mask.row(g, (uint32_t)(t + b * step), gi, G, m[b]);
+    in.arrive(src, G, on);
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+      const VT r1v = vall<VT>(r1[b]), r2v = vall<VT>(r2[b]);
+      VT s_h = vall<VT>(0.f), s_g = s_h, s_c = s_h;  // w dy hn, q (dh + r2 w dy), q hn
+      if (t + b * step < a.rows)
+#pragma unroll
+        for (int k = 0; k < V; ++k)
+          if (on >> k & 1) {
+            VT x[P], h[P], dy[P], dh[P], f[P], wf[P];
+            unpack(in.get(0, b, k), x);
+            unpack(in.get(1, b, k), h);
+            unpack(in.get(2, b, k), dy);
+            unpack(in.get(3, b, k), dh);
+            unpack(kHold ? w[kHold ? k : 0] : load_raw<Rw>(a.w + c0 + k * G * N), wf);
+            if constexpr (!kHold) column_factors<T, N>(a, c0 + k * G * N, f);
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+              const VT wd = vmul(wf[i], dy[i]), hn = vmul(h[i], r2v);
+              VT q = vmul(kHold ? wg[kHold ? k : 0][i] : f[i], vmul(x[i], r1v));
+              if (DROP) q = mask.keep(m[b], k, i, q);
+              s_h = vfma(wd, hn, s_h);
+              s_g = vfma(q, vfma(r2v, wd, dh[i]), s_g);
+              s_c = vfma(q, hn, s_c);
+            }
+          }
+      s[3 * b] = vsum(s_h), s[3 * b + 1] = vsum(s_g), s[3 * b + 2] = vsum(s_c);
+    }
+    group_sums<3 * B>(s, slots[grp][parity], W, wig, grp);
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+      if (t + b * step >= a.rows) break;
+      const float kk = r2[b] * (s[3 * b] * a.inv_h);
+      const float c1 = beta * fmaf(-kk, s[3 * b + 2], s[3 * b + 1]);
+      if (a.dgate_tok != nullptr && gi == 0) a.dgate_tok[t + b * step] = c1;
+      const VT r1v = vall<VT>(r1[b]), r2v = vall<VT>(r2[b]);
+      const VT nkk = vall<VT>(-kk), bg = vall<VT>(beta * gt[b]), rs = vall<VT>(a.res_scale);
+      const VT nam = vall<VT>(a.w_post != nullptr ? -r1[b] * (gt[b] * c1 * a.inv_h) : 0.f);
+#pragma unroll
+      for (int k = 0; k < V; ++k)
+        if (on >> k & 1) {
+          VT x[P], h[P], dy[P], dh[P], f[P], wf[P];
+          unpack(in.get(0, b, k), x);
+          unpack(in.get(1, b, k), h);
+          unpack(in.get(2, b, k), dy);
+          unpack(in.get(3, b, k), dh);
+          unpack(kHold ? w[kHold ? k : 0] : load_raw<Rw>(a.w + c0 + k * G * N), wf);
+          if constexpr (!kHold) column_factors<T, N>(a, c0 + k * G * N, f);
+#pragma unroll
+          for (int i = 0; i < P; ++i) {
+            const VT hn = vmul(h[i], r2v), xn = vmul(x[i], r1v);
+            const VT Gv = vfma(nkk, hn, vfma(r2v, vmul(wf[i], dy[i]), dh[i]));
+            VT gm = vmul(bg, Gv);
+            if (DROP) gm = mask.keep(m[b], k, i, gm);
+            sw[k][i] = vfma(dy[i], hn, sw[k][i]);
+            sx[k][i] = vfma(gm, xn, sx[k][i]);
+            dh[i] = vmul(rs, Gv);
+            x[i] = vfma(nam, xn, vmul(r1v, vmul(gm, kHold ? wg[kHold ? k : 0][i] : f[i])));
+          }
+          Rw o;
+          pack(dh, o);
+          store_raw(drr + b * step * a.lddr + k * G * N, o);
+          pack(x, o);
+          store_raw(dxr + b * step * a.lddx + k * G * N, o);
         }
-      }
-    const float3 s =
-        group_sum3(vsum(s_h), vsum(s_g), vsum(s_c), slots[grp][parity], W, wig, grp);
-    const float kk = r2 * (s.x * a.inv_h);
-    const float c1 = beta * fmaf(-kk, s.z, s.y);
-    if (a.dgate_tok != nullptr && gi == 0) a.dgate_tok[t] = c1;
-    const VT nkk = vall<VT>(-kk), bg = vall<VT>(beta * gt), rs = vall<VT>(a.res_scale);
-    const VT nam = vall<VT>(a.w_post != nullptr ? -r1 * (gt * c1 * a.inv_h) : 0.f);
-#pragma unroll
-    for (int k = 0; k < V; ++k)
-      if (col(k) >= 0) {
-        VT x[P], h[P], dy[P], dh[P], f[P], wf[P];
-        unpack(in.get(0, k), x);
-        unpack(in.get(1, k), h);
-        unpack(in.get(2, k), dy);
-        unpack(in.get(3, k), dh);
-        unpack(kHold ? w[kHold ? k : 0] : load_raw<Rw>(a.w + col(k)), wf);
-        if constexpr (!kHold) column_factors<T, N>(a, col(k), f);
-#pragma unroll
-        for (int i = 0; i < P; ++i) {
-          const VT hn = vmul(h[i], r2v), xn = vmul(x[i], r1v);
-          const VT Gv = vfma(nkk, hn, vfma(r2v, vmul(wf[i], dy[i]), dh[i]));
-          VT gm = vmul(bg, Gv);
-          if (DROP) gm = mask.keep(k, i, gm);
-          sw[k][i] = vfma(dy[i], hn, sw[k][i]);
-          sx[k][i] = vfma(gm, xn, sx[k][i]);
-          dh[i] = vmul(rs, Gv);
-          x[i] = vfma(nam, xn, vmul(r1v, vmul(gm, kHold ? wg[kHold ? k : 0][i] : f[i])));
-        }
-        Rw o;
-        pack(dh, o);
-        store_raw(a.dres + t * a.lddr + col(k), o);
-        pack(x, o);
-        store_raw(a.dx + t * a.lddx + col(k), o);
-      }
+    }
+    dxr += B * step * a.lddx;
+    drr += B * step * a.lddr;
   }
   cp_async_wait<0>();
   if (R > 1) __syncthreads();  // the ring becomes the row groups' sums
   float *const dst = a.ws + (int64_t)blockIdx.x * 2 * a.H;
   float *const comb = reinterpret_cast<float *>(ring);
-  float *const mine = R > 1 ? comb + grp * 2 * a.H : dst;
+  float *const mine = (R > 1 ? comb + grp * 2 * a.H : dst) + c0;
 #pragma unroll
   for (int k = 0; k < V; ++k)
-    if (col(k) >= 0)
+    if (on >> k & 1)
 #pragma unroll
       for (int i = 0; i < P; ++i) {
-        reinterpret_cast<VT *>(mine + col(k))[i] = sw[k][i];
-        reinterpret_cast<VT *>(mine + a.H + col(k))[i] = sx[k][i];
+        reinterpret_cast<VT *>(mine + k * G * N)[i] = sw[k][i];
+        reinterpret_cast<VT *>(mine + a.H + k * G * N)[i] = sx[k][i];
       }
   if (R == 1) return;
   __syncthreads();
@@ -254,7 +274,7 @@ cudaError_t bwd_rows(const BlockPlan &p, const BlockNormArgs &a, const DeviceInf
                      cudaStream_t s) {
   auto kern = a.drop.thr > 0 ? block_norm_bwd_rows<T, N, V, true>
                              : block_norm_bwd_rows<T, N, V, false>;
-  size_t smem = Ahead<T, N, V, 4, kBwdDepth<V>>::bytes(p.threads());
+  size_t smem = Ahead<T, N, V, 4, kBwdRows<N, V>, kBwdDepth<V>>::bytes(p.threads());
   const size_t sums = p.R > 1 ? (size_t)p.R * 2 * (size_t)a.H * sizeof(float) : 0;
   if (sums > smem) smem = sums;
   const int occ = blocks_per_sm((const void *)kern, p.threads(), smem, dev, kMaxBlocksPerSm);

@@ -43,109 +43,141 @@ __global__ void __launch_bounds__(kThreads) block_norm_fwd_any(const BlockNorm<T
   }
 }
 
-// Rows of up to kMaxWarps warps: a persistent grid, W warps a row, the rows ahead on
-// their way while the group works on the current one.
-// rows in the ring, the current one among them (four packets a thread leave room for two)
+// Rows of up to kFwdWarps warps: a persistent grid, W warps a row, B rows at a time (which
+// share the weights in registers, the barriers and the shuffles), the rows ahead on
+// their way while the group works on the current ones.
+constexpr int kFwdWarps = 20, kFwdFirst = 20;
+template <int N, int V> constexpr int kFwdRows = N > 1 && V == 1 ? 2 : 1;
+// turns in the ring, the current one among them: what two CTAs have room for
 template <int V> constexpr int kFwdDepth = V > 2 ? 2 : 3;
 
-constexpr int kFwdWarps = 16, kFwdFirst = 8;
-
 template <typename T, int N, int V, bool DROP>
-__global__ void __launch_bounds__(32 * kFwdWarps, 2)
+__global__ void __launch_bounds__(32 * kFwdWarps)
 block_norm_fwd_rows(const BlockNorm<T> a, int W, int R) {
   using VT = typename Values<N>::V;
   using Rw = typename Raw<T, N>::type;
-  constexpr int P = Values<N>::kCount;
+  constexpr int P = Values<N>::kCount, B = kFwdRows<N, V>;
   constexpr bool kHold = V * N <= 8;  // the weights in registers; else read for each row
   extern __shared__ uint4 ring[];
-  __shared__ __align__(16) float slots[8][2][2][kMaxWarps + 4];  // group, parity, which sum
-  for (int i = threadIdx.x; i < 8 * 4 * (kMaxWarps + 4); i += blockDim.x)
-    (&slots[0][0][0][0])[i] = 0.f;
-  __syncthreads();
+  __shared__ float slots[8][2][2][B * kMaxWarps];  // group, parity, which sum
   pdl_wait();
   pdl_trigger();
   const Philox g = philox_of(a.drop);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int grp = warp / W, wig = warp - grp * W, gi = wig * 32 + lane, G = W * 32;
-  const int hp = a.H / N;
-  auto col = [&](int k) { return gi + k * G < hp ? (gi + k * G) * N : -1; };
-  VT wg[kHold ? V : 1][P];
-  Rw w[kHold ? V : 1];
+  const auto [grp, wig, gi, G] = place_of(W);
+  const int c0 = gi * N;
+  uint32_t on = 0;
+#pragma unroll
+  for (int k = 0; k < V; ++k) on |= (gi + k * G) * N < a.H ? 1u << k : 0u;
+  VT wg[kHold ? V : 1][P], w[kHold ? V : 1][P];
   if constexpr (kHold)
 #pragma unroll
     for (int k = 0; k < V; ++k)
-      if (col(k) >= 0) {
-        column_factors<T, N>(a, col(k), wg[k]);
-        w[k] = load_raw<Rw>(a.w + col(k));
+      if (on >> k & 1) {
+        column_factors<T, N>(a, c0 + k * G * N, wg[k]);
+        unpack(load_raw<Rw>(a.w + c0 + k * G * N), w[k]);
       }
   Mask<N, V> mask;
   if (DROP) mask.init(g, a.drop.thr, gi, G);
   const int64_t step = (int64_t)gridDim.x * R;
-  auto row = [&](int b, int64_t t) { return b == 0 ? a.x + t * a.ldx : a.res + t * a.ldr; };
-  Ahead<T, N, V, 2, kFwdDepth<V>> in;
-  in.init(ring);
   int64_t t = (int64_t)blockIdx.x * R + grp;
-  in.start(t, step, a.rows, row, col);
-  float tok_next = a.gate_tok != nullptr && t < a.rows ? a.gate_tok[t] : 1.f;
+  Sources<T, 2> src{{a.x + t * a.ldx + c0, a.res + t * a.ldr + c0},
+                    {step * a.ldx, step * a.ldr}, t, step, a.rows};
+  Ahead<T, N, V, 2, B, kFwdDepth<V>> in;
+  in.start(ring, src, G, on);
+  T *hr = a.h + t * a.ldh + c0, *yr = a.y + t * a.ldy + c0;
+  float tok[B];
+  auto gates = [&](int64_t n) {
+#pragma unroll
+    for (int b = 0; b < B; ++b)
+      tok[b] = a.gate_tok != nullptr && n + b * step < a.rows ? a.gate_tok[n + b * step] : 1.f;
+  };
+  gates(t);
   const VT rs = vall<VT>(a.res_scale);
-  for (int parity = 0; t < a.rows; t += step, parity ^= 1, in.next()) {  // uniform in the group
-    const float c0 = tok_next * a.x_scale * a.drop.scale;
-    if (a.gate_tok != nullptr && t + step < a.rows) tok_next = a.gate_tok[t + step];
-    if (DROP) mask.row(g, (uint32_t)t, gi, G);
-    in.arrive(t, step, a.rows, row, col);
-    float r1 = 1.f;
+  const float xs = a.x_scale * a.drop.scale;
+  for (int parity = 0; t < a.rows; t += B * step, parity ^= 1, in.next()) {  // group-uniform
+    float f[B], s[B];
+#pragma unroll
+    for (int b = 0; b < B; ++b) f[b] = tok[b] * xs;
+    if (a.gate_tok != nullptr) gates(t + B * step);
+    typename Mask<N, V>::Row m[B];
+    if (DROP)
+#pragma unroll
+      for (int b = 0; b < B; ++b) mask.row(g, (uint32_t)(t + b * step), gi, G, m[b]);
+    in.arrive(src, G, on);
     if (a.w_post != nullptr) {
+#pragma unroll
+      for (int b = 0; b < B; ++b) {
+        VT ss = vall<VT>(0.f);
+#pragma unroll
+        for (int k = 0; k < V; ++k)
+          if (on >> k & 1) {
+            VT x[P];
+            unpack(in.get(0, b, k), x);
+#pragma unroll
+            for (int i = 0; i < P; ++i) ss = vfma(x[i], x[i], ss);
+          }
+        s[b] = vsum(ss);
+      }
+      group_sums<B>(s, slots[grp][parity][0], W, wig, grp);
+#pragma unroll
+      for (int b = 0; b < B; ++b) {
+        const float r1 = rsqrtf(fmaf(s[b], a.inv_h, a.eps));
+        if (a.rstd_post != nullptr && gi == 0 && t + b * step < a.rows)
+          a.rstd_post[t + b * step] = r1;
+        f[b] *= r1;
+      }
+    }
+    Rw h[B][V];
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
       VT ss = vall<VT>(0.f);
+      const VT fv = vall<VT>(f[b]);
 #pragma unroll
       for (int k = 0; k < V; ++k)
-        if (col(k) >= 0) {
-          VT x[P];
-          unpack(in.get(0, k), x);
+        if (on >> k & 1) {
+          VT x[P], o[P], fk[P];
+          unpack(in.get(0, b, k), x);
+          unpack(in.get(1, b, k), o);
+          if constexpr (!kHold) column_factors<T, N>(a, c0 + k * G * N, fk);
 #pragma unroll
-          for (int i = 0; i < P; ++i) ss = vfma(x[i], x[i], ss);
+          for (int i = 0; i < P; ++i) {
+            VT v = vmul(vmul(x[i], fv), kHold ? wg[kHold ? k : 0][i] : fk[i]);
+            if (DROP) v = mask.keep(m[b], k, i, v);
+            o[i] = vfma(rs, o[i], v);
+          }
+          pack(o, h[b][k]);
+          unpack(h[b][k], o);
+#pragma unroll
+          for (int i = 0; i < P; ++i) ss = vfma(o[i], o[i], ss);
+          if (t + b * step < a.rows) store_raw(hr + b * step * a.ldh + k * G * N, h[b][k]);
         }
-      r1 = rsqrtf(fmaf(group_sum(vsum(ss), slots[grp][parity][0], W, wig, grp), a.inv_h, a.eps));
-      if (a.rstd_post != nullptr && gi == 0) a.rstd_post[t] = r1;
+      s[b] = vsum(ss);
     }
-    VT ss = vall<VT>(0.f);
-    const VT r1v = vall<VT>(r1), c0v = vall<VT>(c0);
-    Rw h[V];
+    group_sums<B>(s, slots[grp][parity][1], W, wig, grp);
 #pragma unroll
-    for (int k = 0; k < V; ++k)
-      if (col(k) >= 0) {
-        VT x[P], f[P], o[P];
-        unpack(in.get(0, k), x);
-        unpack(in.get(1, k), o);
-        if constexpr (!kHold) column_factors<T, N>(a, col(k), f);
+    for (int b = 0; b < B; ++b) {
+      if (t + b * step >= a.rows) break;
+      const float r2 = rsqrtf(fmaf(s[b], a.inv_h, a.eps));
+      if (a.rstd != nullptr && gi == 0) a.rstd[t + b * step] = r2;
+      const VT r2v = vall<VT>(r2);
 #pragma unroll
-        for (int i = 0; i < P; ++i) {
-          VT b = vmul(vmul(vmul(x[i], r1v), kHold ? wg[kHold ? k : 0][i] : f[i]), c0v);
-          if (DROP) b = mask.keep(k, i, b);
-          o[i] = vfma(rs, o[i], b);
+      for (int k = 0; k < V; ++k)
+        if (on >> k & 1) {
+          VT o[P], fk[P];
+          unpack(h[b][k], o);
+          if constexpr (!kHold) unpack(load_raw<Rw>(a.w + c0 + k * G * N), fk);
+#pragma unroll
+          for (int i = 0; i < P; ++i)
+            o[i] = vmul(vmul(o[i], r2v), kHold ? w[kHold ? k : 0][i] : fk[i]);
+          Rw y;
+          pack(o, y);
+          store_raw(yr + b * step * a.ldy + k * G * N, y);
         }
-        pack(o, h[k]);
-        store_raw(a.h + t * a.ldh + col(k), h[k]);
-        unpack(h[k], o);
-#pragma unroll
-        for (int i = 0; i < P; ++i) ss = vfma(o[i], o[i], ss);
-      }
-    const float r2 =
-        rsqrtf(fmaf(group_sum(vsum(ss), slots[grp][parity][1], W, wig, grp), a.inv_h, a.eps));
-    if (a.rstd != nullptr && gi == 0) a.rstd[t] = r2;
-    const VT r2v = vall<VT>(r2);
-#pragma unroll
-    for (int k = 0; k < V; ++k)
-      if (col(k) >= 0) {
-        VT o[P], f[P];
-        unpack(h[k], o);
-        unpack(kHold ? w[kHold ? k : 0] : load_raw<Rw>(a.w + col(k)), f);
-#pragma unroll
-        for (int i = 0; i < P; ++i) o[i] = vmul(vmul(o[i], r2v), f[i]);
-        Rw y;
-        pack(o, y);
-        store_raw(a.y + t * a.ldy + col(k), y);
-      }
+    }
+    hr += B * step * a.ldh;
+    yr += B * step * a.ldy;
   }
+  cp_async_wait<0>();
 }
 
 template <typename T, int N, int V>
@@ -153,7 +185,7 @@ cudaError_t fwd_rows(const BlockPlan &p, const BlockNormArgs &a, const DeviceInf
                      cudaStream_t s) {
   auto kern = a.drop.thr > 0 ? block_norm_fwd_rows<T, N, V, true>
                              : block_norm_fwd_rows<T, N, V, false>;
-  const size_t smem = Ahead<T, N, V, 2, kFwdDepth<V>>::bytes(p.threads());
+  const size_t smem = Ahead<T, N, V, 2, kFwdRows<N, V>, kFwdDepth<V>>::bytes(p.threads());
   const int occ = blocks_per_sm((const void *)kern, p.threads(), smem, dev, 8);
   int64_t grid = ceil_div(a.T, (int64_t)p.R);
   if (grid > (int64_t)dev.sms * occ) grid = (int64_t)dev.sms * occ;
