@@ -312,82 +312,97 @@ __device__ __forceinline__ void column_factors(const BlockNorm<T> &a, int64_t c,
   }
 }
 
+// Rows of S tensors, walked in steps of one group's rows.  The addresses are uniform in a
+// warp (its lanes add a 32-bit offset), and the steps are products that the host made:
+// worked out in the loop, they were a sixth of its instructions.
+template <int S> struct Walk {
+  int64_t step[S];  // bytes from a row of the group to its next
+};
+template <int S> struct Rows {
+  const char *at[S];
+  __device__ __forceinline__ void advance(const Walk<S> &w, int rows) {
+#pragma unroll
+    for (int s = 0; s < S; ++s) at[s] += rows * w.step[s];
+  }
+};
+
 // A thread's packets (V of each of S source tensors, B rows at a time) of the rows ahead.
 // Packets of 16 bytes are copied into a ring in shared memory (cp.async: each thread
 // reads back what it copied itself, so that the ring needs no barrier), kDepth - 1 turns
 // ahead; single columns, which are too small for such copies, wait in registers, one
-// turn ahead.
-template <typename T, int S> struct Sources {
-  const T *at[S];   // at the next row to fetch, this thread's first column
-  int64_t row[S];   // elements from one row of the group to its next
-  int64_t t, step, rows;
+// turn ahead.  Columns: offset `off` (bytes) of the row, packet k 32 W packets further.
+struct Turn {
+  uint32_t t, step, rows;  // the next row to fetch, the group's step, the batch's rows
+  uint32_t off, gap, on;   // bytes; bit k: the thread has a packet k
 };
 
 template <typename T, int N, int V, int S, int B, int kDepth> struct Ahead {
-  using R = uint4;
-  uint4 *slot;  // this thread's place in the ring
+  static constexpr int kItems = S * B * V;  // of a turn; 512 bytes each for a warp
+  char *slot;                               // this thread's place in the ring
   int turn;
   static constexpr size_t bytes(int threads) {
-    return (size_t)threads * kDepth * S * B * V * sizeof(uint4);
+    return (size_t)threads * kDepth * kItems * sizeof(uint4);
   }
-  __device__ __forceinline__ uint4 *place(int d, int s, int b, int k) const {
-    return slot + (((d * S + s) * B + b) * V + k) * (int)blockDim.x;
+  __device__ __forceinline__ char *place(int d, int s, int b, int k) const {
+    return slot + (d * kItems + (s * B + b) * V + k) * 512;
   }
-  // on: bit k of the packets that this thread has
-  __device__ __forceinline__ void fetch(int d, Sources<T, S> &src, int G, uint32_t on) {
+  __device__ __forceinline__ void fetch(int d, Rows<S> &src, const Walk<S> &w, Turn &n) {
 #pragma unroll
     for (int b = 0; b < B; ++b)
-      if (src.t + b * src.step < src.rows)
+      if (n.t + b * n.step < n.rows)
 #pragma unroll
         for (int s = 0; s < S; ++s)
 #pragma unroll
           for (int k = 0; k < V; ++k)
-            if (on >> k & 1) cp_async16(place(d, s, b, k), src.at[s] + b * src.row[s] + k * G * N);
+            if (n.on >> k & 1)
+              cp_async16(place(d, s, b, k), src.at[s] + b * w.step[s] + (n.off + k * n.gap));
     cp_async_commit();  // a group for each turn, empty or not
-    src.t += B * src.step;
-#pragma unroll
-    for (int s = 0; s < S; ++s) src.at[s] += B * src.row[s];
+    n.t += B * n.step;
+    src.advance(w, B);
   }
-  __device__ __forceinline__ void start(uint4 *ring, Sources<T, S> &src, int G, uint32_t on) {
-    slot = ring + threadIdx.x;
+  __device__ __forceinline__ void start(uint4 *ring, Rows<S> &src, const Walk<S> &w, Turn &n) {
+    slot = reinterpret_cast<char *>(ring + (threadIdx.x >> 5) * (kDepth * kItems * 32) +
+                                    (threadIdx.x & 31));
     turn = 0;
 #pragma unroll
-    for (int i = 0; i < kDepth - 1; ++i) fetch(i, src, G, on);
+    for (int i = 0; i < kDepth - 1; ++i) fetch(i, src, w, n);
   }
   // the current turn's rows are there, the last of the ring's on their way
-  __device__ __forceinline__ void arrive(Sources<T, S> &src, int G, uint32_t on) {
-    fetch(turn == 0 ? kDepth - 1 : turn - 1, src, G, on);
+  __device__ __forceinline__ void arrive(Rows<S> &src, const Walk<S> &w, Turn &n) {
+    fetch(turn == 0 ? kDepth - 1 : turn - 1, src, w, n);
     cp_async_wait<kDepth - 1>();
   }
-  __device__ __forceinline__ uint4 get(int s, int b, int k) const { return *place(turn, s, b, k); }
+  __device__ __forceinline__ uint4 get(int s, int b, int k) const {
+    return *reinterpret_cast<const uint4 *>(place(turn, s, b, k));
+  }
   __device__ __forceinline__ void next() { turn = turn + 1 == kDepth ? 0 : turn + 1; }
 };
 
 template <typename T, int V, int S, int B, int kDepth> struct Ahead<T, 1, V, S, B, kDepth> {
-  using R = T;
   T now[S][B][V], then[S][B][V];
   static constexpr size_t bytes(int) { return 0; }
-  __device__ __forceinline__ void start(uint4 *, Sources<T, S> &src, int G, uint32_t on) {
+  __device__ __forceinline__ void start(uint4 *, Rows<S> &src, const Walk<S> &w, Turn &n) {
 #pragma unroll
     for (int b = 0; b < B; ++b)
-      if (src.t + b * src.step < src.rows)
+      if (n.t + b * n.step < n.rows)
 #pragma unroll
         for (int s = 0; s < S; ++s)
 #pragma unroll
           for (int k = 0; k < V; ++k)
-            if (on >> k & 1) then[s][b][k] = src.at[s][b * src.row[s] + k * G];
-    src.t += B * src.step;
-#pragma unroll
-    for (int s = 0; s < S; ++s) src.at[s] += B * src.row[s];
+            if (n.on >> k & 1)
+              then[s][b][k] = *reinterpret_cast<const T *>(src.at[s] + b * w.step[s] +
+                                                           (n.off + k * n.gap));
+    n.t += B * n.step;
+    src.advance(w, B);
   }
-  __device__ __forceinline__ void arrive(Sources<T, S> &src, int G, uint32_t on) {
+  __device__ __forceinline__ void arrive(Rows<S> &src, const Walk<S> &w, Turn &n) {
 #pragma unroll
     for (int s = 0; s < S; ++s)
 #pragma unroll
       for (int b = 0; b < B; ++b)
 #pragma unroll
         for (int k = 0; k < V; ++k) now[s][b][k] = then[s][b][k];
-    start(nullptr, src, G, on);
+    start(nullptr, src, w, n);
   }
   __device__ __forceinline__ T get(int s, int b, int k) const { return now[s][b][k]; }
   __device__ __forceinline__ void next() {}

@@ -77,7 +77,8 @@ template <int V> constexpr int kBwdDepth = V <= 2 ? 2 : 1;
 
 template <typename T, int N, int V, bool DROP>
 __global__ void __launch_bounds__(32 * kMaxWarps)
-block_norm_bwd_rows(const BlockNorm<T> a, int W, int R) {
+block_norm_bwd_rows(const BlockNorm<T> a, const Walk<4> walk_in, const Walk<2> walk_out, int W,
+                    int R) {
   using VT = typename Values<N>::V;
   using Rw = typename Raw<T, N>::type;
   constexpr int P = Values<N>::kCount, B = kBwdRows<N, V>;
@@ -106,27 +107,28 @@ block_norm_bwd_rows(const BlockNorm<T> a, int W, int R) {
   }
   Mask<N, V> mask;
   if (DROP) mask.init(g, a.drop.thr, gi, G);
-  const int64_t step = (int64_t)gridDim.x * R;
+  const uint32_t rows = (uint32_t)a.rows, step = gridDim.x * R;
   const float beta = a.x_scale * a.drop.scale;
-  int64_t t = (int64_t)blockIdx.x * R + grp;
-  Sources<T, 4> src{{a.x + t * a.ldx + c0, a.h + t * a.ldh + c0, a.dy + t * a.lddy + c0,
-                     a.dh + t * a.lddh + c0},
-                    {step * a.ldx, step * a.ldh, step * a.lddy, step * a.lddh}, t, step, a.rows};
+  uint32_t t = blockIdx.x * R + grp;
+  Rows<4> src{{(const char *)(a.x + t * a.ldx), (const char *)(a.h + t * a.ldh),
+               (const char *)(a.dy + t * a.lddy), (const char *)(a.dh + t * a.lddh)}};
+  Rows<2> out{{(const char *)(a.dx + t * a.lddx), (const char *)(a.dres + t * a.lddr)}};
+  const uint32_t off = c0 * (int)sizeof(T), gap = G * N * (int)sizeof(T);
+  Turn turn{t, step, rows, off, gap, on};
   Ahead<T, N, V, 4, B, kBwdDepth<V>> in;
-  in.start(ring, src, G, on);
-  T *dxr = a.dx + t * a.lddx + c0, *drr = a.dres + t * a.lddr + c0;
+  in.start(ring, src, walk_in, turn);
   float r1_next[B], r2_next[B], tok_next[B];
-  auto scalars = [&](int64_t n) {
+  auto scalars = [&](uint32_t n) {
 #pragma unroll
     for (int b = 0; b < B; ++b) {
-      const bool there = n + b * step < a.rows;
+      const bool there = n + b * step < rows;
       r1_next[b] = there && a.w_post != nullptr ? a.rstd_post[n + b * step] : 1.f;
       r2_next[b] = there ? a.rstd[n + b * step] : 0.f;
       tok_next[b] = there && a.gate_tok != nullptr ? a.gate_tok[n + b * step] : 1.f;
     }
   };
   scalars(t);
-  for (int parity = 0; t < a.rows; t += B * step, parity ^= 1, in.next()) {  // group-uniform
+  for (int parity = 0; t < rows; t += B * step, parity ^= 1, in.next()) {  // group-uniform
     float r1[B], r2[B], gt[B], s[3 * B];
 #pragma unroll
     for (int b = 0; b < B; ++b) r1[b] = r1_next[b], r2[b] = r2_next[b], gt[b] = tok_next[b];
@@ -134,13 +136,14 @@ block_norm_bwd_rows(const BlockNorm<T> a, int W, int R) {
     typename Mask<N, V>::Row m[B];
     if (DROP)
 #pragma unroll
-      for (int b = 0; b < B; ++b) mask.row(g, (uint32_t)(t + b * step), gi, G, m[b]);
-    in.arrive(src, G, on);
+      for (int b = 0; b < B; ++b) mask.row(g, t + b * step, gi, G, m[b]);
+    in.arrive(src, walk_in, turn);
 #pragma unroll
     for (int b = 0; b < B; ++b) {
-      const VT r1v = vall<VT>(r1[b]), r2v = vall<VT>(r2[b]);
-      VT s_h = vall<VT>(0.f), s_g = s_h, s_c = s_h;  // w dy hn, q (dh + r2 w dy), q hn
-      if (t + b * step < a.rows)
+      // without the rows' own factors: w dy h, m wg x (dh + r2 w dy), m wg x h
+      VT s_h = vall<VT>(0.f), s_g = s_h, s_c = s_h;
+      const VT r2v = vall<VT>(r2[b]);
+      if (t + b * step < rows)
 #pragma unroll
         for (int k = 0; k < V; ++k)
           if (on >> k & 1) {
@@ -153,12 +156,12 @@ block_norm_bwd_rows(const BlockNorm<T> a, int W, int R) {
             if constexpr (!kHold) column_factors<T, N>(a, c0 + k * G * N, f);
 #pragma unroll
             for (int i = 0; i < P; ++i) {
-              const VT wd = vmul(wf[i], dy[i]), hn = vmul(h[i], r2v);
-              VT q = vmul(kHold ? wg[kHold ? k : 0][i] : f[i], vmul(x[i], r1v));
+              const VT wd = vmul(wf[i], dy[i]);
+              VT q = vmul(kHold ? wg[kHold ? k : 0][i] : f[i], x[i]);
               if (DROP) q = mask.keep(m[b], k, i, q);
-              s_h = vfma(wd, hn, s_h);
+              s_h = vfma(wd, h[i], s_h);
               s_g = vfma(q, vfma(r2v, wd, dh[i]), s_g);
-              s_c = vfma(q, hn, s_c);
+              s_c = vfma(q, h[i], s_c);
             }
           }
       s[3 * b] = vsum(s_h), s[3 * b + 1] = vsum(s_g), s[3 * b + 2] = vsum(s_c);
@@ -166,13 +169,14 @@ block_norm_bwd_rows(const BlockNorm<T> a, int W, int R) {
     group_sums<3 * B>(s, slots[grp][parity], W, wig, grp);
 #pragma unroll
     for (int b = 0; b < B; ++b) {
-      if (t + b * step >= a.rows) break;
-      const float kk = r2[b] * (s[3 * b] * a.inv_h);
-      const float c1 = beta * fmaf(-kk, s[3 * b + 2], s[3 * b + 1]);
+      if (t + b * step >= rows) break;
+      const float kr = r2[b] * (r2[b] * (r2[b] * s[3 * b] * a.inv_h));  // k r2
+      const float c1 = beta * (r1[b] * fmaf(-kr, s[3 * b + 2], s[3 * b + 1]));
       if (a.dgate_tok != nullptr && gi == 0) a.dgate_tok[t + b * step] = c1;
-      const VT r1v = vall<VT>(r1[b]), r2v = vall<VT>(r2[b]);
-      const VT nkk = vall<VT>(-kk), bg = vall<VT>(beta * gt[b]), rs = vall<VT>(a.res_scale);
-      const VT nam = vall<VT>(a.w_post != nullptr ? -r1[b] * (gt[b] * c1 * a.inv_h) : 0.f);
+      const VT r2v = vall<VT>(r2[b]), nkr = vall<VT>(-kr), rs = vall<VT>(a.res_scale);
+      const VT bg = vall<VT>(beta * gt[b] * r1[b]);
+      const VT nam =
+          vall<VT>(a.w_post != nullptr ? -r1[b] * (r1[b] * (gt[b] * c1 * a.inv_h)) : 0.f);
 #pragma unroll
       for (int k = 0; k < V; ++k)
         if (on >> k & 1) {
@@ -185,24 +189,23 @@ block_norm_bwd_rows(const BlockNorm<T> a, int W, int R) {
           if constexpr (!kHold) column_factors<T, N>(a, c0 + k * G * N, f);
 #pragma unroll
           for (int i = 0; i < P; ++i) {
-            const VT hn = vmul(h[i], r2v), xn = vmul(x[i], r1v);
-            const VT Gv = vfma(nkk, hn, vfma(r2v, vmul(wf[i], dy[i]), dh[i]));
-            VT gm = vmul(bg, Gv);
+            const VT dyr = vmul(dy[i], r2v);
+            const VT Gv = vfma(nkr, h[i], vfma(wf[i], dyr, dh[i]));
+            VT gm = vmul(bg, Gv);  // beta gate_tok r1 m G
             if (DROP) gm = mask.keep(m[b], k, i, gm);
-            sw[k][i] = vfma(dy[i], hn, sw[k][i]);
-            sx[k][i] = vfma(gm, xn, sx[k][i]);
+            sw[k][i] = vfma(dyr, h[i], sw[k][i]);
+            sx[k][i] = vfma(gm, x[i], sx[k][i]);
             dh[i] = vmul(rs, Gv);
-            x[i] = vfma(nam, xn, vmul(r1v, vmul(gm, kHold ? wg[kHold ? k : 0][i] : f[i])));
+            x[i] = vfma(nam, x[i], vmul(gm, kHold ? wg[kHold ? k : 0][i] : f[i]));
           }
           Rw o;
           pack(dh, o);
-          store_raw(drr + b * step * a.lddr + k * G * N, o);
+          store_raw((T *)(out.at[1] + b * walk_out.step[1] + (off + k * gap)), o);
           pack(x, o);
-          store_raw(dxr + b * step * a.lddx + k * G * N, o);
+          store_raw((T *)(out.at[0] + b * walk_out.step[0] + (off + k * gap)), o);
         }
     }
-    dxr += B * step * a.lddx;
-    drr += B * step * a.lddr;
+    out.advance(walk_out, B);
   }
   cp_async_wait<0>();
   if (R > 1) __syncthreads();  // the ring becomes the row groups' sums
@@ -280,8 +283,11 @@ cudaError_t bwd_rows(const BlockPlan &p, const BlockNormArgs &a, const DeviceInf
   const int occ = blocks_per_sm((const void *)kern, p.threads(), smem, dev, kMaxBlocksPerSm);
   int64_t P = ceil_div(a.T, (int64_t)p.R);
   if (P > (int64_t)dev.sms * occ) P = (int64_t)dev.sms * occ;
-  cudaError_t e = launch_pdl(kern, dim3((unsigned)P), dim3(p.threads()), smem, s,
-                             block_norm_params<T>(a), p.W, p.R);
+  const int64_t step = P * p.R * (int64_t)sizeof(T);
+  cudaError_t e = launch_pdl(
+      kern, dim3((unsigned)P), dim3(p.threads()), smem, s, block_norm_params<T>(a),
+      Walk<4>{{step * a.ldx, step * a.ldh, step * a.lddy, step * a.lddh}},
+      Walk<2>{{step * a.lddx, step * a.lddr}}, p.W, p.R);
   return e != cudaSuccess ? e : reduce<T>(a, P, s);
 }
 

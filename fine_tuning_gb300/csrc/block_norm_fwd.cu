@@ -53,7 +53,8 @@ template <int V> constexpr int kFwdDepth = V > 2 ? 2 : 3;
 
 template <typename T, int N, int V, bool DROP>
 __global__ void __launch_bounds__(32 * kFwdWarps)
-block_norm_fwd_rows(const BlockNorm<T> a, int W, int R) {
+block_norm_fwd_rows(const BlockNorm<T> a, const Walk<2> walk_in, const Walk<2> walk_out, int W,
+                    int R) {
   using VT = typename Values<N>::V;
   using Rw = typename Raw<T, N>::type;
   constexpr int P = Values<N>::kCount, B = kFwdRows<N, V>;
@@ -78,23 +79,24 @@ block_norm_fwd_rows(const BlockNorm<T> a, int W, int R) {
       }
   Mask<N, V> mask;
   if (DROP) mask.init(g, a.drop.thr, gi, G);
-  const int64_t step = (int64_t)gridDim.x * R;
-  int64_t t = (int64_t)blockIdx.x * R + grp;
-  Sources<T, 2> src{{a.x + t * a.ldx + c0, a.res + t * a.ldr + c0},
-                    {step * a.ldx, step * a.ldr}, t, step, a.rows};
+  const uint32_t rows = (uint32_t)a.rows, step = gridDim.x * R;
+  uint32_t t = blockIdx.x * R + grp;
+  Rows<2> src{{(const char *)(a.x + t * a.ldx), (const char *)(a.res + t * a.ldr)}};
+  Rows<2> dst{{(const char *)(a.h + t * a.ldh), (const char *)(a.y + t * a.ldy)}};
+  const uint32_t off = c0 * (int)sizeof(T), gap = G * N * (int)sizeof(T);
+  Turn turn{t, step, rows, off, gap, on};
   Ahead<T, N, V, 2, B, kFwdDepth<V>> in;
-  in.start(ring, src, G, on);
-  T *hr = a.h + t * a.ldh + c0, *yr = a.y + t * a.ldy + c0;
+  in.start(ring, src, walk_in, turn);
   float tok[B];
-  auto gates = [&](int64_t n) {
+  auto gates = [&](uint32_t n) {
 #pragma unroll
     for (int b = 0; b < B; ++b)
-      tok[b] = a.gate_tok != nullptr && n + b * step < a.rows ? a.gate_tok[n + b * step] : 1.f;
+      tok[b] = a.gate_tok != nullptr && n + b * step < rows ? a.gate_tok[n + b * step] : 1.f;
   };
   gates(t);
   const VT rs = vall<VT>(a.res_scale);
   const float xs = a.x_scale * a.drop.scale;
-  for (int parity = 0; t < a.rows; t += B * step, parity ^= 1, in.next()) {  // group-uniform
+  for (int parity = 0; t < rows; t += B * step, parity ^= 1, in.next()) {  // group-uniform
     float f[B], s[B];
 #pragma unroll
     for (int b = 0; b < B; ++b) f[b] = tok[b] * xs;
@@ -102,8 +104,8 @@ block_norm_fwd_rows(const BlockNorm<T> a, int W, int R) {
     typename Mask<N, V>::Row m[B];
     if (DROP)
 #pragma unroll
-      for (int b = 0; b < B; ++b) mask.row(g, (uint32_t)(t + b * step), gi, G, m[b]);
-    in.arrive(src, G, on);
+      for (int b = 0; b < B; ++b) mask.row(g, t + b * step, gi, G, m[b]);
+    in.arrive(src, walk_in, turn);
     if (a.w_post != nullptr) {
 #pragma unroll
       for (int b = 0; b < B; ++b) {
@@ -122,7 +124,7 @@ block_norm_fwd_rows(const BlockNorm<T> a, int W, int R) {
 #pragma unroll
       for (int b = 0; b < B; ++b) {
         const float r1 = rsqrtf(fmaf(s[b], a.inv_h, a.eps));
-        if (a.rstd_post != nullptr && gi == 0 && t + b * step < a.rows)
+        if (a.rstd_post != nullptr && gi == 0 && t + b * step < rows)
           a.rstd_post[t + b * step] = r1;
         f[b] *= r1;
       }
@@ -149,14 +151,15 @@ block_norm_fwd_rows(const BlockNorm<T> a, int W, int R) {
           unpack(h[b][k], o);
 #pragma unroll
           for (int i = 0; i < P; ++i) ss = vfma(o[i], o[i], ss);
-          if (t + b * step < a.rows) store_raw(hr + b * step * a.ldh + k * G * N, h[b][k]);
+          if (t + b * step < rows)
+            store_raw((T *)(dst.at[0] + b * walk_out.step[0] + (off + k * gap)), h[b][k]);
         }
       s[b] = vsum(ss);
     }
     group_sums<B>(s, slots[grp][parity][1], W, wig, grp);
 #pragma unroll
     for (int b = 0; b < B; ++b) {
-      if (t + b * step >= a.rows) break;
+      if (t + b * step >= rows) break;
       const float r2 = rsqrtf(fmaf(s[b], a.inv_h, a.eps));
       if (a.rstd != nullptr && gi == 0) a.rstd[t + b * step] = r2;
       const VT r2v = vall<VT>(r2);
@@ -171,11 +174,10 @@ block_norm_fwd_rows(const BlockNorm<T> a, int W, int R) {
             o[i] = vmul(vmul(o[i], r2v), kHold ? w[kHold ? k : 0][i] : fk[i]);
           Rw y;
           pack(o, y);
-          store_raw(yr + b * step * a.ldy + k * G * N, y);
+          store_raw((T *)(dst.at[1] + b * walk_out.step[1] + (off + k * gap)), y);
         }
     }
-    hr += B * step * a.ldh;
-    yr += B * step * a.ldy;
+    dst.advance(walk_out, B);
   }
   cp_async_wait<0>();
 }
@@ -189,8 +191,10 @@ cudaError_t fwd_rows(const BlockPlan &p, const BlockNormArgs &a, const DeviceInf
   const int occ = blocks_per_sm((const void *)kern, p.threads(), smem, dev, 8);
   int64_t grid = ceil_div(a.T, (int64_t)p.R);
   if (grid > (int64_t)dev.sms * occ) grid = (int64_t)dev.sms * occ;
+  const int64_t step = grid * p.R * (int64_t)sizeof(T);
   return launch_pdl(kern, dim3((unsigned)grid), dim3(p.threads()), smem, s,
-                    block_norm_params<T>(a), p.W, p.R);
+                    block_norm_params<T>(a), Walk<2>{{step * a.ldx, step * a.ldr}},
+                    Walk<2>{{step * a.ldh, step * a.ldy}}, p.W, p.R);
 }
 
 template <typename T, int N>
