@@ -125,13 +125,13 @@ struct BlockPlan {
 
 constexpr int kMaxWarps = 20;  // of a row group
 
-// `first`: the warps up to which a thread takes one packet; `warps`: those of a CTA.
-inline BlockPlan plan_block_row(int64_t hp, int vmax, int first, int warps) {
+inline BlockPlan plan_block_row(int64_t hp, int vmax) {
   for (int v = 1; v <= vmax; v *= 2) {
     const int64_t W = ceil_div(hp, (int64_t)32 * v);
-    if (W > (v == 1 ? first : warps)) continue;
-    // rows of one warp need no barrier; of the others at most four groups have one each
-    const int R = W == 1 ? 8 : warps / (int)W < 4 ? warps / (int)W : 4;
+    if (W > kMaxWarps) continue;
+    // rows of one warp need no barrier; of the others at most four groups have one each,
+    // in CTAs of up to 16 warps
+    const int R = W == 1 ? 8 : W > 8 ? 1 : 16 / (int)W < 4 ? 16 / (int)W : 4;
     return BlockPlan{v, (int)W, R};
   }
   return BlockPlan{0, 0, 0};

@@ -70,7 +70,6 @@ __global__ void __launch_bounds__(kThreads) block_norm_bwd_any(const BlockNorm<T
 // share the weights in registers, the barrier and the shuffles), the rows ahead on their
 // way while the group works on the current ones.  Each thread keeps its columns' sums
 // for the whole kernel; at the end the CTA's row groups are added in their order.
-constexpr int kBwdFirst = 20;
 template <int N, int V> constexpr int kBwdRows = N > 1 && V == 1 ? 2 : 1;
 // turns in the ring, the current one among them: what 227 KB hold
 template <int V> constexpr int kBwdDepth = V <= 2 ? 2 : 1;
@@ -293,7 +292,7 @@ cudaError_t bwd_rows(const BlockPlan &p, const BlockNormArgs &a, const DeviceInf
 
 template <typename T, int N>
 cudaError_t bwd_packets(const BlockNormArgs &a, const DeviceInfo &dev, cudaStream_t s) {
-  const BlockPlan p = plan_block_row(a.H / N, N == 1 ? 8 : 4, kBwdFirst, kMaxWarps);
+  const BlockPlan p = plan_block_row(a.H / N, N == 1 ? 8 : 4);
   switch (p.V) {
     case 1: return bwd_rows<T, N, 1>(p, a, dev, s);
     case 2: return bwd_rows<T, N, 2>(p, a, dev, s);

@@ -43,16 +43,15 @@ __global__ void __launch_bounds__(kThreads) block_norm_fwd_any(const BlockNorm<T
   }
 }
 
-// Rows of up to kFwdWarps warps: a persistent grid, W warps a row, B rows at a time (which
+// Rows of up to kMaxWarps warps: a persistent grid, W warps a row, B rows at a time (which
 // share the weights in registers, the barriers and the shuffles), the rows ahead on
 // their way while the group works on the current ones.
-constexpr int kFwdWarps = 20, kFwdFirst = 20;
 template <int N, int V> constexpr int kFwdRows = N > 1 && V == 1 ? 2 : 1;
-// turns in the ring, the current one among them: what two CTAs have room for
-template <int V> constexpr int kFwdDepth = V > 2 ? 2 : 3;
+constexpr int kFwdDepth = 2;  // turns in the ring, the current one among them
 
-template <typename T, int N, int V, bool DROP>
-__global__ void __launch_bounds__(32 * kFwdWarps)
+// CTAS on an SM: two of up to 16 warps (64 registers a thread), or one of up to 20.
+template <typename T, int N, int V, bool DROP, int CTAS>
+__global__ void __launch_bounds__(CTAS == 2 ? 512 : 32 * kMaxWarps, CTAS)
 block_norm_fwd_rows(const BlockNorm<T> a, const Walk<2> walk_in, const Walk<2> walk_out, int W,
                     int R) {
   using VT = typename Values<N>::V;
@@ -85,7 +84,7 @@ block_norm_fwd_rows(const BlockNorm<T> a, const Walk<2> walk_in, const Walk<2> w
   Rows<2> dst{{(const char *)(a.h + t * a.ldh), (const char *)(a.y + t * a.ldy)}};
   const uint32_t off = c0 * (int)sizeof(T), gap = G * N * (int)sizeof(T);
   Turn turn{t, step, rows, off, gap, on};
-  Ahead<T, N, V, 2, B, kFwdDepth<V>> in;
+  Ahead<T, N, V, 2, B, kFwdDepth> in;
   in.start(ring, src, walk_in, turn);
   float tok[B];
   auto gates = [&](uint32_t n) {
@@ -185,9 +184,12 @@ block_norm_fwd_rows(const BlockNorm<T> a, const Walk<2> walk_in, const Walk<2> w
 template <typename T, int N, int V>
 cudaError_t fwd_rows(const BlockPlan &p, const BlockNormArgs &a, const DeviceInfo &dev,
                      cudaStream_t s) {
-  auto kern = a.drop.thr > 0 ? block_norm_fwd_rows<T, N, V, true>
-                             : block_norm_fwd_rows<T, N, V, false>;
-  const size_t smem = Ahead<T, N, V, 2, kFwdRows<N, V>, kFwdDepth<V>>::bytes(p.threads());
+  const bool two = p.threads() <= 512;
+  auto kern = a.drop.thr > 0 ? (two ? block_norm_fwd_rows<T, N, V, true, 2>
+                                    : block_norm_fwd_rows<T, N, V, true, 1>)
+                             : (two ? block_norm_fwd_rows<T, N, V, false, 2>
+                                    : block_norm_fwd_rows<T, N, V, false, 1>);
+  const size_t smem = Ahead<T, N, V, 2, kFwdRows<N, V>, kFwdDepth>::bytes(p.threads());
   const int occ = blocks_per_sm((const void *)kern, p.threads(), smem, dev, 8);
   int64_t grid = ceil_div(a.T, (int64_t)p.R);
   if (grid > (int64_t)dev.sms * occ) grid = (int64_t)dev.sms * occ;
@@ -199,7 +201,7 @@ cudaError_t fwd_rows(const BlockPlan &p, const BlockNormArgs &a, const DeviceInf
 
 template <typename T, int N>
 cudaError_t fwd_packets(const BlockNormArgs &a, const DeviceInfo &dev, cudaStream_t s) {
-  const BlockPlan p = plan_block_row(a.H / N, N == 1 ? 8 : 4, kFwdFirst, kFwdWarps);
+  const BlockPlan p = plan_block_row(a.H / N, N == 1 ? 8 : 4);
   switch (p.V) {
     case 1: return fwd_rows<T, N, 1>(p, a, dev, s);
     case 2: return fwd_rows<T, N, 2>(p, a, dev, s);
