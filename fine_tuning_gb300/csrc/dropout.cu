@@ -3,8 +3,8 @@
 // Elementwise: 2 es bytes an element, one Philox call for eight.
 #include "common.cuh"
 #include "launch_residual.h"
-#include "pair_math.cuh"
 #include "philox.cuh"
+#include "raw_packet.cuh"
 
 namespace ftk {
 
@@ -12,33 +12,16 @@ namespace {
 
 constexpr int kThreads = 256;
 
-__device__ __forceinline__ uint4 ld_stream(const uint4 *p) {
-  uint4 u;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
-               : "l"(p));
-  return u;
-}
-
 // Eight columns: one packet of bf16, two of fp32.
-__device__ __forceinline__ void unpack_block(const uint4 (&u)[1], float2 (&f)[4]) {
-  unpack8(u[0], f);
+__device__ __forceinline__ void unpack(const uint4 (&u)[1], float2 (&f)[4]) { unpack(u[0], f); }
+__device__ __forceinline__ void unpack(const uint4 (&u)[2], float2 (&f)[4]) {
+  unpack(u[0], reinterpret_cast<float2(&)[2]>(f[0]));
+  unpack(u[1], reinterpret_cast<float2(&)[2]>(f[2]));
 }
-__device__ __forceinline__ void unpack_block(const uint4 (&u)[2], float2 (&f)[4]) {
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    f[2 * k] = make_float2(__uint_as_float(u[k].x), __uint_as_float(u[k].y));
-    f[2 * k + 1] = make_float2(__uint_as_float(u[k].z), __uint_as_float(u[k].w));
-  }
-}
-__device__ __forceinline__ void pack_block(const float2 (&f)[4], uint4 (&u)[1]) {
-  u[0] = pack8(f);
-}
-__device__ __forceinline__ void pack_block(const float2 (&f)[4], uint4 (&u)[2]) {
-#pragma unroll
-  for (int k = 0; k < 2; ++k)
-    u[k] = make_uint4(__float_as_uint(f[2 * k].x), __float_as_uint(f[2 * k].y),
-                      __float_as_uint(f[2 * k + 1].x), __float_as_uint(f[2 * k + 1].y));
+__device__ __forceinline__ void pack(const float2 (&f)[4], uint4 (&u)[1]) { pack(f, u[0]); }
+__device__ __forceinline__ void pack(const float2 (&f)[4], uint4 (&u)[2]) {
+  pack(reinterpret_cast<const float2(&)[2]>(f[0]), u[0]);
+  pack(reinterpret_cast<const float2(&)[2]>(f[2]), u[1]);
 }
 
 // A warp takes 256 columns of a row: each lane makes the eight bits of its own
@@ -94,8 +77,8 @@ dropout_blocks(const T *x, int64_t ldx, T *y, int64_t ldy, int64_t rows, int blo
       if (t0 + i * step < rows)
 #pragma unroll
         for (int k = 0; k < kPackets; ++k)
-          v[i][k] = ld_stream(reinterpret_cast<const uint4 *>(x + (t0 + i * step) * ldx +
-                                                              (int64_t)b * 8) + k);
+          v[i][k] = load_raw_stream<uint4>(x + (t0 + i * step) * ldx + (int64_t)b * 8 +
+                                           k * VecWidth<T>::value);
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
       const int64_t t = t0 + i * step;
@@ -104,14 +87,14 @@ dropout_blocks(const T *x, int64_t ldx, T *y, int64_t ldy, int64_t rows, int blo
           const uint4 u = philox4x32(g, p, philox_row(g, (uint32_t)t));
           const uint32_t w[4] = {u.x, u.y, u.z, u.w};
           float2 f[4];
-          unpack_block(v[i], f);
+          unpack(v[i], f);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             f[e] = __fmul2_rn(f[e], make_float2(d.scale, d.scale));
             if (!keep_low(w[e], cut)) f[e].x = 0.f;
             if (!keep_high(w[e], cut)) f[e].y = 0.f;
           }
-          pack_block(f, v[i]);
+          pack(f, v[i]);
         }
 #pragma unroll
         for (int k = 0; k < kPackets; ++k)

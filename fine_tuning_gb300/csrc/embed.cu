@@ -2,19 +2,21 @@
 // table, dW[v] = scale sum_{t: ids[t] = v} dx[t].  Tokens whose id lies outside
 // [0, V) give a row of zeros and no gradient.
 //
-// The gradient sums every row's tokens in their order, without atomics, so that it
-// is bitwise reproducible:
-//   1. the tokens are sorted by id: a stable radix sort of (id, t), two kernels a
-//      digit (counts of each CTA's part; scatter to where the counts say);
-//   2. the sorted list is cut into chunks of equal length, however the ids are
-//      spread: a CTA walks one chunk's rows of dx for a slab of columns and keeps the
-//      running sum of one id in registers.  Sums of ids that lie inside the chunk go
-//      to dW, those that cross its borders to the workspace;
-//   3. the crossing sums are added in the chunks' order.
-// Rows of dW that no token names are set to zero by a kernel of their own (not when
-// the gradient is added to what is there).
+// The gradient sums every row's tokens in their order, without atomics on shared sums,
+// so that it is bitwise reproducible:
+//   1. embed_sort: the tokens are sorted by id, a stable radix sort of (id, t) by one
+//      cluster of eight CTAs in one launch; digit counts meet through the cluster's
+//      shared memory.  The other CTAs of the launch meanwhile write the zeros of the rows
+//      that no token names (not when the gradient is added to what is there), most of
+//      the work where the vocabulary is larger than the batch;
+//   2. embed_grad: the sorted list is cut into chunks of equal length, however the ids
+//      are spread: a warp walks one chunk's rows of dx for 256 columns and keeps the
+//      running sum of one id in registers.  Sums of ids that lie inside the chunk go to
+//      dW, those that cross its borders to the workspace;
+//   3. embed_join: the crossing sums are added in the chunks' order.
 #include "common.cuh"
 #include "launch_residual.h"
+#include "raw_packet.cuh"
 
 namespace ftk {
 
@@ -58,20 +60,20 @@ cudaError_t fwd_typed(const EmbedFwdArgs &a, const DeviceInfo &dev, cudaStream_t
 
 // ------------------------------------------------------------------- the sort
 
-constexpr int kDigitBits = 9;            // at most, of one pass
+constexpr int kDigitBits = 9;  // at most, of one pass
 constexpr int kDigits = 1 << kDigitBits;
-constexpr int kSortThreads = 512;        // a thread for each digit
+constexpr int kSortThreads = 512;  // a thread for each digit
 constexpr int kSortWarps = kSortThreads / 32;
-constexpr int64_t kSortMaxCtas = 128;
-constexpr int64_t kSortMinPart = 2048;   // tokens a CTA sorts at least
+constexpr int kSortCtas = 8;       // of the cluster
+constexpr int kFlagWords = 8192;   // of a zeroing CTA: 32 rows each
+constexpr int kColumns = 256;      // of a warp of embed_grad
 
-// Everything that follows from the sizes: parts of the sort, chunks of the sums, and
+// Everything that follows from the sizes: passes of the sort, chunks of the sums, and
 // where their data lie in the workspace.
 struct EmbedPlan {
   int passes, digit_bits;
-  int64_t ctas, part;            // sort: CTAs, tokens of each
-  int64_t chunks, chunk;         // sums: chunks, tokens of each
-  size_t off_key[2], off_tok[2], off_counts, off_part, bytes;
+  int64_t chunks, chunk;  // sums: chunks, tokens of each
+  size_t off_key[2], off_tok[2], off_part, bytes;
 };
 
 EmbedPlan plan_embed(int64_t T, int64_t H, int64_t V) {
@@ -80,11 +82,10 @@ EmbedPlan plan_embed(int64_t T, int64_t H, int64_t V) {
   while ((V >> bits) != 0) ++bits;  // V itself marks the tokens without a row
   p.passes = (bits + kDigitBits - 1) / kDigitBits;
   p.digit_bits = (bits + p.passes - 1) / p.passes;
-  p.part = ceil_div(ceil_div(T, kSortMaxCtas), kSortMinPart) * kSortMinPart;
-  p.ctas = ceil_div(T, p.part);
-  p.chunk = ceil_div(T, (int64_t)2048);
+  // some 8,192 warps in all: 54 an SM
+  p.chunk = ceil_div(ceil_div(T * ceil_div(H, (int64_t)kColumns), (int64_t)8192), (int64_t)8) * 8;
   if (p.chunk < 16) p.chunk = 16;
-  if (p.chunk > 4096) p.chunk = 4096;  // its keys and tokens stay in shared memory
+  if (p.chunk > 1024) p.chunk = 1024;
   p.chunks = ceil_div(T, p.chunk);
   size_t at = 0;
   auto take = [&](size_t n) {
@@ -96,110 +97,191 @@ EmbedPlan plan_embed(int64_t T, int64_t H, int64_t V) {
     p.off_key[i] = take((size_t)T * 4);
     p.off_tok[i] = take((size_t)T * 4);
   }
-  p.off_counts = take((size_t)p.ctas * kDigits * 4);
   p.off_part = take((size_t)p.chunks * 2 * (size_t)H * 4);
   p.bytes = at;
   return p;
 }
 
-// The key a token is sorted by: its id, or V (behind every id) where it has no row.
-__device__ __forceinline__ uint32_t sort_key(const uint32_t *keys, int64_t i, bool ids,
-                                             uint32_t V) {
-  const uint32_t k = keys[i];
-  return ids && k >= V ? V : k;  // as unsigned, a negative id is beyond V too
+struct SortParams {
+  const uint32_t *ids;
+  uint32_t V;
+  uint32_t n;
+  int passes, digit_bits;
+  uint32_t *key[2], *tok[2];
+  // the rows to zero (zero_ctas > 0)
+  int zero_ctas;  // a power of two
+  float *dw;
+  int64_t lddw, H;
+};
+
+__device__ __forceinline__ void cluster_sync() {
+  __syncwarp();  // the aligned forms want whole warps
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// A word of the shared memory of the cluster's CTA `cta`, at this CTA's address `p`.
+__device__ __forceinline__ uint32_t cluster_load(const uint32_t *p, int cta) {
+  uint32_t at, v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(p)), "r"(cta));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
 }
 
-// counts[cta][digit] of the CTA's part.
-__global__ void __launch_bounds__(kSortThreads)
-sort_count(const uint32_t *keys, bool ids, uint32_t V, int64_t n, int64_t part, int shift,
-           uint32_t mask, uint32_t *counts) {
-  __shared__ uint32_t cnt[kDigits];
-  for (int d = threadIdx.x; d < kDigits; d += kSortThreads) cnt[d] = 0;
-  pdl_wait();
-  pdl_trigger();
-  __syncthreads();
-  const int64_t lo = blockIdx.x * part, hi = lo + part < n ? lo + part : n;
-  for (int64_t i = lo + threadIdx.x; i < hi; i += kSortThreads)
-    atomicAdd(&cnt[sort_key(keys, i, ids, V) >> shift & mask], 1u);
-  __syncthreads();
-  for (int d = threadIdx.x; d < kDigits; d += kSortThreads)
-    counts[(int64_t)blockIdx.x * kDigits + d] = cnt[d];
-}
+constexpr int kSortBatch = 4;  // keys of a lane in flight
 
-// Moves the CTA's part to its places: digit d of CTA c begins after every smaller
-// digit of all CTAs and after digit d of the CTAs before c; inside the part the
-// warps' runs follow one another, and inside a warp the order is kept by ranks
-// among the lanes of equal digit.
-__global__ void __launch_bounds__(kSortThreads)
-sort_scatter(const uint32_t *keys, const uint32_t *toks, bool ids, uint32_t V, int64_t n,
-             int64_t part, int shift, uint32_t mask, const uint32_t *counts, uint32_t *out_keys,
-             uint32_t *out_toks) {
-  __shared__ uint32_t at[kSortWarps][kDigits];
-  __shared__ uint32_t warp_total[kSortWarps];
-  pdl_wait();
-  pdl_trigger();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int i = threadIdx.x; i < kSortWarps * kDigits; i += kSortThreads) (&at[0][0])[i] = 0;
-  // this thread's digit: how many there are, and how many before this CTA's part
-  uint32_t total = 0, before = 0;
-  for (unsigned c = 0; c < gridDim.x; ++c) {
-    const uint32_t v = __ldcg(counts + (int64_t)c * kDigits + threadIdx.x);
-    if (c < blockIdx.x) before += v;
-    total += v;
-  }
-  uint32_t incl = total;
+// The sort.  In each pass every warp counts the digits of its run of the list; digit d of
+// CTA c begins after every smaller digit of all CTAs and after digit d of the CTAs before
+// c; inside the CTA the warps' runs follow one another, and inside a warp the order is
+// kept by ranks among the lanes of equal digit.
+__device__ void sort_tokens(const SortParams &a, uint32_t *shared) {
+  uint32_t(*at)[kDigits] = reinterpret_cast<uint32_t(*)[kDigits]>(shared);  // [kSortWarps]
+  uint32_t *tot = shared + kSortWarps * kDigits;                            // [kDigits]
+  uint32_t *warp_total = tot + kDigits;                                     // [kSortWarps]
+  const int cta = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t mask = (1u << a.digit_bits) - 1;
+  // runs of whole warps' steps, the last ones shorter or empty
+  const uint32_t per = ceil_div(ceil_div(a.n, (uint32_t)(kSortCtas * kSortWarps)), 32u) * 32;
+  const uint64_t first = (uint64_t)(cta * kSortWarps + warp) * per;
+  const uint32_t lo = first < a.n ? (uint32_t)first : a.n, hi = a.n - lo < per ? a.n : lo + per;
+  for (int pass = 0; pass < a.passes; ++pass) {
+    const int shift = pass * a.digit_bits;
+    const uint32_t *keys = pass == 0 ? a.ids : a.key[(pass - 1) & 1];
+    const uint32_t *toks = a.tok[(pass - 1) & 1];
+    uint32_t *out_key = a.key[pass & 1], *out_tok = a.tok[pass & 1];
+    // from L2: other CTAs wrote the keys of a later pass.  Out of range as unsigned, a
+    // negative id is beyond V too; V itself is behind every id.
+    auto load = [&](uint32_t i) { return min(__ldcg(keys + i), a.V); };
+    for (int i = threadIdx.x; i < kSortWarps * kDigits; i += kSortThreads) (&at[0][0])[i] = 0;
+    __syncthreads();
+    for (uint32_t i = lo + lane; i < hi; i += 32 * kSortBatch) {
+      uint32_t k[kSortBatch];
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
+      for (int b = 0; b < kSortBatch; ++b)
+        if (i + 32 * b < hi) k[b] = load(i + 32 * b);
+#pragma unroll
+      for (int b = 0; b < kSortBatch; ++b)
+        if (i + 32 * b < hi) atomicAdd(&at[warp][k[b] >> shift & mask], 1u);
+    }
+    __syncthreads();
+    uint32_t own = 0;  // of this thread's digit
+#pragma unroll
+    for (int w = 0; w < kSortWarps; ++w) own += at[w][threadIdx.x];
+    tot[threadIdx.x] = own;
+    cluster_sync();
+    uint32_t total = 0, before = 0;
+#pragma unroll
+    for (int c = 0; c < kSortCtas; ++c) {
+      const uint32_t v = cluster_load(tot + threadIdx.x, c);
+      if (c < cta) before += v;
+      total += v;
+    }
+    uint32_t incl = total;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) warp_total[warp] = incl;
+    __syncthreads();
+    uint32_t base = incl - total + before;
+    for (int w = 0; w < warp; ++w) base += warp_total[w];
+#pragma unroll
+    for (int w = 0; w < kSortWarps; ++w) {
+      const uint32_t v = at[w][threadIdx.x];
+      at[w][threadIdx.x] = base;
+      base += v;
+    }
+    __syncthreads();
+    for (uint32_t i0 = lo; i0 < hi; i0 += 32 * kSortBatch) {  // uniform in the warp
+      uint32_t k[kSortBatch], t[kSortBatch];
+#pragma unroll
+      for (int b = 0; b < kSortBatch; ++b) {
+        const uint32_t i = i0 + 32 * b + lane;
+        k[b] = i < hi ? load(i) : 0;
+        t[b] = i < hi && pass > 0 ? __ldcg(toks + i) : i;
+      }
+#pragma unroll
+      for (int b = 0; b < kSortBatch; ++b) {
+        const bool on = i0 + 32 * b + lane < hi;
+        // a digit of its own for the lanes past the end
+        const uint32_t d = on ? k[b] >> shift & mask : kDigits;
+        const uint32_t same = __match_any_sync(0xffffffffu, d);
+        const uint32_t rank = __popc(same & ((1u << lane) - 1));
+        uint32_t to = 0;
+        if (on) to = at[warp][d] + rank;
+        __syncwarp();
+        if (on && rank == 0) at[warp][d] += __popc(same);
+        __syncwarp();
+        if (on) {
+          out_key[to] = k[b];
+          out_tok[to] = t[b];
+        }
+      }
+    }
+    cluster_sync();  // the pass is written, and tot has been read by all
   }
-  if (lane == 31) warp_total[warp] = incl;
-  __syncthreads();
-  uint32_t base = incl - total + before;
-  for (int w = 0; w < warp; ++w) base += warp_total[w];
+}
 
-  const int64_t lo = blockIdx.x * part, hi = lo + part < n ? lo + part : n;
-  const int64_t per = ceil_div(hi - lo, (int64_t)kSortThreads) * 32;  // of one warp
-  const int64_t wlo = lo + warp * per, whi = wlo + per < hi ? wlo + per : hi;
-  for (int64_t i = wlo + lane; i < whi; i += 32)
-    atomicAdd(&at[warp][sort_key(keys, i, ids, V) >> shift & mask], 1u);
+// Zeros in the rows that no token names.  CTA z has the rows whose number / 32 is z modulo
+// zero_ctas (present and absent rows gather at different ends of a vocabulary); it marks
+// its rows that the batch names, then its warps fill the others.
+template <int N>
+__device__ void zero_rows(const SortParams &a, uint32_t *flags) {
+  const uint32_t z = blockIdx.x - kSortCtas, Z = a.zero_ctas;
+  const int log = 31 - __clz(Z);
+  const uint32_t words = (uint32_t)(((uint64_t)a.V + 31) / 32);
+  const uint32_t mine = z < words ? (words - z - 1) / Z + 1 : 0;
+  for (uint32_t i = threadIdx.x; i < mine; i += kSortThreads) flags[i] = 0;
   __syncthreads();
-  for (int w = 0; w < kSortWarps; ++w) {
-    const uint32_t v = at[w][threadIdx.x];
-    at[w][threadIdx.x] = base;
-    base += v;
+  for (uint32_t i = threadIdx.x; i < a.n; i += kSortThreads * 8) {
+    uint32_t id[8];
+#pragma unroll
+    for (int b = 0; b < 8; ++b)
+      id[b] = a.n - i > b * kSortThreads ? a.ids[i + b * kSortThreads] : a.V;
+#pragma unroll
+    for (int b = 0; b < 8; ++b)
+      if (id[b] < a.V && (id[b] >> 5 & (Z - 1)) == z)
+        atomicOr(&flags[id[b] >> 5 >> log], 1u << (id[b] & 31));
   }
   __syncthreads();
-  for (int64_t i = wlo; i < whi; i += 32) {  // uniform in the warp
-    const bool on = i + lane < whi;
-    uint32_t k = 0, d = kDigits;  // a digit of its own for the lanes past the end
-    if (on) {
-      k = sort_key(keys, i + lane, ids, V);
-      d = k >> shift & mask;
-    }
-    const uint32_t same = __match_any_sync(0xffffffffu, d);
-    const uint32_t rank = __popc(same & ((1u << lane) - 1));
-    uint32_t to = 0;
-    if (on) to = at[warp][d] + rank;
-    __syncwarp();
-    if (on && rank == 0) at[warp][d] += __popc(same);
-    __syncwarp();
-    if (on) {
-      out_keys[to] = k;
-      out_toks[to] = toks != nullptr ? toks[i + lane] : (uint32_t)(i + lane);
+  const int lane = threadIdx.x & 31;
+  for (uint32_t r = threadIdx.x >> 5; r < mine * 32; r += kSortWarps) {
+    const uint64_t v = ((uint64_t)(r >> 5) * Z + z) * 32 + (r & 31);
+    if (v >= a.V || (flags[r >> 5] >> (r & 31) & 1)) continue;
+    float *row = a.dw + v * a.lddw;
+    if constexpr (N % 4 == 0) {
+      for (int64_t c = lane * 4; c < a.H; c += 128)
+        *reinterpret_cast<float4 *>(row + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+    } else {
+      for (int64_t c = lane; c < a.H; c += 32) row[c] = 0.f;
     }
   }
+}
+
+constexpr size_t kSortShared = sizeof(uint32_t) * (kSortWarps * kDigits + kDigits + kSortWarps);
+static_assert(kSortShared >= kFlagWords * sizeof(uint32_t), "the flags lie in the sort's memory");
+
+template <int N>
+__global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads, 2)
+embed_sort(const SortParams a) {
+  extern __shared__ uint32_t shared[];
+  pdl_wait();
+  pdl_trigger();
+  if (blockIdx.x < kSortCtas)
+    sort_tokens(a, shared);  // the grid's first cluster
+  else
+    zero_rows<N>(a, shared);
 }
 
 // ------------------------------------------------------------------- the sums
 
-template <typename T, int N> struct GradParams {
+template <typename T> struct GradParams {
   const T *dx;
   int64_t lddx;
   const uint32_t *key, *tok;  // sorted
-  uint32_t V;
-  int64_t T_, chunk;
-  int hp;      // packets of a row
+  uint32_t V, n;
+  int chunk, slabs;  // slabs of kColumns columns
+  uint32_t units;    // chunks x slabs
   int64_t H;
   float scale;
   float *dw;
@@ -207,196 +289,239 @@ template <typename T, int N> struct GradParams {
   float *part;  // [chunks][2][H]: the sum that the chunk's first id brings, the last's
 };
 
-template <int N> __device__ __forceinline__ void load_f32(const float *p, float (&v)[N]) {
-  if constexpr (N % 4 == 0) {
+// N fp32 values of a row of dW or of a partial sum.
+__device__ __forceinline__ void load_f32(const float *p, float2 (&v)[4]) {
+  unpack(load_raw<uint4>(p), reinterpret_cast<float2(&)[2]>(v[0]));
+  unpack(load_raw<uint4>(p + 4), reinterpret_cast<float2(&)[2]>(v[2]));
+}
+__device__ __forceinline__ void load_f32(const float *p, float2 (&v)[2]) {
+  unpack(load_raw<uint4>(p), v);
+}
+__device__ __forceinline__ void load_f32(const float *p, float (&v)[1]) { v[0] = *p; }
+
+template <int P> __device__ __forceinline__ void store_f32(float *p, const float2 (&v)[P]) {
 #pragma unroll
-    for (int e = 0; e < N; e += 4) {
-      const float4 f = *reinterpret_cast<const float4 *>(p + e);
-      v[e] = f.x, v[e + 1] = f.y, v[e + 2] = f.z, v[e + 3] = f.w;
+  for (int i = 0; i < P; i += 2)
+    *reinterpret_cast<float4 *>(p + 2 * i) = make_float4(v[i].x, v[i].y, v[i + 1].x, v[i + 1].y);
+}
+__device__ __forceinline__ void store_f32(float *p, const float (&v)[1]) { *p = v[0]; }
+
+// Adds to global memory without an answer.
+template <int P> __device__ __forceinline__ void add_f32(float *p, const float2 (&v)[P]) {
+#pragma unroll
+  for (int i = 0; i < P; i += 2)
+    asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p + 2 * i), "f"(v[i].x),
+                 "f"(v[i].y), "f"(v[i + 1].x), "f"(v[i + 1].y)
+                 : "memory");
+}
+__device__ __forceinline__ void add_f32(float *p, const float (&v)[1]) { atomicAdd(p, v[0]); }
+
+__device__ __forceinline__ float vadd(float a, float b) { return a + b; }
+__device__ __forceinline__ float2 vadd(float2 a, float2 b) { return __fadd2_rn(a, b); }
+
+// A lane's columns: U packets of N, 32 N apart.
+template <typename T, int N> struct Slab {
+  static constexpr int U = N == 1 ? 8 : kColumns / (32 * N);
+  int64_t c;    // the first column
+  uint32_t on;  // bit u: packet u lies in the row
+  __device__ __forceinline__ Slab(int slab, int64_t H) {
+    c = (int64_t)slab * kColumns + (threadIdx.x & 31) * N;
+    on = 0;
+#pragma unroll
+    for (int u = 0; u < U; ++u) on |= c + u * 32 * N < H ? 1u << u : 0u;
+  }
+};
+
+// dW's row gets scale * acc, with ACC added to what it holds: by a reduction in L2, which
+// needs no answer.  Each element gets one such addition in a call, so that no order can
+// change the result.
+template <typename T, int N, bool ACC, typename VT>
+__device__ __forceinline__ void finish_row(float *row, const Slab<T, N> &s,
+                                           const VT (&acc)[Slab<T, N>::U][Values<N>::kCount],
+                                           float scale) {
+#pragma unroll
+  for (int u = 0; u < Slab<T, N>::U; ++u)
+    if (s.on >> u & 1) {
+      VT o[Values<N>::kCount];
+#pragma unroll
+      for (int i = 0; i < Values<N>::kCount; ++i) o[i] = vmul(vall<VT>(scale), acc[u][i]);
+      if (ACC)
+        add_f32(row + s.c + u * 32 * N, o);
+      else
+        store_f32(row + s.c + u * 32 * N, o);
     }
-  } else {
-#pragma unroll
-    for (int e = 0; e < N; ++e) v[e] = p[e];
-  }
-}
-template <int N> __device__ __forceinline__ void store_f32(float *p, const float (&v)[N]) {
-  if constexpr (N % 4 == 0) {
-#pragma unroll
-    for (int e = 0; e < N; e += 4)
-      *reinterpret_cast<float4 *>(p + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
-  } else {
-#pragma unroll
-    for (int e = 0; e < N; ++e) p[e] = v[e];
-  }
 }
 
-// dW's row gets scale * acc, added to what it holds with ACC.
-template <int N, bool ACC>
-__device__ __forceinline__ void finish_row(float *p, const float (&acc)[N], float scale) {
-  float o[N];
-  if (ACC) {
-    load_f32<N>(p, o);
-#pragma unroll
-    for (int e = 0; e < N; ++e) o[e] = fmaf(scale, acc[e], o[e]);
-  } else {
-#pragma unroll
-    for (int e = 0; e < N; ++e) o[e] = scale * acc[e];
-  }
-  store_f32<N>(p, o);
-}
-
-constexpr int kGradBatch = 8;  // rows of dx in flight for each thread
+constexpr int kGradWarps = 4, kGradCtas = 6;
+template <int N> constexpr int kGradBatch = N == 8 ? 8 : 4;  // rows in flight for a warp
 
 template <typename T, int N, bool ACC>
-__global__ void __launch_bounds__(kThreads) embed_grad(const GradParams<T, N> a) {
-  extern __shared__ uint32_t list[];  // [chunk] keys, [chunk] tokens
+__global__ void __launch_bounds__(32 * kGradWarps, kGradCtas) embed_grad(const GradParams<T> a) {
+  using VT = typename Values<N>::V;
+  using Rw = typename Raw<T, N>::type;
+  constexpr int U = Slab<T, N>::U, B = kGradBatch<N>, P = Values<N>::kCount;
+  constexpr unsigned kAll = 0xffffffffu;
   pdl_wait();
   pdl_trigger();
-  const int64_t lo = blockIdx.x * a.chunk;
-  const int n = (int)(lo + a.chunk < a.T_ ? a.chunk : a.T_ - lo);
-  uint32_t *key = list, *tok = list + a.chunk;
-  for (int i = threadIdx.x; i < n; i += kThreads) {
-    key[i] = a.key[lo + i];
-    tok[i] = a.tok[lo + i];
-  }
-  const uint32_t prev = lo > 0 ? a.key[lo - 1] : a.V;
-  const uint32_t next = lo + n < a.T_ ? a.key[lo + n] : a.V;
-  __syncthreads();
-  const int c = blockIdx.y * kThreads + threadIdx.x;
-  if (c >= a.hp) return;
-  const T *col = a.dx + (int64_t)c * N;
-  float acc[N];
-#pragma unroll
-  for (int e = 0; e < N; ++e) acc[e] = 0.f;
-  bool first = prev == key[0];  // the run came in from the chunk before
-  for (int i0 = 0; i0 < n; i0 += kGradBatch) {
-    Packet<T, N> v[kGradBatch];
-#pragma unroll
-    for (int b = 0; b < kGradBatch; ++b)
-      if (i0 + b < n && key[i0 + b] < a.V)
-        v[b] = load_packet_stream<T, N>(col + (int64_t)tok[i0 + b] * a.lddx);
-#pragma unroll
-    for (int b = 0; b < kGradBatch; ++b) {
-      const int i = i0 + b;
-      if (i >= n) break;
-      const uint32_t k = key[i];
-      if (k >= a.V) return;  // only tokens without a row follow
-#pragma unroll
-      for (int e = 0; e < N; ++e) acc[e] += v[b].get(e);
-      const bool last = i + 1 == n;
-      if (!last && key[i + 1] == k) continue;
-      if (first || (last && next == k)) {
-        store_f32<N>(a.part + ((int64_t)blockIdx.x * 2 + (first ? 0 : 1)) * a.H + (int64_t)c * N,
-                     acc);
-      } else {
-        finish_row<N, ACC>(a.dw + (int64_t)k * a.lddw + (int64_t)c * N, acc, a.scale);
-      }
-      first = false;
-#pragma unroll
-      for (int e = 0; e < N; ++e) acc[e] = 0.f;
-    }
-  }
-}
-
-// Joins the sums of an id that crosses chunks: the CTA of the chunk where its run
-// begins adds the chunks' parts in their order.
-template <int N, bool ACC>
-__global__ void __launch_bounds__(kThreads)
-embed_join(const uint32_t *key, uint32_t V, int64_t n, int64_t chunk, int hp, int64_t H,
-           float scale, const float *part, float *dw, int64_t lddw) {
-  pdl_wait();
-  pdl_trigger();
-  const int64_t lo = blockIdx.x * chunk, hi = lo + chunk;  // hi is in the next chunk
-  if (hi >= n) return;
-  const uint32_t k = key[hi - 1];
-  if (k >= V || key[hi] != k) return;                        // nothing leaves this chunk
-  if (lo > 0 && key[lo - 1] == k && key[lo] == k) return;    // it came in from before
-  const int c = blockIdx.y * kThreads + threadIdx.x;
-  if (c >= hp) return;
-  float acc[N], v[N];
-  load_f32<N>(part + ((int64_t)blockIdx.x * 2 + 1) * H + (int64_t)c * N, acc);
-  for (int64_t b = blockIdx.x + 1;; ++b) {
-    load_f32<N>(part + b * 2 * H + (int64_t)c * N, v);
-#pragma unroll
-    for (int e = 0; e < N; ++e) acc[e] += v[e];
-    const int64_t end = (b + 1) * chunk;
-    if (end >= n || key[end] != k) break;
-  }
-  finish_row<N, ACC>(dw + (int64_t)k * lddw + (int64_t)c * N, acc, scale);
-}
-
-// Zeros in the rows that no token names.  Each lane looks one id up in the sorted
-// list; the warp then fills its absent rows.
-template <int N>
-__global__ void __launch_bounds__(kThreads)
-embed_zero(const uint32_t *key, int64_t n, int64_t V, int hp, float *dw, int64_t lddw) {
-  pdl_wait();
-  pdl_trigger();
+  const uint32_t unit = blockIdx.x * kGradWarps + (threadIdx.x >> 5);
+  if (unit >= a.units) return;
+  const uint32_t ch = unit / a.slabs;
+  const Slab<T, N> s(unit - ch * a.slabs, a.H);
   const int lane = threadIdx.x & 31;
-  const int64_t v0 = ((int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * 32;
-  if (v0 >= V) return;
-  const int64_t v = v0 + lane;
-  int64_t lo = 0, hi = n;  // the first place whose key is v or beyond
-  while (lo < hi) {
-    const int64_t m = (lo + hi) / 2;
-    if ((int64_t)key[m] < v) lo = m + 1; else hi = m;
+  const uint32_t lo = ch * a.chunk, hi = a.n - lo < a.chunk ? a.n : lo + a.chunk;
+  uint32_t prev = lo > 0 ? a.key[lo - 1] : a.V;  // the key before the current position
+  bool came = true;  // the current run began before this chunk (where prev is its key)
+  const T *col = a.dx + s.c;
+  VT acc[U][P];
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+#pragma unroll
+    for (int e = 0; e < P; ++e) acc[u][e] = vall<VT>(0.f);
+  float *const part = a.part + (int64_t)ch * 2 * a.H;
+  bool some = false;  // acc holds a run's terms
+  auto flush = [&](uint32_t k, bool leaves) {
+    if (came || leaves) {
+      float *p = part + (came ? 0 : a.H) + s.c;
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (s.on >> u & 1) store_f32(p + u * 32 * N, acc[u]);
+    } else {
+      finish_row<T, N, ACC>(a.dw + (int64_t)k * a.lddw, s, acc, a.scale);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int e = 0; e < P; ++e) acc[u][e] = vall<VT>(0.f);
+  };
+  for (uint32_t i0 = lo; i0 < hi; i0 += 32) {
+    const uint32_t at = i0 + lane;
+    const uint32_t key = at < hi ? a.key[at] : a.V;
+    const uint32_t tok = at < hi ? a.tok[at] : 0;
+    for (int j0 = 0; j0 < 32 && i0 + j0 < hi; j0 += B) {
+      Rw v[B][U];
+#pragma unroll
+      for (int b = 0; b < B; ++b) {
+        const uint32_t k = __shfl_sync(kAll, key, j0 + b);
+        const T *p = col + (int64_t)__shfl_sync(kAll, tok, j0 + b) * a.lddx;
+        if (k < a.V)
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+            if (s.on >> u & 1) v[b][u] = load_raw_stream<Rw>(p + u * 32 * N);
+      }
+#pragma unroll
+      for (int b = 0; b < B; ++b) {
+        const uint32_t k = __shfl_sync(kAll, key, j0 + b);
+        if (k != prev) {  // a run ends before this position
+          if (some) flush(prev, false);
+          came = some = false;
+        }
+        prev = k;
+        if (k < a.V) {
+          some = true;
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            VT f[P];
+            unpack(v[b][u], f);
+#pragma unroll
+            for (int e = 0; e < P; ++e) acc[u][e] = vadd(acc[u][e], f[e]);
+          }
+        }
+      }
+    }
   }
-  uint32_t todo = __ballot_sync(0xffffffffu, v < V && !(lo < n && (int64_t)key[lo] == v));
-  const float zero[N] = {};
-  while (todo != 0) {
-    float *row = dw + (v0 + __ffs(todo) - 1) * lddw;
-    todo &= todo - 1;
-    for (int c = lane; c < hp; c += 32) store_f32<N>(row + (int64_t)c * N, zero);
+  // the last run: positions past the chunk's end had key V, unless the chunk was full
+  if (some) flush(prev, hi < a.n && a.key[hi] == prev);
+}
+
+// Joins the sums of an id that crosses chunks: the warp of the chunk where its run begins
+// adds the chunks' parts in their order.
+template <typename T, int N, bool ACC>
+__global__ void __launch_bounds__(32 * kGradWarps) embed_join(const GradParams<T> a) {
+  using VT = typename Values<N>::V;
+  constexpr int U = Slab<T, N>::U, B = N == 1 ? 2 : 4, P = Values<N>::kCount;
+  pdl_wait();
+  pdl_trigger();
+  const uint32_t unit = blockIdx.x * kGradWarps + (threadIdx.x >> 5);
+  if (unit >= a.units) return;
+  const uint32_t ch = unit / a.slabs;
+  const uint32_t lo = ch * a.chunk;
+  if (a.n - lo <= a.chunk) return;  // the last chunk
+  const uint32_t hi = lo + a.chunk, k = a.key[hi];
+  if (k >= a.V || a.key[hi - 1] != k) return;                   // nothing leaves this chunk
+  if (lo > 0 && a.key[lo - 1] == k && a.key[lo] == k) return;   // it came in from before
+  const Slab<T, N> s(unit - ch * a.slabs, a.H);
+  // the last chunk that has a part of it: the one with the last place of k
+  uint32_t l = hi, r = a.n;  // key[l] == k, and key[r] (or the end) lies behind k
+  while (r - l > 1) {
+    const uint32_t m = l + (r - l) / 2;
+    if (a.key[m] == k) l = m; else r = m;
   }
+  const uint32_t last = l / a.chunk;
+  VT acc[U][P], v[B][U][P];
+  const float *p = a.part + s.c;
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (s.on >> u & 1) load_f32(p + ((int64_t)ch * 2 + 1) * a.H + u * 32 * N, acc[u]);
+  for (uint32_t c0 = ch + 1; c0 <= last; c0 += B) {
+#pragma unroll
+    for (int b = 0; b < B; ++b)
+      if (c0 + b <= last)
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (s.on >> u & 1)
+            load_f32(p + (int64_t)(c0 + b) * 2 * a.H + u * 32 * N, v[b][u]);
+#pragma unroll
+    for (int b = 0; b < B; ++b)
+      if (c0 + b <= last)
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int e = 0; e < P; ++e) acc[u][e] = vadd(acc[u][e], v[b][u][e]);
+  }
+  finish_row<T, N, ACC>(a.dw + (int64_t)k * a.lddw, s, acc, a.scale);
 }
 
 template <typename T, int N, bool ACC>
-cudaError_t bwd_typed(const EmbedBwdArgs &a, cudaStream_t s) {
-  cudaError_t e;
+cudaError_t bwd_typed(const EmbedBwdArgs &a, const DeviceInfo &dev, cudaStream_t s) {
   const EmbedPlan p = plan_embed(a.T, a.H, a.V);
   unsigned char *const ws = (unsigned char *)a.ws;
-  const uint32_t V = (uint32_t)a.V;
-  const int hp = (int)(a.H / N);
-  uint32_t *key = nullptr, *tok = nullptr;
-  if (a.T > 0) {
-    uint32_t *const counts = (uint32_t *)(ws + p.off_counts);
-    const uint32_t *in_key = (const uint32_t *)a.ids, *in_tok = nullptr;
-    for (int i = 0; i < p.passes; ++i) {
-      key = (uint32_t *)(ws + p.off_key[i & 1]);
-      tok = (uint32_t *)(ws + p.off_tok[i & 1]);
-      const int shift = i * p.digit_bits;
-      const uint32_t mask = (1u << p.digit_bits) - 1;
-      e = launch_pdl(sort_count, dim3((unsigned)p.ctas), dim3(kSortThreads), 0, s, in_key, i == 0,
-                     V, a.T, p.part, shift, mask, counts);
-      if (e != cudaSuccess) return e;
-      e = launch_pdl(sort_scatter, dim3((unsigned)p.ctas), dim3(kSortThreads), 0, s, in_key,
-                     in_tok, i == 0, V, a.T, p.part, shift, mask, counts, key, tok);
-      if (e != cudaSuccess) return e;
-      in_key = key;
-      in_tok = tok;
-    }
-    const GradParams<T, N> g{(const T *)a.dx, a.lddx, key, tok, V,   a.T,    p.chunk,
-                             hp,              a.H,    a.scale,  a.dw, a.lddw,
-                             (float *)(ws + p.off_part)};
-    const dim3 grid((unsigned)p.chunks, (unsigned)ceil_div(hp, kThreads));
-    e = launch_pdl(embed_grad<T, N, ACC>, grid, dim3(kThreads), (size_t)p.chunk * 8, s, g);
-    if (e != cudaSuccess) return e;
-    e = launch_pdl(embed_join<N, ACC>, grid, dim3(kThreads), 0, s, key, V, a.T, p.chunk, hp, a.H,
-                   a.scale, g.part, a.dw, a.lddw);
-    if (e != cudaSuccess) return e;
+  SortParams q{};
+  q.ids = (const uint32_t *)a.ids;
+  q.V = (uint32_t)a.V;
+  q.n = (uint32_t)a.T;
+  q.passes = a.T > 0 ? p.passes : 0;
+  q.digit_bits = p.digit_bits;
+  for (int i = 0; i < 2; ++i) {
+    q.key[i] = (uint32_t *)(ws + p.off_key[i]);
+    q.tok[i] = (uint32_t *)(ws + p.off_tok[i]);
   }
   if (!ACC) {
-    const int64_t warps = ceil_div(a.V, (int64_t)32);
-    e = launch_pdl(embed_zero<N>, dim3((unsigned)ceil_div(warps, (int64_t)(kThreads / 32))),
-                   dim3(kThreads), 0, s, key, a.T, a.V, hp, a.dw, a.lddw);
-    if (e != cudaSuccess) return e;
+    q.zero_ctas = 256;  // with the sort's, what two CTAs on each of 152 SMs hold
+    const int64_t words = ceil_div(a.V, (int64_t)32);
+    while ((int64_t)q.zero_ctas * kFlagWords < words) q.zero_ctas *= 2;
+    q.dw = a.dw;
+    q.lddw = a.lddw;
+    q.H = a.H;
   }
-  return cudaGetLastError();
+  (void)blocks_per_sm((const void *)embed_sort<N>, kSortThreads, kSortShared, dev, 2);
+  cudaError_t e = launch_pdl(embed_sort<N>, dim3((unsigned)(kSortCtas + q.zero_ctas)),
+                             dim3(kSortThreads), kSortShared, s, q);
+  if (e != cudaSuccess || a.T == 0) return e != cudaSuccess ? e : cudaGetLastError();
+  const int64_t slabs = ceil_div(a.H, (int64_t)kColumns);
+  const int last = (p.passes - 1) & 1;
+  const GradParams<T> g{(const T *)a.dx, a.lddx, q.key[last], q.tok[last], q.V, q.n,
+                        (int)p.chunk, (int)slabs, (uint32_t)(p.chunks * slabs), a.H, a.scale,
+                        a.dw, a.lddw, (float *)(ws + p.off_part)};
+  const dim3 grid((unsigned)ceil_div(p.chunks * slabs, (int64_t)kGradWarps));
+  e = launch_pdl(embed_grad<T, N, ACC>, grid, dim3(32 * kGradWarps), 0, s, g);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(embed_join<T, N, ACC>, grid, dim3(32 * kGradWarps), 0, s, g);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 template <typename T, int N>
-cudaError_t bwd_acc(const EmbedBwdArgs &a, cudaStream_t s) {
-  return a.accumulate ? bwd_typed<T, N, true>(a, s) : bwd_typed<T, N, false>(a, s);
+cudaError_t bwd_acc(const EmbedBwdArgs &a, const DeviceInfo &dev, cudaStream_t s) {
+  return a.accumulate ? bwd_typed<T, N, true>(a, dev, s) : bwd_typed<T, N, false>(a, dev, s);
 }
 
 }  // namespace
@@ -411,10 +536,10 @@ cudaError_t launch_embed_fwd(DType dt, bool vec, const EmbedFwdArgs &a, const De
   return vec ? fwd_typed<bf16, 8>(a, dev, s) : fwd_typed<bf16, 1>(a, dev, s);
 }
 
-cudaError_t launch_embed_bwd(DType dt, bool vec, const EmbedBwdArgs &a, const DeviceInfo &,
+cudaError_t launch_embed_bwd(DType dt, bool vec, const EmbedBwdArgs &a, const DeviceInfo &dev,
                              cudaStream_t s) {
-  if (dt == DType::F32) return vec ? bwd_acc<float, 4>(a, s) : bwd_acc<float, 1>(a, s);
-  return vec ? bwd_acc<bf16, 8>(a, s) : bwd_acc<bf16, 1>(a, s);
+  if (dt == DType::F32) return vec ? bwd_acc<float, 4>(a, dev, s) : bwd_acc<float, 1>(a, dev, s);
+  return vec ? bwd_acc<bf16, 8>(a, dev, s) : bwd_acc<bf16, 1>(a, dev, s);
 }
 
 }  // namespace ftk
