@@ -24,37 +24,63 @@ namespace {
 
 constexpr int kThreads = 256;
 
+// A thread stays with one packet of columns and walks the rows, kRows of them at a time:
+// all their ids first, then all their packets.  `cols` threads lie along a row
+// (gridDim.y such parts make it up), blockDim.x / cols rows side by side.
+constexpr int kRows = 4;
+
 template <typename T, int N>
 __global__ void __launch_bounds__(kThreads)
-embed_fwd_rows(const T *w, int64_t ldw, int64_t V, const int32_t *ids, T *x, int64_t ldx,
-               int64_t rows, int hp, float scale) {
+embed_fwd_rows(const T *w, int64_t ldw, uint32_t V, const int32_t *ids, T *x, int64_t ldx,
+               int64_t rows, int hp, int cols, float scale) {
+  using VT = typename Values<N>::V;
+  using Rw = typename Raw<T, N>::type;
+  constexpr int P = Values<N>::kCount;
   pdl_wait();
   pdl_trigger();
-  const int64_t n = rows * hp, step = (int64_t)gridDim.x * kThreads;
-  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += step) {
-    const int64_t t = i / hp, c = (i - t * hp) * N;
-    const int64_t id = ids[t];
-    Packet<T, N> o;
-    if (id >= 0 && id < V) {
-      const Packet<T, N> v = load_packet<T, N>(w + id * ldw + c);
+  const int r = threadIdx.x / cols, c = blockIdx.y * cols + threadIdx.x - r * cols;
+  const int side = blockDim.x / cols;
+  if (c >= hp) return;
+  w += (int64_t)c * N;
+  x += (int64_t)c * N;
+  const int64_t step = (int64_t)gridDim.x * side;
+  for (int64_t t0 = (int64_t)blockIdx.x * side + r; t0 < rows; t0 += kRows * step) {
+    uint32_t id[kRows];
+    Rw v[kRows];
 #pragma unroll
-      for (int e = 0; e < N; ++e) o.set(e, v.get(e) * scale);
-    } else {
+    for (int i = 0; i < kRows; ++i)
+      id[i] = t0 + i * step < rows ? (uint32_t)ids[t0 + i * step] : V;
 #pragma unroll
-      for (int e = 0; e < N; ++e) o.set(e, 0.f);
-    }
-    store_packet<T, N>(x + t * ldx + c, o);
+    for (int i = 0; i < kRows; ++i)
+      if (id[i] < V) v[i] = load_raw<Rw>(w + (int64_t)id[i] * ldw);  // as unsigned: never < 0
+#pragma unroll
+    for (int i = 0; i < kRows; ++i)
+      if (t0 + i * step < rows) {
+        VT f[P];
+        if (id[i] < V) {
+          unpack(v[i], f);
+#pragma unroll
+          for (int e = 0; e < P; ++e) f[e] = vmul(f[e], vall<VT>(scale));
+        } else {
+#pragma unroll
+          for (int e = 0; e < P; ++e) f[e] = vall<VT>(0.f);
+        }
+        pack(f, v[i]);
+        store_raw(x + (t0 + i * step) * ldx, v[i]);
+      }
   }
 }
 
 template <typename T, int N>
 cudaError_t fwd_typed(const EmbedFwdArgs &a, const DeviceInfo &dev, cudaStream_t s) {
-  const int64_t hp = a.H / N;
-  int64_t grid = ceil_div(a.T * hp, (int64_t)kThreads);
-  if (grid > (int64_t)dev.sms * 32) grid = (int64_t)dev.sms * 32;
-  cudaError_t e = launch_pdl(embed_fwd_rows<T, N>, dim3((unsigned)grid), dim3(kThreads), 0, s,
-                             (const T *)a.w, a.ldw, a.V, a.ids, (T *)a.x, a.ldx, a.T, (int)hp,
-                             a.scale);
+  const int hp = (int)(a.H / N), parts = ceil_div(hp, kThreads), cols = ceil_div(hp, parts);
+  const int side = kThreads / cols;
+  int64_t grid = ceil_div(a.T, (int64_t)side);
+  const int64_t most = ceil_div((int64_t)dev.sms * 8, (int64_t)parts);
+  if (grid > most) grid = most;
+  cudaError_t e = launch_pdl(embed_fwd_rows<T, N>, dim3((unsigned)grid, (unsigned)parts),
+                             dim3((unsigned)(side * cols)), 0, s, (const T *)a.w, a.ldw,
+                             (uint32_t)a.V, a.ids, (T *)a.x, a.ldx, a.T, hp, cols, a.scale);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -352,14 +378,14 @@ __device__ __forceinline__ void finish_row(float *row, const Slab<T, N> &s,
     }
 }
 
-constexpr int kGradWarps = 4, kGradCtas = 6;
-template <int N> constexpr int kGradBatch = N == 8 ? 8 : 4;  // rows in flight for a warp
+constexpr int kGradWarps = 4, kGradCtas = 8;
+constexpr int kGradBatch = 4;  // rows in flight for a warp
 
 template <typename T, int N, bool ACC>
 __global__ void __launch_bounds__(32 * kGradWarps, kGradCtas) embed_grad(const GradParams<T> a) {
   using VT = typename Values<N>::V;
   using Rw = typename Raw<T, N>::type;
-  constexpr int U = Slab<T, N>::U, B = kGradBatch<N>, P = Values<N>::kCount;
+  constexpr int U = Slab<T, N>::U, B = kGradBatch, P = Values<N>::kCount;
   constexpr unsigned kAll = 0xffffffffu;
   pdl_wait();
   pdl_trigger();
@@ -438,7 +464,7 @@ __global__ void __launch_bounds__(32 * kGradWarps, kGradCtas) embed_grad(const G
 template <typename T, int N, bool ACC>
 __global__ void __launch_bounds__(32 * kGradWarps) embed_join(const GradParams<T> a) {
   using VT = typename Values<N>::V;
-  constexpr int U = Slab<T, N>::U, B = N == 1 ? 2 : 4, P = Values<N>::kCount;
+  constexpr int U = Slab<T, N>::U, B = N == 8 ? 8 : N == 4 ? 4 : 2, P = Values<N>::kCount;
   pdl_wait();
   pdl_trigger();
   const uint32_t unit = blockIdx.x * kGradWarps + (threadIdx.x >> 5);
@@ -450,13 +476,15 @@ __global__ void __launch_bounds__(32 * kGradWarps) embed_join(const GradParams<T
   if (k >= a.V || a.key[hi - 1] != k) return;                   // nothing leaves this chunk
   if (lo > 0 && a.key[lo - 1] == k && a.key[lo] == k) return;   // it came in from before
   const Slab<T, N> s(unit - ch * a.slabs, a.H);
-  // the last chunk that has a part of it: the one with the last place of k
-  uint32_t l = hi, r = a.n;  // key[l] == k, and key[r] (or the end) lies behind k
-  while (r - l > 1) {
-    const uint32_t m = l + (r - l) / 2;
-    if (a.key[m] == k) l = m; else r = m;
+  // the last chunk that has a part of it: those from here on that begin with k
+  const int lane = threadIdx.x & 31;
+  uint32_t last = ch;
+  for (;;) {
+    const uint64_t c0 = ((uint64_t)last + 1 + lane) * a.chunk;
+    const uint32_t out = ~__ballot_sync(0xffffffffu, c0 < a.n && a.key[c0 < a.n ? c0 : 0] == k);
+    last += out == 0 ? 32 : __ffs(out) - 1;
+    if (out != 0) break;
   }
-  const uint32_t last = l / a.chunk;
   VT acc[U][P], v[B][U][P];
   const float *p = a.part + s.c;
 #pragma unroll
