@@ -255,9 +255,9 @@ template <int S> struct Walk {
 };
 template <int S> struct Rows {
   const char *at[S];
-  __device__ __forceinline__ void advance(const Walk<S> &w, int rows) {
+  __device__ __forceinline__ void advance(const Walk<S> &w) {
 #pragma unroll
-    for (int s = 0; s < S; ++s) at[s] += rows * w.step[s];
+    for (int s = 0; s < S; ++s) at[s] += w.step[s];
   }
 };
 
@@ -266,51 +266,62 @@ template <int S> struct Rows {
 // reads back what it copied itself, so that the ring needs no barrier), kDepth - 1 turns
 // ahead; single columns, which are too small for such copies, wait in registers, one
 // turn ahead.  Columns: offset `off` (bytes) of the row, packet k 32 W packets further.
+// With one packet a thread, threads past the row's end take its first packet along (with
+// weights of zero, and without storing anything), which spares the branches.
 struct Turn {
   uint32_t t, step, rows;  // the next row to fetch, the group's step, the batch's rows
   uint32_t off, gap, on;   // bytes; bit k: the thread has a packet k
 };
 
+__device__ __forceinline__ uint4 load_shared(uint32_t p) {
+  uint4 u;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
+               : "r"(p));  // volatile: stays behind the wait for the copies
+  return u;
+}
+
 template <typename T, int N, int V, int S, int B, int kDepth> struct Ahead {
   static constexpr int kItems = S * B * V;  // of a turn; 512 bytes each for a warp
-  char *slot;                               // this thread's place in the ring
-  int turn;
+  uint32_t base, slot;  // shared addresses: this thread's place in the ring, in the turn
   static constexpr size_t bytes(int threads) {
     return (size_t)threads * kDepth * kItems * sizeof(uint4);
   }
-  __device__ __forceinline__ char *place(int d, int s, int b, int k) const {
-    return slot + (d * kItems + (s * B + b) * V + k) * 512;
-  }
-  __device__ __forceinline__ void fetch(int d, Rows<S> &src, const Walk<S> &w, Turn &n) {
+  static constexpr uint32_t kTurn = kItems * 512;
+  __device__ __forceinline__ void fetch(uint32_t to, Rows<S> &src, const Walk<S> &w, Turn &n) {
 #pragma unroll
-    for (int b = 0; b < B; ++b)
-      if (n.t + b * n.step < n.rows)
+    for (int b = 0; b < B; ++b) {
+      if (n.t < n.rows)
 #pragma unroll
         for (int s = 0; s < S; ++s)
 #pragma unroll
           for (int k = 0; k < V; ++k)
-            if (n.on >> k & 1)
-              cp_async16(place(d, s, b, k), src.at[s] + b * w.step[s] + (n.off + k * n.gap));
+            if (V == 1 || n.on >> k & 1)
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                               to + ((s * B + b) * V + k) * 512),
+                           "l"(src.at[s] + (n.off + k * n.gap))
+                           : "memory");
+      n.t += n.step;
+      src.advance(w);
+    }
     cp_async_commit();  // a group for each turn, empty or not
-    n.t += B * n.step;
-    src.advance(w, B);
   }
   __device__ __forceinline__ void start(uint4 *ring, Rows<S> &src, const Walk<S> &w, Turn &n) {
-    slot = reinterpret_cast<char *>(ring + (threadIdx.x >> 5) * (kDepth * kItems * 32) +
-                                    (threadIdx.x & 31));
-    turn = 0;
+    base = slot = smem_addr(ring) + (threadIdx.x >> 5) * (kDepth * kTurn) + (threadIdx.x & 31) * 16;
 #pragma unroll
-    for (int i = 0; i < kDepth - 1; ++i) fetch(i, src, w, n);
+    for (int i = 0; i < kDepth - 1; ++i) fetch(base + i * kTurn, src, w, n);
   }
   // the current turn's rows are there, the last of the ring's on their way
   __device__ __forceinline__ void arrive(Rows<S> &src, const Walk<S> &w, Turn &n) {
-    fetch(turn == 0 ? kDepth - 1 : turn - 1, src, w, n);
+    fetch(slot == base ? base + (kDepth - 1) * kTurn : slot - kTurn, src, w, n);
     cp_async_wait<kDepth - 1>();
   }
   __device__ __forceinline__ uint4 get(int s, int b, int k) const {
-    return *reinterpret_cast<const uint4 *>(place(turn, s, b, k));
+    return load_shared(slot + ((s * B + b) * V + k) * 512);
   }
-  __device__ __forceinline__ void next() { turn = turn + 1 == kDepth ? 0 : turn + 1; }
+  __device__ __forceinline__ void next() {
+    slot = slot == base + (kDepth - 1) * kTurn ? base : slot + kTurn;
+  }
 };
 
 template <typename T, int V, int S, int B, int kDepth> struct Ahead<T, 1, V, S, B, kDepth> {
@@ -318,17 +329,17 @@ template <typename T, int V, int S, int B, int kDepth> struct Ahead<T, 1, V, S, 
   static constexpr size_t bytes(int) { return 0; }
   __device__ __forceinline__ void start(uint4 *, Rows<S> &src, const Walk<S> &w, Turn &n) {
 #pragma unroll
-    for (int b = 0; b < B; ++b)
-      if (n.t + b * n.step < n.rows)
+    for (int b = 0; b < B; ++b) {
+      if (n.t < n.rows)
 #pragma unroll
         for (int s = 0; s < S; ++s)
 #pragma unroll
           for (int k = 0; k < V; ++k)
-            if (n.on >> k & 1)
-              then[s][b][k] = *reinterpret_cast<const T *>(src.at[s] + b * w.step[s] +
-                                                           (n.off + k * n.gap));
-    n.t += B * n.step;
-    src.advance(w, B);
+            if (V == 1 || n.on >> k & 1)
+              then[s][b][k] = *reinterpret_cast<const T *>(src.at[s] + (n.off + k * n.gap));
+      n.t += n.step;
+      src.advance(w);
+    }
   }
   __device__ __forceinline__ void arrive(Rows<S> &src, const Walk<S> &w, Turn &n) {
 #pragma unroll

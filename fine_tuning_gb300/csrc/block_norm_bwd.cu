@@ -96,11 +96,15 @@ block_norm_bwd_rows(const BlockNorm<T> a, const Walk<4> walk_in, const Walk<2> w
   Rw w[kHold ? V : 1];
 #pragma unroll
   for (int k = 0; k < V; ++k) {
-    if constexpr (kHold)
+    if constexpr (kHold) {
+#pragma unroll
+      for (int i = 0; i < P; ++i) wg[k][i] = vall<VT>(0.f);
+      w[k] = Rw{};
       if (on >> k & 1) {
         column_factors<T, N>(a, c0 + k * G * N, wg[k]);
         w[k] = load_raw<Rw>(a.w + c0 + k * G * N);
       }
+    }
 #pragma unroll
     for (int i = 0; i < P; ++i) sw[k][i] = sx[k][i] = vall<VT>(0.f);
   }
@@ -112,7 +116,7 @@ block_norm_bwd_rows(const BlockNorm<T> a, const Walk<4> walk_in, const Walk<2> w
   Rows<4> src{{(const char *)(a.x + t * a.ldx), (const char *)(a.h + t * a.ldh),
                (const char *)(a.dy + t * a.lddy), (const char *)(a.dh + t * a.lddh)}};
   Rows<2> out{{(const char *)(a.dx + t * a.lddx), (const char *)(a.dres + t * a.lddr)}};
-  const uint32_t off = c0 * (int)sizeof(T), gap = G * N * (int)sizeof(T);
+  const uint32_t off = V > 1 || on ? c0 * (int)sizeof(T) : 0, gap = G * N * (int)sizeof(T);
   Turn turn{t, step, rows, off, gap, on};
   Ahead<T, N, V, 4, B, kBwdDepth<V>> in;
   in.start(ring, src, walk_in, turn);
@@ -142,10 +146,10 @@ block_norm_bwd_rows(const BlockNorm<T> a, const Walk<4> walk_in, const Walk<2> w
       // without the rows' own factors: w dy h, m wg x (dh + r2 w dy), m wg x h
       VT s_h = vall<VT>(0.f), s_g = s_h, s_c = s_h;
       const VT r2v = vall<VT>(r2[b]);
-      if (t + b * step < rows)
+      if (b == 0 || t + b * step < rows)
 #pragma unroll
         for (int k = 0; k < V; ++k)
-          if (on >> k & 1) {
+          if (V == 1 || on >> k & 1) {
             VT x[P], h[P], dy[P], dh[P], f[P], wf[P];
             unpack(in.get(0, b, k), x);
             unpack(in.get(1, b, k), h);
@@ -163,12 +167,15 @@ block_norm_bwd_rows(const BlockNorm<T> a, const Walk<4> walk_in, const Walk<2> w
               s_c = vfma(q, h[i], s_c);
             }
           }
-      s[3 * b] = vsum(s_h), s[3 * b + 1] = vsum(s_g), s[3 * b + 2] = vsum(s_c);
+      const bool mine = V > 1 || on;
+      s[3 * b] = mine ? vsum(s_h) : 0.f;
+      s[3 * b + 1] = mine ? vsum(s_g) : 0.f;
+      s[3 * b + 2] = mine ? vsum(s_c) : 0.f;
     }
     group_sums<3 * B>(s, slots[grp][parity], W, wig, grp);
 #pragma unroll
     for (int b = 0; b < B; ++b) {
-      if (t + b * step >= rows) break;
+      if (b > 0 && t + b * step >= rows) break;
       const float kr = r2[b] * (r2[b] * (r2[b] * s[3 * b] * a.inv_h));  // k r2
       const float c1 = beta * (r1[b] * fmaf(-kr, s[3 * b + 2], s[3 * b + 1]));
       if (a.dgate_tok != nullptr && gi == 0) a.dgate_tok[t + b * step] = c1;
@@ -178,7 +185,7 @@ block_norm_bwd_rows(const BlockNorm<T> a, const Walk<4> walk_in, const Walk<2> w
           vall<VT>(a.w_post != nullptr ? -r1[b] * (r1[b] * (gt[b] * c1 * a.inv_h)) : 0.f);
 #pragma unroll
       for (int k = 0; k < V; ++k)
-        if (on >> k & 1) {
+        if (V == 1 || on >> k & 1) {
           VT x[P], h[P], dy[P], dh[P], f[P], wf[P];
           unpack(in.get(0, b, k), x);
           unpack(in.get(1, b, k), h);
@@ -197,14 +204,16 @@ block_norm_bwd_rows(const BlockNorm<T> a, const Walk<4> walk_in, const Walk<2> w
             dh[i] = vmul(rs, Gv);
             x[i] = vfma(nam, x[i], vmul(gm, kHold ? wg[kHold ? k : 0][i] : f[i]));
           }
-          Rw o;
-          pack(dh, o);
-          store_raw((T *)(out.at[1] + b * walk_out.step[1] + (off + k * gap)), o);
-          pack(x, o);
-          store_raw((T *)(out.at[0] + b * walk_out.step[0] + (off + k * gap)), o);
+          Rw oh, ox;
+          pack(dh, oh);
+          pack(x, ox);
+          if (on >> k & 1) {
+            store_raw((T *)(out.at[1] + (off + k * gap)), oh);
+            store_raw((T *)(out.at[0] + (off + k * gap)), ox);
+          }
         }
+      out.advance(walk_out);
     }
-    out.advance(walk_out, B);
   }
   cp_async_wait<0>();
   if (R > 1) __syncthreads();  // the ring becomes the row groups' sums

@@ -71,18 +71,21 @@ block_norm_fwd_rows(const BlockNorm<T> a, const Walk<2> walk_in, const Walk<2> w
   VT wg[kHold ? V : 1][P], w[kHold ? V : 1][P];
   if constexpr (kHold)
 #pragma unroll
-    for (int k = 0; k < V; ++k)
+    for (int k = 0; k < V; ++k) {
+#pragma unroll
+      for (int i = 0; i < P; ++i) wg[k][i] = w[k][i] = vall<VT>(0.f);
       if (on >> k & 1) {
         column_factors<T, N>(a, c0 + k * G * N, wg[k]);
         unpack(load_raw<Rw>(a.w + c0 + k * G * N), w[k]);
       }
+    }
   Mask<N, V> mask;
   if (DROP) mask.init(g, a.drop.thr, gi, G);
   const uint32_t rows = (uint32_t)a.rows, step = gridDim.x * R;
   uint32_t t = blockIdx.x * R + grp;
   Rows<2> src{{(const char *)(a.x + t * a.ldx), (const char *)(a.res + t * a.ldr)}};
   Rows<2> dst{{(const char *)(a.h + t * a.ldh), (const char *)(a.y + t * a.ldy)}};
-  const uint32_t off = c0 * (int)sizeof(T), gap = G * N * (int)sizeof(T);
+  const uint32_t off = V > 1 || on ? c0 * (int)sizeof(T) : 0, gap = G * N * (int)sizeof(T);
   Turn turn{t, step, rows, off, gap, on};
   Ahead<T, N, V, 2, B, kFwdDepth> in;
   in.start(ring, src, walk_in, turn);
@@ -111,13 +114,13 @@ block_norm_fwd_rows(const BlockNorm<T> a, const Walk<2> walk_in, const Walk<2> w
         VT ss = vall<VT>(0.f);
 #pragma unroll
         for (int k = 0; k < V; ++k)
-          if (on >> k & 1) {
+          if (V == 1 || on >> k & 1) {
             VT x[P];
             unpack(in.get(0, b, k), x);
 #pragma unroll
             for (int i = 0; i < P; ++i) ss = vfma(x[i], x[i], ss);
           }
-        s[b] = vsum(ss);
+        s[b] = V > 1 || on ? vsum(ss) : 0.f;
       }
       group_sums<B>(s, slots[grp][parity][0], W, wig, grp);
 #pragma unroll
@@ -129,13 +132,14 @@ block_norm_fwd_rows(const BlockNorm<T> a, const Walk<2> walk_in, const Walk<2> w
       }
     }
     Rw h[B][V];
+    const char *hr = dst.at[0];
 #pragma unroll
-    for (int b = 0; b < B; ++b) {
+    for (int b = 0; b < B; ++b, hr += walk_out.step[0]) {
       VT ss = vall<VT>(0.f);
       const VT fv = vall<VT>(f[b]);
 #pragma unroll
       for (int k = 0; k < V; ++k)
-        if (on >> k & 1) {
+        if (V == 1 || on >> k & 1) {
           VT x[P], o[P], fk[P];
           unpack(in.get(0, b, k), x);
           unpack(in.get(1, b, k), o);
@@ -150,15 +154,15 @@ block_norm_fwd_rows(const BlockNorm<T> a, const Walk<2> walk_in, const Walk<2> w
           unpack(h[b][k], o);
 #pragma unroll
           for (int i = 0; i < P; ++i) ss = vfma(o[i], o[i], ss);
-          if (t + b * step < rows)
-            store_raw((T *)(dst.at[0] + b * walk_out.step[0] + (off + k * gap)), h[b][k]);
+          if ((on >> k & 1) && (b == 0 || t + b * step < rows))
+            store_raw((T *)(hr + (off + k * gap)), h[b][k]);
         }
-      s[b] = vsum(ss);
+      s[b] = V > 1 || on ? vsum(ss) : 0.f;
     }
     group_sums<B>(s, slots[grp][parity][1], W, wig, grp);
 #pragma unroll
     for (int b = 0; b < B; ++b) {
-      if (t + b * step >= rows) break;
+      if (b > 0 && t + b * step >= rows) break;
       const float r2 = rsqrtf(fmaf(s[b], a.inv_h, a.eps));
       if (a.rstd != nullptr && gi == 0) a.rstd[t + b * step] = r2;
       const VT r2v = vall<VT>(r2);
@@ -173,10 +177,11 @@ block_norm_fwd_rows(const BlockNorm<T> a, const Walk<2> walk_in, const Walk<2> w
             o[i] = vmul(vmul(o[i], r2v), kHold ? w[kHold ? k : 0][i] : fk[i]);
           Rw y;
           pack(o, y);
-          store_raw((T *)(dst.at[1] + b * walk_out.step[1] + (off + k * gap)), y);
+          store_raw((T *)(dst.at[1] + (off + k * gap)), y);
         }
+      dst.advance(walk_out);
     }
-    dst.advance(walk_out, B);
+    if (B > 1 && t + step >= rows) break;  // the last turn may be short
   }
   cp_async_wait<0>();
 }
