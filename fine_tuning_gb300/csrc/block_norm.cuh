@@ -263,9 +263,9 @@ template <int S> struct Rows {
 
 // A thread's packets (V of each of S source tensors, B rows at a time) of the rows ahead.
 // Packets of 16 bytes are copied into a ring in shared memory (cp.async: each thread
-// reads back what it copied itself, so that the ring needs no barrier), kDepth - 1 turns
-// ahead; single columns, which are too small for such copies, wait in registers, one
-// turn ahead.  Columns: offset `off` (bytes) of the row, packet k 32 W packets further.
+// reads back what it copied itself, so that the ring needs no barrier): kDepth rows, the
+// current ones among them; single columns, which are too small for such copies, wait in
+// registers, one turn ahead.  Columns: offset `off` (bytes) of the row, packet k 32 W packets further.
 // With one packet a thread, threads past the row's end take its first packet along (with
 // weights of zero, and without storing anything), which spares the branches.
 struct Turn {
@@ -282,45 +282,51 @@ __device__ __forceinline__ uint4 load_shared(uint32_t p) {
 }
 
 template <typename T, int N, int V, int S, int B, int kDepth> struct Ahead {
-  static constexpr int kItems = S * B * V;  // of a turn; 512 bytes each for a warp
-  uint32_t base, slot;  // shared addresses: this thread's place in the ring, in the turn
+  static_assert(kDepth >= B, "the current rows have to fit");
+  static constexpr uint32_t kRow = S * V * 512;  // bytes of a row's packets of one warp
+  uint32_t base, cur[B], to;  // shared addresses: the ring, the current rows, the next to fill
   static constexpr size_t bytes(int threads) {
-    return (size_t)threads * kDepth * kItems * sizeof(uint4);
+    return (size_t)threads * kDepth * S * V * sizeof(uint4);
   }
-  static constexpr uint32_t kTurn = kItems * 512;
-  __device__ __forceinline__ void fetch(uint32_t to, Rows<S> &src, const Walk<S> &w, Turn &n) {
+  __device__ __forceinline__ uint32_t after(uint32_t p) const {
+    return p == base + (kDepth - 1) * kRow ? base : p + kRow;
+  }
+  __device__ __forceinline__ void fetch(Rows<S> &src, const Walk<S> &w, Turn &n) {
+    if (n.t < n.rows)
 #pragma unroll
-    for (int b = 0; b < B; ++b) {
-      if (n.t < n.rows)
+      for (int s = 0; s < S; ++s)
 #pragma unroll
-        for (int s = 0; s < S; ++s)
-#pragma unroll
-          for (int k = 0; k < V; ++k)
-            if (V == 1 || n.on >> k & 1)
-              asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                               to + ((s * B + b) * V + k) * 512),
-                           "l"(src.at[s] + (n.off + k * n.gap))
-                           : "memory");
-      n.t += n.step;
-      src.advance(w);
-    }
-    cp_async_commit();  // a group for each turn, empty or not
+        for (int k = 0; k < V; ++k)
+          if (V == 1 || n.on >> k & 1)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + (s * V + k) * 512),
+                         "l"(src.at[s] + (n.off + k * n.gap))
+                         : "memory");
+    cp_async_commit();  // a group for each row, empty or not
+    n.t += n.step;
+    src.advance(w);
+    to = after(to);
   }
   __device__ __forceinline__ void start(uint4 *ring, Rows<S> &src, const Walk<S> &w, Turn &n) {
-    base = slot = smem_addr(ring) + (threadIdx.x >> 5) * (kDepth * kTurn) + (threadIdx.x & 31) * 16;
+    base = smem_addr(ring) + (threadIdx.x >> 5) * (kDepth * kRow) + (threadIdx.x & 31) * 16;
+    to = cur[0] = base;
 #pragma unroll
-    for (int i = 0; i < kDepth - 1; ++i) fetch(base + i * kTurn, src, w, n);
+    for (int b = 1; b < B; ++b) cur[b] = after(cur[b - 1]);
+#pragma unroll
+    for (int i = 0; i < kDepth - B; ++i) fetch(src, w, n);
   }
-  // the current turn's rows are there, the last of the ring's on their way
+  // the current turn's rows are there, kDepth - B rows behind them on their way
   __device__ __forceinline__ void arrive(Rows<S> &src, const Walk<S> &w, Turn &n) {
-    fetch(slot == base ? base + (kDepth - 1) * kTurn : slot - kTurn, src, w, n);
-    cp_async_wait<kDepth - 1>();
+#pragma unroll
+    for (int b = 0; b < B; ++b) fetch(src, w, n);
+    cp_async_wait<kDepth - B>();
   }
   __device__ __forceinline__ uint4 get(int s, int b, int k) const {
-    return load_shared(slot + ((s * B + b) * V + k) * 512);
+    return load_shared(cur[b] + (s * V + k) * 512);
   }
   __device__ __forceinline__ void next() {
-    slot = slot == base + (kDepth - 1) * kTurn ? base : slot + kTurn;
+    cur[0] = after(cur[B - 1]);
+#pragma unroll
+    for (int b = 1; b < B; ++b) cur[b] = after(cur[b - 1]);
   }
 };
 

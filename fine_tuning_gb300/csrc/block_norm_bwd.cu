@@ -71,8 +71,8 @@ __global__ void __launch_bounds__(kThreads) block_norm_bwd_any(const BlockNorm<T
 // way while the group works on the current ones.  Each thread keeps its columns' sums
 // for the whole kernel; at the end the CTA's row groups are added in their order.
 template <int N, int V> constexpr int kBwdRows = N > 1 && V == 1 ? 2 : 1;
-// turns in the ring, the current one among them: what 227 KB hold
-template <int V> constexpr int kBwdDepth = V <= 2 ? 2 : 1;
+// rows in the ring, the current ones among them: what 227 KB hold
+template <int V> constexpr int kBwdDepth = V == 1 ? 5 : V == 2 ? 2 : 1;
 
 template <typename T, int N, int V, bool DROP>
 __global__ void __launch_bounds__(32 * kMaxWarps)

@@ -47,7 +47,8 @@ __global__ void __launch_bounds__(kThreads) block_norm_fwd_any(const BlockNorm<T
 // share the weights in registers, the barriers and the shuffles), the rows ahead on
 // their way while the group works on the current ones.
 template <int N, int V> constexpr int kFwdRows = N > 1 && V == 1 ? 2 : 1;
-constexpr int kFwdDepth = 2;  // turns in the ring, the current one among them
+// rows in the ring, the current ones among them: two turns
+template <int N, int V> constexpr int kFwdDepth = 2 * kFwdRows<N, V>;
 
 // CTAS on an SM: two of up to 16 warps (64 registers a thread), or one of up to 20.
 template <typename T, int N, int V, bool DROP, int CTAS>
@@ -87,7 +88,7 @@ block_norm_fwd_rows(const BlockNorm<T> a, const Walk<2> walk_in, const Walk<2> w
   Rows<2> dst{{(const char *)(a.h + t * a.ldh), (const char *)(a.y + t * a.ldy)}};
   const uint32_t off = V > 1 || on ? c0 * (int)sizeof(T) : 0, gap = G * N * (int)sizeof(T);
   Turn turn{t, step, rows, off, gap, on};
-  Ahead<T, N, V, 2, B, kFwdDepth> in;
+  Ahead<T, N, V, 2, B, kFwdDepth<N, V>> in;
   in.start(ring, src, walk_in, turn);
   float tok[B];
   auto gates = [&](uint32_t n) {
@@ -194,7 +195,7 @@ cudaError_t fwd_rows(const BlockPlan &p, const BlockNormArgs &a, const DeviceInf
                                     : block_norm_fwd_rows<T, N, V, true, 1>)
                              : (two ? block_norm_fwd_rows<T, N, V, false, 2>
                                     : block_norm_fwd_rows<T, N, V, false, 1>);
-  const size_t smem = Ahead<T, N, V, 2, kFwdRows<N, V>, kFwdDepth>::bytes(p.threads());
+  const size_t smem = Ahead<T, N, V, 2, kFwdRows<N, V>, kFwdDepth<N, V>>::bytes(p.threads());
   const int occ = blocks_per_sm((const void *)kern, p.threads(), smem, dev, 8);
   int64_t grid = ceil_div(a.T, (int64_t)p.R);
   if (grid > (int64_t)dev.sms * occ) grid = (int64_t)dev.sms * occ;
