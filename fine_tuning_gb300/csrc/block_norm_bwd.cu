@@ -75,7 +75,7 @@ template <int N, int V> constexpr int kBwdRows = N > 1 && V == 1 ? 2 : 1;
 template <int V> constexpr int kBwdDepth = V == 1 ? 5 : V == 2 ? 2 : 1;
 
 template <typename T, int N, int V, bool DROP>
-__global__ void __launch_bounds__(32 * kMaxWarps)
+__global__ void __launch_bounds__(32 * kMaxWarps, 1)
 block_norm_bwd_rows(const BlockNorm<T> a, const Walk<4> walk_in, const Walk<2> walk_out, int W,
                     int R) {
   using VT = typename Values<N>::V;
