@@ -125,9 +125,12 @@ struct BlockPlan {
 
 constexpr int kMaxWarps = 20;  // of a row group
 
-inline BlockPlan plan_block_row(int64_t hp, int vmax) {
-  for (int v = 1; v <= vmax; v *= 2) {
-    const int64_t W = ceil_div(hp, (int64_t)32 * v);
+// Packets of 16 bytes: as few a thread as fit, so that the columns' sums and weights stay
+// in registers.  Single columns: four a thread where the row has them, since a warp makes
+// the random numbers of 256 columns at a time.
+inline BlockPlan plan_block_row(int64_t H, int N) {
+  for (int v = N == 1 && H > 32 ? 4 : 1; v <= (N == 1 ? 8 : 4); v *= 2) {
+    const int64_t W = ceil_div(H / N, (int64_t)32 * v);
     if (W > kMaxWarps) continue;
     // rows of one warp need no barrier; of the others at most four groups have one each,
     // in CTAs of up to 16 warps

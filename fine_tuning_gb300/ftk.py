@@ -757,8 +757,11 @@ def attn_bwd(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor
 # ---------------------------------------------------------------- dropout
 
 def _ld(t: torch.Tensor, name: str) -> int:
-    """_rows, for batches without a row too (whose strides may be anything)."""
-    return _rows(t, name) if t.dim() != 2 or t.shape[0] > 0 else max(1, t.shape[1])
+    """_rows in one look at the strides, and for batches without a row too."""
+    st = t.stride()
+    if len(st) == 2 and st[1] == 1 and t.shape[0] > 1:
+        return st[0]
+    return _rows(t, name) if len(st) != 2 or t.shape[0] > 0 else max(1, t.shape[1])
 
 
 def _rows_like(x: torch.Tensor, t: torch.Tensor, name: str) -> int:
