@@ -124,18 +124,31 @@ struct BlockPlan {
 };
 
 constexpr int kMaxWarps = 20;  // of a row group
+constexpr int kMaxGroups = 6;  // of more than one warp, in a CTA
+
+// Barrier 1 + g of row group g.  Each case names its barrier by a constant: one computed
+// at run time makes the compiler reserve all 16 for every CTA.
+__device__ __forceinline__ void row_barrier(int g, int threads) {
+  switch (g) {
+    case 0: asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory"); break;
+    case 1: asm volatile("bar.sync 2, %0;" ::"r"(threads) : "memory"); break;
+    case 2: asm volatile("bar.sync 3, %0;" ::"r"(threads) : "memory"); break;
+    case 3: asm volatile("bar.sync 4, %0;" ::"r"(threads) : "memory"); break;
+    case 4: asm volatile("bar.sync 5, %0;" ::"r"(threads) : "memory"); break;
+    default: asm volatile("bar.sync 6, %0;" ::"r"(threads) : "memory"); break;
+  }
+}
 
 // Packets of 16 bytes: as few a thread as fit, so that the columns' sums and weights stay
 // in registers.  Single columns: four a thread where the row has them, since a warp makes
-// the random numbers of 256 columns at a time.
-inline BlockPlan plan_block_row(int64_t H, int N) {
+// the random numbers of 256 columns at a time.  Short rows share a CTA of up to `warps`.
+inline BlockPlan plan_block_row(int64_t H, int N, int warps) {
   for (int v = N == 1 && H > 32 ? 4 : 1; v <= (N == 1 ? 8 : 4); v *= 2) {
     const int64_t W = ceil_div(H / N, (int64_t)32 * v);
     if (W > kMaxWarps) continue;
-    // rows of one warp need no barrier; of the others at most four groups have one each,
-    // in CTAs of up to 16 warps
-    const int R = W == 1 ? 8 : W > 8 ? 1 : 16 / (int)W < 4 ? 16 / (int)W : 4;
-    return BlockPlan{v, (int)W, R};
+    // rows of one warp need no barrier; of the others up to kMaxGroups groups have one each
+    const int R = W == 1 ? 8 : warps / (int)W < kMaxGroups ? warps / (int)W : kMaxGroups;
+    return BlockPlan{v, (int)W, R > 0 ? R : 1};
   }
   return BlockPlan{0, 0, 0};
 }
@@ -174,7 +187,7 @@ __device__ __forceinline__ void group_sums(float (&v)[n], float *slots, int W, i
   if (W > 1) {
     const int i = lane / L, sub = lane % L;
     if (sub == 0 && i < n) slots[i * kMaxWarps + wig] = d[0];
-    group_barrier(grp, 32 * W);
+    row_barrier(grp, 32 * W);
     d[0] = 0.f;
 #pragma unroll
     for (int k = 0; k < (kMaxWarps + L - 1) / L; ++k)

@@ -238,6 +238,7 @@ block_norm_bwd_rows(const BlockNorm<T> a, const Walk<4> walk_in, const Walk<2> w
 }
 
 constexpr int kReduceWarps = 32;
+constexpr int kReduceBatch = 5;  // rows of a warp in flight: 160, the sums of one CTA an SM
 
 // dw[j] = sum_p ws[p][j]; S[j] = sum_p ws[p][H + j], dw_post = gate S, dgate = w_post S.
 // A CTA owns 32 columns; its warps take the rows p = warp, warp + 32, ... and their
@@ -253,9 +254,19 @@ block_norm_dw(const float *ws, int P, int H, const T *w_post, const T *gate, flo
   const int j = blockIdx.x * 32 + lane;
   const bool shared = blockIdx.y != 0;  // the column sums that dw_post and dgate share
   float s = 0.f;
-  if (j < H)
-    for (int p = warp; p < P; p += kReduceWarps)
-      s += __ldcg(ws + ((int64_t)p * 2 + (shared ? 1 : 0)) * H + j);
+  if (j < H) {
+    const float *col = ws + (shared ? H : 0) + j;
+    for (int p0 = warp; p0 < P; p0 += kReduceWarps * kReduceBatch) {
+      float v[kReduceBatch];
+#pragma unroll
+      for (int i = 0; i < kReduceBatch; ++i) {
+        const int p = p0 + i * kReduceWarps;
+        v[i] = p < P ? __ldcg(col + (int64_t)p * 2 * H) : 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < kReduceBatch; ++i) s += v[i];
+    }
+  }
   part[warp][lane] = s;
   __syncthreads();
   if (warp != 0 || j >= H) return;
@@ -301,7 +312,7 @@ cudaError_t bwd_rows(const BlockPlan &p, const BlockNormArgs &a, const DeviceInf
 
 template <typename T, int N>
 cudaError_t bwd_packets(const BlockNormArgs &a, const DeviceInfo &dev, cudaStream_t s) {
-  const BlockPlan p = plan_block_row(a.H, N);
+  const BlockPlan p = plan_block_row(a.H, N, kMaxWarps);
   switch (p.V) {
     case 1: return bwd_rows<T, N, 1>(p, a, dev, s);
     case 2: return bwd_rows<T, N, 2>(p, a, dev, s);

@@ -207,7 +207,7 @@ cudaError_t fwd_rows(const BlockPlan &p, const BlockNormArgs &a, const DeviceInf
 
 template <typename T, int N>
 cudaError_t fwd_packets(const BlockNormArgs &a, const DeviceInfo &dev, cudaStream_t s) {
-  const BlockPlan p = plan_block_row(a.H, N);
+  const BlockPlan p = plan_block_row(a.H, N, 16);
   switch (p.V) {
     case 1: return fwd_rows<T, N, 1>(p, a, dev, s);
     case 2: return fwd_rows<T, N, 2>(p, a, dev, s);
