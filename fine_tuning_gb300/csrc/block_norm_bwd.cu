@@ -55,7 +55,9 @@ __global__ void __launch_bounds__(kThreads) block_norm_bwd_any(const BlockNorm<T
     const float am = a.w_post != nullptr ? r1 * (gt * c * a.inv_h) : 0.f;
     const float bg = beta * gt;
     for_columns(g, a.drop.thr, t, a.H, [&](int j, bool kept) {
-      const float dyf = to_float(gy[j]), hn = to_float(hr[j]) * r2, xn = to_float(xr[j]) * r1;
+      const float dyf = to_float(gy[j]), hn = to_float(hr[j]) * r2;
+      // without w_post what is dropped may hold anything
+      const float xn = kept || a.w_post != nullptr ? to_float(xr[j]) * r1 : 0.f;
       const float G = fmaf(-k, hn, fmaf(r2, to_float(a.w[j]) * dyf, to_float(gh[j])));
       const float gm = kept ? bg * G : 0.f;
       sum_w[j] = fmaf(dyf, hn, sum_w[j]);
@@ -193,6 +195,9 @@ block_norm_bwd_rows(const BlockNorm<T> a, const Walk<4> walk_in, const Walk<2> w
           unpack(in.get(3, b, k), dh);
           unpack(kHold ? w[kHold ? k : 0] : load_raw<Rw>(a.w + c0 + k * G * N), wf);
           if constexpr (!kHold) column_factors<T, N>(a, c0 + k * G * N, f);
+          if (DROP && a.w_post == nullptr)  // then what is dropped may hold anything
+#pragma unroll
+            for (int i = 0; i < P; ++i) x[i] = mask.keep(m[b], k, i, x[i]);
 #pragma unroll
           for (int i = 0; i < P; ++i) {
             const VT dyr = vmul(dy[i], r2v);

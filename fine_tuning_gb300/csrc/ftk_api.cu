@@ -1001,10 +1001,10 @@ FTK_API ftk_status ftk_attn_bwd(const void *do_, int64_t ld_do, const void *q, i
 
 namespace {
 
-// Rows and columns are counted in 32 bits inside the kernels, columns with room for
-// the last step of a CTA.
+// Rows and columns are counted in 32 bits inside the kernels; 2^23 single columns make
+// 2^15 parts of 256, which fit a grid's second axis.
 constexpr int64_t kMaxRows = int64_t(1) << 31;
-constexpr int64_t kMaxCols = int64_t(1) << 24;
+constexpr int64_t kMaxCols = int64_t(1) << 23;
 
 bool residual_sizes(int64_t T, int64_t H) {
   return T >= 0 && T < kMaxRows && H >= 1 && H < kMaxCols;

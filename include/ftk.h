@@ -541,7 +541,7 @@ FTK_API ftk_status ftk_attn_bwd(const void *do_, int64_t ld_do, const void *q, i
  * The backward needs the same value.
  * x [T, ldx], y [T, ldy]; y may be x exactly (same pointer and stride), otherwise
  * they must not overlap; step overlaps neither.  0 <= p <= 1, T < 2^31,
- * H < 2^24, else FTK_ERR_SHAPE. */
+ * H < 2^23, else FTK_ERR_SHAPE. */
 FTK_API ftk_status ftk_dropout_fwd(const void *x, int64_t ldx, void *y, int64_t ldy, int64_t T,
                                    int64_t H, double p, uint64_t seed, uint64_t offset,
                                    const int64_t *step, ftk_dtype dtype, ftk_stream_t stream);
@@ -560,7 +560,7 @@ FTK_API ftk_status ftk_dropout_bwd(const void *dy, int64_t lddy, void *dx, int64
  *   x[t,j] = scale * W[ids[t], j]   (0 when ids[t] lies outside [0, V))
  * so that -100, or any negative value, marks padding, as in ftk_cce_fwd.
  * W [V, ldw], x [T, ldx] (dtype); ids: DEVICE int32 [T].  x overlaps neither.
- * 1 <= V < 2^31, T < 2^31, 1 <= H < 2^24, scale finite, else FTK_ERR_SHAPE. */
+ * 1 <= V < 2^31, T < 2^31, 1 <= H < 2^23, scale finite, else FTK_ERR_SHAPE. */
 FTK_API ftk_status ftk_embed_fwd(const void *w, int64_t ldw, int64_t V, const int32_t *ids,
                                  void *x, int64_t ldx, int64_t T, int64_t H, float scale,
                                  ftk_dtype dtype, ftk_stream_t stream);
@@ -569,13 +569,14 @@ FTK_API ftk_status ftk_embed_fwd(const void *w, int64_t ldw, int64_t V, const in
 FTK_API size_t ftk_embed_bwd_workspace_bytes(int64_t T, int64_t H, int64_t V);
 
 /* The table's gradient, from dx [T, lddx] (dtype):
- *   g[v,j] = scale * sum over t with ids[t] = v, in the order of t, of dx[t,j]
+ *   g[v,j] = scale * sum over t with ids[t] = v of dx[t,j]
  * dW fp32 [V, lddw]: accumulate == 0 overwrites every row (zeros in the rows that
  * no token names, T = 0 included); accumulate != 0 adds g to the rows that a token
  * names and leaves the others as they are, so that several batches, or a tied LM
  * head (ftk_cce_bwd's dW), share one gradient.  Sums are fp32 in a fixed order
- * (no atomics): bitwise reproducible.  Columns past H of a row are left as they
- * were.  workspace: >= ftk_embed_bwd_workspace_bytes(T, H, V) bytes, 16-byte
+ * (by t, in stretches of 16 tokens or more of the list sorted by id whose sums
+ * are then added in turn): bitwise reproducible, on any device.  Columns past H
+ * of a row are left as they were.  workspace: >= ftk_embed_bwd_workspace_bytes(T, H, V) bytes, 16-byte
  * aligned, contents ignored and clobbered; calls that overlap on the GPU need one
  * each.  dW, workspace and the inputs must not overlap.  Limits as above. */
 FTK_API ftk_status ftk_embed_bwd(const void *dx, int64_t lddx, const int32_t *ids, float *dw,
@@ -599,10 +600,12 @@ FTK_API ftk_status ftk_embed_bwd(const void *dx, int64_t lddx, const int32_t *id
  * w_post [H] (dtype; without it r1 = w_post = 1), gate [H] (dtype), gate_tok [T]
  * (fp32).  dropout: ftk_dropout_fwd's, of the [T, H] values b with the same p,
  * seed, offset and step (the same mask; p = 0: none), not rounded in between.
- * rstd_post, rstd [T] fp32, nullable: r1 (untouched without w_post) and r.
+ * rstd_post, rstd [T] fp32, nullable: r1 (untouched without w_post) and r.  An
+ * infinity or NaN in x reaches its own row alone; without w_post, and dropped, it
+ * reaches nothing, here and in the backward.
  * h may be x or res exactly (same pointer and stride), y overlaps nothing, rstd
  * outputs nothing either.  eps >= 0, res_scale and x_scale finite; T < 2^31,
- * 1 <= H < 2^24, else FTK_ERR_SHAPE. */
+ * 1 <= H < 2^23, else FTK_ERR_SHAPE. */
 FTK_API ftk_status ftk_rmsnorm_block_fwd(const void *x, int64_t ldx, const void *res,
                                          int64_t ldr, const void *w_post, const void *gate,
                                          const float *gate_tok, const void *w, void *h,

@@ -11,7 +11,8 @@ pytestmark = pytest.mark.gpu
 DT = {"f32": torch.float32, "bf16": torch.bfloat16}
 EPS = 1e-5
 SIZES = [(1, 1), (1, 8), (3, 7), (64, 64), (5, 257), (33, 896), (9, 1001), (70, 2048), (4, 4096),
-         (7, 5120), (2, 8200), (3, 16384), (2, 20000), (2, 5003), (1000, 24), (2500, 128)]
+         (7, 5120), (2, 8200), (3, 16384), (2, 20000), (2, 5003), (3, 5131), (2, 20487), (1000, 24),
+         (2500, 128), (650, 640), (613, 321), (331, 5120)]
 
 
 def ftk():
@@ -145,6 +146,26 @@ def test_mask_is_the_dropouts(H):
     step = torch.tensor([2], device="cuda")
     h = ftk().rmsnorm_block_fwd(x, res, x[0], EPS, p=0.3, seed=77, offset=9, step=step)[0]
     assert torch.equal(h, ftk().dropout_fwd(x, 0.3, 77, 9, step))
+
+
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("H", [64, 61, 5131])
+def test_dropped_infinities_reach_nothing(dtype, H):
+    T, p = 9, 0.5
+    c, f = case(T, H, dtype, post=False)
+    kw = dict(**f, p=p, seed=1)
+    keep = R.keep_mask(T, H, p, 1).cuda()
+    bad = c["x"].clone()
+    bad[~keep] = float("inf")
+    bad[:, ::2][~keep[:, ::2]] = float("nan")
+    out = ftk().rmsnorm_block_fwd(c["x"], c["res"], c["w"], EPS, **kw)
+    got = ftk().rmsnorm_block_fwd(bad, c["res"], c["w"], EPS, **kw)
+    for a, b in zip(out[:3], got[:3]):
+        assert torch.equal(a, b)
+    h, _, r, _ = out
+    for a, b in zip(ftk().rmsnorm_block_bwd(c["dy"], c["dh"], c["x"], h, c["w"], r, **kw),
+                    ftk().rmsnorm_block_bwd(c["dy"], c["dh"], bad, h, c["w"], r, **kw)):
+        assert (a is None and b is None) or torch.equal(a, b)
 
 
 @pytest.mark.parametrize("H", [64, 61])
