@@ -147,7 +147,7 @@ inline BlockPlan plan_block_row(int64_t H, int N, int warps) {
     const int64_t W = ceil_div(H / N, (int64_t)32 * v);
     if (W > kMaxWarps) continue;
     // rows of one warp need no barrier; of the others up to kMaxGroups groups have one each
-    const int R = W == 1 ? 8 : warps / (int)W < kMaxGroups ? warps / (int)W : kMaxGroups;
+    const int R = W == 1 || warps / (int)W < kMaxGroups ? warps / (int)W : kMaxGroups;
     return BlockPlan{v, (int)W, R > 0 ? R : 1};
   }
   return BlockPlan{0, 0, 0};

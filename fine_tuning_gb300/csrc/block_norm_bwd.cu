@@ -20,12 +20,12 @@ namespace ftk {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kMaxBlocksPerSm = 8;
+constexpr int kThreads = 512;
+constexpr int kMaxBlocksPerSm = 2;  // each has its row of the workspace
 
 // Rows of any length and alignment: a CTA walks one row at a time, twice.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) block_norm_bwd_any(const BlockNorm<T> a) {
+__global__ void __launch_bounds__(kThreads, kMaxBlocksPerSm) block_norm_bwd_any(const BlockNorm<T> a) {
   __shared__ float red[kThreads / 32];
   pdl_wait();
   pdl_trigger();
@@ -74,22 +74,25 @@ __global__ void __launch_bounds__(kThreads) block_norm_bwd_any(const BlockNorm<T
 // for the whole kernel; at the end the CTA's row groups are added in their order.
 template <int N, int V> constexpr int kBwdRows = N > 1 && V == 1 ? 2 : 1;
 // rows in the ring, the current ones among them: what 227 KB hold
-template <int V> constexpr int kBwdDepth = V == 1 ? 5 : V == 2 ? 2 : 1;
+template <int V, int WARPS> constexpr int kBwdDepth = V == 1 ? 5 : V == 2 ? (WARPS > 16 ? 2 : 3) : 1;
 
-template <typename T, int N, int V, bool DROP>
-__global__ void __launch_bounds__(32 * kMaxWarps, 1)
+// One CTA an SM, of up to WARPS warps: 16 (128 registers a thread) or 20 (96).
+template <typename T, int N, int V, bool DROP, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS, 1)
 block_norm_bwd_rows(const BlockNorm<T> a, const Walk<4> walk_in, const Walk<2> walk_out, int W,
                     int R) {
   using VT = typename Values<N>::V;
   using Rw = typename Raw<T, N>::type;
   constexpr int P = Values<N>::kCount, B = kBwdRows<N, V>;
-  constexpr bool kHold = V * N <= 8;  // the weights in registers; else read for each row
-  extern __shared__ uint4 ring[];     // the rows ahead, then [R][2 H] sums when R > 1
-  __shared__ float slots[8][2][3 * B * kMaxWarps];  // group, parity
+  // the weights in registers; else read for each row
+  constexpr bool kHold = V * N <= (WARPS > 16 ? 8 : 16);
+  extern __shared__ uint4 ring[];  // the rows ahead, then [R][2 H] sums when R > 1
+  __shared__ float slots[kMaxGroups][2][3 * B * kMaxWarps];  // group, parity
   pdl_wait();
   pdl_trigger();
   const Philox g = philox_of(a.drop);
   const auto [grp, wig, gi, G] = place_of(W);
+  auto &sums = slots[W > 1 ? grp : 0];  // rows of one warp need none
   const int c0 = gi * N;
   uint32_t on = 0;
 #pragma unroll
@@ -120,7 +123,7 @@ block_norm_bwd_rows(const BlockNorm<T> a, const Walk<4> walk_in, const Walk<2> w
   Rows<2> out{{(const char *)(a.dx + t * a.lddx), (const char *)(a.dres + t * a.lddr)}};
   const uint32_t off = V > 1 || on ? c0 * (int)sizeof(T) : 0, gap = G * N * (int)sizeof(T);
   Turn turn{t, step, rows, off, gap, on};
-  Ahead<T, N, V, 4, B, kBwdDepth<V>> in;
+  Ahead<T, N, V, 4, B, kBwdDepth<V, WARPS>> in;
   in.start(ring, src, walk_in, turn);
   float r1_next[B], r2_next[B], tok_next[B];
   auto scalars = [&](uint32_t n) {
@@ -174,7 +177,7 @@ block_norm_bwd_rows(const BlockNorm<T> a, const Walk<4> walk_in, const Walk<2> w
       s[3 * b + 1] = mine ? vsum(s_g) : 0.f;
       s[3 * b + 2] = mine ? vsum(s_c) : 0.f;
     }
-    group_sums<3 * B>(s, slots[grp][parity], W, wig, grp);
+    group_sums<3 * B>(s, sums[parity], W, wig, grp);
 #pragma unroll
     for (int b = 0; b < B; ++b) {
       if (b > 0 && t + b * step >= rows) break;
@@ -296,12 +299,12 @@ cudaError_t reduce(const BlockNormArgs &a, int64_t P, cudaStream_t s) {
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-template <typename T, int N, int V>
+template <typename T, int N, int V, int WARPS>
 cudaError_t bwd_rows(const BlockPlan &p, const BlockNormArgs &a, const DeviceInfo &dev,
                      cudaStream_t s) {
-  auto kern = a.drop.thr > 0 ? block_norm_bwd_rows<T, N, V, true>
-                             : block_norm_bwd_rows<T, N, V, false>;
-  size_t smem = Ahead<T, N, V, 4, kBwdRows<N, V>, kBwdDepth<V>>::bytes(p.threads());
+  auto kern = a.drop.thr > 0 ? block_norm_bwd_rows<T, N, V, true, WARPS>
+                             : block_norm_bwd_rows<T, N, V, false, WARPS>;
+  size_t smem = Ahead<T, N, V, 4, kBwdRows<N, V>, kBwdDepth<V, WARPS>>::bytes(p.threads());
   const size_t sums = p.R > 1 ? (size_t)p.R * 2 * (size_t)a.H * sizeof(float) : 0;
   if (sums > smem) smem = sums;
   const int occ = blocks_per_sm((const void *)kern, p.threads(), smem, dev, kMaxBlocksPerSm);
@@ -317,16 +320,23 @@ cudaError_t bwd_rows(const BlockPlan &p, const BlockNormArgs &a, const DeviceInf
 
 template <typename T, int N>
 cudaError_t bwd_packets(const BlockNormArgs &a, const DeviceInfo &dev, cudaStream_t s) {
-  const BlockPlan p = plan_block_row(a.H, N, kMaxWarps);
+  const BlockPlan p = plan_block_row(a.H, N, 16);
+#define FTK_BWD_V(VV)                                                     \
+  case VV:                                                                \
+    return p.threads() <= 512 ? bwd_rows<T, N, VV, 16>(p, a, dev, s)      \
+                              : bwd_rows<T, N, VV, kMaxWarps>(p, a, dev, s);
   switch (p.V) {
-    case 1: return bwd_rows<T, N, 1>(p, a, dev, s);
-    case 2: return bwd_rows<T, N, 2>(p, a, dev, s);
-    case 4: return bwd_rows<T, N, 4>(p, a, dev, s);
+    FTK_BWD_V(1)
+    FTK_BWD_V(2)
+    FTK_BWD_V(4)
     case 8:
-      if constexpr (N == 1) return bwd_rows<T, N, 8>(p, a, dev, s);
+      if constexpr (N == 1)
+        return p.threads() <= 512 ? bwd_rows<T, N, 8, 16>(p, a, dev, s)
+                                  : bwd_rows<T, N, 8, kMaxWarps>(p, a, dev, s);
     default: break;
   }
-  const int64_t P = a.T < (int64_t)dev.sms * 4 ? a.T : (int64_t)dev.sms * 4;
+#undef FTK_BWD_V
+  const int64_t P = block_norm_partial_rows(a.T, dev);
   cudaError_t e = launch_pdl(block_norm_bwd_any<T>, dim3((unsigned)P), dim3(kThreads), 0, s,
                              block_norm_params<T>(a));
   return e != cudaSuccess ? e : reduce<T>(a, P, s);

@@ -60,11 +60,12 @@ block_norm_fwd_rows(const BlockNorm<T> a, const Walk<2> walk_in, const Walk<2> w
   constexpr int P = Values<N>::kCount, B = kFwdRows<N, V>;
   constexpr bool kHold = V * N <= 8;  // the weights in registers; else read for each row
   extern __shared__ uint4 ring[];
-  __shared__ float slots[8][2][2][B * kMaxWarps];  // group, parity, which sum
+  __shared__ float slots[kMaxGroups][2][2][B * kMaxWarps];  // group, parity, which sum
   pdl_wait();
   pdl_trigger();
   const Philox g = philox_of(a.drop);
   const auto [grp, wig, gi, G] = place_of(W);
+  auto &sums = slots[W > 1 ? grp : 0];  // rows of one warp need none
   const int c0 = gi * N;
   uint32_t on = 0;
 #pragma unroll
@@ -123,7 +124,7 @@ block_norm_fwd_rows(const BlockNorm<T> a, const Walk<2> walk_in, const Walk<2> w
           }
         s[b] = V > 1 || on ? vsum(ss) : 0.f;
       }
-      group_sums<B>(s, slots[grp][parity][0], W, wig, grp);
+      group_sums<B>(s, sums[parity][0], W, wig, grp);
 #pragma unroll
       for (int b = 0; b < B; ++b) {
         const float r1 = rsqrtf(fmaf(s[b], a.inv_h, a.eps));
@@ -160,7 +161,7 @@ block_norm_fwd_rows(const BlockNorm<T> a, const Walk<2> walk_in, const Walk<2> w
         }
       s[b] = V > 1 || on ? vsum(ss) : 0.f;
     }
-    group_sums<B>(s, slots[grp][parity][1], W, wig, grp);
+    group_sums<B>(s, sums[parity][1], W, wig, grp);
 #pragma unroll
     for (int b = 0; b < B; ++b) {
       if (b > 0 && t + b * step >= rows) break;
