@@ -904,10 +904,9 @@ def rmsnorm_block_fwd(x: torch.Tensor, res: torch.Tensor, w: torch.Tensor, eps: 
     y, ldy = _new_rows(x, y, "y")
     rstd = rstd_post = None
     if save_rstd:
-        if w_post is None:
-            rstd = torch.empty(T, dtype=torch.float32, device=x.device)
-        else:  # an allocation costs a small call more than two views of one
-            rstd, rstd_post = torch.empty((2, T), dtype=torch.float32, device=x.device).unbind()
+        rstd = torch.empty(T, dtype=torch.float32, device=x.device)
+        if w_post is not None:
+            rstd_post = torch.empty(T, dtype=torch.float32, device=x.device)
     _call_on(dev, "ftk_rmsnorm_block_fwd", x.data_ptr(), ldx, res.data_ptr(), ldr,
              _vector(w_post, H, x.dtype, "w_post"), _vector(gate, H, x.dtype, "gate"),
              _vector(gate_tok, T, torch.float32, "gate_tok"), _vector(w, H, x.dtype, "w"),
@@ -944,12 +943,10 @@ def rmsnorm_block_bwd(dy: torch.Tensor, dh: torch.Tensor, x: torch.Tensor, h: to
     dx, lddx = _new_rows(x, dx, "dx")
     dres, lddr = _new_rows(x, dres, "dres")
 
-    # the columns' sums in one allocation, which costs a small call more than views of it
-    cols = torch.empty((1 + (w_post is not None) + (gate is not None), H), dtype=torch.float32,
-                       device=x.device).unbind()
-    dw, dw_post = cols[0], None if w_post is None else cols[1]
-    dgate = None if gate is None else cols[-1]
-    dgate_tok = None if gate_tok is None else torch.empty(T, dtype=torch.float32, device=x.device)
+    def sums(factor, n):
+        return None if factor is None else torch.empty(n, dtype=torch.float32, device=x.device)
+
+    dw, dw_post, dgate, dgate_tok = sums(w, H), sums(w_post, H), sums(gate, H), sums(gate_tok, T)
     if workspace is None:
         if dev == torch._C._cuda_getDevice():
             n = rmsnorm_block_bwd_workspace_bytes(T, H, x.dtype)
