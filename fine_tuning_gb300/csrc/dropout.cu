@@ -110,9 +110,7 @@ cudaError_t launch_typed(bool vec, const DropoutArgs &a, const DeviceInfo &dev, 
     const int blocks = (int)(a.H / 8);
     const int parts = ceil_div(blocks, kThreads), cols = ceil_div(blocks, parts);
     const int side = kThreads / cols;
-    int64_t grid = ceil_div(a.T, (int64_t)side);
-    const int64_t most = ceil_div((int64_t)dev.sms * 8, (int64_t)parts);
-    if (grid > most) grid = most;
+    const int64_t grid = row_grid(a.T, side, parts, dev);
     auto kern = a.drop.thr > 0 ? dropout_blocks<T, true> : dropout_blocks<T, false>;
     return launch_pdl(kern, dim3((unsigned)grid, (unsigned)parts),
                       dim3((unsigned)(side * cols)), 0, s, (const T *)a.x, a.ldx, (T *)a.y, a.ldy,

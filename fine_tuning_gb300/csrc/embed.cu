@@ -6,13 +6,15 @@
 // so that it is bitwise reproducible:
 //   1. embed_sort: the tokens are sorted by id, a stable radix sort of (id, t) by one
 //      cluster of eight CTAs in one launch; digit counts meet through the cluster's
-//      shared memory.  The other CTAs of the launch meanwhile write the zeros of the rows
-//      that no token names (not when the gradient is added to what is there), most of
-//      the work where the vocabulary is larger than the batch;
+//      shared memory.  The other CTAs of the launch meanwhile write zeros to rows that no
+//      token names (not when the gradient is added to what is there), as many as the
+//      sort leaves time for;
 //   2. embed_grad: the sorted list is cut into chunks of equal length, however the ids
 //      are spread: a warp walks one chunk's rows of dx for 256 columns and keeps the
 //      running sum of one id in registers.  Sums of ids that lie inside the chunk go to
-//      dW, those that cross its borders to the workspace;
+//      dW, those that cross its borders to the workspace.  Warps between them write the
+//      other rows' zeros, which is most of the work where the vocabulary is larger than
+//      the batch;
 //   3. embed_join: the crossing sums are added in the chunks' order.
 #include "common.cuh"
 #include "launch_residual.h"
@@ -75,9 +77,7 @@ template <typename T, int N>
 cudaError_t fwd_typed(const EmbedFwdArgs &a, const DeviceInfo &dev, cudaStream_t s) {
   const int hp = (int)(a.H / N), parts = ceil_div(hp, kThreads), cols = ceil_div(hp, parts);
   const int side = kThreads / cols;
-  int64_t grid = ceil_div(a.T, (int64_t)side);
-  const int64_t most = ceil_div((int64_t)dev.sms * 8, (int64_t)parts);
-  if (grid > most) grid = most;
+  const int64_t grid = row_grid(a.T, side, parts, dev);
   cudaError_t e = launch_pdl(embed_fwd_rows<T, N>, dim3((unsigned)grid, (unsigned)parts),
                              dim3((unsigned)(side * cols)), 0, s, (const T *)a.w, a.ldw,
                              (uint32_t)a.V, a.ids, (T *)a.x, a.ldx, a.T, hp, cols, a.scale);
@@ -91,6 +91,7 @@ constexpr int kDigits = 1 << kDigitBits;
 constexpr int kSortThreads = 512;  // a thread for each digit
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortCtas = 8;       // of the cluster
+constexpr int64_t kZeroBytes = 128 << 20;  // written beside the sort at least
 constexpr int kFlagWords = 8192;   // of a zeroing CTA: 32 rows each
 constexpr int kColumns = 256;      // of a warp of embed_grad
 
@@ -134,8 +135,9 @@ struct SortParams {
   uint32_t n;
   int passes, digit_bits;
   uint32_t *key[2], *tok[2];
-  // the rows to zero (zero_ctas > 0)
+  // the rows to zero (zero_ctas > 0): those below zero_rows
   int zero_ctas;  // a power of two
+  uint32_t zero_rows;
   float *dw;
   int64_t lddw, H;
 };
@@ -248,6 +250,16 @@ __device__ void sort_tokens(const SortParams &a, uint32_t *shared) {
   }
 }
 
+// A row of zeros, by a warp.
+template <int N> __device__ __forceinline__ void zero_row(float *row, int64_t H, int lane) {
+  if constexpr (N % 4 == 0) {
+    for (int64_t c = lane * 4; c < H; c += 128)
+      *reinterpret_cast<float4 *>(row + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+  } else {
+    for (int64_t c = lane; c < H; c += 32) row[c] = 0.f;
+  }
+}
+
 // Zeros in the rows that no token names.  CTA z has the rows whose number / 32 is z modulo
 // zero_ctas (present and absent rows gather at different ends of a vocabulary); it marks
 // its rows that the batch names, then its warps fill the others.
@@ -255,7 +267,7 @@ template <int N>
 __device__ void zero_rows(const SortParams &a, uint32_t *flags) {
   const uint32_t z = blockIdx.x - kSortCtas, Z = a.zero_ctas;
   const int log = 31 - __clz(Z);
-  const uint32_t words = (uint32_t)(((uint64_t)a.V + 31) / 32);
+  const uint32_t words = (uint32_t)(((uint64_t)a.zero_rows + 31) / 32);
   const uint32_t mine = z < words ? (words - z - 1) / Z + 1 : 0;
   for (uint32_t i = threadIdx.x; i < mine; i += kSortThreads) flags[i] = 0;
   __syncthreads();
@@ -266,21 +278,15 @@ __device__ void zero_rows(const SortParams &a, uint32_t *flags) {
       id[b] = a.n - i > b * kSortThreads ? a.ids[i + b * kSortThreads] : a.V;
 #pragma unroll
     for (int b = 0; b < 8; ++b)
-      if (id[b] < a.V && (id[b] >> 5 & (Z - 1)) == z)
+      if (id[b] < a.zero_rows && (id[b] >> 5 & (Z - 1)) == z)
         atomicOr(&flags[id[b] >> 5 >> log], 1u << (id[b] & 31));
   }
   __syncthreads();
   const int lane = threadIdx.x & 31;
   for (uint32_t r = threadIdx.x >> 5; r < mine * 32; r += kSortWarps) {
     const uint64_t v = ((uint64_t)(r >> 5) * Z + z) * 32 + (r & 31);
-    if (v >= a.V || (flags[r >> 5] >> (r & 31) & 1)) continue;
-    float *row = a.dw + v * a.lddw;
-    if constexpr (N % 4 == 0) {
-      for (int64_t c = lane * 4; c < a.H; c += 128)
-        *reinterpret_cast<float4 *>(row + c) = make_float4(0.f, 0.f, 0.f, 0.f);
-    } else {
-      for (int64_t c = lane; c < a.H; c += 32) row[c] = 0.f;
-    }
+    if (v < a.zero_rows && !(flags[r >> 5] >> (r & 31) & 1))
+      zero_row<N>(a.dw + v * a.lddw, a.H, lane);
   }
 }
 
@@ -313,6 +319,9 @@ template <typename T> struct GradParams {
   float *dw;
   int64_t lddw;
   float *part;  // [chunks][2][H]: the sum that the chunk's first id brings, the last's
+  // the rows to zero, from zero_from on: zero_units of kZeroRows, by CTAs spread among the
+  // others (of `ctas` in all, `sums` work on units of chunks)
+  uint32_t zero_from, zero_units, ctas, sums;
 };
 
 // N fp32 values of a row of dW or of a partial sum.
@@ -379,6 +388,25 @@ __device__ __forceinline__ void finish_row(float *row, const Slab<T, N> &s,
 }
 
 constexpr int kGradWarps = 4, kGradCtas = 8;
+constexpr int kZeroRows = 4;  // of a zeroing warp
+
+// Zeros in those of a unit's rows that no token names: each of the first lanes looks one
+// id up in the sorted list.
+template <typename T, int N>
+__device__ void zero_unseen(const GradParams<T> &a, uint32_t unit) {
+  if (unit >= a.zero_units) return;
+  const int lane = threadIdx.x & 31;
+  const uint32_t v0 = a.zero_from + unit * kZeroRows, v = v0 + lane;
+  const bool mine = lane < kZeroRows && v < a.V;
+  uint32_t lo = 0, hi = mine ? a.n : 0;  // the first place whose key is v or beyond
+  while (lo < hi) {
+    const uint32_t m = lo + (hi - lo) / 2;
+    if (a.key[m] < v) lo = m + 1; else hi = m;
+  }
+  uint32_t todo = __ballot_sync(0xffffffffu, mine && !(lo < a.n && a.key[lo] == v));
+  for (; todo != 0; todo &= todo - 1)
+    zero_row<N>(a.dw + (int64_t)(v0 + __ffs(todo) - 1) * a.lddw, a.H, lane);
+}
 constexpr int kGradBatch = 4;  // rows in flight for a warp
 
 template <typename T, int N, bool ACC>
@@ -389,7 +417,17 @@ __global__ void __launch_bounds__(32 * kGradWarps, kGradCtas) embed_grad(const G
   constexpr unsigned kAll = 0xffffffffu;
   pdl_wait();
   pdl_trigger();
-  const uint32_t unit = blockIdx.x * kGradWarps + (threadIdx.x >> 5);
+  uint32_t cta = blockIdx.x;
+  if constexpr (!ACC) {
+    // CTAs 0 .. ctas - 1 hold the `sums` ones at even distances
+    const uint32_t before = (uint32_t)((uint64_t)cta * a.sums / a.ctas);
+    if ((uint32_t)((uint64_t)(cta + 1) * a.sums / a.ctas) == before) {
+      zero_unseen<T, N>(a, (cta - before) * kGradWarps + (threadIdx.x >> 5));
+      return;
+    }
+    cta = before;
+  }
+  const uint32_t unit = cta * kGradWarps + (threadIdx.x >> 5);
   if (unit >= a.units) return;
   const uint32_t ch = unit / a.slabs;
   const Slab<T, N> s(unit - ch * a.slabs, a.H);
@@ -524,8 +562,18 @@ cudaError_t bwd_typed(const EmbedBwdArgs &a, const DeviceInfo &dev, cudaStream_t
     q.tok[i] = (uint32_t *)(ws + p.off_tok[i]);
   }
   if (!ACC) {
+    // Beside the sort about what it leaves time for (some 10 us, and 0.2 us for each
+    // 1,024 tokens, at 6 TB/s); the rest beside the sums, which wait for latencies more
+    // than for memory.  All of it beside the sort where that is not much more: the sums
+    // then have the memory to themselves.  Measured, all beside the sort and split:
+    // 16,384 x 896 (0.5 GB) 106.4 and 107.5 us, 32,768 x 2,048 fp32 over 32,000 ids (0.3
+    // GB) 102 and 107, 333 x 4,096 (2.5 GB) 410 and 352, 2 x 32,768 x 5,120 (3.1 GB) 811
+    // and 738.
+    const int64_t some = kZeroBytes + a.T * 1024, row = 4 * a.H;
+    const int64_t rows = a.V <= 4 * some / row ? a.V : some / row / 32 * 32;
+    q.zero_rows = (uint32_t)(a.T == 0 ? a.V : rows);
     q.zero_ctas = 256;  // with the sort's, what two CTAs on each of 152 SMs hold
-    const int64_t words = ceil_div(a.V, (int64_t)32);
+    const int64_t words = ceil_div((int64_t)q.zero_rows, (int64_t)32);
     while ((int64_t)q.zero_ctas * kFlagWords < words) q.zero_ctas *= 2;
     q.dw = a.dw;
     q.lddw = a.lddw;
@@ -537,13 +585,18 @@ cudaError_t bwd_typed(const EmbedBwdArgs &a, const DeviceInfo &dev, cudaStream_t
   if (e != cudaSuccess || a.T == 0) return e != cudaSuccess ? e : cudaGetLastError();
   const int64_t slabs = ceil_div(a.H, (int64_t)kColumns);
   const int last = (p.passes - 1) & 1;
-  const GradParams<T> g{(const T *)a.dx, a.lddx, q.key[last], q.tok[last], q.V, q.n,
-                        (int)p.chunk, (int)slabs, (uint32_t)(p.chunks * slabs), a.H, a.scale,
-                        a.dw, a.lddw, (float *)(ws + p.off_part)};
-  const dim3 grid((unsigned)ceil_div(p.chunks * slabs, (int64_t)kGradWarps));
-  e = launch_pdl(embed_grad<T, N, ACC>, grid, dim3(32 * kGradWarps), 0, s, g);
+  GradParams<T> g{(const T *)a.dx, a.lddx, q.key[last], q.tok[last], q.V, q.n,
+                  (int)p.chunk, (int)slabs, (uint32_t)(p.chunks * slabs), a.H, a.scale,
+                  a.dw, a.lddw, (float *)(ws + p.off_part)};
+  g.sums = g.ctas = (uint32_t)ceil_div(p.chunks * slabs, (int64_t)kGradWarps);
+  if (!ACC) {
+    g.zero_from = q.zero_rows;
+    g.zero_units = (uint32_t)ceil_div(a.V - (int64_t)q.zero_rows, (int64_t)kZeroRows);
+    g.ctas += (uint32_t)ceil_div((int64_t)g.zero_units, (int64_t)kGradWarps);
+  }
+  e = launch_pdl(embed_grad<T, N, ACC>, dim3(g.ctas), dim3(32 * kGradWarps), 0, s, g);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(embed_join<T, N, ACC>, grid, dim3(32 * kGradWarps), 0, s, g);
+  e = launch_pdl(embed_join<T, N, ACC>, dim3(g.sums), dim3(32 * kGradWarps), 0, s, g);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
