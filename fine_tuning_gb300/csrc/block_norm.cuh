@@ -140,8 +140,10 @@ __device__ __forceinline__ void row_barrier(int g, int threads) {
 }
 
 // Packets of 16 bytes: as few a thread as fit, so that the columns' sums and weights stay
-// in registers.  Single columns: four a thread where the row has them, since a warp makes
-// the random numbers of 256 columns at a time.  Short rows share a CTA of up to `warps`.
+// in registers (backward 65,536 x 5,120: one a thread 879 us, two 1,160).  Single columns:
+// four a thread where the row has them, since a warp makes the random numbers of 256
+// columns at a time (backward 32,767 x 1,001: four 180 us, two 252, eight, which spill,
+// 257).  Short rows share a CTA of up to `warps`.
 inline BlockPlan plan_block_row(int64_t H, int N, int warps) {
   for (int v = N == 1 && H > 32 ? 4 : 1; v <= (N == 1 ? 8 : 4); v *= 2) {
     const int64_t W = ceil_div(H / N, (int64_t)32 * v);
@@ -277,13 +279,10 @@ template <int S> struct Rows {
   }
 };
 
-// A thread's packets (V of each of S source tensors, B rows at a time) of the rows ahead.
-// Packets of 16 bytes are copied into a ring in shared memory (cp.async: each thread
-// reads back what it copied itself, so that the ring needs no barrier): kDepth rows, the
-// current ones among them; single columns, which are too small for such copies, wait in
-// registers, one turn ahead.  Columns: offset `off` (bytes) of the row, packet k 32 W packets further.
-// With one packet a thread, threads past the row's end take its first packet along (with
-// weights of zero, and without storing anything), which spares the branches.
+// The row to fetch next, and where in a row the thread's packets lie: `off` bytes from
+// its start, each `gap` bytes behind the one before.  With one packet a thread, threads
+// past the row's end take its first packet along (with weights of zero, and without
+// storing anything), which spares the branches.
 struct Turn {
   uint32_t t, step, rows;  // the next row to fetch, the group's step, the batch's rows
   uint32_t off, gap, on;   // bytes; bit k: the thread has a packet k
@@ -297,6 +296,11 @@ __device__ __forceinline__ uint4 load_shared(uint32_t p) {
   return u;
 }
 
+// A thread's packets (V of each of S source tensors, B rows at a time) of the rows ahead.
+// Packets of 16 bytes are copied into a ring in shared memory (cp.async: each thread
+// reads back what it copied itself, so that the ring needs no barrier): kDepth rows, the
+// current ones among them.  Single columns, which are too small for such copies, wait in
+// registers, one turn ahead.
 template <typename T, int N, int V, int S, int B, int kDepth> struct Ahead {
   static_assert(kDepth >= B, "the current rows have to fit");
   static constexpr uint32_t kRow = S * V * 512;  // bytes of a row's packets of one warp

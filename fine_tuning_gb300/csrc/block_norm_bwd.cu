@@ -9,11 +9,21 @@
 //   dgate_tok[t] = c / gate_tok, formed without the division
 // Both row sums come from one pass over the row: with q = m wg xn,
 //   sum q G = sum q (dh + r2 w dy) - k sum q hn.
-// The normalised xn and hn enter the sums, not x and h: no r^3 is formed, which
-// overflows for rows near zero.
+// No r^3 is formed, which overflows for rows near zero: each r multiplies a sum of x's or
+// h's that it brings back to the size of one.
 //
 // A CTA's column sums go to its own row of the workspace; a second kernel adds the
 // rows in a fixed order and applies gate and w_post.
+//
+// Memory bound by its bytes (four tensors read, two written, 6 es a column), and in fact
+// close to the SM's issue rate: about 450 instructions a packet of eight columns with
+// dropout.  What helped was what gives a warp independent work: two rows at a time
+// (65,536 x 5,120: 1,108 us with one, 861 with two, 797 with three), and registers: one
+// CTA an SM of 16 warps with 128 registers a thread takes 264 us for 32,768 x 4,096 (0.91
+// of the copy rate), with 96 346, two CTAs with 64 334.  Rows of 20 warps have 96:
+// 65,536 x 5,120 705 us, 5,710 GB/s, 0.85.  Measured and left: the columns' sums in shared
+// memory 739; the first pass of the next row before the second of this one 1,188 against
+// 760.
 #include "block_norm.cuh"
 
 namespace ftk {
@@ -23,9 +33,11 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kMaxBlocksPerSm = 2;  // each has its row of the workspace
 
-// Rows of any length and alignment: a CTA walks one row at a time, twice.
+// Rows of any length and alignment: a CTA walks one row at a time, twice (4,095 x 5,131
+// bf16: 264 us, 960 GB/s).
 template <typename T>
-__global__ void __launch_bounds__(kThreads, kMaxBlocksPerSm) block_norm_bwd_any(const BlockNorm<T> a) {
+__global__ void __launch_bounds__(kThreads, kMaxBlocksPerSm)
+block_norm_bwd_any(const BlockNorm<T> a) {
   __shared__ float red[kThreads / 32];
   pdl_wait();
   pdl_trigger();
@@ -74,9 +86,12 @@ __global__ void __launch_bounds__(kThreads, kMaxBlocksPerSm) block_norm_bwd_any(
 // for the whole kernel; at the end the CTA's row groups are added in their order.
 template <int N, int V> constexpr int kBwdRows = N > 1 && V == 1 ? 2 : 1;
 // rows in the ring, the current ones among them: what 227 KB hold
-template <int V, int WARPS> constexpr int kBwdDepth = V == 1 ? 5 : V == 2 ? (WARPS > 16 ? 2 : 3) : 1;
+template <int V, int WARPS> constexpr int kBwdDepth =
+    V == 1 ? 5 : V == 2 ? (WARPS > 16 ? 2 : 3) : 1;
 
-// One CTA an SM, of up to WARPS warps: 16 (128 registers a thread) or 20 (96).
+// One CTA an SM, of up to WARPS warps: 16 (128 registers a thread) or 20 (96), by the
+// plan's threads.  Measured, 16 and 20 for rows that 16 hold: 32,768 x 4,096 264 and 346
+// us, 65,536 x 2,048 251 and 290, 16,384 x 8,192 325 and 401, 4,095 x 1,001 26.0 and 29.4.
 template <typename T, int N, int V, bool DROP, int WARPS>
 __global__ void __launch_bounds__(32 * WARPS, 1)
 block_norm_bwd_rows(const BlockNorm<T> a, const Walk<4> walk_in, const Walk<2> walk_out, int W,

@@ -16,6 +16,12 @@
 //      other rows' zeros, which is most of the work where the vocabulary is larger than
 //      the batch;
 //   3. embed_join: the crossing sums are added in the chunks' order.
+//
+// Bound by memory.  Lookup of 65,536 x 4,096 bf16 over 151,936 ids: 122 us, 0.87 of the
+// copy rate with every named row read once.  Gradient: 16,384 x 896 over 151,936 ids 106
+// us, 5,400 GB/s, 0.81; two parts of 32,768 x 5,120, the second accumulated, 734 us, 0.87.
+// The first form (a launch for each step of the sort, one for the zeros, a CTA a chunk)
+// took 181 and 1,814.  An accumulating call waits for the sort: 20 us for 32,768 tokens.
 #include "common.cuh"
 #include "launch_residual.h"
 #include "raw_packet.cuh"
@@ -109,7 +115,9 @@ EmbedPlan plan_embed(int64_t T, int64_t H, int64_t V) {
   while ((V >> bits) != 0) ++bits;  // V itself marks the tokens without a row
   p.passes = (bits + kDigitBits - 1) / kDigitBits;
   p.digit_bits = (bits + p.passes - 1) / p.passes;
-  // some 8,192 warps in all: 54 an SM
+  // Some 8,192 warps in all, 54 an SM.  Measured, 131,072 x 4,096: 727 us, with 4,096
+  // warps 822; in the present form 646, with 12,288 657.  16 tokens at least, since each
+  // border may cost two rows of fp32 sums.
   p.chunk = ceil_div(ceil_div(T * ceil_div(H, (int64_t)kColumns), (int64_t)8192), (int64_t)8) * 8;
   if (p.chunk < 16) p.chunk = 16;
   if (p.chunk > 1024) p.chunk = 1024;
@@ -387,7 +395,7 @@ __device__ __forceinline__ void finish_row(float *row, const Slab<T, N> &s,
     }
 }
 
-constexpr int kGradWarps = 4, kGradCtas = 8;
+constexpr int kGradWarps = 4, kGradCtas = 8;  // of a CTA; of an SM (10, fewer registers: 8% slower)
 constexpr int kZeroRows = 4;  // of a zeroing warp
 
 // Zeros in those of a unit's rows that no token names: each of the first lanes looks one
@@ -613,7 +621,8 @@ size_t embed_bwd_workspace_bytes(int64_t T, int64_t H, int64_t V) {
 
 cudaError_t launch_embed_fwd(DType dt, bool vec, const EmbedFwdArgs &a, const DeviceInfo &dev,
                              cudaStream_t s) {
-  if (dt == DType::F32) return vec ? fwd_typed<float, 4>(a, dev, s) : fwd_typed<float, 1>(a, dev, s);
+  if (dt == DType::F32)
+    return vec ? fwd_typed<float, 4>(a, dev, s) : fwd_typed<float, 1>(a, dev, s);
   return vec ? fwd_typed<bf16, 8>(a, dev, s) : fwd_typed<bf16, 1>(a, dev, s);
 }
 

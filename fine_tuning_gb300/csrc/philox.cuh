@@ -5,10 +5,10 @@
 //
 // key = the caller's seed; counter = (j / 8, t, offset + step): one call gives the
 // eight 16-bit numbers of columns 8 (j / 8) .. + 7 of row t, column j taking number
-// j % 8 (the low half of a word first).  Sixteen bits an element halve the integer
-// work of the usual 32 (a bf16 stream would otherwise be bound by it); the
-// probability then counts in steps of 2^-16, and the scale is the reciprocal of the
-// probability as counted, so that the mean is kept.
+// j % 8 (the low half of a word first).  Sixteen bits an element are a choice: they halve
+// the integer work of 32 (by which a bf16 stream would be bound), and the probability
+// then counts in steps of 2^-16.  The scale is the reciprocal of the probability as
+// counted, so that the mean is kept.
 #pragma once
 
 #include "common.cuh"
