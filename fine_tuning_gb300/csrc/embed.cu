@@ -395,7 +395,8 @@ __device__ __forceinline__ void finish_row(float *row, const Slab<T, N> &s,
     }
 }
 
-constexpr int kGradWarps = 4, kGradCtas = 8;  // of a CTA; of an SM (10, fewer registers: 8% slower)
+constexpr int kGradWarps = 4;  // of a CTA
+constexpr int kGradCtas = 8;   // of an SM (10, with fewer registers: 8% slower)
 constexpr int kZeroRows = 4;  // of a zeroing warp
 
 // Zeros in those of a unit's rows that no token names: each of the first lanes looks one
@@ -415,6 +416,7 @@ __device__ void zero_unseen(const GradParams<T> &a, uint32_t unit) {
   for (; todo != 0; todo &= todo - 1)
     zero_row<N>(a.dw + (int64_t)(v0 + __ffs(todo) - 1) * a.lddw, a.H, lane);
 }
+
 constexpr int kGradBatch = 4;  // rows in flight for a warp
 
 template <typename T, int N, bool ACC>

@@ -12,7 +12,8 @@ DT = {"f32": torch.float32, "bf16": torch.bfloat16}
 EPS = 1e-5
 SIZES = [(1, 1), (1, 8), (3, 7), (64, 64), (5, 257), (33, 896), (9, 1001), (70, 2048), (4, 4096),
          (7, 5120), (2, 8200), (3, 16384), (2, 20000), (2, 5003), (3, 5131), (2, 20487), (1000, 24),
-         (2500, 128), (650, 640), (613, 321), (331, 5120)]
+         (2500, 128), (650, 640), (613, 321), (331, 5120), (400, 5131), (500, 6000), (350, 12000), (320, 18000),
+         (400, 9600), (1300, 4993)]
 
 
 def ftk():
@@ -136,6 +137,53 @@ def test_views_and_in_place(dtype, H):
                                       dx=dh if swap else dy, dres=dy if swap else dh)
         for g, b in zip(got, ref):
             assert torch.equal(g, b)
+
+
+@pytest.mark.parametrize("dtype", DT)
+def test_halves_of_one_buffer_and_weights_anywhere(dtype):
+    T, H = 200, 128
+    c, f = case(T, H, dtype)
+    pool = torch.zeros(4 * H + 8, device="cuda", dtype=DT[dtype])
+    for shift in (0, 1):
+        both = torch.cat([c["x"], c["res"]], 1)
+        w, wp, g = (pool[shift + i * (H + 1) * (1 if shift else 0) + i * H * (0 if shift else 1):][:H]
+                    for i in range(3))
+        w.copy_(c["w"]), wp.copy_(f["w_post"]), g.copy_(f["gate"])
+        kw = dict(w_post=wp, gate=g, gate_tok=f["gate_tok"], p=0.25, seed=1)
+        out = torch.empty(T, 2 * H, device="cuda", dtype=DT[dtype])
+        got = ftk().rmsnorm_block_fwd(both[:, :H], both[:, H:], w, EPS, **kw, h=out[:, :H],
+                                      y=out[:, H:])
+        check_fwd(c, f, 1.0, 1.0, 0.25, got)
+        grads = torch.cat([c["dy"], c["dh"]], 1)
+        res = ftk().rmsnorm_block_bwd(grads[:, :H], grads[:, H:], both[:, :H], out[:, :H], w, got[2],
+                                      got[3], **kw, dx=grads[:, H:], dres=grads[:, :H])
+        check_bwd(c, f, 1.0, 1.0, 0.25, got[0], got[2], got[3], res)
+
+
+def test_refusals():
+    from fine_tuning_gb300.ftk import FtkError
+    c, f = case(40, 64, "bf16")
+    fwd = lambda **kw: ftk().rmsnorm_block_fwd(c["x"], c["res"], c["w"], EPS, **{**f, **kw})
+    h, y, r, r1 = fwd()
+    assert fwd(save_rstd=False)[2:] == (None, None)
+    for kw in (dict(y=c["x"]), dict(y=c["res"]), dict(h=h, y=h), dict(p=1.5), dict(x_scale=float("nan"))):
+        with pytest.raises(FtkError):
+            fwd(**kw)
+    for kw in (dict(w_post=c["w"][:32]), dict(gate=c["w"].float()), dict(gate_tok=f["gate_tok"].half()),
+               dict(h=h[:3]), dict(seed=-1), dict(step=torch.zeros(1, device="cuda"))):
+        with pytest.raises(ValueError):
+            fwd(**kw)
+    bwd = lambda **kw: ftk().rmsnorm_block_bwd(c["dy"], c["dh"], c["x"], h, c["w"], r,
+                                               **{"rstd_post": r1, **f, **kw})
+    for kw in (dict(dx=c["x"]), dict(dx=h), dict(dx=c["dy"], dres=c["dy"]),
+               dict(workspace=torch.empty(1024, dtype=torch.uint8, device="cuda"))):
+        with pytest.raises(FtkError):
+            bwd(**kw)
+    for kw in (dict(rstd_post=None), dict(rstd_post=r1[:3]), dict(dres=y[:, :8])):
+        with pytest.raises(ValueError):
+            bwd(**kw)
+    with pytest.raises(TypeError):
+        ftk().dropout_fwd(c["x"].half(), 0.1, 1)
 
 
 @pytest.mark.parametrize("H", [64, 61])

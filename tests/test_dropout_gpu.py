@@ -29,7 +29,8 @@ def check(y, ref):
 
 @pytest.mark.parametrize("dtype", DT)
 @pytest.mark.parametrize("T, H", [(1, 1), (1, 8), (3, 7), (5, 16), (33, 64), (2, 257), (17, 1001),
-                                  (64, 896), (3, 4104), (1, 70000), (4099, 24)])
+                                  (64, 896), (3, 4104), (1, 70000), (4099, 24), (5, 12), (9, 20),
+                                  (20000, 40), (3001, 2048)])
 @pytest.mark.parametrize("p", [0.0, 0.1, 0.5, 1.0])
 def test_forward_and_backward(dtype, T, H, p):
     x = values(T, H, DT[dtype])
@@ -66,6 +67,12 @@ def test_dropped_infinities_are_zero():
     keep = R.keep_mask(32, 64, 0.5, 3)
     assert (y[~keep] == 0).all() and not torch.isfinite(y[keep]).any()
     assert (ftk().dropout_fwd(x, 1.0, 3) == 0).all()
+
+
+@pytest.mark.parametrize("p", [2.0 ** -18, 2.0 ** -17, 1 - 2.0 ** -16, 1 - 2.0 ** -18])
+def test_probabilities_at_the_ends(p):
+    x = values(600, 1024, torch.bfloat16)
+    check(ftk().dropout_fwd(x, p, SEED), R.dropout(x, p, SEED))
 
 
 @pytest.mark.parametrize("offset, step", [(0, 0), (2 ** 32 - 1, 1), (2 ** 64 - 1, 1), (5, -3),

@@ -108,6 +108,24 @@ def test_gradient_of_a_vocabulary_of_31_bits():
     assert dW[7, 0] == 2 * dx[2, 0] and int(torch.count_nonzero(dW)) == 4
 
 
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("T, H, V, kind", [(300, 1024, 151936, "skewed"), (4097, 1000, 151913, "mixed"),
+                                           (333, 1001, 150001, "mixed"), (5, 1024, 151936, "none"),
+                                           (70000, 1024, 200003, "distinct")])
+def test_gradient_of_a_large_table(dtype, T, H, V, kind):
+    # more zeros than are written beside the sort
+    dx, ids = rand(T, H, dtype=DT[dtype]), token_ids(kind, T, V)
+    dW = torch.full((V, H), float("nan"), device="cuda")
+    ftk().embed_bwd(dx, ids, V, dW=dW)
+    ok = ids[(ids >= 0) & (ids < V)].long()
+    seen, place = torch.unique(ok, return_inverse=True)
+    small = torch.full_like(ids, -1)
+    small[(ids >= 0) & (ids < V)] = place.to(torch.int32)
+    close(dW[seen], *R.embed_bwd(dx, small, max(1, seen.numel())) if seen.numel() else (dW[seen].cpu(), 0))
+    dW[seen] = 0
+    assert not dW.any()
+
+
 @pytest.mark.parametrize("accumulate", [False, True])
 def test_gradient_into_views(accumulate):
     ids = token_ids("mixed", 100, 30)
@@ -118,6 +136,25 @@ def test_gradient_into_views(accumulate):
         ftk().embed_bwd(dx, ids, 30, dW=buf[:, a:a + H], accumulate=accumulate)
         close(buf[:, a:a + H], *R.embed_bwd(dx, ids, 30, base=was[:, a:a + H] if accumulate else None))
         assert torch.equal(buf[:, :a], was[:, :a]) and torch.equal(buf[:, a + H:], was[:, a + H:])
+
+
+def test_refusals():
+    from fine_tuning_gb300.ftk import FtkError
+    dx, ids, W = rand(10, 16), token_ids("mixed", 10, 20), rand(20, 16)
+    for call in (lambda: ftk().embed_fwd(W, ids, x=W[:10]), lambda: ftk().embed_fwd(W, ids, float("inf")),
+                 lambda: ftk().embed_bwd(dx, ids, 20, float("nan")), lambda: ftk().embed_bwd(dx, ids, 0),
+                 lambda: ftk().embed_bwd(W[:10], ids, 20, dW=W),
+                 lambda: ftk().embed_bwd(dx, ids, 20, workspace=torch.empty(64, dtype=torch.uint8,
+                                                                            device="cuda"))):
+        with pytest.raises(FtkError):
+            call()
+    for call in (lambda: ftk().embed_bwd(dx, ids, 20, accumulate=True),
+                 lambda: ftk().embed_bwd(dx[:9], ids, 20), lambda: ftk().embed_bwd(dx, ids.long(), 20),
+                 lambda: ftk().embed_bwd(dx, ids, 20, dW=rand(20, 16, dtype=torch.bfloat16)),
+                 lambda: ftk().embed_bwd(dx, ids, 20, dW=rand(16, 20).T),
+                 lambda: ftk().embed_fwd(W, ids, x=rand(10, 8)), lambda: ftk().embed_fwd(W, ids.cpu())):
+        with pytest.raises(ValueError):
+            call()
 
 
 def test_empty_batch():
