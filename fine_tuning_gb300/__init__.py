@@ -13,7 +13,9 @@ __version__ = "0.1.0"
 
 _BINDING = ("rmsnorm_fwd", "rmsnorm_bwd", "rmsnorm_bwd_workspace_bytes", "swiglu_fwd",
             "swiglu_bwd", "qk_rope_fwd", "qk_rope_bwd", "qk_mrope_fwd", "qk_mrope_bwd", "attn_fwd",
-            "attn_bwd", "attn_bwd_workspace_bytes", "FtkError", "library")
+            "attn_bwd", "attn_bwd_workspace_bytes", "embed_fwd", "embed_bwd",
+            "embed_bwd_workspace_bytes", "dropout_fwd", "dropout_bwd", "rmsnorm_block_fwd",
+            "rmsnorm_block_bwd", "rmsnorm_block_bwd_workspace_bytes", "FtkError", "library")
 
 
 def __getattr__(name):
