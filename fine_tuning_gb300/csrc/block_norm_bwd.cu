@@ -333,34 +333,51 @@ cudaError_t bwd_rows(const BlockPlan &p, const BlockNormArgs &a, const DeviceInf
   return e != cudaSuccess ? e : reduce<T>(a, P, s);
 }
 
-template <typename T, int N>
-cudaError_t bwd_packets(const BlockNormArgs &a, const DeviceInfo &dev, cudaStream_t s) {
-  const BlockPlan p = plan_block_row(a.H, N, 16);
-#define FTK_BWD_V(VV)                                                     \
-  case VV:                                                                \
-    return p.threads() <= 512 ? bwd_rows<T, N, VV, 16>(p, a, dev, s)      \
-                              : bwd_rows<T, N, VV, kMaxWarps>(p, a, dev, s);
-  switch (p.V) {
-    FTK_BWD_V(1)
-    FTK_BWD_V(2)
-    FTK_BWD_V(4)
-    case 8:
-      if constexpr (N == 1)
-        return p.threads() <= 512 ? bwd_rows<T, N, 8, 16>(p, a, dev, s)
-                                  : bwd_rows<T, N, 8, kMaxWarps>(p, a, dev, s);
-    default: break;
-  }
-#undef FTK_BWD_V
+template <typename T>
+cudaError_t bwd_any(const BlockNormArgs &a, const DeviceInfo &dev, cudaStream_t s) {
   const int64_t P = block_norm_partial_rows(a.T, dev);
   cudaError_t e = launch_pdl(block_norm_bwd_any<T>, dim3((unsigned)P), dim3(kThreads), 0, s,
                              block_norm_params<T>(a));
   return e != cudaSuccess ? e : reduce<T>(a, P, s);
 }
 
+// The instance with 16 or 20 warps, by the plan's threads.
+template <typename T, int N, int V>
+cudaError_t bwd_warps(const BlockPlan &p, const BlockNormArgs &a, const DeviceInfo &dev,
+                      cudaStream_t s) {
+  return p.threads() <= 512 ? bwd_rows<T, N, V, 16>(p, a, dev, s)
+                            : bwd_rows<T, N, V, kMaxWarps>(p, a, dev, s);
+}
+
+// Rows of whole packets.
+template <typename T>
+cudaError_t bwd_packets(const BlockNormArgs &a, const DeviceInfo &dev, cudaStream_t s) {
+  constexpr int N = VecWidth<T>::value;
+  const BlockPlan p = plan_block_row(a.H, N, 16);
+  switch (p.V) {
+    case 1: return bwd_warps<T, N, 1>(p, a, dev, s);
+    case 2: return bwd_warps<T, N, 2>(p, a, dev, s);
+    case 4: return bwd_warps<T, N, 4>(p, a, dev, s);
+    default: return bwd_any<T>(a, dev, s);
+  }
+}
+
+// Rows of single columns.
+template <typename T>
+cudaError_t bwd_columns(const BlockNormArgs &a, const DeviceInfo &dev, cudaStream_t s) {
+  const BlockPlan p = plan_block_row(a.H, 1, 16);
+  switch (p.V) {
+    case 1: return bwd_rows<T, 1, 1, 16>(p, a, dev, s);
+    case 4: return bwd_warps<T, 1, 4>(p, a, dev, s);
+    case 8: return bwd_warps<T, 1, 8>(p, a, dev, s);
+    default: return bwd_any<T>(a, dev, s);
+  }
+}
+
 template <typename T>
 cudaError_t bwd_typed(bool vec, const BlockNormArgs &a, const DeviceInfo &dev, cudaStream_t s) {
   if (a.T == 0) return reduce<T>(a, 0, s);
-  return vec ? bwd_packets<T, VecWidth<T>::value>(a, dev, s) : bwd_packets<T, 1>(a, dev, s);
+  return vec ? bwd_packets<T>(a, dev, s) : bwd_columns<T>(a, dev, s);
 }
 
 }  // namespace

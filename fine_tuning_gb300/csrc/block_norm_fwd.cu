@@ -55,22 +55,21 @@ __global__ void __launch_bounds__(kThreads) block_norm_fwd_any(const BlockNorm<T
 // Rows of up to kMaxWarps warps: a persistent grid, W warps a row, B rows at a time (which
 // share the weights in registers, the barriers and the shuffles), the rows ahead on
 // their way while the group works on the current ones.
-template <int N, int V> constexpr int kFwdRows = N > 1 && V == 1 ? 2 : 1;
+template <int N, int V, int WARPS> constexpr int kFwdRows =
+    N > 1 && (V == 1 || (V == 2 && WARPS <= 16)) ? 2 : 1;
 // rows in the ring, the current ones among them: two turns
-template <int N, int V> constexpr int kFwdDepth = 2 * kFwdRows<N, V>;
+template <int N, int V, int WARPS> constexpr int kFwdDepth = 2 * kFwdRows<N, V, WARPS>;
 
-// CTAS on an SM: two of up to 16 warps (64 registers a thread), or one of up to 20 (96).
-// Measured, rows of 16 warps with two CTAs and with one: 65,536 x 4,096 352 and 405 us;
-// rows of 20 warps (H = 5,120) do not fit twice: 243 us for 32,768 x 5,120, where two
-// packets a thread and ten warps took 266.
-template <typename T, int N, int V, bool DROP, int CTAS>
-__global__ void __launch_bounds__(CTAS == 2 ? 512 : 32 * kMaxWarps, CTAS)
+// Up to WARPS warps a CTA, CTAS of them an SM; see fwd_packets for the choice.
+template <typename T, int N, int V, bool DROP, int WARPS, int CTAS>
+__global__ void __launch_bounds__(32 * WARPS, CTAS)
 block_norm_fwd_rows(const BlockNorm<T> a, const Walk<2> walk_in, const Walk<2> walk_out, int W,
                     int R) {
   using VT = typename Values<N>::V;
   using Rw = typename Raw<T, N>::type;
-  constexpr int P = Values<N>::kCount, B = kFwdRows<N, V>;
-  constexpr bool kHold = V * N <= 8;  // the weights in registers; else read for each row
+  constexpr int P = Values<N>::kCount, B = kFwdRows<N, V, WARPS>;
+  // the weights in registers; else read for each row
+  constexpr bool kHold = V * N <= 8 || (V == 2 && WARPS <= 16);
   extern __shared__ uint4 ring[];
   __shared__ float slots[kMaxGroups][2][2][B * kMaxWarps];  // group, parity, which sum
   pdl_wait();
@@ -101,7 +100,7 @@ block_norm_fwd_rows(const BlockNorm<T> a, const Walk<2> walk_in, const Walk<2> w
   Rows<2> dst{{(const char *)(a.h + t * a.ldh), (const char *)(a.y + t * a.ldy)}};
   const uint32_t off = V > 1 || on ? c0 * (int)sizeof(T) : 0, gap = G * N * (int)sizeof(T);
   Turn turn{t, step, rows, off, gap, on};
-  Ahead<T, N, V, 2, B, kFwdDepth<N, V>> in;
+  Ahead<T, N, V, 2, B, kFwdDepth<N, V, WARPS>> in;
   in.start(ring, src, walk_in, turn);
   float tok[B];
   auto gates = [&](uint32_t n) {
@@ -200,15 +199,13 @@ block_norm_fwd_rows(const BlockNorm<T> a, const Walk<2> walk_in, const Walk<2> w
   cp_async_wait<0>();
 }
 
-template <typename T, int N, int V>
+template <typename T, int N, int V, int WARPS, int CTAS, int CTAS_DROP = CTAS>
 cudaError_t fwd_rows(const BlockPlan &p, const BlockNormArgs &a, const DeviceInfo &dev,
                      cudaStream_t s) {
-  const bool two = p.threads() <= 512 && (N == 1 || V <= 2);  // four packets' ring fits once
-  auto kern = a.drop.thr > 0 ? (two ? block_norm_fwd_rows<T, N, V, true, 2>
-                                    : block_norm_fwd_rows<T, N, V, true, 1>)
-                             : (two ? block_norm_fwd_rows<T, N, V, false, 2>
-                                    : block_norm_fwd_rows<T, N, V, false, 1>);
-  const size_t smem = Ahead<T, N, V, 2, kFwdRows<N, V>, kFwdDepth<N, V>>::bytes(p.threads());
+  auto kern = a.drop.thr > 0 ? block_norm_fwd_rows<T, N, V, true, WARPS, CTAS_DROP>
+                             : block_norm_fwd_rows<T, N, V, false, WARPS, CTAS>;
+  const size_t smem =
+      Ahead<T, N, V, 2, kFwdRows<N, V, WARPS>, kFwdDepth<N, V, WARPS>>::bytes(p.threads());
   const int occ = blocks_per_sm((const void *)kern, p.threads(), smem, dev, 8);
   int64_t grid = ceil_div(a.T, (int64_t)p.R);
   if (grid > (int64_t)dev.sms * occ) grid = (int64_t)dev.sms * occ;
@@ -218,26 +215,54 @@ cudaError_t fwd_rows(const BlockPlan &p, const BlockNormArgs &a, const DeviceInf
                     Walk<2>{{step * a.ldh, step * a.ldy}}, p.W, p.R);
 }
 
-template <typename T, int N>
-cudaError_t fwd_packets(const BlockNormArgs &a, const DeviceInfo &dev, cudaStream_t s) {
-  const BlockPlan p = plan_block_row(a.H, N, 16);
-  switch (p.V) {
-    case 1: return fwd_rows<T, N, 1>(p, a, dev, s);
-    case 2: return fwd_rows<T, N, 2>(p, a, dev, s);
-    case 4: return fwd_rows<T, N, 4>(p, a, dev, s);
-    case 8:
-      if constexpr (N == 1) return fwd_rows<T, N, 8>(p, a, dev, s);
-    default: break;
-  }
-  int64_t grid = a.T < (int64_t)dev.sms * 8 ? a.T : (int64_t)dev.sms * 8;
+template <typename T>
+cudaError_t fwd_any(const BlockNormArgs &a, const DeviceInfo &dev, cudaStream_t s) {
+  const int64_t grid = a.T < (int64_t)dev.sms * 8 ? a.T : (int64_t)dev.sms * 8;
   return launch_pdl(block_norm_fwd_any<T>, dim3((unsigned)grid), dim3(kThreads), 0, s,
                     block_norm_params<T>(a));
 }
 
+// Rows of whole packets, by the warps that they take with one packet a thread; with
+// dropout, measured with the other choices:
+//   up to 16  one packet, two CTAs of 64 registers (65,536 x 4,096: 331 us; one CTA 405)
+//   up to 20  two packets, half the warps: two CTAs of 96 registers (32,768 x 5,120: 211
+//             us; one packet and one CTA 243), or without dropout one (207; two 232)
+//   up to 32  two packets, one CTA of 128 registers (16,384 x 8,192: 166 us; one row at a
+//             time in two CTAs of 64 registers 200)
+// then two and four packets with the weights read for each row.
+template <typename T>
+cudaError_t fwd_packets(const BlockNormArgs &a, const DeviceInfo &dev, cudaStream_t s) {
+  constexpr int N = VecWidth<T>::value;
+  BlockPlan p = plan_block_row(a.H, N, 16);
+  if (p.V == 1 && p.W > 16) p = BlockPlan{2, (p.W + 1) / 2, 1};
+  switch (p.V) {
+    case 1: return fwd_rows<T, N, 1, 16, 2>(p, a, dev, s);
+    case 2:
+      if (p.W <= 10) return fwd_rows<T, N, 2, 10, 1, 2>(p, a, dev, s);
+      if (p.W <= 16) return fwd_rows<T, N, 2, 16, 1>(p, a, dev, s);
+      return fwd_rows<T, N, 2, kMaxWarps, 1>(p, a, dev, s);
+    case 4: return fwd_rows<T, N, 4, kMaxWarps, 1>(p, a, dev, s);
+    default: return fwd_any<T>(a, dev, s);
+  }
+}
+
+// Rows of single columns.
+template <typename T>
+cudaError_t fwd_columns(const BlockNormArgs &a, const DeviceInfo &dev, cudaStream_t s) {
+  const BlockPlan p = plan_block_row(a.H, 1, 16);
+  switch (p.V) {
+    case 1: return fwd_rows<T, 1, 1, 16, 2>(p, a, dev, s);
+    case 4:
+      if (p.threads() <= 512) return fwd_rows<T, 1, 4, 16, 2>(p, a, dev, s);
+      return fwd_rows<T, 1, 4, kMaxWarps, 1>(p, a, dev, s);
+    case 8: return fwd_rows<T, 1, 8, kMaxWarps, 1>(p, a, dev, s);
+    default: return fwd_any<T>(a, dev, s);
+  }
+}
+
 template <typename T>
 cudaError_t fwd_typed(bool vec, const BlockNormArgs &a, const DeviceInfo &dev, cudaStream_t s) {
-  cudaError_t e =
-      vec ? fwd_packets<T, VecWidth<T>::value>(a, dev, s) : fwd_packets<T, 1>(a, dev, s);
+  cudaError_t e = vec ? fwd_packets<T>(a, dev, s) : fwd_columns<T>(a, dev, s);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

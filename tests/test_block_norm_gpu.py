@@ -13,7 +13,7 @@ EPS = 1e-5
 SIZES = [(1, 1), (1, 8), (3, 7), (64, 64), (5, 257), (33, 896), (9, 1001), (70, 2048), (4, 4096),
          (7, 5120), (2, 8200), (3, 16384), (2, 20000), (2, 5003), (3, 5131), (2, 20487), (1000, 24),
          (2500, 128), (650, 640), (613, 321), (331, 5120), (400, 5131), (500, 6000), (350, 12000), (320, 18000),
-         (400, 9600), (1300, 4993)]
+         (400, 9600), (1300, 4993), (700, 2500), (310, 4096)]
 
 
 def ftk():
