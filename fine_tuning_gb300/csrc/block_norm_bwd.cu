@@ -21,7 +21,7 @@
 // (65,536 x 5,120: 1,108 us with one, 861 with two, 797 with three), and registers: one
 // CTA an SM of 16 warps with 128 registers a thread takes 264 us for 32,768 x 4,096 (0.91
 // of the copy rate), with 96 346, two CTAs with 64 334.  Rows of 20 warps have 96:
-// 65,536 x 5,120 705 us, 5,710 GB/s, 0.85.  Measured and left: the columns' sums in shared
+// 65,536 x 5,120 705 to 725 us on several GPUs, 5,600 GB/s, 0.84.  Measured and left: the columns' sums in shared
 // memory 739; the first pass of the next row before the second of this one 1,188 against
 // 760.
 #include "block_norm.cuh"

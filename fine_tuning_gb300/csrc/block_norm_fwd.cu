@@ -229,16 +229,18 @@ cudaError_t fwd_any(const BlockNormArgs &a, const DeviceInfo &dev, cudaStream_t 
 //             us; one packet and one CTA 243), or without dropout one (207; two 232)
 //   up to 32  two packets, one CTA of 128 registers (16,384 x 8,192: 166 us; one row at a
 //             time in two CTAs of 64 registers 200)
-// then two and four packets with the weights read for each row.
+// then two and four packets with the weights read for each row.  fp32, with half the
+// arithmetic for the bytes, always has one CTA (32,768 x 2,048: 172 us, two 184; 32,768 x
+// 2,560: 202, two 233).
 template <typename T>
 cudaError_t fwd_packets(const BlockNormArgs &a, const DeviceInfo &dev, cudaStream_t s) {
-  constexpr int N = VecWidth<T>::value;
+  constexpr int N = VecWidth<T>::value, kTwo = sizeof(T) == 2 ? 2 : 1;
   BlockPlan p = plan_block_row(a.H, N, 16);
   if (p.V == 1 && p.W > 16) p = BlockPlan{2, (p.W + 1) / 2, 1};
   switch (p.V) {
-    case 1: return fwd_rows<T, N, 1, 16, 2>(p, a, dev, s);
+    case 1: return fwd_rows<T, N, 1, 16, kTwo>(p, a, dev, s);
     case 2:
-      if (p.W <= 10) return fwd_rows<T, N, 2, 10, 1, 2>(p, a, dev, s);
+      if (p.W <= 10) return fwd_rows<T, N, 2, 10, 1, kTwo>(p, a, dev, s);
       if (p.W <= 16) return fwd_rows<T, N, 2, 16, 1>(p, a, dev, s);
       return fwd_rows<T, N, 2, kMaxWarps, 1>(p, a, dev, s);
     case 4: return fwd_rows<T, N, 4, kMaxWarps, 1>(p, a, dev, s);
