@@ -18,12 +18,12 @@
 // Memory bound by its bytes (four tensors read, two written, 6 es a column), and in fact
 // close to the SM's issue rate: about 450 instructions a packet of eight columns with
 // dropout.  What helped was what gives a warp independent work: two rows at a time
-// (65,536 x 5,120: 1,108 us with one, 861 with two, 797 with three), and registers: one
+// (65,536 x 5,120: 1,061 us with one, 705 with two, 797 with three), and registers: one
 // CTA an SM of 16 warps with 128 registers a thread takes 264 us for 32,768 x 4,096 (0.91
 // of the copy rate), with 96 346, two CTAs with 64 334.  Rows of 20 warps have 96:
-// 65,536 x 5,120 705 to 725 us on several GPUs, 5,600 GB/s, 0.84.  Measured and left: the columns' sums in shared
-// memory 739; the first pass of the next row before the second of this one 1,188 against
-// 760.
+// 65,536 x 5,120 705 to 725 us on several GPUs, 5,600 GB/s, 0.84.  Measured and left: the
+// columns' sums in shared memory 739 against 721; ten warps with two packets a thread 743;
+// the first pass of the next row before the second of this one 1,188 against 760.
 #include "block_norm.cuh"
 
 namespace ftk {

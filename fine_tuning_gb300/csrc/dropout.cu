@@ -1,7 +1,7 @@
 // Dropout of T rows of H features, forward and backward alike:
 //   y[t, j] = keep[t, j] ? x[t, j] * scale : 0,   keep from philox.cuh.
 // Elementwise: 2 es bytes a column, one generator call for eight.  65,535 x 4,096 bf16:
-// 164 us, 6,550 GB/s, 0.98 of the copy rate; 16,384 x 896, which L2 holds, 10.6 us.  The
+// 164 us, 6,550 GB/s, 0.98 of the copy rate; 16,384 x 896, which L2 holds, 10.2 us.  The
 // integer work (some 80 instructions for eight columns) is hidden behind the memory only
 // because a thread stays with its columns: a part of the generator's rounds depends on
 // them alone and is made once (443 us before, by single columns and full rounds).
@@ -58,7 +58,7 @@ dropout_cols(const T *x, int64_t ldx, T *y, int64_t ldy, int64_t rows, int64_t H
 // Rows of whole 16-byte packets: a thread stays with one block of eight columns and
 // walks the rows, kRows of them at a time, all loads first.  `cols` threads lie along a
 // row (gridDim.y such parts make it up), blockDim.x / cols rows side by side.
-constexpr int kRows = 4;
+constexpr int kRows = kRowsTurn;
 
 template <typename T, bool DROP>
 __global__ void __launch_bounds__(kThreads)

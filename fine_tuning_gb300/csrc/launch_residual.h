@@ -18,13 +18,15 @@ struct DropArgs {
 };
 
 // CTAs along the rows for kernels whose threads stay with a packet of columns and walk the
-// rows four at a time (`side` rows of a CTA side by side, `parts` CTAs to a row): 32 an
+// rows three at a time (`side` rows of a CTA side by side, `parts` CTAs to a row): 64 an
 // SM while that leaves a thread two turns, since more CTAs keep the rows in flight closer
-// together, and 8 at least.  Measured, dropout, 8 and 32 an SM: 65,535 x 4,096 bf16 184
-// and 164 us, 16,384 x 896 (7 rows a thread with 8) 10.6 and 12.9.
+// together, and 8 at least.  Measured with 8, 32 and 64 an SM: dropout 65,535 x 4,096 bf16
+// 184, 165 and 164 us, lookup of 65,536 x 4,096 126, 117 and 116; dropout 16,384 x 896 (7
+// rows a thread with 8) with 8 and 32 10.2 and 12.9.
+constexpr int kRowsTurn = 3;
 inline int64_t row_grid(int64_t T, int side, int parts, const DeviceInfo &dev) {
-  const int64_t all = (T + side - 1) / side, two_turns = all / 8;
-  const int64_t least = ((int64_t)dev.sms * 8 + parts - 1) / parts, most = 4 * least;
+  const int64_t all = (T + side - 1) / side, two_turns = all / (2 * kRowsTurn);
+  const int64_t least = ((int64_t)dev.sms * 8 + parts - 1) / parts, most = 8 * least;
   const int64_t grid = two_turns < least ? least : two_turns > most ? most : two_turns;
   return grid < all ? grid : all;
 }
