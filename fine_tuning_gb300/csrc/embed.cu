@@ -258,20 +258,20 @@ __device__ void sort_tokens(const SortParams &a, uint32_t *shared) {
   }
 }
 
-// A row of zeros, by a warp.
-template <int N> __device__ __forceinline__ void zero_row(float *row, int64_t H, int lane) {
-  if constexpr (N % 4 == 0) {
-    for (int64_t c = lane * 4; c < H; c += 128)
-      *reinterpret_cast<float4 *>(row + c) = make_float4(0.f, 0.f, 0.f, 0.f);
-  } else {
-    for (int64_t c = lane; c < H; c += 32) row[c] = 0.f;
-  }
+// A row of zeros, by a warp: 16 bytes a lane from the first aligned column on, whatever
+// the row's alignment.
+__device__ __forceinline__ void zero_row(float *row, int64_t H, int lane) {
+  const int64_t head = min(H, (int64_t)(-(intptr_t)((uintptr_t)row / 4) & 3));
+  const int64_t packets = (H - head) / 4, tail = H - head - 4 * packets;
+  if (lane < head) row[lane] = 0.f;
+  float4 *body = reinterpret_cast<float4 *>(row + head);
+  for (int64_t c = lane; c < packets; c += 32) body[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (lane < tail) row[head + 4 * packets + lane] = 0.f;
 }
 
 // Zeros in the rows that no token names.  CTA z has the rows whose number / 32 is z modulo
 // zero_ctas (present and absent rows gather at different ends of a vocabulary); it marks
 // its rows that the batch names, then its warps fill the others.
-template <int N>
 __device__ void zero_rows(const SortParams &a, uint32_t *flags) {
   const uint32_t z = blockIdx.x - kSortCtas, Z = a.zero_ctas;
   const int log = 31 - __clz(Z);
@@ -294,14 +294,13 @@ __device__ void zero_rows(const SortParams &a, uint32_t *flags) {
   for (uint32_t r = threadIdx.x >> 5; r < mine * 32; r += kSortWarps) {
     const uint64_t v = ((uint64_t)(r >> 5) * Z + z) * 32 + (r & 31);
     if (v < a.zero_rows && !(flags[r >> 5] >> (r & 31) & 1))
-      zero_row<N>(a.dw + v * a.lddw, a.H, lane);
+      zero_row(a.dw + v * a.lddw, a.H, lane);
   }
 }
 
 constexpr size_t kSortShared = sizeof(uint32_t) * (kSortWarps * kDigits + kDigits + kSortWarps);
 static_assert(kSortShared >= kFlagWords * sizeof(uint32_t), "the flags lie in the sort's memory");
 
-template <int N>
 __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads, 2)
 embed_sort(const SortParams a) {
   extern __shared__ uint32_t shared[];
@@ -310,7 +309,7 @@ embed_sort(const SortParams a) {
   if (blockIdx.x < kSortCtas)
     sort_tokens(a, shared);  // the grid's first cluster
   else
-    zero_rows<N>(a, shared);
+    zero_rows(a, shared);
 }
 
 // ------------------------------------------------------------------- the sums
@@ -401,7 +400,7 @@ constexpr int kZeroRows = 4;  // of a zeroing warp
 
 // Zeros in those of a unit's rows that no token names: each of the first lanes looks one
 // id up in the sorted list.
-template <typename T, int N>
+template <typename T>
 __device__ void zero_unseen(const GradParams<T> &a, uint32_t unit) {
   if (unit >= a.zero_units) return;
   const int lane = threadIdx.x & 31;
@@ -414,7 +413,7 @@ __device__ void zero_unseen(const GradParams<T> &a, uint32_t unit) {
   }
   uint32_t todo = __ballot_sync(0xffffffffu, mine && !(lo < a.n && a.key[lo] == v));
   for (; todo != 0; todo &= todo - 1)
-    zero_row<N>(a.dw + (int64_t)(v0 + __ffs(todo) - 1) * a.lddw, a.H, lane);
+    zero_row(a.dw + (int64_t)(v0 + __ffs(todo) - 1) * a.lddw, a.H, lane);
 }
 
 constexpr int kGradBatch = 4;  // rows in flight for a warp
@@ -432,7 +431,7 @@ __global__ void __launch_bounds__(32 * kGradWarps, kGradCtas) embed_grad(const G
     // CTAs 0 .. ctas - 1 hold the `sums` ones at even distances
     const uint32_t before = (uint32_t)((uint64_t)cta * a.sums / a.ctas);
     if ((uint32_t)((uint64_t)(cta + 1) * a.sums / a.ctas) == before) {
-      zero_unseen<T, N>(a, (cta - before) * kGradWarps + (threadIdx.x >> 5));
+      zero_unseen(a, (cta - before) * kGradWarps + (threadIdx.x >> 5));
       return;
     }
     cta = before;
@@ -589,8 +588,8 @@ cudaError_t bwd_typed(const EmbedBwdArgs &a, const DeviceInfo &dev, cudaStream_t
     q.lddw = a.lddw;
     q.H = a.H;
   }
-  (void)blocks_per_sm((const void *)embed_sort<N>, kSortThreads, kSortShared, dev, 2);
-  cudaError_t e = launch_pdl(embed_sort<N>, dim3((unsigned)(kSortCtas + q.zero_ctas)),
+  (void)blocks_per_sm((const void *)embed_sort, kSortThreads, kSortShared, dev, 2);
+  cudaError_t e = launch_pdl(embed_sort, dim3((unsigned)(kSortCtas + q.zero_ctas)),
                              dim3(kSortThreads), kSortShared, s, q);
   if (e != cudaSuccess || a.T == 0) return e != cudaSuccess ? e : cudaGetLastError();
   const int64_t slabs = ceil_div(a.H, (int64_t)kColumns);
