@@ -18,8 +18,8 @@
 //   3. embed_join: the crossing sums are added in the chunks' order.
 //
 // Bound by memory.  Lookup of 65,536 x 4,096 bf16 over 151,936 ids: 116 us, 0.92 of the
-// copy rate with every named row read once.  Gradient: 16,384 x 896 over 151,936 ids 106
-// us, 5,400 GB/s, 0.81; two parts of 32,768 x 5,120, the second accumulated, 734 us, 0.87.
+// copy rate with every named row read once.  Gradient: 16,384 x 896 over 151,936 ids 98
+// us, 5,830 GB/s, 0.87; two parts of 32,768 x 5,120, the second accumulated, 734 us, 0.87.
 // The first form (a launch for each step of the sort, one for the zeros, a CTA a chunk)
 // took 181 and 1,814.  An accumulating call waits for the sort: 20 us for 32,768 tokens.
 #include "common.cuh"
@@ -573,15 +573,17 @@ cudaError_t bwd_typed(const EmbedBwdArgs &a, const DeviceInfo &dev, cudaStream_t
   if (!ACC) {
     // Beside the sort about what it leaves time for (some 10 us, and 0.2 us for each
     // 1,024 tokens, at 6 TB/s); the rest beside the sums, which wait for latencies more
-    // than for memory.  All of it beside the sort where that is not much more: the sums
-    // then have the memory to themselves.  Measured, all beside the sort and split:
-    // 16,384 x 896 (0.5 GB) 106.4 and 107.5 us, 32,768 x 2,048 fp32 over 32,000 ids (0.3
-    // GB) 102 and 107, 333 x 4,096 (2.5 GB) 410 and 352, 2 x 32,768 x 5,120 (3.1 GB) 811
-    // and 738.
+    // than for memory.  All of it beside the sort where that is not much more and the
+    // sums are long enough to want the memory for themselves.  Measured, all beside the
+    // sort and split: 16,384 x 896 (0.5 GB) 98 and 108 us, 32,768 x 2,048 over 32,000 ids
+    // (0.3 GB) 89 and 92; 4,096 x 1,024 over 100,000 (0.4 GB) 81 and 76, 333 x 4,096 (2.5
+    // GB) 410 and 352, 2 x 32,768 x 5,120 (3.1 GB) 811 and 736.
     const int64_t some = kZeroBytes + a.T * 1024, row = 4 * a.H;
-    const int64_t rows = a.V <= 4 * some / row ? a.V : some / row / 32 * 32;
+    const int64_t most = a.T >= 8192 ? 4 * some : some;
+    const int64_t rows = a.V <= most / row ? a.V : some / row / 32 * 32;
     q.zero_rows = (uint32_t)(a.T == 0 ? a.V : rows);
-    q.zero_ctas = 256;  // with the sort's, what two CTAs on each of 152 SMs hold
+    // two waves of two CTAs an SM, which even out (16,384 x 896: 256 106 us, 1,024 102)
+    q.zero_ctas = 512;
     const int64_t words = ceil_div((int64_t)q.zero_rows, (int64_t)32);
     while ((int64_t)q.zero_ctas * kFlagWords < words) q.zero_ctas *= 2;
     q.dw = a.dw;
