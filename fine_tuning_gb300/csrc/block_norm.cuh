@@ -233,13 +233,17 @@ template <int N, int V> struct Mask {
 };
 template <int V> struct Mask<1, V> {
   static_assert(V <= 8, "a warp makes 32 blocks");
-  int thr;
+  PhiloxBlock p;
+  uint32_t cut;
   using Row = uint32_t[V];
-  __device__ __forceinline__ void init(const Philox &, int t, int, int) { thr = t; }
-  __device__ __forceinline__ void row(const Philox &g, uint32_t t, int gi, int G, Row &m) const {
+  __device__ __forceinline__ void init(const Philox &g, int thr, int gi, int G) {
     const int lane = threadIdx.x & 31;
-    const int mine = (gi - lane + (lane >> 2) * G) / 8 + (lane & 3);
-    const uint32_t b = keep_bits(g, thr, (uint32_t)mine, t);
+    cut = keep_cut(thr);
+    p = philox_block(g, (uint32_t)((gi - lane + (lane >> 2) * G) / 8 + (lane & 3)));
+  }
+  __device__ __forceinline__ void row(const Philox &g, uint32_t t, int, int, Row &m) const {
+    const int lane = threadIdx.x & 31;
+    const uint32_t b = keep_bits(philox4x32(g, p, philox_row(g, t)), cut);
 #pragma unroll
     for (int k = 0; k < V; ++k)
       m[k] = __shfl_sync(0xffffffffu, b, k * 4 + (lane >> 3)) >> (lane & 7);

@@ -91,20 +91,20 @@ __device__ __forceinline__ uint32_t keep_cut(int thr) {
 __device__ __forceinline__ bool keep_low(uint32_t word, uint32_t cut) { return word << 16 > cut; }
 __device__ __forceinline__ bool keep_high(uint32_t word, uint32_t cut) { return word > cut; }
 
-// Number e (0..7) of a call's bits.
-__device__ __forceinline__ int philox_u16(const uint4 &u, int e) {
-  const uint32_t w = e < 2 ? u.x : e < 4 ? u.y : e < 6 ? u.z : u.w;
-  return (int)(e & 1 ? w >> 16 : w & 0xffffu);
-}
-
-// Bit e: column 8 block + e of row t is kept.
-__device__ __forceinline__ uint32_t keep_bits(const Philox &g, int thr, uint32_t block,
-                                              uint32_t t) {
-  const uint4 u = philox4x32(g, block, t);
+// Bit e: number e of a call's bits is kept.
+__device__ __forceinline__ uint32_t keep_bits(const uint4 &u, uint32_t cut) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
   uint32_t m = 0;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) m |= philox_u16(u, e) >= thr ? 1u << e : 0u;
+  for (int i = 0; i < 4; ++i) {
+    m |= keep_low(w[i], cut) ? 1u << (2 * i) : 0u;
+    m |= keep_high(w[i], cut) ? 2u << (2 * i) : 0u;
+  }
   return m;
+}
+__device__ __forceinline__ uint32_t keep_bits(const Philox &g, int thr, uint32_t block,
+                                              uint32_t t) {
+  return keep_bits(philox4x32(g, block, t), keep_cut(thr));  // thr >= 1
 }
 
 }  // namespace
