@@ -9,8 +9,8 @@
 //   dgate_tok[t] = c / gate_tok, formed without the division
 // Both row sums come from one pass over the row: with q = m wg xn,
 //   sum q G = sum q (dh + r2 w dy) - k sum q hn.
-// No r^3 is formed, which overflows for rows near zero: each r multiplies a sum of x's or
-// h's that it brings back to the size of one.
+// No product of two r is formed where it may overflow, for rows near zero: each r multiplies
+// an h, an x or a sum of them, which it brings back to the size of one.
 //
 // A CTA's column sums go to its own row of the workspace; a second kernel adds the
 // rows in a fixed order and applies gate and w_post.
@@ -24,6 +24,8 @@
 // 65,536 x 5,120 705 to 725 us on several GPUs, 5,600 GB/s, 0.84.  Measured and left: the
 // columns' sums in shared memory 739 against 721; ten warps with two packets a thread 743;
 // the first pass of the next row before the second of this one 1,188 against 760.
+#include <cfloat>
+
 #include "block_norm.cuh"
 
 namespace ftk {
@@ -99,6 +101,12 @@ block_norm_bwd_rows(const BlockNorm<T> a, const Walk<4> walk_in, const Walk<2> w
   using VT = typename Values<N>::V;
   using Rw = typename Raw<T, N>::type;
   constexpr int P = Values<N>::kCount, B = kBwdRows<N, V>;
+  // One packet a thread: k r2 and am r1 are one factor each where they fit fp32; where they
+  // do not, the row's h and x are multiplied by their r behind a branch, which the whole row
+  // takes alike.  Otherwise they always are.  Measured, the branch and the multiplications
+  // in every row: 65,536 x 5,120 722 and 784 us, 65,536 x 2,048 251 and 258, but 16,384 x
+  // 8,192 340 and 333, 32,767 x 1,001 158 and 155.
+  constexpr bool kOneFactor = N > 1 && V == 1;
   // the weights in registers; else read for each row
   constexpr bool kHold = V * N <= (WARPS > 16 ? 8 : 16);
   extern __shared__ uint4 ring[];  // the rows ahead, then [R][2 H] sums when R > 1
@@ -196,13 +204,15 @@ block_norm_bwd_rows(const BlockNorm<T> a, const Walk<4> walk_in, const Walk<2> w
 #pragma unroll
     for (int b = 0; b < B; ++b) {
       if (b > 0 && t + b * step >= rows) break;
-      const float kr = r2[b] * (r2[b] * (r2[b] * s[3 * b] * a.inv_h));  // k r2
-      const float c1 = beta * (r1[b] * fmaf(-kr, s[3 * b + 2], s[3 * b + 1]));
+      const float kn = r2[b] * (r2[b] * s[3 * b] * a.inv_h);  // k
+      const float c1 = beta * (r1[b] * fmaf(-kn, r2[b] * s[3 * b + 2], s[3 * b + 1]));
       if (a.dgate_tok != nullptr && gi == 0) a.dgate_tok[t + b * step] = c1;
-      const VT r2v = vall<VT>(r2[b]), nkr = vall<VT>(-kr), rs = vall<VT>(a.res_scale);
+      const float am = a.w_post != nullptr ? r1[b] * (gt[b] * c1 * a.inv_h) : 0.f;
+      const bool fits = fabsf(kn * r2[b]) <= FLT_MAX && fabsf(am * r1[b]) <= FLT_MAX;
+      const bool one = kOneFactor && fits, apart = kOneFactor && !fits;
+      const VT r1v = vall<VT>(r1[b]), r2v = vall<VT>(r2[b]), rs = vall<VT>(a.res_scale);
+      const VT nk = vall<VT>(one ? -kn * r2[b] : -kn), nam = vall<VT>(one ? -am * r1[b] : -am);
       const VT bg = vall<VT>(beta * gt[b] * r1[b]);
-      const VT nam =
-          vall<VT>(a.w_post != nullptr ? -r1[b] * (r1[b] * (gt[b] * c1 * a.inv_h)) : 0.f);
 #pragma unroll
       for (int k = 0; k < V; ++k)
         if (V == 1 || on >> k & 1) {
@@ -218,15 +228,33 @@ block_norm_bwd_rows(const BlockNorm<T> a, const Walk<4> walk_in, const Walk<2> w
             for (int i = 0; i < P; ++i) x[i] = mask.keep(m[b], k, i, x[i]);
 #pragma unroll
           for (int i = 0; i < P; ++i) {
-            const VT dyr = vmul(dy[i], r2v);
-            const VT Gv = vfma(nkr, h[i], vfma(wf[i], dyr, dh[i]));
+            if (kOneFactor) {
+              dy[i] = vmul(dy[i], r2v);
+              dh[i] = vfma(wf[i], dy[i], dh[i]);
+            } else {
+              h[i] = vmul(h[i], r2v);
+              dh[i] = vfma(r2v, vmul(wf[i], dy[i]), dh[i]);
+            }
+            sw[k][i] = vfma(dy[i], h[i], sw[k][i]);
+          }
+          if (apart)
+#pragma unroll
+            for (int i = 0; i < P; ++i) h[i] = vmul(h[i], r2v);
+#pragma unroll
+          for (int i = 0; i < P; ++i) {
+            const VT Gv = vfma(nk, h[i], dh[i]);
             VT gm = vmul(bg, Gv);  // beta gate_tok r1 m G
             if (DROP) gm = mask.keep(m[b], k, i, gm);
-            sw[k][i] = vfma(dyr, h[i], sw[k][i]);
             sx[k][i] = vfma(gm, x[i], sx[k][i]);
             dh[i] = vmul(rs, Gv);
-            x[i] = vfma(nam, x[i], vmul(gm, kHold ? wg[kHold ? k : 0][i] : f[i]));
+            h[i] = vmul(gm, kHold ? wg[kHold ? k : 0][i] : f[i]);
           }
+          if (apart)
+#pragma unroll
+            for (int i = 0; i < P; ++i) x[i] = vmul(x[i], r1v);
+#pragma unroll
+          for (int i = 0; i < P; ++i)
+            x[i] = vfma(nam, kOneFactor ? x[i] : vmul(x[i], r1v), h[i]);
           Rw oh, ox;
           pack(dh, oh);
           pack(x, ox);
