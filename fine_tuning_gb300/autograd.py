@@ -245,14 +245,12 @@ class BlockRMSNorm(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dh, dy):
         *saved, step = ctx.saved_tensors
-        w_post, gate = saved[5:7]
-        dx, dres, dw, dw_post, dgate, dgate_tok = ftk.rmsnorm_block_bwd(
-            dy.contiguous(), dh.contiguous(), *saved, *ctx.numbers, step)
-        dw = dw.to(saved[2].dtype)
-        if dw_post is not None:
-            dw_post = dw_post.to(w_post.dtype)
-        if dgate is not None:
-            dgate = dgate.to(gate.dtype)
+        dx, dres, *sums = ftk.rmsnorm_block_bwd(dy.contiguous(), dh.contiguous(), *saved,
+                                                *ctx.numbers, step)
+        # of w, w_post, gate, gate_tok, which may have any shape of as many values
+        dw, dw_post, dgate, dgate_tok = (
+            None if g is None else g.to(f.dtype).view_as(f)
+            for g, f in zip(sums, (saved[2], *saved[5:8])))
         return dx, dres, dw, None, dw_post, dgate, dgate_tok, *([None] * 6)
 
 
