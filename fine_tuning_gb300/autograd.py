@@ -195,7 +195,8 @@ class CrossEntropyHead(torch.autograd.Function):
 
 class Dropout(torch.autograd.Function):
     """ftk.dropout_fwd; the mask is made again in the backward pass, from the same
-    step (torch refuses the backward when step was changed in between)."""
+    step (torch refuses the backward when step was changed in between).  Offsets of
+    one seed lie further apart than the run has steps: a mask depends on the sum."""
 
     @staticmethod
     def forward(ctx, x, p: float, seed: int, offset: int = 0, step=None):

@@ -11,7 +11,7 @@ namespace ftk {
 // What a dropout mask is made from (philox.cuh); thr == 0: no dropout.
 struct DropArgs {
   uint32_t k0 = 0, k1 = 0;        // the seed's halves
-  uint64_t offset = 0;
+  uint64_t offset = 0;            // further from another's than the run has steps
   const int64_t *step = nullptr;  // DEVICE, nullable: added to offset
   int thr = 0;                    // of 65536: elements whose number is below are dropped
   float scale = 1.f;              // 65536 / (65536 - thr), 0 when everything is dropped

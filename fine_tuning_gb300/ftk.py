@@ -811,7 +811,9 @@ def dropout_fwd(x: torch.Tensor, p: float, seed: int, offset: int = 0,
     The mask is a function of seed, offset + step, row and column, and is
     never stored; p counts in steps of 2^-16.  step: int64 [1] on the device,
     read when the kernel runs (advance it between replays of a captured
-    graph; the backward needs the same value).  y=x drops in place."""
+    graph; the backward needs the same value).  Only the sum counts: keep the
+    offsets of one seed further apart than the run has steps (n << 40 for
+    dropout n), or neighbours repeat one another's masks.  y=x drops in place."""
     return _dropout("ftk_dropout_fwd", x, p, seed, offset, step, y, "y")
 
 

@@ -535,10 +535,14 @@ FTK_API ftk_status ftk_attn_bwd(const void *do_, int64_t ld_do, const void *q, i
  * T or the device.  A dropped element is 0 whatever x holds there (inf and NaN
  * included).  Probabilities count in steps of 2^-16 (p below 2^-17 drops
  * nothing), and the scale is that of the probability as counted.
- * offset: tells the dropouts of one seed apart (a layer's number, say);
+ * offset: tells the dropouts of one seed apart;
  * step: DEVICE int64, nullable, 8-byte aligned, read when the kernel runs: a
  * captured graph makes new masks when the value is advanced between replays.
  * The backward needs the same value.
+ * Only the sum offset + *step counts: offset 1 at step 0 and offset 0 at step 1
+ * give the same mask.  So either the offsets of one seed lie further apart than
+ * the run has steps (dropout n of a step: n << 40), or *step advances by the number
+ * of a step's dropouts.
  * x [T, ldx], y [T, ldy]; y may be x exactly (same pointer and stride), otherwise
  * they must not overlap; step overlaps neither.  0 <= p <= 1, T < 2^31,
  * H < 2^23, else FTK_ERR_SHAPE. */

@@ -82,3 +82,16 @@ def test_the_examples_gradients():
     ref = dict(zip(leaf, torch.autograd.grad(loss, list(leaf.values()))))
     for name, got in (("W", names["dW"] - base), ("w", names["dw"]), ("w_next", names["dw_next"])):
         assert (got - ref[name]).abs().max() <= 1e-10 * ref[name].abs().max(), name
+
+
+def test_the_examples_masks_differ_between_dropouts_and_steps():
+    seen = run()[3]
+    a, b = seen[:2]
+    assert sorted(seen) == sorted([a, a, b, b])  # each backward has its forward's
+    assert abs(a - b) >= 2 ** 32  # more than the steps of any run
+    masks = [R.keep_mask(64, 64, P, SEED, offset, step) for offset in (a, b) for step in (0, 1, 2)]
+    for i, one in enumerate(masks):
+        for other in masks[i + 1:]:
+            # two independent masks agree in (1 - p)^2 + p^2 = 0.82 of the places; 64 x 64 places
+            # have a standard deviation of 0.006
+            assert (one == other).double().mean() < 0.9
