@@ -860,7 +860,7 @@ def embed_bwd(dx: torch.Tensor, ids: torch.Tensor, V: int, scale: float = 1.0,
     """dW fp32 [V, H]: scale * the sum of dx [T, H] over each id's tokens, in
     their order (bitwise reproducible).  Overwrites dW, zeros in the rows of no
     token; with accumulate it adds to the rows that tokens name (of an earlier
-    batch, or of a tied head's cce_bwd)."""
+    batch, or of a tied head's cce_bwd; values below 2^-126 count as zero there)."""
     lddx, T = _ld(dx, "dx"), _ids(ids)
     dev = _same_device(dx, ids, dW, workspace)
     V, H = int(V), dx.shape[1]

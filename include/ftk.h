@@ -577,7 +577,9 @@ FTK_API size_t ftk_embed_bwd_workspace_bytes(int64_t T, int64_t H, int64_t V);
  * dW fp32 [V, lddw]: accumulate == 0 overwrites every row (zeros in the rows that
  * no token names, T = 0 included); accumulate != 0 adds g to the rows that a token
  * names and leaves the others as they are, so that several batches, or a tied LM
- * head (ftk_cce_bwd's dW), share one gradient.  Sums are fp32 in a fixed order
+ * head (ftk_cce_bwd's dW), share one gradient.  The addition counts values below
+ * 2^-126 as zero: in g, in what the row holds and in their sum (the overwriting form
+ * keeps them).  Sums are fp32 in a fixed order
  * (by t, in stretches of 16 tokens or more of the list sorted by id whose sums
  * are then added in turn): bitwise reproducible, on any device.  Columns past H
  * of a row are left as they were.  workspace: >= ftk_embed_bwd_workspace_bytes(T, H, V) bytes, 16-byte
