@@ -277,6 +277,7 @@ __device__ void zero_rows(const SortParams &a, uint32_t *flags) {
   const int log = 31 - __clz(Z);
   const uint32_t words = (uint32_t)(((uint64_t)a.zero_rows + 31) / 32);
   const uint32_t mine = z < words ? (words - z - 1) / Z + 1 : 0;
+  if (mine == 0) return;  // no rows: nothing to look the ids through for
   for (uint32_t i = threadIdx.x; i < mine; i += kSortThreads) flags[i] = 0;
   __syncthreads();
   for (uint32_t i = threadIdx.x; i < a.n; i += kSortThreads * 8) {
