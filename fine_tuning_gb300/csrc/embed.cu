@@ -98,6 +98,7 @@ constexpr int kSortThreads = 512;  // a thread for each digit
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortCtas = 8;       // of the cluster
 constexpr int64_t kZeroBytes = 128 << 20;  // written beside the sort at least
+constexpr int64_t kLongSums = 12 << 20;    // elements of dx
 constexpr int kFlagWords = 8192;   // of a zeroing CTA: 32 rows each
 constexpr int kColumns = 256;      // of a warp of embed_grad
 
@@ -574,16 +575,16 @@ cudaError_t bwd_typed(const EmbedBwdArgs &a, const DeviceInfo &dev, cudaStream_t
     q.tok[i] = (uint32_t *)(ws + p.off_tok[i]);
   }
   if (!ACC) {
-    // Beside the sort about what it leaves time for (some 10 us, and 0.2 us for each
-    // 1,024 tokens, at 6 TB/s); the rest beside the sums, which wait for latencies more
-    // than for memory.  All of it beside the sort where that is not much more and the
-    // sums are long enough to want the memory for themselves.  Measured, all beside the
-    // sort and split: 16,384 x 896 (0.5 GB) 98 and 108 us, 32,768 x 2,048 over 32,000 ids
-    // (0.3 GB) 89 and 92; 4,096 x 1,024 over 100,000 (0.4 GB) 81 and 76, 333 x 4,096 (2.5
-    // GB) 410 and 352, 2 x 32,768 x 5,120 (3.1 GB) 811 and 736.
+    // Long sums want the memory for themselves: all of the zeros beside the sort.  Shorter
+    // ones wait for latencies more than for memory: beside the sort about what it leaves time
+    // for (some 10 us, and 0.2 us for each 1,024 tokens, at 6 TB/s), the rest beside the sums.
+    // Measured, all beside the sort and split, over 151,936 ids: 2,048 x 1,024 112 and 102 us,
+    // 4,096 x 2,048 204 and 195, 8,192 x 1,024 115 and 109; 12,288 x 1,024 110 and 113 (ids
+    // spread evenly 113 and 113), 4,096 x 4,096 364 and 380, 16,384 x 896 99 and 107, 32,768 x
+    // 5,120 526 and 556.  They meet at some 12 million elements, whatever the table's size.
     const int64_t some = kZeroBytes + a.T * 1024, row = 4 * a.H;
-    const int64_t most = a.T >= 8192 ? 4 * some : some;
-    const int64_t rows = a.V <= most / row ? a.V : some / row / 32 * 32;
+    const bool all = a.T * a.H >= kLongSums || a.V <= some / row;
+    const int64_t rows = all ? a.V : some / row / 32 * 32;
     q.zero_rows = (uint32_t)(a.T == 0 ? a.V : rows);
     // two waves of two CTAs an SM, which even out (16,384 x 896: 256 106 us, 1,024 102)
     q.zero_ctas = 512;
