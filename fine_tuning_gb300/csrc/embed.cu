@@ -302,6 +302,7 @@ __device__ void zero_rows(const SortParams &a, uint32_t *flags) {
 
 constexpr size_t kSortShared = sizeof(uint32_t) * (kSortWarps * kDigits + kDigits + kSortWarps);
 static_assert(kSortShared >= kFlagWords * sizeof(uint32_t), "the flags lie in the sort's memory");
+static_assert(kSortShared <= 48 << 10, "what a launch may have without asking");
 
 __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads, 2)
 embed_sort(const SortParams a) {
@@ -561,7 +562,7 @@ __global__ void __launch_bounds__(32 * kGradWarps) embed_join(const GradParams<T
 }
 
 template <typename T, int N, bool ACC>
-cudaError_t bwd_typed(const EmbedBwdArgs &a, const DeviceInfo &dev, cudaStream_t s) {
+cudaError_t bwd_typed(const EmbedBwdArgs &a, cudaStream_t s) {
   const EmbedPlan p = plan_embed(a.T, a.H, a.V);
   unsigned char *const ws = (unsigned char *)a.ws;
   SortParams q{};
@@ -594,7 +595,6 @@ cudaError_t bwd_typed(const EmbedBwdArgs &a, const DeviceInfo &dev, cudaStream_t
     q.lddw = a.lddw;
     q.H = a.H;
   }
-  (void)blocks_per_sm((const void *)embed_sort, kSortThreads, kSortShared, dev, 2);
   cudaError_t e = launch_pdl(embed_sort, dim3((unsigned)(kSortCtas + q.zero_ctas)),
                              dim3(kSortThreads), kSortShared, s, q);
   if (e != cudaSuccess || a.T == 0) return e != cudaSuccess ? e : cudaGetLastError();
@@ -616,8 +616,8 @@ cudaError_t bwd_typed(const EmbedBwdArgs &a, const DeviceInfo &dev, cudaStream_t
 }
 
 template <typename T, int N>
-cudaError_t bwd_acc(const EmbedBwdArgs &a, const DeviceInfo &dev, cudaStream_t s) {
-  return a.accumulate ? bwd_typed<T, N, true>(a, dev, s) : bwd_typed<T, N, false>(a, dev, s);
+cudaError_t bwd_acc(const EmbedBwdArgs &a, cudaStream_t s) {
+  return a.accumulate ? bwd_typed<T, N, true>(a, s) : bwd_typed<T, N, false>(a, s);
 }
 
 }  // namespace
@@ -633,10 +633,9 @@ cudaError_t launch_embed_fwd(DType dt, bool vec, const EmbedFwdArgs &a, const De
   return vec ? fwd_typed<bf16, 8>(a, dev, s) : fwd_typed<bf16, 1>(a, dev, s);
 }
 
-cudaError_t launch_embed_bwd(DType dt, bool vec, const EmbedBwdArgs &a, const DeviceInfo &dev,
-                             cudaStream_t s) {
-  if (dt == DType::F32) return vec ? bwd_acc<float, 4>(a, dev, s) : bwd_acc<float, 1>(a, dev, s);
-  return vec ? bwd_acc<bf16, 8>(a, dev, s) : bwd_acc<bf16, 1>(a, dev, s);
+cudaError_t launch_embed_bwd(DType dt, bool vec, const EmbedBwdArgs &a, cudaStream_t s) {
+  if (dt == DType::F32) return vec ? bwd_acc<float, 4>(a, s) : bwd_acc<float, 1>(a, s);
+  return vec ? bwd_acc<bf16, 8>(a, s) : bwd_acc<bf16, 1>(a, s);
 }
 
 }  // namespace ftk

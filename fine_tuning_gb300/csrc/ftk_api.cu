@@ -1138,11 +1138,8 @@ FTK_API ftk_status ftk_embed_bwd(const void *dx, int64_t lddx, const int32_t *id
     if (any_overlap(vdw, {vdx, vi, vws}) || any_overlap(vws, {vdx, vi})) return FTK_ERR_ALIAS;
   }
   const bool vec = all_aligned({dx, dw}, 16) && packets({H, lddx}, 16 / es) && lddw % 4 == 0;
-  ftk::DeviceInfo dev;
-  cudaError_t e = device_info(&dev);
-  if (e != cudaSuccess) return cuda_fail(e);
   const ftk::EmbedBwdArgs a{dx, lddx, ids, dw, lddw, V, T, H, scale, accumulate != 0, workspace};
-  return finish(ftk::launch_embed_bwd(dt, vec, a, dev, (cudaStream_t)stream));
+  return finish(ftk::launch_embed_bwd(dt, vec, a, (cudaStream_t)stream));
 }
 
 FTK_API ftk_status ftk_rmsnorm_block_fwd(const void *x, int64_t ldx, const void *res,

@@ -67,8 +67,7 @@ struct EmbedBwdArgs {
 };
 // Does not depend on the device: a plan of the sizes alone.
 size_t embed_bwd_workspace_bytes(int64_t T, int64_t H, int64_t V);
-cudaError_t launch_embed_bwd(DType dt, bool vec, const EmbedBwdArgs &a, const DeviceInfo &dev,
-                             cudaStream_t s);
+cudaError_t launch_embed_bwd(DType dt, bool vec, const EmbedBwdArgs &a, cudaStream_t s);
 
 // The joint h = res_scale res + x_scale dropout(gate gate_tok norm(x)), y = norm(h).
 struct BlockNormArgs {
