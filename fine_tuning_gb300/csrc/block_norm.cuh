@@ -140,10 +140,10 @@ __device__ __forceinline__ void row_barrier(int g, int threads) {
 }
 
 // Packets of 16 bytes: as few a thread as fit, so that the columns' sums and weights stay
-// in registers (backward 65,536 x 5,120: one a thread 879 us, two 1,160).  Single columns:
+// in registers (backward 65,536 x 5,120: one a thread 716 us, two 1,046).  Single columns:
 // four a thread where the row has them, since a warp makes the random numbers of 256
-// columns at a time (backward 32,767 x 1,001: four 180 us, two 252, eight, which spill,
-// 257).  Short rows share a CTA of up to `warps`.
+// columns at a time (32,767 x 1,001: backward two 234 us, four 155, eight 151, forward
+// four 112, eight 116).  Short rows share a CTA of up to `warps`.
 inline BlockPlan plan_block_row(int64_t H, int N, int warps) {
   for (int v = N == 1 && H > 32 ? 4 : 1; v <= (N == 1 ? 8 : 4); v *= 2) {
     const int64_t W = ceil_div(H / N, (int64_t)32 * v);

@@ -16,14 +16,24 @@
 // rows in a fixed order and applies gate and w_post.
 //
 // Memory bound by its bytes (four tensors read, two written, 6 es a column), and in fact
-// close to the SM's issue rate: about 450 instructions a packet of eight columns with
-// dropout.  What helped was what gives a warp independent work: two rows at a time
-// (65,536 x 5,120: 1,061 us with one, 705 with two, 797 with three), and registers: one
-// CTA an SM of 16 warps with 128 registers a thread takes 264 us for 32,768 x 4,096 (0.91
-// of the copy rate), with 96 346, two CTAs with 64 334.  Rows of 20 warps have 96:
-// 65,536 x 5,120 705 to 725 us on several GPUs, 5,600 GB/s, 0.84.  Measured and left: the
-// columns' sums in shared memory 739 against 721; ten warps with two packets a thread 743;
-// the first pass of the next row before the second of this one 1,188 against 760.
+// close to the SM's issue rate with dropout: 400 to 460 instructions a packet of eight
+// columns.  What helped was what gives a warp independent work: two rows at a time
+// (65,536 x 5,120: 1,146 us with one, 716 with two; in an earlier form 797 with three beside
+// 705), and registers: one CTA an SM of 16 warps with 128 registers a thread takes 264 us
+// for 32,768 x 4,096 (0.91 of the copy rate), with 96 327, in an earlier form two CTAs with
+// 64 334.  Rows of 20 warps have 96: 65,536 x 5,120 716 to 725 us on several GPUs, 5,600
+// GB/s, 0.84; 32,768 x 4,608 348, 0.78.  Wider rows take two packets a thread and one row
+// at a time, for lack of registers: 16,384 x 8,192 333 us, 0.72; 32,768 x 5,376 527, 0.60.
+// Without dropout: 16,384 x 896 32 us (0.82; with it 38.4, 0.68), 32,768 x 4,096 244 (0.99),
+// 65,536 x 5,120 650 (0.93), 16,384 x 8,192 298 (0.81), 32,768 x 5,376 468 (0.68).  fp32 with
+// dropout: 32,768 x 2,048 243 us (0.99), 32,768 x 4,096 (two packets a thread) 583 (0.83).
+// Measured in earlier forms and left: the columns' sums in shared memory 739 against 721;
+// ten warps with two packets a thread and two rows 743; the first pass of the next row
+// before the second of this one 1,188 against 760.
+//
+// Spills (bytes a thread, -Xptxas -v): bf16 by four packets a thread with dropout 156 with 16
+// warps and 412 with 20, without 0 and 108; by two packets with 20 warps 52 and 16; single
+// columns by eight with 20 warps 336 and up to 152; fp32 by four packets with dropout 16.
 #include <cfloat>
 
 #include "block_norm.cuh"
@@ -36,7 +46,7 @@ constexpr int kThreads = 512;
 constexpr int kMaxBlocksPerSm = 2;  // each has its row of the workspace
 
 // Rows of any length and alignment: a CTA walks one row at a time, twice (4,095 x 5,131
-// bf16: 264 us, 960 GB/s).
+// bf16: 265 us, 950 GB/s).
 template <typename T>
 __global__ void __launch_bounds__(kThreads, kMaxBlocksPerSm)
 block_norm_bwd_any(const BlockNorm<T> a) {
@@ -92,8 +102,8 @@ template <int V, int WARPS> constexpr int kBwdDepth =
     V == 1 ? 5 : V == 2 ? (WARPS > 16 ? 2 : 3) : 1;
 
 // One CTA an SM, of up to WARPS warps: 16 (128 registers a thread) or 20 (96), by the
-// plan's threads.  Measured, 16 and 20 for rows that 16 hold: 32,768 x 4,096 264 and 346
-// us, 65,536 x 2,048 251 and 290, 16,384 x 8,192 325 and 401, 4,095 x 1,001 26.0 and 29.4.
+// plan's threads.  Measured, 16 and 20 for rows that 16 hold: 32,768 x 4,096 264 and 327
+// us, 65,536 x 2,048 251 and 300, 16,384 x 8,192 333 and 441, 4,095 x 1,001 25.9 and 28.2.
 template <typename T, int N, int V, bool DROP, int WARPS>
 __global__ void __launch_bounds__(32 * WARPS, 1)
 block_norm_bwd_rows(const BlockNorm<T> a, const Walk<4> walk_in, const Walk<2> walk_out, int W,

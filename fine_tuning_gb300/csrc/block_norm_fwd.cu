@@ -224,7 +224,9 @@ cudaError_t fwd_any(const BlockNormArgs &a, const DeviceInfo &dev, cudaStream_t 
 
 // Rows of whole packets, by the warps that they take with one packet a thread; with
 // dropout, measured with the other choices:
-//   up to 16  one packet, two CTAs of 64 registers (65,536 x 4,096: 331 us; one CTA 405)
+//   up to 16  one packet, two CTAs of 64 registers (65,536 x 4,096: 331 us; one CTA 405).
+//             Without dropout two and one: 16,384 x 896 19.6 and 22.2 us, 32,768 x 3,200 139
+//             and 149, but 65,536 x 2,048 189 and 166, 65,536 x 4,096 366 and 342
 //   up to 20  two packets, half the warps: two CTAs of 96 registers (32,768 x 5,120: 211
 //             us; one packet and one CTA 243), or without dropout one (207; two 232)
 //   up to 32  two packets, one CTA of 128 registers (16,384 x 8,192: 166 us; one row at a

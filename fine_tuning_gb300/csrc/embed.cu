@@ -17,11 +17,16 @@
 //      the batch;
 //   3. embed_join: the crossing sums are added in the chunks' order.
 //
-// Bound by memory.  Lookup of 65,536 x 4,096 bf16 over 151,936 ids: 116 us, 0.92 of the
-// copy rate with every named row read once.  Gradient: 16,384 x 896 over 151,936 ids 98
-// us, 5,830 GB/s, 0.87; two parts of 32,768 x 5,120, the second accumulated, 734 us, 0.87.
-// The first form (a launch for each step of the sort, one for the zeros, a CTA a chunk)
-// took 181 and 1,814.  An accumulating call waits for the sort: 20 us for 32,768 tokens.
+// Bound by memory, over 151,936 ids: lookup of 65,536 x 4,096 bf16 116 us, 0.92 of the copy
+// rate with every named row read once; of 32,768 x 4,096 fp32 128 us, 0.88; rows that are
+// not whole packets move two bytes at a time (32,767 x 1,001 49 us, 0.28).  Gradient: 16,384
+// x 896 98 us, 5,830 GB/s, 0.87; two parts of 32,768 x 5,120, the second accumulated, 726
+// us, 0.88; fp32 16,384 x 896 105 us (0.86), 32,768 x 4,096 460 (0.98); bf16 32,767 x 1,001
+// 156 (0.65).  The first form (a launch for each step of the sort, one for the zeros, a CTA
+// a chunk) took 181 and 1,814 for the first two.  What does not scale: the sort is eight
+// CTAs, for which an accumulating call waits (20 us for 32,768 tokens; 524,288 x 896 537 us,
+// 0.52), and a run of one id is joined by one warp for 256 columns (131,072 x 896 191 us,
+// with 30% of the batch one id 240).  Spills of embed_grad: 4 to 28 bytes a thread.
 #include "common.cuh"
 #include "launch_residual.h"
 #include "raw_packet.cuh"

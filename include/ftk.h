@@ -579,12 +579,12 @@ FTK_API size_t ftk_embed_bwd_workspace_bytes(int64_t T, int64_t H, int64_t V);
  * names and leaves the others as they are, so that several batches, or a tied LM
  * head (ftk_cce_bwd's dW), share one gradient.  The addition counts values below
  * 2^-126 as zero: in g, in what the row holds and in their sum (the overwriting form
- * keeps them).  Sums are fp32 in a fixed order
- * (by t, in stretches of 16 tokens or more of the list sorted by id whose sums
- * are then added in turn): bitwise reproducible, on any device.  Columns past H
- * of a row are left as they were.  workspace: >= ftk_embed_bwd_workspace_bytes(T, H, V) bytes, 16-byte
- * aligned, contents ignored and clobbered; calls that overlap on the GPU need one
- * each.  dW, workspace and the inputs must not overlap.  Limits as above. */
+ * keeps them).  Sums are fp32 in a fixed order (by t, in stretches of 16 tokens or
+ * more of the list sorted by id whose sums are then added in turn): bitwise
+ * reproducible, on any device.  Columns past H of a row are left as they were.
+ * workspace: >= ftk_embed_bwd_workspace_bytes(T, H, V) bytes, 16-byte aligned,
+ * contents ignored and clobbered; calls that overlap on the GPU need one each.  dW,
+ * workspace and the inputs must not overlap.  Limits as above. */
 FTK_API ftk_status ftk_embed_bwd(const void *dx, int64_t lddx, const int32_t *ids, float *dw,
                                  int64_t lddw, int64_t V, int64_t T, int64_t H, float scale,
                                  int32_t accumulate, void *workspace, size_t workspace_bytes,
