@@ -2,10 +2,10 @@
 //   y[t, j] = keep[t, j] ? x[t, j] * scale : 0,   keep from philox.cuh.
 // Elementwise: 2 es bytes a column, one generator call for eight.  65,535 x 4,096 bf16:
 // 164 us, 6,550 GB/s, 0.98 of the copy rate; 16,384 x 896, which L2 holds, 10.2 us.  fp32:
-// 327 us (0.98) and 19.1 (0.92).  The
-// integer work (some 80 instructions for eight columns) is hidden behind the memory only
-// because a thread stays with its columns: a part of the generator's rounds depends on
-// them alone and is made once (443 us before, by single columns and full rounds).
+// 327 us (0.98) and 19.1 (0.92).  The integer work (some 80 instructions for eight columns)
+// is hidden behind the memory only because a thread stays with its columns: a part of the
+// generator's rounds depends on them alone and is made once (443 us before, by single
+// columns and full rounds).
 #include "common.cuh"
 #include "launch_residual.h"
 #include "philox.cuh"

@@ -385,8 +385,8 @@ template <typename T, int N> struct Slab {
 // dW's row gets scale * acc, with ACC added to what it holds: by a reduction in L2, which
 // needs no answer.  Each element gets one such addition in a call, so that no order can
 // change the result.  fp32 reductions in global memory flush subnormal operands and results
-// to zero, which the header states.  Measured, and with a load, an addition and a store: 32,768 x 5,120
-// 186 and 198 us, 131,072 x 4,096 429 and 507.
+// to zero, which the header states.  Measured, and with a load, an addition and a store:
+// 32,768 x 5,120 186 and 198 us, 131,072 x 4,096 429 and 507.
 template <typename T, int N, bool ACC, typename VT>
 __device__ __forceinline__ void finish_row(float *row, const Slab<T, N> &s,
                                            const VT (&acc)[Slab<T, N>::U][Values<N>::kCount],
